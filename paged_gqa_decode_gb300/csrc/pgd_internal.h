@@ -85,7 +85,13 @@ inline int short_row_tiles(int head_dim, int max_pages) {
 }
 
 // Padded query-group sizes that have a decode kernel instantiation.
-int padded_group(int group);  // 0 if unsupported
+inline int padded_group(int group) {  // 0 if unsupported
+  if (group == 1) return 1;
+  if (group == 2) return 2;
+  if (group >= 3 && group <= 4) return 4;
+  if (group >= 5 && group <= 8) return 8;
+  return 0;
+}
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 
