@@ -1,12 +1,13 @@
 """Paged grouped-query decode attention for GB300 (sm_103a).
 
-A thin binding over libpgd's C ABI (include/pgd.h): it turns torch tensors
-into device pointers, sizes and the current CUDA stream, and nothing else.
-Every step of the computation runs in the library's CUDA kernels; there is
-no CPU or PyTorch fallback, and every call fails loudly if the library is
-missing or the tensors are not on a CUDA device.
+A thin binding over the C ABIs of libpgd (include/pgd.h) and libpgd_ext
+(include/pgd_ext.h): it turns torch tensors into device pointers, sizes and
+the current CUDA stream, and nothing else.  Every step of the computation runs
+in the libraries' CUDA kernels; there is no CPU or PyTorch fallback, and every
+call fails loudly if a library is missing or the tensors are not on a CUDA
+device.
 
-Entry points (same names as the C ABI, without the ``pgd_`` prefix):
+Entry points (same names as the C ABI, without the ``pgd_`` / ``pgdx_`` prefix):
 
 - ``kv_append_paged``: write each row's new key and value at its page slot.
 - ``paged_decode_attention``: grouped-query decode attention of each row over
@@ -16,6 +17,10 @@ Entry points (same names as the C ABI, without the ``pgd_`` prefix):
   prompt tokens (prefill) and prompts plus decode steps in one pass.
 - ``kv_append_rows``, ``decode_rows_attention``: the same step over dense
   per-row caches [Batch, KvHeads, MaxSeq, D] (decode_rows).
+- ``assign_pages``: block-table entries, slots, rows and positions of a pass
+  from the requests' lengths.
+- ``rotary_append_paged``: rotary positions (``Rotary``: half or interleaved
+  pairs, part of the head, scaled frequencies) fused with the append.
 - ``paged_decode_workspace_bytes``, ``get_device_error``.
 """
 from __future__ import annotations
@@ -24,6 +29,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -36,9 +42,11 @@ OK, EINVAL, EUNSUPPORTED, ECUDA, EDEVICE_BOUNDS, EDEVICE_TIMEOUT, EWORKSPACE = r
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libpgd.so")
+EXT_PATH = os.path.join(_PKG, "_build", "libpgd_ext.so")
 
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 
 class PgdError(RuntimeError):
@@ -116,6 +124,46 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             lib.pgd_version.restype = ctypes.c_int
             _lib = lib
     return _lib
+
+
+class RotaryConfig(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "rotary_dim", "interleaved", "scaling", "exact_bounds")] + [
+        (name, ctypes.c_double) for name in (
+            "theta", "factor", "original_positions", "beta_fast", "beta_slow", "low_band",
+            "high_band", "attention_factor")]
+
+
+class RotaryPlan(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+def load_extension(path: str | None = None) -> ctypes.CDLL:
+    """Loads libpgd_ext.so (built beside libpgd.so); raises if absent."""
+    global _ext
+    if _ext is None:
+        with _lock:
+            if _ext is None:
+                path = path or EXT_PATH
+                if not os.path.exists(path):
+                    raise RuntimeError(
+                        f"libpgd_ext is not built ({path} missing): run "
+                        "`python -c 'import __graft_entry__ as g; g.build()'`")
+                lib = ctypes.CDLL(path)
+                vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+                dims_p = ctypes.POINTER(Dims)
+                plan_p = ctypes.POINTER(RotaryPlan)
+                lib.pgdx_assign_pages.argtypes = [i32] * 4 + [vp] * 4 + [i32] + [vp] * 8
+                lib.pgdx_rotary_init.argtypes = [ctypes.POINTER(RotaryConfig), plan_p]
+                lib.pgdx_rotary_append.argtypes = [dims_p, plan_p, vp, i64, vp, vp, i64, vp, i64,
+                                                   vp, i32, vp, vp, vp, vp, vp, vp]
+                lib.pgdx_get_device_error.argtypes = [vp]
+                for name in ("assign_pages", "rotary_init", "rotary_append", "get_device_error"):
+                    getattr(lib, "pgdx_" + name).restype = ctypes.c_int
+                _ext = lib
+    return _ext
 
 
 def status_string(status: int) -> str:
@@ -586,5 +634,173 @@ def selftest_bounded_wait(stream: torch.cuda.Stream | None = None) -> tuple[int,
 
 
 def get_device_error(stream: torch.cuda.Stream | None = None) -> int:
-    """Synchronises the stream and returns (and clears) the device error word."""
-    return load_library().pgd_get_device_error(_stream_handle(stream))
+    """Synchronises the stream and returns (and clears) the device error words
+    of libpgd and, where it is in use, libpgd_ext (the first that is set)."""
+    handle = _stream_handle(stream)
+    status = load_library().pgd_get_device_error(handle)
+    if _ext is not None:
+        ext = _ext.pgdx_get_device_error(handle)
+        status = status if status != OK else ext
+    return status
+
+
+# ---------------------------------------------------------------------------
+# A step's set-up on the GPU (libpgd_ext).
+
+class PagePlan(NamedTuple):
+    """What assign_pages makes, int32 on the GPU: per token of the packed pass
+    its table row, position and pool slot (padding: 0, -1, -1); per request its
+    first token (and the tokens' count) and its length after the pass; the index
+    of the next free page."""
+    rows: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    starts: torch.Tensor
+    lengths: torch.Tensor
+    free_head: torch.Tensor
+
+
+def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Tensor,
+                 free_pages: torch.Tensor, *, num_tokens: int, num_pages: int,
+                 free_head: torch.Tensor | None = None, out: PagePlan | None = None,
+                 stream: torch.cuda.Stream | None = None) -> PagePlan:
+    """Gives each request the pages of its new tokens and lays out the pass.
+
+    table: int32 [R, W], its new entries written in place; cached, new_tokens:
+    int32 [R], positions in the cache and positions of this pass; free_pages:
+    int32 [F], handed out in order from free_head (int32 [1] or None for 0);
+    num_tokens: the packed pass's fixed token count (the rest is padding);
+    num_pages: the pool's pages.  Requests that do not fit are left out and
+    reported (get_device_error: EDEVICE_BOUNDS).  ``out`` reuses a plan."""
+    dev = _check_cuda(table, cached, new_tokens, free_pages, free_head)
+    for t, n in ((table, "table"), (cached, "cached"), (new_tokens, "new_tokens"),
+                 (free_pages, "free_pages"), (free_head, "free_head")):
+        if t is not None:
+            _dtype(t, torch.int32, n)
+    if table.dim() != 2 or cached.shape != (table.shape[0],) or new_tokens.shape != cached.shape \
+            or free_pages.dim() != 1 or (free_head is not None and free_head.numel() != 1):
+        raise ValueError("inconsistent shapes")
+    requests, width = table.shape
+    sizes = [num_tokens, num_tokens, num_tokens, requests + 1, requests, 1]
+    with torch.cuda.device(dev):
+        if out is None:
+            out = PagePlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+        else:
+            if _check_cuda(*out) != dev:
+                raise ValueError("all tensors must be on one device")
+            for t, n, size in zip(out, PagePlan._fields, sizes):
+                _dtype(t, torch.int32, n)
+                if t.shape != (size,):
+                    raise ValueError(f"out.{n} must have {size} entries")
+        rc = load_extension().pgdx_assign_pages(
+            requests, width, num_pages, num_tokens, _ptr(table), _ptr(cached), _ptr(new_tokens),
+            _ptr(free_pages), free_pages.shape[0], _ptr(free_head), *(t.data_ptr() for t in out),
+            _stream_handle(stream))
+    if rc != OK:
+        raise PgdError(rc, "assign_pages")
+    return out
+
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+
+
+class Rotary:
+    """Rotary frequencies, computed once and passed to rotary_append_paged.
+
+    rotary_dim: leading dims of each head that are rotated (a multiple of 16);
+    interleaved: dims 2i and 2i + 1 pair up (else i and i + rotary_dim / 2);
+    scaling: "none", "linear", "ntk", "yarn" or "banded", with their factor,
+    original_positions, beta_fast / beta_slow (yarn; exact_bounds leaves its
+    ramp's ends unrounded) and low_band / high_band (banded), as
+    include/pgd_ext.h defines them; attention_factor: factor of cos and sin
+    (None: the scaling's own)."""
+
+    def __init__(self, rotary_dim: int, theta: float, *, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_positions: float = 0.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, exact_bounds: bool = False,
+                 low_band: float = 1.0, high_band: float = 4.0,
+                 attention_factor: float | None = None):
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+        if attention_factor is not None and not attention_factor > 0:
+            raise ValueError("attention_factor must be positive")
+        config = RotaryConfig(rotary_dim, int(interleaved), _SCALINGS[scaling], int(exact_bounds),
+                              theta, factor, original_positions, beta_fast, beta_slow, low_band,
+                              high_band, attention_factor or 0.0)
+        self.plan = RotaryPlan()
+        rc = load_extension().pgdx_rotary_init(ctypes.byref(config), ctypes.byref(self.plan))
+        if rc != OK:
+            raise PgdError(rc, "rotary_init")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Values from token to token of a [P, heads, D] tensor whose tokens are
+    contiguous (a view of a fused projection, say)."""
+    _, heads, d = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+
+
+def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
+                        positions: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, *,
+                        rotary: Rotary, slots: torch.Tensor | None = None,
+                        table: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                        table_rows: int | None = None, layout: int = PAGE_MAJOR,
+                        max_pages_per_row: int | None = None, q_out: torch.Tensor | None = None,
+                        stream: torch.cuda.Stream | None = None) -> torch.Tensor | None:
+    """Rotates q and k_new at positions[p] and writes rotated k and v into the
+    pools, at slots[p] or, without slots, at position positions[p] of table row
+    rows[p] (None: row p).
+
+    q (bf16 [P, Hq, D]), k_new and v_new (bf16 [P, Hkv, D]) may be views with a
+    token stride of their own (a multiple of 8 values).  Returns the rotated q:
+    q_out if given (q itself for in place), else a new contiguous tensor.
+    Tokens with a negative position or slot are left alone, their q_out rows
+    too.  With ROW_MAJOR pools the table may be None (then max_pages_per_row,
+    and with rows table_rows, give its shape)."""
+    dev = _check_cuda(positions, k_pool, v_pool, slots, table, rows, q_out)
+    for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+        if t is not None:
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("all tensors must be on one CUDA device")
+            if t.dim() != 3:
+                raise ValueError(f"{n} must be [P, heads, D]")
+            _dtype(t, torch.bfloat16, n)
+    _dtype(k_pool, torch.bfloat16, "k_pool")
+    _dtype(v_pool, torch.bfloat16, "v_pool")
+    for t, n in ((positions, "positions"), (slots, "slots"), (table, "table"), (rows, "rows")):
+        if t is not None:
+            _dtype(t, torch.int32, n)
+    tokens, hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or positions.shape != (tokens,) or k_pool.shape != v_pool.shape \
+            or (q is not None and (q.shape[0] != tokens or q.shape[2] != d)) \
+            or (slots is not None and slots.shape != (tokens,)) \
+            or (rows is not None and rows.shape != (tokens,)) \
+            or (table is not None and table.dim() != 2):
+        raise ValueError("inconsistent shapes")
+    if slots is None and rows is None and table is not None and table.shape[0] != tokens:
+        raise ValueError("without rows, the table needs one row per token")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q_out is not None:
+        _dtype(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+    width = table.shape[1] if table is not None else (max_pages_per_row or 1)
+    count = table.shape[0] if table is not None else (table_rows or 0)
+    dims = make_dims(rows=tokens, num_q_heads=q.shape[1] if q is not None else hkv,
+                     num_kv_heads=hkv, head_dim=d, num_pages=_pool_pages(k_pool, hkv, d),
+                     max_pages_per_row=width, layout=layout)
+    with torch.cuda.device(dev):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        rc = load_extension().pgdx_rotary_append(
+            ctypes.byref(dims), ctypes.byref(rotary.plan), _ptr(q),
+            0 if q is None else _token_stride(q, "q"), _ptr(q_out), _ptr(k_new),
+            _token_stride(k_new, "k_new"), _ptr(v_new), _token_stride(v_new, "v_new"),
+            _ptr(table), count, _ptr(rows), _ptr(positions), _ptr(slots), _ptr(k_pool),
+            _ptr(v_pool), _stream_handle(stream))
+    if rc != OK:
+        raise PgdError(rc, "rotary_append_paged")
+    return q_out
