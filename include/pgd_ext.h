@@ -5,7 +5,10 @@
  *   - pgdx_assign_pages: the step's block-table entries, slots, rows and
  *     positions, made on the GPU from the requests' lengths;
  *   - pgdx_rotary_append: rotary positions (half or interleaved pairs, part of
- *     the head, scaled frequencies) on q and k, fused with the paged append.
+ *     the head, scaled frequencies) on q and k, fused with the paged append;
+ *   - pgdx_paged_decode, pgdx_paged_prefill: the attention of pgd.h with a
+ *     tanh score cap, a distance bias, a first visible key per token
+ *     (documents) and, for prefill, a bidirectional prefix.
  *
  * The conventions are those of pgd.h: its types, dims, options, status codes,
  * layouts, alignment (16 bytes for bf16 tensors and the workspace; int32 and
@@ -147,6 +150,59 @@ PGD_API int pgdx_rotary_append(const pgd_dims* dims, const pgdx_rotary* rotary, 
                                const int32_t* token_rows, const int32_t* positions,
                                const int32_t* slots, void* k_pool, void* v_pool,
                                pgd_stream_t stream);
+
+/* How the attention's scores differ from scale * q . k.  For the query at
+ * position n and the key at position j:
+ *   x_j = softcap * tanh(scale q . k_j / softcap)   (softcap > 0; else scale q . k_j)
+ *         - alibi_slopes[h] * |n - j|               (alibi_slopes not NULL)
+ * for the keys j with lo <= j <= hi, where hi = max(n, prefix_len - 1) and
+ * lo = max(0, first_key, n - window + 1 with a window).  The sinks join the
+ * denominator as they are, neither capped nor biased.  A token that sees no
+ * key (first_key > hi) gives zeros.
+ * K may hold anything at positions that a token does not see.  So may V, except
+ * that in prefill the tokens of one run (same table row and first key,
+ * consecutive positions and places in the pass) need finite V wherever one of
+ * them sees it. */
+typedef struct {
+  float softcap;              /* > 0, or <= 0 for none */
+  const float* alibi_slopes;  /* device fp32 [Hq], or NULL */
+  const int32_t* first_key;   /* device int32 [rows]: first visible position of each row or
+                                 token (the start of its document), or NULL for 0 */
+  const int32_t* prefix_len;  /* prefill: device int32 [table_rows], positions of each row that
+                                 its tokens see whatever their own (a bidirectional prefix,
+                                 <= 0: none); NULL otherwise, and for decode */
+} pgdx_score;
+
+/*
+ * paged_decode -- pgd_paged_decode_attention (k_new and v_new NULL) or
+ * pgd_paged_decode_step (both given) with the scores of *score.  Arguments,
+ * workspace (pgd_paged_decode_workspace_bytes), results and device errors as
+ * there; with a step, the new token is appended whether or not its row sees
+ * it.  opts->kernel: AUTO or TENSOR_CORE (else PGD_EUNSUPPORTED).
+ * score->prefix_len must be NULL.
+ */
+PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, const void* q,
+                              const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                              const int32_t* table, const int32_t* positions, const float* sinks,
+                              int32_t window, float scale, void* out, void* workspace,
+                              size_t workspace_bytes, const pgd_decode_options* opts,
+                              pgd_stream_t stream);
+
+/*
+ * paged_prefill -- pgd_paged_prefill_attention (k_new and v_new NULL) or
+ * pgd_paged_prefill_step (both given) with the scores of *score.  A prefix of
+ * more positions than the table row holds is a device error
+ * (PGD_EDEVICE_BOUNDS, the row's tokens give zeros); the prefix's keys must be
+ * in the pools (or written by this step).  opts->kernel: AUTO (PREFILL_UMMA
+ * when the tokens average at least 8 a table row, with key parts for few
+ * items; else per token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).
+ */
+PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
+                               const void* q, const void* k_new, const void* v_new, void* k_pool,
+                               void* v_pool, const int32_t* table, const int32_t* rows,
+                               const int32_t* positions, const float* sinks, int32_t window,
+                               float scale, void* out, void* workspace, size_t workspace_bytes,
+                               const pgd_decode_options* opts, pgd_stream_t stream);
 
 /* As pgd_get_device_error, for this library's error word. */
 PGD_API int pgdx_get_device_error(pgd_stream_t stream);

@@ -21,6 +21,9 @@ Entry points (same names as the C ABI, without the ``pgd_`` / ``pgdx_`` prefix):
   from the requests' lengths.
 - ``rotary_append_paged``: rotary positions (``Rotary``: half or interleaved
   pairs, part of the head, scaled frequencies) fused with the append.
+- decode, prefill and their steps take ``softcap`` (tanh score cap),
+  ``alibi_slopes`` (distance bias), ``first_key`` (documents) and, for prefill,
+  ``prefix_len`` (bidirectional prefixes); without them they are libpgd's.
 - ``paged_decode_workspace_bytes``, ``get_device_error``.
 """
 from __future__ import annotations
@@ -140,6 +143,11 @@ class RotaryPlan(ctypes.Structure):
                 ("turns", ctypes.c_uint64 * 64)]
 
 
+class Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
+                ("first_key", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
 def load_extension(path: str | None = None) -> ctypes.CDLL:
     """Loads libpgd_ext.so (built beside libpgd.so); raises if absent."""
     global _ext
@@ -159,8 +167,13 @@ def load_extension(path: str | None = None) -> ctypes.CDLL:
                 lib.pgdx_rotary_init.argtypes = [ctypes.POINTER(RotaryConfig), plan_p]
                 lib.pgdx_rotary_append.argtypes = [dims_p, plan_p, vp, i64, vp, vp, i64, vp, i64,
                                                    vp, i32, vp, vp, vp, vp, vp, vp]
+                score_p, opts_p = ctypes.POINTER(Score), ctypes.POINTER(DecodeOptions)
+                tail = [i32, ctypes.c_float, vp, vp, ctypes.c_size_t, opts_p, vp]
+                lib.pgdx_paged_decode.argtypes = [dims_p, score_p] + [vp] * 8 + tail
+                lib.pgdx_paged_prefill.argtypes = [dims_p, i32, score_p] + [vp] * 9 + tail
                 lib.pgdx_get_device_error.argtypes = [vp]
-                for name in ("assign_pages", "rotary_init", "rotary_append", "get_device_error"):
+                for name in ("assign_pages", "rotary_init", "rotary_append", "paged_decode",
+                             "paged_prefill", "get_device_error"):
                     getattr(lib, "pgdx_" + name).restype = ctypes.c_int
                 _ext = lib
     return _ext
@@ -264,15 +277,21 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
                            scale: float | None = None, *, num_kv_heads: int,
                            layout: int = PAGE_MAJOR, out: torch.Tensor | None = None,
                            workspace: torch.Tensor | None = None, pages_per_split: int = 0,
-                           kernel: int = KERNEL_AUTO,
+                           kernel: int = KERNEL_AUTO, softcap: float = 0.0,
+                           alibi_slopes: torch.Tensor | None = None,
+                           first_key: torch.Tensor | None = None,
                            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Grouped-query decode attention of each row over its pages.
 
     q: bf16 [R, Hq, D]; pools: bf16 with num_kv_heads kv heads in ``layout``;
     table: int32 [R, max_pages]; positions: int32 [R]; sinks: fp32 [Hq] or
-    None; window <= 0 for full attention.  Returns bf16 [R, Hq, D]."""
+    None; window <= 0 for full attention.  softcap > 0: scores softcap *
+    tanh(scale q.k / softcap); alibi_slopes (fp32 [Hq]): less slope * distance;
+    first_key (int32 [R]): row b sees positions from first_key[b] on.  Returns
+    bf16 [R, Hq, D]."""
     return _decode(q, None, None, k_pool, v_pool, table, positions, sinks, window, scale,
-                   num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream)
+                   num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
+                   _score(softcap, alibi_slopes, first_key))
 
 
 def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -281,17 +300,44 @@ def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                       window: int = 0, scale: float | None = None, *, num_kv_heads: int,
                       layout: int = PAGE_MAJOR, out: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, pages_per_split: int = 0,
-                      kernel: int = KERNEL_AUTO,
+                      kernel: int = KERNEL_AUTO, softcap: float = 0.0,
+                      alibi_slopes: torch.Tensor | None = None,
+                      first_key: torch.Tensor | None = None,
                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """kv_append_paged then paged_decode_attention in one launch: each row's
     new K/V (bf16 [R, Hkv, D]) goes to its slot in the pools and the row
     attends over its pages, the new token included."""
     return _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
-                   num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream)
+                   num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
+                   _score(softcap, alibi_slopes, first_key))
+
+
+def _score(softcap, alibi_slopes, first_key, prefix_len=None):
+    """What changes the scores, or None where nothing does."""
+    if softcap == 0.0 and alibi_slopes is None and first_key is None and prefix_len is None:
+        return None
+    return float(softcap), alibi_slopes, first_key, prefix_len
+
+
+def _check_score(score, dev, rows, hq, table_rows) -> Score:
+    softcap, slopes, first_key, prefix_len = score
+    if not math.isfinite(softcap) or softcap < 0.0:
+        raise ValueError("softcap must be finite and >= 0 (0: none)")
+    other = _check_cuda(slopes, first_key, prefix_len)
+    if other is not None and other != dev:
+        raise ValueError("all tensors must be on one device")
+    for t, n, dtype, size in ((slopes, "alibi_slopes", torch.float32, hq),
+                              (first_key, "first_key", torch.int32, rows),
+                              (prefix_len, "prefix_len", torch.int32, table_rows)):
+        if t is not None:
+            _dtype(t, dtype, n)
+            if t.shape != (size,):
+                raise ValueError(f"{n} must have {size} entries")
+    return Score(softcap, _ptr(slopes), _ptr(first_key), _ptr(prefix_len))
 
 
 def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
-            num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream):
+            num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream, score=None):
     dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, out, workspace)
     _dtype(q, torch.bfloat16, "q")
     _dtype(k_pool, torch.bfloat16, "k_pool")
@@ -327,7 +373,13 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
         tail = (_ptr(table), _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                 ctypes.byref(opts), _stream_handle(stream))
-        if k_new is None:
+        if score is not None:
+            mod = _check_score(score, dev, rows, hq, rows)
+            rc = load_extension().pgdx_paged_decode(
+                ctypes.byref(dims), ctypes.byref(mod), _ptr(q), _ptr(k_new), _ptr(v_new),
+                _ptr(k_pool), _ptr(v_pool), *tail)
+            what = "paged_decode_attention" if k_new is None else "paged_decode_step"
+        elif k_new is None:
             rc = lib.pgd_paged_decode_attention(ctypes.byref(dims), _ptr(q), _ptr(k_pool),
                                                 _ptr(v_pool), *tail)
             what = "paged_decode_attention"
@@ -423,13 +475,20 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
                             scale: float | None = None, *, num_kv_heads: int,
                             layout: int = PAGE_MAJOR, out: torch.Tensor | None = None,
                             workspace: torch.Tensor | None = None, pages_per_split: int = 0,
-                            kernel: int = KERNEL_AUTO,
+                            kernel: int = KERNEL_AUTO, softcap: float = 0.0,
+                            alibi_slopes: torch.Tensor | None = None,
+                            first_key: torch.Tensor | None = None,
+                            prefix_len: torch.Tensor | None = None,
                             stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Packed prompt tokens: token p (q bf16 [P, Hq, D]) attends over table row
     rows[p]'s pages up to positions[p].  Prompts and decode steps can share one
-    call (a step of row b is a token with rows[p] = b).  Returns bf16 [P, Hq, D]."""
+    call (a step of row b is a token with rows[p] = b).  softcap, alibi_slopes
+    and first_key (int32 [P]: the first position of each token's document) as
+    for paged_decode_attention; prefix_len (int32 [table rows]): positions of
+    each row that all of its tokens see.  Returns bf16 [P, Hq, D]."""
     return _prefill(q, None, None, k_pool, v_pool, table, rows, positions, sinks, window, scale,
-                    num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream)
+                    num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
+                    _score(softcap, alibi_slopes, first_key, prefix_len))
 
 
 def paged_prefill_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -439,7 +498,10 @@ def paged_prefill_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
                        scale: float | None = None, *, num_kv_heads: int,
                        layout: int = PAGE_MAJOR, out: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None, pages_per_split: int = 0,
-                       kernel: int = KERNEL_AUTO,
+                       kernel: int = KERNEL_AUTO, softcap: float = 0.0,
+                       alibi_slopes: torch.Tensor | None = None,
+                       first_key: torch.Tensor | None = None,
+                       prefix_len: torch.Tensor | None = None,
                        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The prefill call with the tokens' writes in it: token p's k_new / v_new
     (bf16 [P, Hkv, D]) go to its slot of table row rows[p] at positions[p],
@@ -447,11 +509,12 @@ def paged_prefill_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     page_slots + kv_write_slots + paged_prefill_attention.  Returns bf16
     [P, Hq, D]."""
     return _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, window,
-                    scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream)
+                    scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
+                    _score(softcap, alibi_slopes, first_key, prefix_len))
 
 
 def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, window, scale,
-             num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream):
+             num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream, score=None):
     step = k_new is not None
     dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, out,
                       workspace)
@@ -493,7 +556,12 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
               ctypes.byref(opts), _stream_handle(stream))
         tail = (_ptr(table), _ptr(rows), _ptr(positions), _ptr(sinks), int(window),
                 float(scale))
-        if step:
+        if score is not None:
+            mod = _check_score(score, dev, tokens, hq, table.shape[0])
+            rc = load_extension().pgdx_paged_prefill(
+                ctypes.byref(dims), table.shape[0], ctypes.byref(mod), _ptr(q), _ptr(k_new),
+                _ptr(v_new), _ptr(k_pool), _ptr(v_pool), *tail, *ws)
+        elif step:
             rc = lib.pgd_paged_prefill_step(ctypes.byref(dims), table.shape[0], _ptr(q),
                                             _ptr(k_new), _ptr(v_new), _ptr(k_pool),
                                             _ptr(v_pool), *tail, *ws)
@@ -556,11 +624,15 @@ def decode_rows_attention(q: torch.Tensor, cache_k: torch.Tensor, cache_v: torch
                           window: int = 0, scale: float | None = None, *,
                           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                           pages_per_split: int = 0, kernel: int = KERNEL_AUTO,
+                          softcap: float = 0.0, alibi_slopes: torch.Tensor | None = None,
+                          first_key: torch.Tensor | None = None,
                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """decode_rows: row b's queries (q bf16 [R, Hq, D]) attend over row b of the
-    dense caches (bf16 [Batch, Hkv, MaxSeq, D]) up to positions[b]."""
+    dense caches (bf16 [Batch, Hkv, MaxSeq, D]) up to positions[b]; softcap,
+    alibi_slopes and first_key as for paged_decode_attention."""
     return _decode_rows(q, None, None, cache_k, cache_v, positions, sinks, window, scale, out,
-                        workspace, pages_per_split, kernel, stream)
+                        workspace, pages_per_split, kernel, stream,
+                        _score(softcap, alibi_slopes, first_key))
 
 
 def decode_rows_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -568,15 +640,18 @@ def decode_rows_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                      sinks: torch.Tensor | None = None, window: int = 0,
                      scale: float | None = None, *, out: torch.Tensor | None = None,
                      workspace: torch.Tensor | None = None, pages_per_split: int = 0,
-                     kernel: int = KERNEL_AUTO,
+                     kernel: int = KERNEL_AUTO, softcap: float = 0.0,
+                     alibi_slopes: torch.Tensor | None = None,
+                     first_key: torch.Tensor | None = None,
                      stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """kv_append_rows then decode_rows_attention in one launch."""
     return _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, scale, out,
-                        workspace, pages_per_split, kernel, stream)
+                        workspace, pages_per_split, kernel, stream,
+                        _score(softcap, alibi_slopes, first_key))
 
 
 def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, scale, out,
-                 workspace, pages_per_split, kernel, stream):
+                 workspace, pages_per_split, kernel, stream, score=None):
     dev = _check_cuda(q, k_new, v_new, cache_k, cache_v, positions, sinks, out, workspace)
     _dtype(q, torch.bfloat16, "q")
     _dtype(cache_k, torch.bfloat16, "cache_k")
@@ -607,7 +682,13 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
         tail = (None, _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                 ctypes.byref(opts), _stream_handle(stream))
-        if k_new is None:
+        if score is not None:
+            mod = _check_score(score, dev, rows, hq, rows)
+            rc = load_extension().pgdx_paged_decode(
+                ctypes.byref(dims), ctypes.byref(mod), _ptr(q), _ptr(k_new), _ptr(v_new),
+                _ptr(cache_k), _ptr(cache_v), *tail)
+            what = "decode_rows_attention" if k_new is None else "decode_rows_step"
+        elif k_new is None:
             rc = lib.pgd_paged_decode_attention(ctypes.byref(dims), _ptr(q), _ptr(cache_k),
                                                 _ptr(cache_v), *tail)
             what = "decode_rows_attention"

@@ -1,0 +1,26 @@
+// Decode kernels for modified scores (paged_score.cuh) at one head_dim: the
+// split kernel of paged_decode.cuh with the tensor-core consumer, its ring no
+// deeper than the pages a split can stream.
+#pragma once
+
+#include "paged_decode.cuh"
+#include "pgd_ext_internal.h"
+
+namespace pgd {
+
+template <int D>
+cudaError_t launch_mod_decode(const ModParams& p, const CUtensorMap& k_map,
+                              const CUtensorMap& v_map, int grid_splits, int pages_per_cta,
+                              cudaStream_t stream) {
+  using Consumer = MmaConsumer<D, ModScore>;
+  if (pages_per_cta <= 1)
+    return launch_decode<D, 1, Consumer, kShortWarps>(p, k_map, v_map, grid_splits, stream);
+  if (pages_per_cta <= 2)
+    return launch_decode<D, 2, Consumer, kShortWarps>(p, k_map, v_map, grid_splits, stream);
+  if (D == 64 && pages_per_cta <= 3)
+    return launch_decode<D, kShortStages3, Consumer, kShortWarps>(p, k_map, v_map, grid_splits,
+                                                                  stream);
+  return launch_decode<D, D == 128 ? 3 : 6, Consumer>(p, k_map, v_map, grid_splits, stream);
+}
+
+}  // namespace pgd

@@ -59,6 +59,7 @@
 #include <type_traits>
 
 #include "pgd_device.cuh"
+#include "paged_score.cuh"
 #include "pgd_internal.h"
 
 namespace pgd {
@@ -118,9 +119,12 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 // Fragment ownership (m16n8k16): lane = 4 * gid + tig.  Score tile t covers
 // page rows 16t..16t+15; the lane holds rows 16t + gid (+8) of heads 2tig and
 // 2tig + 1.  Output tile mt covers dims 16mt..16mt+15; the lane holds dims
-// 16mt + gid (+8) of the same two heads.
-template <int D>
+// 16mt + gid (+8) of the same two heads.  ScorePolicy: how scores differ from
+// scale * q . k (paged_score.cuh).
+template <int D, class ScorePolicy = PlainScore>
 struct MmaConsumer {
+  using Score = ScorePolicy;
+  using Params = typename Score::Params;
   static constexpr int kHeads = 8;
   static constexpr int kSteps = D / 16;  // k-steps of Q.K^T and dim tiles of P.V
   static constexpr int kSharedFloats = 0;
@@ -131,13 +135,24 @@ struct MmaConsumer {
   uint32_t off_k[4], off_v[4];
   int gid, tig;
   float c;
+  // ModScore: the cap (see cap_near), and per head the bias per position of
+  // distance in log2 units (negated slope); page() gets the query's position
+  // relative to the page in `here`
+  float cap_in, cap_out, bias[2], here;
 
-  __device__ static void prepare_shared(float*, const DecodeParams&, int, int, int, int) {}
+  __device__ static void prepare_shared(float*, const Params&, int, int, int, int) {}
 
-  __device__ void init(const DecodeParams& p, int b, int h0, int lane, const float*) {
+  __device__ void init(const Params& p, int b, int h0, int lane, const float*) {
     gid = lane >> 2;
     tig = lane & 3;
     c = p.q_scale_log2;
+    if constexpr (Score::kMod) {
+      cap_in = p.cap_in;
+      cap_out = p.cap_out;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        bias[e] = p.slopes && 2 * tig + e < p.group ? -p.slopes[h0 + 2 * tig + e] * kLog2e : 0.f;
+    }
     const bool live = gid < p.group;
     const uint32_t* qrow =
         reinterpret_cast<const uint32_t*>(p.q + ((size_t)b * p.hq + h0 + (live ? gid : 0)) * D);
@@ -164,6 +179,39 @@ struct MmaConsumer {
     }
   }
 
+  // ModScore: raw products to scores in log2 units.
+  template <int NT>
+  __device__ __forceinline__ void score(float (&s)[NT][4]) {
+    if (cap_in != 0.f) {
+      float top = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        top = fmax3(top, fmax3(fabsf(s[t][0]), fabsf(s[t][1]), fabsf(s[t][2])), fabsf(s[t][3]));
+      if (__all_sync(0xffffffffu, top * fabsf(cap_in) <= 1.f)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] = cap_near(s[t][e], cap_in, c);
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] = cap_far(s[t][e], cap_in, cap_out);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] *= c;
+    }
+    const float row0 = (float)gid - here;  // signed distance of page row gid
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[t][e] = fmaf(bias[e & 1], fabsf(row0 + (float)(16 * t + ((e & 2) ? 8 : 0))), s[t][e]);
+  }
+
   // One page (NT = 4: 64 rows), or NT / 4 of one (the window kernel's
   // 32-row slices): kt is the shared address of its K rows, vt_ptr its V
   // rows, valid rows [rlo, rhi].  Returns true if it wrote zeros into V.
@@ -186,12 +234,24 @@ struct MmaConsumer {
       }
 
     const bool full = rlo == 0 && rhi == 16 * NT - 1;
+    if constexpr (Score::kMod) {
+      if (!full) {  // what a masked place holds has no say in how the others are capped
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 16 * t + gid + ((e & 2) ? 8 : 0);
+            s[t][e] = row >= rlo && row <= rhi ? s[t][e] : 0.f;
+          }
+      }
+      score<NT>(s);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = 16 * t + gid + ((e & 2) ? 8 : 0);
-        const float v = s[t][e] * c;
+        const float v = Score::kMod ? s[t][e] : s[t][e] * c;
         s[t][e] = (full || (row >= rlo && row <= rhi)) ? v : -INFINITY;
       }
     float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -306,6 +366,7 @@ struct MmaConsumer {
 // CUDA-core consumer for a group padded to GP heads.
 template <int D, int GP>
 struct ScalarConsumer {
+  using Score = PlainScore;
   static constexpr int kHeads = GP;
   static constexpr int kDims = D / 32;  // output dims per lane
   // q (fp32, scaled to log2 units) and a per-warp probability buffer
@@ -467,6 +528,28 @@ struct ScalarConsumer {
 
 // ------------------------------------------------------------------ split kernel
 
+// Pages and positions row b attends to (n its position; ModScore: a row that
+// sees no key gets the page of its position, all of it masked, so that a
+// step's append finds its page as always).
+template <class Score>
+__device__ __forceinline__ RowSpan decode_span(const typename Score::Params& p, int b, int n) {
+  if constexpr (!Score::kMod) {
+    return row_span(n, p.window);
+  } else {
+    RowSpan r = row_span(n, 0);
+    r.hi = n;
+    if (n < 0) return r;
+    const int row = p.row_of ? p.row_of[b] : b;
+    if (p.row_of && (row < 0 || row >= p.table_rows)) return r;  // reported by the caller
+    const TokenSpan s = mod_span(p, b, row, n);
+    r.hi = s.hi;
+    r.lo = s.lo;
+    r.first_page = min(s.lo, s.hi) / kPage;
+    r.pages = s.hi / kPage - r.first_page + 1;
+    return r;
+  }
+}
+
 // What a split CTA leaves behind when it gives up on its pages (a table
 // entry outside the pool, or a pipeline wait that timed out): with one split
 // per row it writes zeros as its query heads' outputs; otherwise it marks its
@@ -518,9 +601,11 @@ template <int D, int STAGES, class Consumer, int WARPS>
 __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThreads,
                                   DecodeCfg<D, STAGES, Consumer, WARPS>::kMinBlocks)
     paged_decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
-                              const __grid_constant__ CUtensorMap v_map, const DecodeParams p) {
+                              const __grid_constant__ CUtensorMap v_map,
+                              const typename Consumer::Score::Params p) {
   using C = DecodeCfg<D, STAGES, Consumer, WARPS>;
   constexpr int GP = C::kHeads;
+  constexpr bool kMod = Consumer::Score::kMod;
   pdl_wait();
   pdl_allow_dependents();
   const int split = blockIdx.x;
@@ -533,12 +618,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
   // Without a window a split's pages start at index split * pages_per_split
   // of its table row whatever the position, so the table entries it may need
   // are loaded together with the position rather than after it.
-  const bool spec = p.window == 0 && p.table != nullptr && p.row_of == nullptr;
+  bool spec = p.window == 0 && p.table != nullptr && p.row_of == nullptr;
+  if constexpr (kMod) spec = spec && p.first_key == nullptr;
   int pg_spec = -1;
   if (spec && tid < p.pages_per_split && split * p.pages_per_split + tid < p.maxp)
     pg_spec = p.table[(size_t)b * p.maxp + split * p.pages_per_split + tid];
   const int n = p.positions[b];
-  const RowSpan span = row_span(n, p.window);
+  const RowSpan span = decode_span<typename Consumer::Score>(p, b, n);
+  const int last = kMod ? span.hi : n;  // last attended position
   const int nsplit = (span.pages + p.pages_per_split - 1) / p.pages_per_split;
   const int h0 = kvh * p.group;
   // With one split per row (a grid one split wide) no combine kernel runs:
@@ -554,7 +641,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
     return;
   }
   const int table_row = p.row_of ? p.row_of[b] : b;
-  if (n / kPage >= p.maxp || (p.row_of && (table_row < 0 || table_row >= p.table_rows))) {
+  if (last / kPage >= p.maxp || (p.row_of && (table_row < 0 || table_row >= p.table_rows))) {
     // otherwise reported and zeroed by the combine kernel
     if (alone) {
       zero_heads();
@@ -675,7 +762,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
     unsigned char* kt = stages + s * C::kStageBytes;
     const int pos0 = (page0 + i) * kPage;
     const int rlo = max(span.lo - pos0, 0);
-    const int rhi = min(n - pos0, kPage - 1);
+    const int rhi = min(last - pos0, kPage - 1);
+    if constexpr (kMod) cons.here = (float)(n - pos0);
     bool wrote;
     if constexpr (Consumer::kSharedFloats > 0)
       wrote = cons.page(0u, kt, rlo, rhi, lane);
@@ -704,11 +792,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) mx = fmaxf(mx, red[(w * GP + g) * (D + 2) + D]);
+    float ref = mx;
+    if constexpr (kMod) ref = mx == -INFINITY ? 0.f : mx;  // no key seen: sums of 0
     float a = 0.f, den = 0.f;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
       const float* rw = red + (w * GP + g) * (D + 2);
-      const float f = exp2_approx(rw[D] - mx);  // warps without pages: m = -inf -> 0
+      const float f = exp2_approx(rw[D] - ref);  // warps without pages: m = -inf -> 0
       a = fmaf(rw[d], f, a);
       den = fmaf(rw[D + 1], f, den);
     }
@@ -719,7 +809,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
       const float mf = fmaxf(mx, sk);
       const float sc = exp2_approx(mx - mf);
       const float total = fmaf(den, sc, exp2_approx(sk - mf));
-      p.out[bh * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(a * sc / total));
+      float res = a * sc / total;
+      if constexpr (kMod) res = den == 0.f ? 0.f : res;  // no key seen
+      p.out[bh * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(res));
     } else {
       p.ws_acc[(bh * p.max_splits + split) * D + d] = a;
       if (d == 0) {
@@ -806,8 +898,8 @@ __device__ __forceinline__ void merge_partials(const float* ml, int ml_stride, c
 // more splits (merge_partials).  Also zeroes inactive rows and rows whose
 // position lies beyond their table or whose table row is out of range
 // (recording PGD_EDEVICE_BOUNDS).  One warp per (row, query head).
-template <int D>
-__global__ void __launch_bounds__(128) paged_decode_combine_kernel(const DecodeParams p) {
+template <int D, class Score = PlainScore>
+__global__ void __launch_bounds__(128) paged_decode_combine_kernel(const typename Score::Params p) {
   constexpr int kDims = D / 32;
   const int b = blockIdx.y;
   const int h = blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -825,7 +917,8 @@ __global__ void __launch_bounds__(128) paged_decode_combine_kernel(const DecodeP
   pdl_allow_dependents();
   if (!live) return;
   uint16_t* o = p.out + bh * D + lane * kDims;
-  const bool beyond = n >= 0 && (n / kPage >= p.maxp ||
+  const RowSpan span = decode_span<Score>(p, b, n);
+  const bool beyond = n >= 0 && ((Score::kMod ? span.hi : n) / kPage >= p.maxp ||
                                  (p.row_of && (table_row < 0 || table_row >= p.table_rows)));
   if (n < 0 || beyond) {
     if (beyond && h == 0 && lane == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
@@ -833,7 +926,6 @@ __global__ void __launch_bounds__(128) paged_decode_combine_kernel(const DecodeP
     for (int j = 0; j < kDims; ++j) o[j] = 0;
     return;
   }
-  const RowSpan span = row_span(n, p.window);
   const int nsplit = (span.pages + p.pages_per_split - 1) / p.pages_per_split;
   if (nsplit <= 1) return;  // written by the split kernel
   merge_partials<D>(p.ws_ml + bh * p.max_splits * 2, 2,
@@ -1125,7 +1217,7 @@ cudaError_t launch_window(const DecodeParams& p, cudaStream_t stream) {
 }
 
 template <int D, int STAGES, class Consumer, int WARPS = 4>
-cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& k_map,
+cudaError_t launch_decode(const typename Consumer::Score::Params& p, const CUtensorMap& k_map,
                           const CUtensorMap& v_map, int grid_splits, cudaStream_t stream) {
   using C = DecodeCfg<D, STAGES, Consumer, WARPS>;
   auto kern = paged_decode_split_kernel<D, STAGES, Consumer, WARPS>;
@@ -1148,7 +1240,8 @@ cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& k_map,
   e = launch_pdl(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, k_map, v_map, p);
   if (e != cudaSuccess || grid_splits == 1) return e;  // one split: written directly
   dim3 cgrid((p.hq + 3) / 4, p.rows);
-  return launch_pdl(paged_decode_combine_kernel<D>, cgrid, dim3(128), 0, stream, p);
+  return launch_pdl(paged_decode_combine_kernel<D, typename Consumer::Score>, cgrid, dim3(128), 0,
+                    stream, p);
 }
 
 // Splits of at most 3 pages (windows, short tables) are latency-bound: they

@@ -178,24 +178,13 @@ static int decode_impl(const pgd_dims* dims, int32_t table_rows, const int32_t* 
   int rc = check_dims(dims);
   if (rc != PGD_OK) return rc;
   if (dims->rows == 0) return PGD_OK;
-  if (!q || !k_pool || !v_pool || !positions || !out) return PGD_EINVAL;
-  if (!table && dims->layout != PGD_ROW_MAJOR) return PGD_EINVAL;
-  if (row_of != nullptr && table_rows <= 0) return PGD_EINVAL;
-  if (!table && (int64_t)(row_of ? table_rows : dims->rows) * dims->max_pages_per_row >
-                    dims->num_pages)
-    return PGD_EINVAL;  // dense rows: every row needs its own P pages
-  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
-    return PGD_EINVAL;
-  if ((k_new == nullptr) != (v_new == nullptr) ||
-      (k_new && (!aligned16(k_new) || !aligned16(v_new))))
-    return PGD_EINVAL;
-  if (!std::isfinite(scale)) return PGD_EINVAL;
   DeviceInfo* dev = nullptr;
-  if ((rc = current_device(&dev)) != PGD_OK) return rc;
-  const Plan pl = make_plan(dims, opts, dev->sm_count);
-  const size_t need = workspace_bytes(dims, pl);
-  if (workspace_size < need) return PGD_EWORKSPACE;
-  if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
+  Plan pl;
+  DecodeParams p;
+  if ((rc = prepare_attention(dims, table_rows, row_of, q, k_pool, v_pool, table, positions, sinks,
+                              window, scale, out, workspace, workspace_size, opts, k_new, v_new,
+                              &dev, &pl, &p)) != PGD_OK)
+    return rc;
 
   int kernel = 0, parts = 1;
   if ((rc = resolve_kernel(dims, table_rows, row_of != nullptr, opts, &kernel, dev->sm_count,
@@ -210,37 +199,6 @@ static int decode_impl(const pgd_dims* dims, int32_t table_rows, const int32_t* 
   CUtensorMap k_map, v_map;
   if ((rc = encode_pool_map(&k_map, k_pool, dims, k_kind)) != PGD_OK) return rc;
   if ((rc = encode_pool_map(&v_map, v_pool, dims, v_kind)) != PGD_OK) return rc;
-
-  DecodeParams p;
-  p.q = static_cast<const uint16_t*>(q);
-  p.table = table;
-  p.positions = positions;
-  p.row_of = row_of;
-  p.table_rows = table_rows;
-  p.sinks = sinks;
-  p.out = static_cast<uint16_t*>(out);
-  const size_t acc_floats =
-      (size_t)dims->rows * dims->num_q_heads * pl.max_splits * dims->head_dim;
-  p.ws_acc = static_cast<float*>(workspace);
-  p.ws_ml = p.ws_acc + acc_floats;
-  p.err = dev->err;
-  p.rows = dims->rows;
-  p.hq = dims->num_q_heads;
-  p.hkv = dims->num_kv_heads;
-  p.group = dims->num_q_heads / dims->num_kv_heads;
-  p.maxp = dims->max_pages_per_row;
-  p.num_pages = dims->num_pages;
-  p.layout = dims->layout;
-  p.window = window > 0 ? window : 0;
-  p.pages_per_split = pl.pages_per_split;
-  p.max_splits = pl.max_splits;
-  p.q_scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.k_new = static_cast<const uint16_t*>(k_new);
-  p.v_new = static_cast<const uint16_t*>(v_new);
-  p.k_pool = k_new ? static_cast<uint16_t*>(const_cast<void*>(k_pool)) : nullptr;
-  p.v_pool = k_new ? static_cast<uint16_t*>(const_cast<void*>(v_pool)) : nullptr;
-  p.k_read = static_cast<const uint16_t*>(k_pool);
-  p.v_read = static_cast<const uint16_t*>(v_pool);
 
   const int grid_pages = span_pages(dims, p.window);
   const int grid_splits = (grid_pages + pl.pages_per_split - 1) / pl.pages_per_split;

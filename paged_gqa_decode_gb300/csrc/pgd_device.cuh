@@ -215,6 +215,7 @@ __device__ __forceinline__ int page_of(const int32_t* table, int r, int j, int m
 struct RowSpan {
   int n;           // position of the new token (< 0: inactive)
   int lo;          // first attended position
+  int hi;          // last attended position (decode_span of ModScore only)
   int first_page;  // page index (within the row) of lo
   int pages;       // attended pages
 };

@@ -207,6 +207,103 @@ int pgdx_rotary_append(const pgd_dims* dims, const pgdx_rotary* rotary, const vo
              : PGD_ECUDA;
 }
 
+static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_t* row_of,
+                          const pgdx_score* score, const void* q, const void* k_new,
+                          const void* v_new, void* k_pool, void* v_pool, const int32_t* table,
+                          const int32_t* positions, const float* sinks, int32_t window,
+                          float scale, void* out, void* workspace, size_t workspace_size,
+                          const pgd_decode_options* opts, pgd_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != PGD_OK) return rc;
+  const bool prefill = row_of != nullptr;
+  if (!score || !std::isfinite(score->softcap) || !aligned4(score->alibi_slopes) ||
+      !aligned4(score->first_key) || !aligned4(score->prefix_len))
+    return PGD_EINVAL;
+  if (!prefill && score->prefix_len) return PGD_EINVAL;
+  const int32_t asked = opts ? opts->kernel : PGD_KERNEL_AUTO;
+  if (asked < PGD_KERNEL_AUTO || asked > PGD_KERNEL_PREFILL_PAIR) return PGD_EINVAL;
+  if (asked == PGD_KERNEL_PREFILL_UMMA && !prefill) return PGD_EINVAL;
+  if (asked != PGD_KERNEL_AUTO && asked != PGD_KERNEL_TENSOR_CORE &&
+      asked != PGD_KERNEL_PREFILL_UMMA)
+    return PGD_EUNSUPPORTED;
+  if (dims->rows == 0) return PGD_OK;
+  DeviceInfo* dev = nullptr;
+  Plan pl;
+  ModParams p;
+  if ((rc = prepare_attention(dims, table_rows, row_of, q, k_pool, v_pool, table, positions, sinks,
+                              window, scale, out, workspace, workspace_size, opts, k_new, v_new,
+                              &dev, &pl, &p)) != PGD_OK)
+    return rc;
+  const bool capped = score->softcap > 0.f && scale != 0.f;  // a zero score is its own cap
+  p.cap_in = capped ? scale / score->softcap : 0.f;
+  p.cap_out = capped ? (float)((double)score->softcap * 1.4426950408889634) : 0.f;
+  if (capped && (p.cap_in == 0.f || !std::isfinite(p.cap_in))) return PGD_EINVAL;
+  p.slopes = score->alibi_slopes;
+  p.first_key = score->first_key;
+  p.prefix_len = score->prefix_len;
+
+  // The pages a token may span: a window bounds them, unless a prefix adds to it.
+  const int32_t bound = p.prefix_len ? 0 : window;
+  int kernel = 0, parts = 1;
+  if ((rc = resolve_kernel(dims, table_rows, prefill, opts, &kernel, dev->sm_count, &parts,
+                           bound)) != PGD_OK)
+    return rc;
+  if (kernel == PGD_KERNEL_PREFILL_PAIR) kernel = PGD_KERNEL_PREFILL_UMMA;  // AUTO's only
+  const bool tcgen05 = kernel == PGD_KERNEL_PREFILL_UMMA;
+  CUtensorMap k_map, v_map, q_map;
+  const int kind = tcgen05 ? kMapWholeTile : kMapBoxes;
+  if ((rc = encode_pool_map(&k_map, k_pool, dims, kind)) != PGD_OK) return rc;
+  if ((rc = encode_pool_map(&v_map, v_pool, dims, kind)) != PGD_OK) return rc;
+  if (tcgen05 && (rc = encode_q_map(&q_map, q, dims)) != PGD_OK) return rc;
+
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool prefill_write = k_new != nullptr && prefill;
+  if (prefill_write) {
+    if (launch_mod_prefill_write(p, dims->head_dim, tcgen05, st) != cudaSuccess) return PGD_ECUDA;
+    p.k_new = p.v_new = nullptr;
+    p.k_pool = p.v_pool = nullptr;
+  }
+  cudaError_t e;
+  if (tcgen05) {
+    e = dims->head_dim == 64 ? launch_mod_prefill_d64(p, k_map, v_map, q_map, dev->sm_count,
+                                                      prefill_write, parts, st)
+                             : launch_mod_prefill_d128(p, k_map, v_map, q_map, dev->sm_count,
+                                                       prefill_write, parts, st);
+  } else {
+    const int pages = span_pages(dims, bound);
+    const int splits = (pages + pl.pages_per_split - 1) / pl.pages_per_split;
+    const int per_cta = pages < pl.pages_per_split ? pages : pl.pages_per_split;
+    e = dims->head_dim == 64 ? launch_mod_decode_d64(p, k_map, v_map, splits, per_cta, st)
+                             : launch_mod_decode_d128(p, k_map, v_map, splits, per_cta, st);
+  }
+  return e == cudaSuccess ? PGD_OK : PGD_ECUDA;
+}
+
+int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, const void* q,
+                      const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                      const int32_t* table, const int32_t* positions, const float* sinks,
+                      int32_t window, float scale, void* out, void* workspace,
+                      size_t workspace_size, const pgd_decode_options* opts,
+                      pgd_stream_t stream) {
+  return attention_impl(dims, dims ? dims->rows : 0, nullptr, score, q, k_new, v_new, k_pool,
+                        v_pool, table, positions, sinks, window, scale, out, workspace,
+                        workspace_size, opts, stream);
+}
+
+int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
+                       const void* q, const void* k_new, const void* v_new, void* k_pool,
+                       void* v_pool, const int32_t* table, const int32_t* rows,
+                       const int32_t* positions, const float* sinks, int32_t window, float scale,
+                       void* out, void* workspace, size_t workspace_size,
+                       const pgd_decode_options* opts, pgd_stream_t stream) {
+  const int rc = check_dims(dims);
+  if (rc != PGD_OK) return rc;
+  if (!rows || table_rows <= 0) return dims->rows == 0 ? PGD_OK : PGD_EINVAL;
+  return attention_impl(dims, table_rows, rows, score, q, k_new, v_new, k_pool, v_pool, table,
+                        positions, sinks, window, scale, out, workspace, workspace_size, opts,
+                        stream);
+}
+
 int pgdx_get_device_error(pgd_stream_t stream) {
   DeviceInfo* dev = nullptr;
   const int rc = current_device(&dev);

@@ -2,6 +2,7 @@
 // by its host API (pgd_ext_api.cu) and the kernel translation units.
 #pragma once
 
+#include "paged_score.cuh"
 #include "pgd_ext.h"
 #include "pgd_internal.h"
 
@@ -41,5 +42,23 @@ struct RotaryParams {
   pgdx_rotary rotary;
 };
 cudaError_t launch_rotary_append(const RotaryParams& p, int head_dim, cudaStream_t stream);
+
+// Attention with the scores of ModParams: the split decode (and its combine),
+// the tcgen05 prefill (and its block order or key-part combine), and the
+// prefill step's write, as their namesakes in pgd_internal.h.
+cudaError_t launch_mod_decode_d64(const ModParams& p, const CUtensorMap& k_map,
+                                  const CUtensorMap& v_map, int grid_splits, int pages_per_cta,
+                                  cudaStream_t stream);
+cudaError_t launch_mod_decode_d128(const ModParams& p, const CUtensorMap& k_map,
+                                   const CUtensorMap& v_map, int grid_splits, int pages_per_cta,
+                                   cudaStream_t stream);
+cudaError_t launch_mod_prefill_d64(const ModParams& p, const CUtensorMap& k_map,
+                                   const CUtensorMap& v_map, const CUtensorMap& q_map,
+                                   int sm_count, bool prepared, int parts, cudaStream_t stream);
+cudaError_t launch_mod_prefill_d128(const ModParams& p, const CUtensorMap& k_map,
+                                    const CUtensorMap& v_map, const CUtensorMap& q_map,
+                                    int sm_count, bool prepared, int parts, cudaStream_t stream);
+cudaError_t launch_mod_prefill_write(const ModParams& p, int head_dim, bool umma,
+                                     cudaStream_t stream);
 
 }  // namespace pgd

@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -308,6 +309,68 @@ int encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pgd_dims*
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PGD_OK : PGD_ECUDA;
+}
+
+// The attention calls' common part, after check_dims and the check for no
+// rows: the arguments' checks, the split plan against the workspace, and the
+// launch parameters.
+int prepare_attention(const pgd_dims* dims, int32_t table_rows, const int32_t* row_of,
+                      const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
+                      const int32_t* positions, const float* sinks, int32_t window, float scale,
+                      void* out, void* workspace, size_t workspace_size,
+                      const pgd_decode_options* opts, const void* k_new, const void* v_new,
+                      DeviceInfo** device, Plan* plan, DecodeParams* params) {
+  if (!q || !k_pool || !v_pool || !positions || !out) return PGD_EINVAL;
+  if (!table && dims->layout != PGD_ROW_MAJOR) return PGD_EINVAL;
+  if (row_of != nullptr && table_rows <= 0) return PGD_EINVAL;
+  if (!table && (int64_t)(row_of ? table_rows : dims->rows) * dims->max_pages_per_row >
+                    dims->num_pages)
+    return PGD_EINVAL;  // dense rows: every row needs its own P pages
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return PGD_EINVAL;
+  if ((k_new == nullptr) != (v_new == nullptr) ||
+      (k_new && (!aligned16(k_new) || !aligned16(v_new))))
+    return PGD_EINVAL;
+  if (!std::isfinite(scale)) return PGD_EINVAL;
+  const int rc = current_device(device);
+  if (rc != PGD_OK) return rc;
+  const Plan pl = make_plan(dims, opts, (*device)->sm_count);
+  const size_t need = workspace_bytes(dims, pl);
+  if (workspace_size < need) return PGD_EWORKSPACE;
+  if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
+  *plan = pl;
+
+  DecodeParams& p = *params;
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = table;
+  p.positions = positions;
+  p.row_of = row_of;
+  p.table_rows = table_rows;
+  p.sinks = sinks;
+  p.out = static_cast<uint16_t*>(out);
+  const size_t acc_floats =
+      (size_t)dims->rows * dims->num_q_heads * pl.max_splits * dims->head_dim;
+  p.ws_acc = static_cast<float*>(workspace);
+  p.ws_ml = p.ws_acc + acc_floats;
+  p.err = (*device)->err;
+  p.rows = dims->rows;
+  p.hq = dims->num_q_heads;
+  p.hkv = dims->num_kv_heads;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.maxp = dims->max_pages_per_row;
+  p.num_pages = dims->num_pages;
+  p.layout = dims->layout;
+  p.window = window > 0 ? window : 0;
+  p.pages_per_split = pl.pages_per_split;
+  p.max_splits = pl.max_splits;
+  p.q_scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.k_pool = k_new ? static_cast<uint16_t*>(const_cast<void*>(k_pool)) : nullptr;
+  p.v_pool = k_new ? static_cast<uint16_t*>(const_cast<void*>(v_pool)) : nullptr;
+  p.k_read = static_cast<const uint16_t*>(k_pool);
+  p.v_read = static_cast<const uint16_t*>(v_pool);
+  return PGD_OK;
 }
 
 }  // namespace

@@ -95,3 +95,56 @@ def rotate(x, positions, freq, factor, interleaved):
     else:
         x[..., : rd // 2], x[..., rd // 2: rd] = ra, rb
     return x
+
+
+def visible(n, first=0, window=0, prefix=0):
+    """First and last position seen from position n (lo > hi: none)."""
+    hi = max(n, prefix - 1)
+    lo = max(0, first, n - window + 1 if window > 0 else 0)
+    return lo, hi
+
+
+def attention(q, k_rows, v_rows, rows, positions, *, scale, softcap=0.0, slopes=None, sinks=None,
+              first=None, window=0, prefix=None):
+    """Token by token: q float64 [P, Hq, D]; k_rows, v_rows: per table row float64
+    [Hkv, positions, D].  Returns the outputs and, for bounds on a kernel's error,
+    per output sum_j p_j |v_j|, per token and head max_j scale sum_i |q_i k_ij| and
+    max_j |bias_j|."""
+    tokens, hq, d = q.shape
+    out = np.zeros_like(q)
+    mass = np.zeros_like(q)
+    size = np.zeros((tokens, hq, 1))
+    far = np.zeros((tokens, hq, 1))
+    for t in range(tokens):
+        n, r = int(positions[t]), int(rows[t])
+        if n < 0:
+            continue
+        lo, hi = visible(n, 0 if first is None else int(first[t]), window,
+                         0 if prefix is None else int(prefix[r]))
+        if lo > hi:
+            continue
+        k, v = k_rows[r][:, lo:hi + 1], v_rows[r][:, lo:hi + 1]
+        group = hq // k.shape[0]
+        qt = q[t].reshape(k.shape[0], group, d)
+        x = scale * np.einsum("gud,gsd->gus", qt, k)
+        s = abs(scale) * np.einsum("gud,gsd->gus", np.abs(qt), np.abs(k))
+        if softcap > 0:
+            x = softcap * np.tanh(x / softcap)
+        if slopes is not None:
+            bias = np.asarray(slopes, dtype=np.float64).reshape(k.shape[0], group, 1) * np.abs(
+                np.arange(lo, hi + 1) - n)
+            x = x - bias
+            far[t] = np.abs(bias).max(-1).reshape(hq, 1)
+        top = x.max(-1, keepdims=True)
+        if sinks is not None:
+            sk = np.asarray(sinks, dtype=np.float64).reshape(k.shape[0], group, 1)
+            top = np.maximum(top, sk)
+        e = np.exp(x - top)
+        total = e.sum(-1, keepdims=True)
+        if sinks is not None:
+            total = total + np.exp(sk - top)
+        p = e / total
+        out[t] = np.einsum("gus,gsd->gud", p, v).reshape(hq, d)
+        mass[t] = np.einsum("gus,gsd->gud", p, np.abs(v)).reshape(hq, d)
+        size[t] = s.max(-1).reshape(hq, 1)
+    return out, mass, size, far
