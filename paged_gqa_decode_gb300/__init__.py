@@ -28,6 +28,7 @@ Entry points (same names as the C ABI, without the ``pgd_`` / ``pgdx_`` prefix):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -75,6 +76,8 @@ class DecodeOptions(ctypes.Structure):
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Loads libpgd.so (built by ``paged_gqa_decode_gb300.build``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = path or LIB_PATH
@@ -183,28 +186,44 @@ def status_string(status: int) -> str:
     return load_library().pgd_status_string(status).decode()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream: torch.cuda.Stream | None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:  # the current stream's handle, without a Stream object for it
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+_no_switch = contextlib.nullcontext()
+
+
+def _on_device(index: int):
+    """Makes a device the current one; most calls find it so (and the guard of
+    torch.cuda.device costs as much as a small call's kernel runs)."""
+    return _no_switch if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _check_cuda(*tensors: torch.Tensor | None) -> torch.device:
+def _check_cuda(*tensors: torch.Tensor | None) -> int | None:
+    """The index of the device all tensors given are on, checking that it is one
+    and that they are contiguous (None: no tensor)."""
     device = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("paged_gqa_decode_gb300 runs on CUDA tensors only")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError("all tensors must be on one device")
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("paged_gqa_decode_gb300 runs on CUDA tensors only")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            if device is None:
+                device = t.get_device()
+            elif t.get_device() != device:
+                raise ValueError("all tensors must be on one device")
     return device
 
 
@@ -243,7 +262,7 @@ def kv_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, table: torch.Tenso
     dims = make_dims(rows=rows, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d,
                      num_pages=_pool_pages(k_pool, hkv, d), max_pages_per_row=table.shape[1],
                      layout=layout)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         rc = load_library().pgd_kv_append_paged(
             ctypes.byref(dims), _ptr(k_new), _ptr(v_new), _ptr(table), _ptr(positions),
             _ptr(k_pool), _ptr(v_pool), _stream_handle(stream))
@@ -362,13 +381,13 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
                      max_pages_per_row=table.shape[1], layout=layout)
     opts = DecodeOptions(pages_per_split, kernel)
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if out is None:
             out = torch.empty_like(q)
         elif out.shape != q.shape or out.dtype != torch.bfloat16:
             raise ValueError("out must be bf16 shaped like q")
-        need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-        if workspace is None:
+        if workspace is None:  # (one that is given is checked by the call)
+            need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         tail = (_ptr(table), _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -414,7 +433,7 @@ def rope_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.
     dims = make_dims(rows=rows, num_q_heads=q.shape[1] if q is not None else hkv,
                      num_kv_heads=hkv, head_dim=d, num_pages=_pool_pages(k_pool, hkv, d),
                      max_pages_per_row=width, layout=layout)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         rc = load_library().pgd_rope_append_paged(
             ctypes.byref(dims), float(theta), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(table),
             _ptr(positions), _ptr(slots), _ptr(k_pool), _ptr(v_pool), _stream_handle(stream))
@@ -438,7 +457,7 @@ def page_slots(table: torch.Tensor, positions: torch.Tensor, rows: torch.Tensor 
     tokens = positions.shape[0]
     dims = make_dims(rows=tokens, num_q_heads=1, num_kv_heads=1, head_dim=64,
                      num_pages=num_pages, max_pages_per_row=table.shape[1])
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         slots = torch.empty(tokens, dtype=torch.int32, device=dev)
         rc = load_library().pgd_page_slots(ctypes.byref(dims), table.shape[0], _ptr(table),
                                            _ptr(rows), _ptr(positions), _ptr(slots),
@@ -461,7 +480,7 @@ def kv_write_slots(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor
         raise ValueError("inconsistent shapes")
     dims = make_dims(rows=tokens, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d,
                      num_pages=_pool_pages(k_pool, hkv, d), max_pages_per_row=1, layout=layout)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         rc = load_library().pgd_kv_write_slots(ctypes.byref(dims), _ptr(k_new), _ptr(v_new),
                                                _ptr(slots), _ptr(k_pool), _ptr(v_pool),
                                                _stream_handle(stream))
@@ -544,13 +563,13 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
                      max_pages_per_row=table.shape[1], layout=layout)
     opts = DecodeOptions(pages_per_split, kernel)
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if out is None:
             out = torch.empty_like(q)
         elif out.shape != q.shape or out.dtype != torch.bfloat16:
             raise ValueError("out must be bf16 shaped like q")
-        need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-        if workspace is None:
+        if workspace is None:  # (one that is given is checked by the call)
+            need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         ws = (_ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
               ctypes.byref(opts), _stream_handle(stream))
@@ -611,7 +630,7 @@ def kv_append_rows(k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Te
             or positions.shape != (k_new.shape[0],):
         raise ValueError("inconsistent shapes")
     dims = _dense_dims(cache_k, k_new.shape[0], k_new.shape[1])
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         rc = load_library().pgd_kv_append_paged(
             ctypes.byref(dims), _ptr(k_new), _ptr(v_new), None, _ptr(positions), _ptr(cache_k),
             _ptr(cache_v), _stream_handle(stream))
@@ -673,11 +692,11 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
     dims = _dense_dims(cache_k, rows, hq)
     opts = DecodeOptions(pages_per_split, kernel)
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if out is None:
             out = torch.empty_like(q)
-        need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-        if workspace is None:
+        if workspace is None:  # (one that is given is checked by the call)
+            need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         tail = (None, _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -756,16 +775,19 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
     dev = _check_cuda(table, cached, new_tokens, free_pages, free_head)
     for t, n in ((table, "table"), (cached, "cached"), (new_tokens, "new_tokens"),
                  (free_pages, "free_pages"), (free_head, "free_head")):
-        if t is not None:
+        if t is not None and t.dtype != torch.int32:
             _dtype(t, torch.int32, n)
-    if table.dim() != 2 or cached.shape != (table.shape[0],) or new_tokens.shape != cached.shape \
-            or free_pages.dim() != 1 or (free_head is not None and free_head.numel() != 1):
+    requests, width = table.shape if table.dim() == 2 else (-1, 0)
+    if cached.shape != (requests,) or new_tokens.shape != (requests,) or free_pages.dim() != 1 \
+            or (free_head is not None and free_head.numel() != 1):
         raise ValueError("inconsistent shapes")
-    requests, width = table.shape
-    sizes = [num_tokens, num_tokens, num_tokens, requests + 1, requests, 1]
-    with torch.cuda.device(dev):
-        if out is None:
-            out = PagePlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+    sizes = (num_tokens, num_tokens, num_tokens, requests + 1, requests, 1)
+    with _on_device(dev):
+        if out is None:  # one allocation, cut into the plan's arrays
+            if num_tokens < 0:
+                raise ValueError("num_tokens must be >= 0")
+            whole = table.new_empty(3 * num_tokens + 2 * requests + 2)
+            out = PagePlan(*torch.unsafe_split_with_sizes(whole, sizes))
         else:
             if _check_cuda(*out) != dev:
                 raise ValueError("all tensors must be on one device")
@@ -773,10 +795,12 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
                 _dtype(t, torch.int32, n)
                 if t.shape != (size,):
                     raise ValueError(f"out.{n} must have {size} entries")
+        rows, positions, slots, starts, lengths, head = out
         rc = load_extension().pgdx_assign_pages(
-            requests, width, num_pages, num_tokens, _ptr(table), _ptr(cached), _ptr(new_tokens),
-            _ptr(free_pages), free_pages.shape[0], _ptr(free_head), *(t.data_ptr() for t in out),
-            _stream_handle(stream))
+            requests, width, num_pages, num_tokens, table.data_ptr(), cached.data_ptr(),
+            new_tokens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], _ptr(free_head),
+            rows.data_ptr(), positions.data_ptr(), slots.data_ptr(), starts.data_ptr(),
+            lengths.data_ptr(), head.data_ptr(), _stream_handle(stream))
     if rc != OK:
         raise PgdError(rc, "assign_pages")
     return out
@@ -817,10 +841,13 @@ class Rotary:
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Values from token to token of a [P, heads, D] tensor whose tokens are
     contiguous (a view of a fused projection, say)."""
-    _, heads, d = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    tokens, heads, d = t.shape
+    if t.is_contiguous():
+        return heads * d
+    token, head, value = t.stride()
+    if value != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+    return token if tokens > 1 else heads * d
 
 
 def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -843,7 +870,7 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     dev = _check_cuda(positions, k_pool, v_pool, slots, table, rows, q_out)
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         if t is not None:
-            if not t.is_cuda or t.device != dev:
+            if t.get_device() != dev:
                 raise ValueError("all tensors must be on one CUDA device")
             if t.dim() != 3:
                 raise ValueError(f"{n} must be [P, heads, D]")
@@ -873,7 +900,7 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     dims = make_dims(rows=tokens, num_q_heads=q.shape[1] if q is not None else hkv,
                      num_kv_heads=hkv, head_dim=d, num_pages=_pool_pages(k_pool, hkv, d),
                      max_pages_per_row=width, layout=layout)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         rc = load_extension().pgdx_rotary_append(

@@ -228,6 +228,23 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// One word of a rotated pair of words: two pairs across the halves of a head
+// (x in wx, y in wy), or four adjacent pairs of a chunk.
+__device__ __forceinline__ void turn_across(uint32_t& wx, uint32_t& wy, float c0, float s0,
+                                            float c1, float s1) {
+  const float x0 = bf16_lo(wx), x1 = bf16_hi(wx), y0 = bf16_lo(wy), y1 = bf16_hi(wy);
+  wx = pack_pair(fmaf(x0, c0, -(y0 * s0)), fmaf(x1, c1, -(y1 * s1)));
+  wy = pack_pair(fmaf(y0, c0, x0 * s0), fmaf(y1, c1, x1 * s1));
+}
+__device__ __forceinline__ void turn_adjacent(uint32_t* w, const float4& c, const float4& s) {
+  const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = bf16_lo(w[k]), y = bf16_hi(w[k]);
+    w[k] = pack_pair(fmaf(x, cs[k], -(y * sn[k])), fmaf(y, cs[k], x * sn[k]));
+  }
+}
+
 // Pair (x, y) of frequency i at position n: (x c - y s, y c + x s) with c + i s
 // = factor e^{2 pi i n f}, f in turns.  The phase is an integer product: n
 // times the 64-bit fraction f, its overflow dropping whole turns exactly, so
@@ -239,29 +256,49 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 // (rd the rotary_dim) -- the pairs across the halves, or eight adjacent pairs
 // of the interleaved layout -- and the units past rd / 16 copy the rest of the
 // head, as all of v's do.  A thread's units are a multiple of D / 16 apart, so
-// it needs the same eight frequencies for all of them.
+// it needs the same eight frequencies for all of them.  Bound by memory: a
+// thread has its (nearly always only) unit in flight while the token's
+// position, slot and angles are found.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(512) rotary_append_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(512, 4) rotary_append_kernel(const RotaryParams p) {
   constexpr int kUnits = D / 16;
-  __shared__ float cos_t[64], sin_t[64];
+  __shared__ __align__(16) float cos_t[64], sin_t[64];
   pdl_wait();
   pdl_allow_dependents();
   const int b = blockIdx.x;
+  const int rot = p.rotary.rotary_dim / 16;  // rotating units of a head
+  const int u = threadIdx.x % kUnits;
+  const bool rotates = u < rot;
+  const int ca = rotates ? u : 2 * u, cb = rotates ? u + rot : 2 * u + 1;  // the unit's chunks
+  const int hq = p.q ? p.hq : 0;
+  const int heads = hq + 2 * p.hkv;
+  auto load = [&](int h, uint4& a, uint4& z) {
+    const uint16_t* src = h < hq           ? p.q + (size_t)b * p.q_stride + h * D
+                          : h < hq + p.hkv ? p.k_new + (size_t)b * p.k_stride + (h - hq) * D
+                                           : p.v_new + (size_t)b * p.v_stride + (h - hq - p.hkv) * D;
+    a = *reinterpret_cast<const uint4*>(src + 8 * ca);
+    z = *reinterpret_cast<const uint4*>(src + 8 * cb);
+  };
+  // The first unit's values do not wait for the token's position.
+  int h = threadIdx.x / kUnits;
+  uint4 a, z;
+  if (h < heads) load(h, a, z);
+
   const int n = p.positions[b];
-  if (n < 0) return;  // left alone
-  int page, in_page;
+  int page = -1, in_page = 0;
+  bool skip = n < 0;  // left alone
   if (p.slots) {
     const int slot = p.slots[b];
-    if (slot < 0) return;
+    skip = skip || slot < 0;
     page = slot / kPage;
     in_page = slot % kPage;
-    if (page >= p.num_pages) page = -1;
-  } else {
+  } else if (!skip) {
     const int row = p.row_of ? p.row_of[b] : b;
-    const bool in_table = (!p.row_of || (row >= 0 && row < p.table_rows)) && n / kPage < p.maxp;
-    page = in_table ? page_of(p.table, row, n / kPage, p.maxp) : -1;
+    if ((!p.row_of || (row >= 0 && row < p.table_rows)) && n / kPage < p.maxp)
+      page = page_of(p.table, row, n / kPage, p.maxp);
     in_page = n % kPage;
   }
+  if (skip) return;
   if (page < 0 || page >= p.num_pages) {
     if (threadIdx.x == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
     return;
@@ -276,55 +313,36 @@ __global__ void __launch_bounds__(512) rotary_append_kernel(const RotaryParams p
     sin_t[i] = s * p.rotary.factor;
   }
   __syncthreads();
-  const int rot = p.rotary.rotary_dim / 16;  // rotating units of a head
-  const int u = threadIdx.x % kUnits;
-  const bool rotates = u < rot;
-  const int ca = rotates ? u : 2 * u, cb = rotates ? u + rot : 2 * u + 1;  // the unit's chunks
-  float c[8], s[8];
-  if (rotates) {
+  for (; h < heads; h += blockDim.x / kUnits) {
+    if (h >= blockDim.x / kUnits) load(h, a, z);
+    if (rotates && h < hq + p.hkv) {
+      uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+      uint32_t* wz = reinterpret_cast<uint32_t*>(&z);
+      if constexpr (kInterleaved) {
+        const float4 c0 = *reinterpret_cast<const float4*>(cos_t + 4 * ca);
+        const float4 s0 = *reinterpret_cast<const float4*>(sin_t + 4 * ca);
+        const float4 c1 = *reinterpret_cast<const float4*>(cos_t + 4 * cb);
+        const float4 s1 = *reinterpret_cast<const float4*>(sin_t + 4 * cb);
+        turn_adjacent(wa, c0, s0);
+        turn_adjacent(wz, c1, s1);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = kInterleaved ? 4 * (e < 4 ? ca : cb) + (e & 3) : 8 * u + e;
-      c[e] = cos_t[i];
-      s[e] = sin_t[i];
+        for (int w = 0; w < 4; w += 2) {
+          const float4 c = *reinterpret_cast<const float4*>(cos_t + 8 * u + 2 * w);
+          const float4 s = *reinterpret_cast<const float4*>(sin_t + 8 * u + 2 * w);
+          turn_across(wa[w], wz[w], c.x, s.x, c.y, s.y);
+          turn_across(wa[w + 1], wz[w + 1], c.z, s.z, c.w, s.w);
+        }
+      }
     }
-  }
-  const int hq = p.q ? p.hq : 0;
-  const int heads = hq + 2 * p.hkv;
-  for (int h = threadIdx.x / kUnits; h < heads; h += blockDim.x / kUnits) {
-    const uint16_t* src;
     uint16_t* dst;
     if (h < hq) {
-      src = p.q + (size_t)b * p.q_stride + h * D;
       dst = p.q_out + (size_t)b * p.q_out_stride + h * D;
     } else {
       const bool is_k = h < hq + p.hkv;
       const int g = h - hq - (is_k ? 0 : p.hkv);
-      src = (is_k ? p.k_new + (size_t)b * p.k_stride : p.v_new + (size_t)b * p.v_stride) + g * D;
       const int64_t row0 = tile_first_row(p.layout, page, g, p.hkv, p.num_pages, p.maxp);
       dst = (is_k ? p.k_pool : p.v_pool) + ((size_t)row0 + in_page) * D;
-    }
-    uint4 a = *reinterpret_cast<const uint4*>(src + 8 * ca);
-    uint4 z = *reinterpret_cast<const uint4*>(src + 8 * cb);
-    if (rotates && h < hq + p.hkv) {
-      uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-      uint32_t* wz = reinterpret_cast<uint32_t*>(&z);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if constexpr (kInterleaved) {
-          const float x0 = bf16_lo(wa[w]), y0 = bf16_hi(wa[w]);
-          const float x1 = bf16_lo(wz[w]), y1 = bf16_hi(wz[w]);
-          wa[w] = pack_pair(fmaf(x0, c[w], -(y0 * s[w])), fmaf(y0, c[w], x0 * s[w]));
-          wz[w] = pack_pair(fmaf(x1, c[w + 4], -(y1 * s[w + 4])),
-                            fmaf(y1, c[w + 4], x1 * s[w + 4]));
-        } else {
-          const float x0 = bf16_lo(wa[w]), x1 = bf16_hi(wa[w]);
-          const float y0 = bf16_lo(wz[w]), y1 = bf16_hi(wz[w]);
-          const int e = 2 * w;
-          wa[w] = pack_pair(fmaf(x0, c[e], -(y0 * s[e])), fmaf(x1, c[e + 1], -(y1 * s[e + 1])));
-          wz[w] = pack_pair(fmaf(y0, c[e], x0 * s[e]), fmaf(y1, c[e + 1], x1 * s[e + 1]));
-        }
-      }
     }
     *reinterpret_cast<uint4*>(dst + 8 * ca) = a;
     *reinterpret_cast<uint4*>(dst + 8 * cb) = z;
