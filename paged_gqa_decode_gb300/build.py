@@ -22,7 +22,8 @@ SOURCES = ["pgd_api.cu", "kv_append.cu", "paged_decode_d64.cu", "paged_decode_d1
            "paged_prefill.cu", "paged_prefill_umma.cu", "paged_prefill_umma_d64.cu",
            "paged_prefill_pair.cu"]
 EXT_SOURCES = ["pgd_ext_api.cu", "batch_ops.cu", "mod_decode_d64.cu", "mod_decode_d128.cu",
-               "mod_prefill_d64.cu", "mod_prefill_d128.cu"]
+               "mod_prefill.cu"] + [f"mod_prefill_d{d}_{kind}.cu" for d in (64, 128)
+                                    for kind in ("mask", "cap", "bias", "cap_bias")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-Xptxas", "-v", f"-I{INCLUDE}", f"-I{CSRC}"]

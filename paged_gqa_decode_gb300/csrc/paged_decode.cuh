@@ -135,7 +135,7 @@ struct MmaConsumer {
   uint32_t off_k[4], off_v[4];
   int gid, tig;
   float c;
-  // ModScore: the cap (see cap_near), and per head the bias per position of
+  // ModScore: the cap (see cap_mid), and per head the bias per position of
   // distance in log2 units (negated slope); page() gets the query's position
   // relative to the page in `here`
   float cap_in, cap_out, bias[2], here;
@@ -187,11 +187,11 @@ struct MmaConsumer {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         top = fmax3(top, fmax3(fabsf(s[t][0]), fabsf(s[t][1]), fabsf(s[t][2])), fabsf(s[t][3]));
-      if (__all_sync(0xffffffffu, top * fabsf(cap_in) <= 1.f)) {
+      if (__all_sync(0xffffffffu, top * fabsf(cap_in) <= kTanhMid)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] = cap_near(s[t][e], cap_in, c);
+          for (int e = 0; e < 4; ++e) s[t][e] = cap_mid(s[t][e], cap_in, cap_out);
       } else {
 #pragma unroll
         for (int t = 0; t < NT; ++t)

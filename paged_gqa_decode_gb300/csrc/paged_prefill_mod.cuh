@@ -1,0 +1,1114 @@
+// Prefill attention with modified scores (paged_score.cuh) on the tcgen05
+// tensor cores, sm_103a.
+//
+// What it computes (include/pgd_ext.h, pgdx_score): packed token p at position
+// n of table row r attends, with each query head h of its group, over the keys
+// lo .. hi of that row, lo = max(0, first_key, n - window + 1), hi = max(n,
+// prefix_len - 1), with scores cap tanh(scale q.k / cap) - slope_h |n - j|, the
+// sink in the denominator only; no key seen: zeros.
+//
+// Work items, their order and runs are those of the one-SM kernel without
+// modified scores (paged_prefill_umma.cuh): (block of 2 x 128 / G consecutive
+// packed tokens, kv head), two query tiles of 128 (token, head) rows; the
+// tokens of a run share table row and first key and have consecutive
+// positions, and a run is one pass over the pages that its tokens see.
+//
+// What bounds it is the softmax: 64 exponentials a row and page are 256 cycles
+// of a sub-partition's special function unit for each of its four softmax
+// warps, and every trip to TMEM or through a barrier costs hundreds of cycles
+// that only other warps can fill.  So
+//   - the two warpgroups of a tile take its pages in turn, each with S columns
+//     of its own, a whole row of 64 scores to a thread: four independent
+//     warps a sub-partition, in different phases of their pages.  (Warpgroups
+//     that share a page and exchange its maxima at a barrier move in lockstep
+//     and queue at one pipe after the other: 128-key steps in that form
+//     measured 1.5 times slower, with one thread to 128 keys 1.7 times.)
+//   - all that a page needs from the one before is the row's reference m, handed
+//     from warp to warp through shared memory; it rises only when a score
+//     exceeds it by more than 2^8;
+//   - S is read from TMEM once;
+//   - a capped score is a polynomial in s^2 times s plus what the exponent needs
+//     anyway: y = s Q(s^2) + (bias - m), four packed instructions for two keys;
+//   - P is rounded to bf16 once, without a residual product: an output is off
+//     by at most 2^-8 sum_j p_j |v_j| and typically by as much again as its own
+//     rounding to bf16; the row sums take the unrounded values;
+//   - a tile without rows of a run (a block that reaches into another row or
+//     document) takes no part in it.
+//
+// Warps (640 threads):
+//   0-15  softmax: tile t has two warpgroups (warps 4t .. and 8 + 4t ..), one
+//         thread per query row in each; warpgroup h takes the tile's pages
+//         i = h mod 2 (and half of the O columns for the store), and zeroes a
+//         boundary page's V rows outside the run's range (the first tile that
+//         takes part).
+//   16    producer: takes items from the counter, lays out their runs (checks
+//         the table, zeroes uncovered outputs), copies Q and streams K pages.
+//   17    S issuer and TMEM owner, 18 P V issuer (one thread each), 19 V pages.
+// Shared memory: K and V rings of page tiles (four each at head_dim 128, eight
+// at 64), Q (two buffers at 64, so that the next item's is there early); 192 KB
+// of both.  TMEM: O_t at t D, then S of (tile, h), 64 columns each; P, 32 columns
+// of bf16 pairs, at head_dim 64 after them (S of the page after next is computed
+// as soon as S is read), at 128 over S (it then waits for P V).
+// Key parts as in the one-SM kernel.
+// Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
+// roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.
+#pragma once
+
+#include "paged_prefill_umma.cuh"
+#include "pgd_ext_internal.h"
+
+namespace pgd {
+
+template <int D>
+struct ModPrefillCfg {
+  static constexpr int kRows = 128, kTiles = 2;
+  static constexpr int kSoftmaxWarps = 16;
+  static constexpr int kProducerWarp = 16, kMmaWarp = 17, kPvWarp = 18, kVWarp = 19;
+  static constexpr int kThreads = 640;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kPage * D * 2;
+  static constexpr int kRing = D == 128 ? 4 : 8;
+  static constexpr int kQBufs = D == 128 ? 1 : 2;
+  static constexpr int kQBoxBytes = kRows * 128;
+  static constexpr int kQTileBytes = kRows * D * 2;
+  static constexpr int kQBytes = kTiles * kQTileBytes;
+  static constexpr int kVOff = kRing * kTileBytes;
+  static constexpr int kQOff = 2 * kRing * kTileBytes;
+  static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
+  static constexpr int kNumBars = 4 * kRing + 8 * kTiles + 16 + 4 + 2 * kQBufs + 2;
+  static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr bool kOwnP = D == 64;  // P beside S (else over it)
+  static constexpr uint32_t kOCol = 0, kSCol = kTiles * D;
+  // S of (tile t, parity h): kSCol + (2 t + h) kPage; P: kPCol + (2 t + h) kPStride
+  static constexpr uint32_t kPCol = kOwnP ? kSCol + 2 * kTiles * kPage : kSCol;
+  static constexpr uint32_t kPStride = kOwnP ? kPage / 2 : kPage;
+  static constexpr uint32_t kIdescS = umma_idesc_bf16(128, kPage, 0, 0);
+  static constexpr uint32_t kIdescPV = umma_idesc_bf16(128, D, 0, 1);
+  static_assert(D == 64 || D == 128, "head_dim");
+  static_assert(kPCol + 3 * kPStride + kPage / 2 <= kTmemCols &&
+                    kSCol + 2 * kTiles * kPage <= kTmemCols,
+                "TMEM columns");
+  static_assert(kSmemBytes + 24 * 1024 <= 227 * 1024, "shared memory (dynamic + static)");
+};
+
+// One work item as the producer laid it out for the other roles.
+struct ModItem {
+  int valid;  // 0: no more items
+  int t_begin, t_end, kvh, runs;
+  int part, parts;
+  int run_end[257];
+  int tok_row[256], tok_pos[256];    // row -1: no pass covers the token
+  int tok_first[256], tok_hi[256];   // first key, last visible position
+  int run_pg[256], run_last[256];    // pages of the run (of this key part); run_pg -1: no pass
+  __device__ int lo(int k, int window) const {
+    return max(window > 0 ? tok_pos[k] - window + 1 : 0, tok_first[k]);
+  }
+  // Whether tile t (of T tokens) has rows of the run of tokens rs .. re - 1.
+  __device__ static bool takes_part(int t, int T, int rs, int re) {
+    return rs < (t + 1) * T && re > t * T;
+  }
+};
+
+// What the scores of a kernel may differ by (kernels are built for each, so that
+// the page loop holds only its own case).
+enum ModKind { kModMask = 0, kModCap = 1, kModBias = 2 };
+
+// A row's scores in log2 units, less m: y_k = s_k Q(s_k^2) + A_k for N raw
+// products s at positions rel, rel + 1, .. from the query's.
+//   Q: c = scale log2 e without a cap, else the cap's polynomial with the
+//      powers of a = scale / cap and the cap folded into its coefficients
+//      (near, mid), or cap_far in its place.
+//   A: the bias less m, linear in k where every key is at or before the query.
+// On the packed fp32 pipe, two keys at a time, but cap_far and the bias of
+// keys past the query.
+struct ModRow {
+  float c, nslope;  // scale log2 e; bias per position of distance (log2 units, <= 0 usually)
+  float near[3];    // coefficients of the near form
+  float a2;         // a^2, for the mid form
+  float cap_in, cap_out, limit_near, limit_mid;  // |s| up to which a form holds
+};
+
+enum CapForm { kNoCap, kCapNear, kCapMid, kCapFar };
+
+__device__ __forceinline__ float2 scaled2(float2 v, float2 add, const ModRow& r) {
+  return __ffma2_rn(v, make_float2(r.c, r.c), add);
+}
+__device__ __forceinline__ float2 near2(float2 v, float2 add, const ModRow& r) {
+  const float2 u = __fmul2_rn(v, v);
+  float2 q = __ffma2_rn(make_float2(r.near[2], r.near[2]), u, make_float2(r.near[1], r.near[1]));
+  q = __ffma2_rn(q, u, make_float2(r.near[0], r.near[0]));
+  return __ffma2_rn(v, q, add);
+}
+__device__ __forceinline__ float2 mid2(float2 v, float2 add, const ModRow& r) {
+  const float2 u = __fmul2_rn(__fmul2_rn(v, v), make_float2(r.a2, r.a2));
+  float2 q = __ffma2_rn(make_float2(kMid5, kMid5), u, make_float2(kMid4, kMid4));
+  q = __ffma2_rn(q, u, make_float2(kMid3, kMid3));
+  q = __ffma2_rn(q, u, make_float2(kMid2, kMid2));
+  q = __ffma2_rn(q, u, make_float2(kMid1, kMid1));
+  q = __ffma2_rn(q, u, make_float2(kMid0, kMid0));
+  return __ffma2_rn(__fmul2_rn(v, make_float2(r.c, r.c)), q, add);
+}
+
+// A page's usual case: near form (or no cap), every key at or before the query
+// where there is a bias.
+template <int KIND, int N>
+__device__ __forceinline__ void usual_scores(float (&s)[N], const ModRow& r, int rel, float m) {
+  const float b0 = KIND & kModBias ? fmaf(-r.nslope, (float)rel, -m) : -m;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float2 add = make_float2(b0, b0);
+    if constexpr (KIND & kModBias)
+      add = __ffma2_rn(make_float2(-r.nslope, -r.nslope), make_float2((float)k, (float)(k + 1)),
+                       add);
+    float2 v = make_float2(s[k], s[k + 1]);
+    if constexpr (KIND & kModCap)
+      v = near2(v, add, r);
+    else
+      v = scaled2(v, add, r);
+    s[k] = v.x;
+    s[k + 1] = v.y;
+  }
+}
+
+// Any case, for few keys at a time.
+template <int KIND, int N>
+__device__ __forceinline__ void any_scores(float (&s)[N], const ModRow& r, int form, int rel,
+                                           float m) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float2 add = make_float2(-m, -m);
+    if constexpr (KIND & kModBias) {
+      add.x = fmaf(r.nslope, fabsf((float)(rel + k)), -m);
+      add.y = fmaf(r.nslope, fabsf((float)(rel + k + 1)), -m);
+    }
+    float2 v = make_float2(s[k], s[k + 1]);
+    if constexpr (KIND & kModCap) {
+      if (form == kCapNear) {
+        v = near2(v, add, r);
+      } else if (form == kCapMid) {
+        v = mid2(v, add, r);
+      } else {
+        v.x = cap_far(v.x, r.cap_in, r.cap_out) + add.x;
+        v.y = cap_far(v.y, r.cap_in, r.cap_out) + add.y;
+      }
+    } else {
+      v = scaled2(v, add, r);
+    }
+    s[k] = v.x;
+    s[k + 1] = v.y;
+  }
+}
+
+// The score, without a bias, of the raw product s.
+template <int KIND>
+__device__ __forceinline__ float one_score(float s, const ModRow& r, int form) {
+  if constexpr ((KIND & kModCap) == 0) return s * r.c;
+  return form == kCapFar ? cap_far(s, r.cap_in, r.cap_out) : cap_mid(s, r.cap_in, r.cap_out);
+}
+
+// The largest of N values (N a multiple of 16).
+template <int N>
+__device__ __forceinline__ float row_max(const float (&s)[N]) {
+  float top[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top[j] = fmaxf(s[j], s[8 + j]);
+#pragma unroll
+  for (int k = 16; k < N; k += 16)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top[j] = fmax3(top[j], s[k + j], s[k + 8 + j]);
+  return fmax3(fmax3(top[0], top[1], top[2]), fmax3(top[3], top[4], top[5]),
+               fmaxf(top[6], top[7]));
+}
+template <int N>
+__device__ __forceinline__ float row_min(const float (&s)[N]) {
+  float low[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) low[j] = fminf(s[j], s[4 + j]);
+#pragma unroll
+  for (int k = 8; k < N; k += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) low[j] = fmin3(low[j], s[k + j], s[k + 4 + j]);
+  return fminf(fminf(low[0], low[1]), fminf(low[2], low[3]));
+}
+
+// As mbar_wait_abortable, but the thread is suspended between looks at the
+// barrier (20 us, or until the phase completes), and the waiting laid out of
+// the way of the satisfied case.
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity,
+                                                    unsigned int* err, volatile int* abort) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      record_error(err, PGD_EDEVICE_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+
+// kParts: built for key parts (`parts` units per item, partials to
+// part_acc / part_ml for the combine launch); otherwise parts is 1 and each
+// item's outputs are written directly.
+template <int D, bool kParts, int KIND>
+__global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
+    paged_prefill_mod_kernel(const __grid_constant__ CUtensorMap k_map,
+                             const __grid_constant__ CUtensorMap v_map,
+                             const __grid_constant__ CUtensorMap q_map, const ModParams p,
+                             int* item_counter, const int* block_order, int parts,
+                             float* part_acc, float* part_ml) {
+  using C = ModPrefillCfg<D>;
+  constexpr int R = C::kRing, QB = C::kQBufs;
+  const int G = p.group;
+  const int T = C::kRows / G;  // tokens per tile
+  const int tokens = C::kTiles * T;
+  const int n_blocks = (p.rows + tokens - 1) / tokens;
+  const int n_items = n_blocks * p.hkv;
+  const int n_units = kParts ? n_items * parts : n_items;
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* k_slots = base;
+  unsigned char* v_slots = base + C::kVOff;
+  unsigned char* q_smem = base + C::kQOff;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + C::kBarOff);  // K page landed
+  uint64_t* k_empty = k_full + R;          // S of the tiles taking part done
+  uint64_t* v_full = k_empty + R;          // V page landed
+  uint64_t* v_empty = v_full + R;          // their P V done
+  // [2 tile + parity of the tile's page]:
+  uint64_t* s_full = v_empty + R;              // S of the page in TMEM
+  uint64_t* s_free = s_full + 2 * C::kTiles;   // S in the warpgroup's registers
+  uint64_t* p_full = s_free + 2 * C::kTiles;   // P in TMEM (O rescaled, V rows zeroed)
+  uint64_t* o_done = p_full + 2 * C::kTiles;   // P V of the page done
+  uint64_t* m_set = o_done + 2 * C::kTiles;    // [softmax warp] its rows' reference written
+  uint64_t* item_ready = m_set + 16;           // [item % 2] descriptor written
+  uint64_t* item_free = item_ready + 2;        // [item % 2] read for the last time
+  uint64_t* q_full = item_free + 2;            // [item % QB] Q landed
+  uint64_t* q_free = q_full + QB;              // [item % QB] the item's S products done
+  uint64_t* fin = q_free + QB;                 // [issuer] every MMA it issued done
+  __shared__ ModItem items[2];
+  __shared__ float m_ref[C::kTiles][C::kRows];  // the rows' references (log2 units)
+  // [tile][slot][warpgroup][row]: row sums and references at the end of a run
+  __shared__ float2 xval[C::kTiles][2][2][C::kRows];
+  __shared__ volatile int abort_flag;
+  __shared__ uint32_t tmem_slot;
+
+  if (tid == 0) {
+    for (int s = 0; s < R; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int b = 0; b < 2 * C::kTiles; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);  // the warpgroup's warps
+      mbar_init(&p_full[b], 4);
+      mbar_init(&o_done[b], 1);
+    }
+    for (int w = 0; w < C::kSoftmaxWarps; ++w) mbar_init(&m_set[w], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&item_ready[b], 1);
+      mbar_init(&item_free[b], C::kSoftmaxWarps + 3);  // softmax warps, issuers, V producer
+    }
+    for (int b = 0; b < QB; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_free[b], 1);
+    }
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
+    mbar_init_fence();
+    abort_flag = 0;
+  }
+  {
+    // rows past T * G of each Q tile hold no token: zero them once (the
+    // per-item copies fill rows 0 .. T * G - 1 only)
+    const int filled = T * G, gap = C::kRows - filled;
+    for (int e = tid; e < QB * C::kTiles * C::kBoxes * gap * 8; e += C::kThreads) {
+      const int ch = e & 7, r = filled + (e >> 3) % gap, box = (e >> 3) / gap;
+      *reinterpret_cast<uint4*>(q_smem + box * C::kQBoxBytes + r * 128 + ch * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_shared();
+  }
+  if (warp == C::kMmaWarp) tmem_alloc(&tmem_slot, C::kTmemCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  // the set-up above touches only this CTA's shared memory and TMEM, so it
+  // overlaps the kernel before; everything from here may read its writes
+  pdl_wait();
+  pdl_allow_dependents();
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_suspended(bar, parity, p.err, &abort_flag);
+  };
+  auto all_ok = [&](bool v) { return __all_sync(0xffffffffu, v); };
+
+  // One page tile (64 rows x D): head_dim 128 comes through its 3-D map as
+  // both 64-wide boxes in one copy.
+  auto load_tile = [&](unsigned char* dst, const CUtensorMap* map, int y, uint64_t* bar) {
+    if constexpr (D == 128)
+      tma_load_3d(dst, map, 0, y, 0, bar);
+    else
+      tma_load_2d(dst, map, 0, y, bar);
+  };
+  // Streams the pages of item `it` into one ring (whole warp), page number i
+  // onwards: the table is looked up 16 pages at a time, one page a lane, one
+  // look-up ahead.  `is_k`: K pages, and both pools' pages pulled into L2 when
+  // they are looked up (the token blocks of a request reach each page together).
+  auto stream_item = [&](const ModItem& it, bool is_k, int& i) -> bool {
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    unsigned char* slots = is_k ? k_slots : v_slots;
+    const CUtensorMap* map = is_k ? &k_map : &v_map;
+    for (int r = 0; r < it.runs; ++r) {
+      const int first = it.run_pg[r], last = it.run_last[r];
+      if (first < 0 || first > last) continue;
+      const int row = it.tok_row[r == 0 ? 0 : it.run_end[r - 1]];
+      auto look_up = [&](int pg0) -> int {
+        if (lane >= 16 || pg0 + lane > last) return 0;
+        return (int)tile_first_row(p.layout, page_of(p.table, row, pg0 + lane, p.maxp), it.kvh,
+                                   p.hkv, p.num_pages, p.maxp);
+      };
+      int y_next = look_up(first);
+      for (int pg0 = first; pg0 <= last; pg0 += 16) {
+        const int y = y_next;
+        if (is_k && lane < 16 && pg0 + lane <= last && pg0 + lane >= first + R) {
+          if constexpr (D == 128) {
+            tma_prefetch_l2_3d(&k_map, 0, y, 0);
+            tma_prefetch_l2_3d(&v_map, 0, y, 0);
+          } else {
+            tma_prefetch_l2_2d(&k_map, 0, y);
+            tma_prefetch_l2_2d(&v_map, 0, y);
+          }
+        }
+        y_next = look_up(pg0 + 16);
+        for (int j = 0; j < 16 && pg0 + j <= last; ++j, ++i) {
+          const int yj = __shfl_sync(0xffffffffu, y, j);
+          const int s = i % R;
+          if (i >= R && !all_ok(wait(&empty[s], ((i / R) - 1) & 1))) return false;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[s], C::kTileBytes);
+            load_tile(slots + s * C::kTileBytes, map, yj, &full[s]);
+          }
+        }
+      }
+    }
+    return true;
+  };
+  // no copy may still be landing in shared memory when the CTA exits
+  auto drain = [&](uint64_t* full, int issued) {
+    if (lane == 0)
+      for (int j = max(0, issued - R); j < issued; ++j)
+        mbar_wait_bounded(&full[j % R], (j / R) & 1, p.err);
+  };
+
+  // The softmax warpgroups hold 64 scores a thread: registers from the other
+  // warpgroup (4 x 128 x 104 + 128 x 64 = 640 x 96, the launch's total).
+  if (warp >= C::kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == C::kProducerWarp) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+        prefetch_tensormap(&q_map);
+      }
+      int ik = 0, seq = 0;  // K pages issued, items with Q issued
+      for (bool ok = true; ok; ++seq) {
+        const int d = seq & 1;
+        ModItem& it = items[d];
+        int j = 0;
+        if (lane == 0) j = atomicAdd(item_counter, 1);
+        j = __shfl_sync(0xffffffffu, j, 0);
+        // the descriptor slot holds item seq - 2 until every role is done with it
+        if (seq >= 2 && !all_ok(wait(&item_free[d], ((seq >> 1) - 1) & 1))) break;
+        if (j >= n_units) {
+          if (lane == 0) {
+            it.valid = 0;
+            mbar_arrive(&item_ready[d]);
+          }
+          break;
+        }
+        // an item's key parts are taken one after another, so they run side by
+        // side on different SMs
+        const int item = kParts ? j / parts : j;
+        const int blk = block_order ? block_order[item / p.hkv] : n_blocks - 1 - item / p.hkv;
+        const int kvh = item % p.hkv;
+        const int t_begin = blk * tokens, t_end = min(t_begin + tokens, p.rows);
+        // the item's Q rows, [token][head] rows of 64 values, once the S products
+        // that read the buffer last are done
+        const int qb = seq % QB;
+        if (seq >= QB && !all_ok(wait(&q_free[qb], ((seq / QB) - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[qb], C::kTiles * C::kBoxes * T * G * 128);
+          for (int t = 0; t < C::kTiles; ++t)
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_3d(q_smem + qb * C::kQBytes + t * C::kQTileBytes + bx * C::kQBoxBytes, &q_map,
+                          64 * bx, kvh * G, t_begin + t * T, &q_full[qb]);
+        }
+        // tokens: bad ones are reported, and left out of every run with those
+        // that see no key (their outputs are zeroed below)
+        for (int k = lane; k < tokens; k += 32) {
+          const int t = t_begin + k;
+          int row = -1, pos = -1, first = 0, hi = -1;
+          if (t < t_end) {
+            row = p.row_of[t];
+            pos = p.positions[t];
+            bool bad = row < 0 || row >= p.table_rows || (pos >= 0 && pos / kPage >= p.maxp);
+            if (!bad && pos >= 0) {
+              const TokenSpan span = mod_span(p, t, row, pos);
+              hi = span.hi;
+              first = p.first_key ? max(p.first_key[t], 0) : 0;
+              bad = hi / kPage >= p.maxp;
+              if (span.lo > hi) row = -1;
+            }
+            if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+            if (bad || pos < 0) row = -1;
+          }
+          it.tok_row[k] = row;
+          it.tok_pos[k] = pos;
+          it.tok_first[k] = first;
+          it.tok_hi[k] = hi;
+        }
+        __syncwarp();
+        // runs: token k ends one when k + 1 starts another (or is past the end)
+        int runs = 0;
+        for (int k0 = 0; k0 < tokens; k0 += 32) {
+          const int k = k0 + lane;
+          bool brk = false;
+          if (k < tokens)
+            brk = k + 1 == tokens || it.tok_row[k + 1] != it.tok_row[k] ||
+                  it.tok_pos[k + 1] != it.tok_pos[k] + 1 || it.tok_row[k] < 0 ||
+                  it.tok_first[k + 1] != it.tok_first[k];
+          const unsigned bal = __ballot_sync(0xffffffffu, brk);
+          if (brk) it.run_end[runs + __popc(bal & ((1u << lane) - 1u))] = k + 1;
+          runs += __popc(bal);
+        }
+        if (lane == 0) {
+          it.runs = runs;
+          it.valid = 1;
+          it.t_begin = t_begin;
+          it.t_end = t_end;
+          it.kvh = kvh;
+          it.part = kParts ? j % parts : 0;
+          it.parts = kParts ? parts : 1;
+        }
+        __syncwarp();
+        // each run's pages; a table entry outside the pool among them (all of the
+        // run's, whatever the key part) leaves it out: zero outputs, reported,
+        // before any copy is issued
+        for (int r = 0; r < runs; ++r) {
+          const int rs = r == 0 ? 0 : it.run_end[r - 1], re = it.run_end[r];
+          const int row = it.tok_row[rs];
+          int first = -1, last = -1;
+          if (row >= 0) {
+            first = it.lo(rs, p.window) / kPage;
+            last = it.tok_hi[re - 1] / kPage;
+            bool bad = false;
+            for (int pg = first + lane; pg <= last; pg += 32) {
+              const int page = page_of(p.table, row, pg, p.maxp);
+              bad |= page < 0 || page >= p.num_pages;
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+              if (lane == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
+              first = -1;
+            } else if constexpr (kParts) {
+              const int64_t n = last - first + 1;
+              const int f = first;
+              first = f + (int)(n * it.part / it.parts);
+              last = f + (int)(n * (it.part + 1) / it.parts) - 1;
+            }
+          }
+          if (lane == 0) {
+            it.run_pg[r] = first;
+            it.run_last[r] = last;
+          }
+          if (first >= 0) continue;
+          // outputs of tokens that no pass covers
+          const int per_token = G * (D / 8);
+          for (int e = lane; e < (re - rs) * per_token; e += 32) {
+            const int tl = rs + e / per_token;
+            if (t_begin + tl >= t_end) continue;
+            const int g = (e / (D / 8)) % G, ch = e % (D / 8);
+            reinterpret_cast<uint4*>(p.out + ((size_t)(t_begin + tl) * p.hq + kvh * G + g) * D)[ch] =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_ready[d]);
+        ok = stream_item(it, true, ik);
+      }
+      drain(k_full, ik);
+      if (lane == 0)
+        for (int j = max(0, seq - QB); j < seq; ++j)
+          mbar_wait_bounded(&q_full[j % QB], (j / QB) & 1, p.err);
+    } else if (warp == C::kVWarp) {
+      // ------------------------------------------------------------ V producer
+      int iv = 0;
+      for (int seq = 0;; ++seq) {
+        const int d = seq & 1;
+        if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) break;
+        const ModItem& it = items[d];
+        if (!it.valid) break;
+        if (!stream_item(it, false, iv)) break;
+        if (lane == 0) mbar_arrive(&item_free[d]);
+      }
+      drain(v_full, iv);
+    } else if (warp == C::kMmaWarp || warp == C::kPvWarp) {
+      // ------------------------------------------------------------ issuers
+      if (lane == 0) {
+        const bool is_s = warp == C::kMmaWarp;
+        const uint32_t k_addr = smem_addr(k_slots), v_addr = smem_addr(v_slots);
+        int i = 0;                    // page over all items
+        int it_[C::kTiles] = {0, 0};  // pages that each tile took part in
+        bool issued = false, ok = true;
+        for (int seq = 0; ok; ++seq) {
+          const int d = seq & 1, qb = seq % QB;
+          if (!wait(&item_ready[d], (seq >> 1) & 1)) break;
+          const ModItem& it = items[d];
+          if (!it.valid) break;
+          if (is_s && !wait(&q_full[qb], (seq / QB) & 1)) break;
+          const uint32_t q_addr = smem_addr(q_smem + qb * C::kQBytes);
+          int rs = 0;
+          for (int r = 0; r < it.runs && ok; ++r) {
+            const int first = it.run_pg[r], last = it.run_last[r], re = it.run_end[r];
+            const bool part[2] = {ModItem::takes_part(0, T, rs, re),
+                                  ModItem::takes_part(1, T, rs, re)};
+            rs = re;
+            if (first < 0) continue;
+            for (int pg = first; pg <= last && ok; ++pg, ++i) {
+              const int s = i % R;
+              if (!wait(is_s ? &k_full[s] : &v_full[s], (i / R) & 1)) {
+                ok = false;
+                break;
+              }
+              if (is_s) {
+                const uint64_t kd = umma_desc_sw128(k_addr + s * C::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t) {
+                  if (!part[t]) continue;
+                  const int n = it_[t], b = 2 * t + (n & 1);
+                  // the columns are free: S of the tile's page before last is
+                  // in registers, or, with P over S, its P V is done
+                  if (n >= 2 &&
+                      !wait(C::kOwnP ? &s_free[b] : &o_done[b], ((n >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after_sync();
+                  const uint64_t qd = umma_desc_sw128(q_addr + t * C::kQTileBytes, 16, 1024);
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16(tmem + C::kSCol + b * kPage,
+                              umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
+                              umma_desc_advance(kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32),
+                              C::kIdescS, kk > 0);
+                  issued = true;
+                  umma_commit(&s_full[b]);
+                  it_[t] = n + 1;
+                }
+                if (ok) umma_commit(&k_empty[s]);
+              } else {
+                const uint64_t vd = umma_desc_sw128(v_addr + s * C::kTileBytes, kBoxBytes, 1024);
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t) {
+                  if (!part[t]) continue;
+                  const int n = it_[t], b = 2 * t + (n & 1);
+                  if (!wait(&p_full[b], (n >> 1) & 1)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after_sync();
+                  const uint32_t pa = tmem + C::kPCol + b * C::kPStride;
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16_tmem_a(tmem + C::kOCol + t * D, pa + 8 * kk,
+                                     umma_desc_advance(vd, kk * 2048), C::kIdescPV,
+                                     !(pg == first && kk == 0));
+                  issued = true;
+                  umma_commit(&o_done[b]);
+                  it_[t] = n + 1;
+                }
+                if (ok) umma_commit(&v_empty[s]);
+              }
+            }
+          }
+          if (ok && is_s) umma_commit(&q_free[qb]);
+          if (ok) mbar_arrive(&item_free[d]);
+        }
+        // every MMA this thread issued completes before TMEM is freed
+        if (issued) {
+          umma_commit(&fin[is_s ? 0 : 1]);
+          mbar_wait_bounded(&fin[is_s ? 0 : 1], 0, p.err);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ------------------------------------------------------------ softmax
+    // row; tile; parity h of the tile's pages that this warpgroup takes (and the
+    // half of the O columns that it stores)
+    const int m = tid & 127, t = (tid >> 7) & 1, h = tid >> 8;
+    const int sb = 2 * t + h;
+    int xn = 0;  // runs whose sums were exchanged
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_col = lane_base + C::kSCol + sb * kPage;
+    const uint32_t p_col = lane_base + C::kPCol + sb * C::kPStride;
+    const uint32_t o_row = lane_base + C::kOCol + t * D, o_col = o_row + h * (D / 2);
+    uint64_t* m_mine = &m_set[warp];
+    uint64_t* m_theirs = &m_set[warp ^ 8];  // the other warpgroup's warp on these rows
+    constexpr bool kCap = (KIND & kModCap) != 0, kBias = (KIND & kModBias) != 0;
+    ModRow row;
+    row.c = p.q_scale_log2;
+    row.nslope = 0.f;
+    {
+      const float a2 = p.cap_in * p.cap_in;
+      row.near[0] = kNear0 * row.c;
+      row.near[1] = kNear1 * row.c * a2;
+      row.near[2] = kNear2 * row.c * a2 * a2;
+      row.a2 = a2;
+      row.cap_in = p.cap_in;
+      row.cap_out = p.cap_out;
+      // where the folded coefficients would leave the normal range, the far
+      // form serves all scores
+      const bool folds = fabsf(p.cap_in) >= 0x1p-16f && fabsf(p.cap_in) <= 0x1p16f &&
+                         fabsf(row.c) >= 0x1p-40f && fabsf(row.c) <= 0x1p40f;
+      row.limit_near = folds ? kTanhNear / fabsf(p.cap_in) : -1.f;
+      row.limit_mid = folds ? kTanhMid / fabsf(p.cap_in) : -1.f;
+    }
+    int i = 0, gi = 0;  // this tile's pages, all pages (over all items)
+    // A thread whose wait gave up (`mine` false) carries on to the next
+    // exchange, which ORs the failures, so the tile's threads stop together.
+    bool ok = true, mine = true;
+    const uint32_t xid = 1 + t, xcount = 2 * C::kRows;
+    const int tl = t * T + m / G, g = m % G;  // token of the block, head of the group
+    const bool in_tile = m / G < T;
+    auto next_item = [&](int seq) -> bool {
+      const int d = seq & 1;
+      if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) {
+        mine = false;
+        return false;
+      }
+      return items[d].valid != 0;
+    };
+    bool have = next_item(0);
+    ok = !named_sync_or(xid, xcount, !mine);
+    for (int seq = 0; ok && have; ++seq) {
+      const int d = seq & 1;
+      const ModItem& it = items[d];
+      const int t_begin = it.t_begin, h0 = it.kvh * G;
+      const bool row_ok = in_tile && t_begin + tl < it.t_end;
+      if constexpr (kBias) row.nslope = -p.slopes[h0 + g] * kLog2e;
+      int rs = 0, re = 0;
+      for (int r = 0; r < it.runs && ok; ++r) {
+        rs = re;
+        re = it.run_end[r];
+        const int first = it.run_pg[r], last = it.run_last[r];
+        const bool live = row_ok && tl >= rs && tl < re;
+        // with key parts, a row's partial of this part at [token][head][part]
+        auto unit_of = [&]() {
+          return ((size_t)(it.t_begin + tl) * p.hq + it.kvh * G + g) * it.parts + it.part;
+        };
+        if (first < 0 || first > last) {
+          // no pass covers these tokens (their outputs are zeroed, the combine
+          // leaves them), or the key part has none of their pages
+          if constexpr (kParts) {
+            if (h == 0 && live) {
+              const size_t u = unit_of();
+              part_ml[2 * u] = -INFINITY;
+              part_ml[2 * u + 1] = first < 0 ? -1.f : 0.f;
+            }
+          }
+          continue;
+        }
+        if (!ModItem::takes_part(t, T, rs, re)) {
+          gi += last - first + 1;
+          continue;
+        }
+        // keys lo .. hi of this row, and of the run, in these pages
+        const int pos = live ? it.tok_pos[tl] : 1 << 30;  // (other rows: behind every key)
+        const int lo = live ? it.lo(tl, p.window) : 0;
+        const int hi = live ? min(it.tok_hi[tl], last * kPage + kPage - 1) : -1;
+        const int lo_run = it.lo(rs, p.window), hi_run = it.tok_hi[re - 1];
+        const bool zeroes = t == 0 || !ModItem::takes_part(0, T, rs, re);
+        float m_run = -INFINITY;  // the reference that l is relative to, log2 units
+        float l = 0.f;            // sum of this thread's pages
+        // this warpgroup's pages of the run; i, gi: their numbers
+        const int i_end = i + (last - first + 1), gi_end = gi + (last - first + 1);
+        const int skip = (i ^ h) & 1;
+        i += skip;
+        gi += skip;
+        for (int pg = first + skip; pg <= last; pg += 2, i += 2, gi += 2) {
+          if (!all_ok(wait(&s_full[sb], (i >> 1) & 1))) {
+            mine = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const int pos0 = pg * kPage;
+          bool usual = pos0 >= lo && pos0 + kPage - 1 <= hi;  // the whole page is seen
+          if constexpr (kBias) usual = usual && pos0 + kPage - 1 <= pos;
+          usual = __all_sync(0xffffffffu, usual);
+
+          auto s_read = [&]() {  // S is in registers: its columns are free
+            if constexpr (C::kOwnP) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_free[sb]);
+            }
+          };
+          // The row's reference: the page before's, unless this page's maximum
+          // mx exceeds it by the slack; handed on at once.  False: a wait failed.
+          auto settle = [&](float mx) -> bool {
+            float m_prev = -INFINITY;
+            if (pg > first) {
+              if (!all_ok(wait(m_theirs, ((i - 1) >> 1) & 1))) return false;
+              m_prev = m_ref[t][m];
+            }
+            const float m_new = mx > m_prev + kLazyRescaleLog2 ? mx : m_prev;
+            m_ref[t][m] = m_new;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m_mine);
+            if (m_new != m_run) {  // (m_run -inf: l is 0)
+              l *= m_run == -INFINITY ? 0.f : exp2_approx(m_run - m_new);
+              m_run = m_new;
+            }
+            if (__builtin_expect(
+                    __any_sync(0xffffffffu, m_new != m_prev && m_prev != -INFINITY), 0)) {
+              // O holds the pages before, once P V of the last of them is done
+              if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) return false;
+              tc_fence_after_sync();
+              const float alpha = m_prev == -INFINITY ? 1.f : exp2_approx(m_prev - m_new);
+#pragma unroll 1
+              for (int j = 0; j < D / 16; ++j) {
+                float ov[16];
+                tmem_ld16(o_row + 16 * j, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) ov[k] *= alpha;
+                tmem_st16(o_row + 16 * j, ov);
+              }
+            }
+            // P V of this warpgroup's page before has read P (P over S: S waited)
+            if (C::kOwnP && i >= 2) {
+              if (!all_ok(wait(&o_done[sb], ((i >> 1) - 1) & 1))) return false;
+              tc_fence_after_sync();
+            }
+            return true;
+          };
+
+          bool done = false;
+          if (__builtin_expect(usual, 1)) {
+            float sv[kPage];
+#pragma unroll
+            for (int q = 0; q < kPage / 16; ++q)
+              tmem_ld16(s_col + 16 * q, *reinterpret_cast<float(*)[16]>(&sv[16 * q]));
+            tmem_wait_ld();
+            // the page's maximum: of the products (a score without a bias grows,
+            // or falls, with them), or with a bias of the scores
+            float mx = 0.f;
+            done = true;
+            if constexpr (kCap) {
+              const float mn = row_min(sv);
+              mx = row_max(sv);
+              done = __all_sync(0xffffffffu, fmaxf(fabsf(mx), fabsf(mn)) <= row.limit_near);
+              mx = fmaxf(one_score<KIND>(mx, row, kCapNear), one_score<KIND>(mn, row, kCapNear));
+            } else if constexpr (!kBias) {
+              mx = row.c > 0.f ? row_max(sv) * row.c : row_min(sv) * row.c;
+            }
+            if (__builtin_expect(done, 1)) {
+              s_read();
+              if constexpr (kBias) {
+                usual_scores<KIND>(sv, row, pos0 - pos, 0.f);
+                mx = row_max(sv);
+              }
+              if (!settle(mx)) {
+                mine = false;
+                break;
+              }
+              const float ref = m_run == -INFINITY ? 0.f : m_run;
+              if constexpr (!kBias) usual_scores<KIND>(sv, row, 0, ref);
+              float2 sum2[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < kPage / 32; ++q) {
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  float2 y = make_float2(sv[32 * q + 2 * j], sv[32 * q + 2 * j + 1]);
+                  if constexpr (kBias) y = __fadd2_rn(y, make_float2(-ref, -ref));
+                  const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                  sum2[j & 3] = __fadd2_rn(sum2[j & 3], x);
+                  w[j] = pack_bf16x2(x.x, x.y);
+                }
+                tmem_st16(p_col + 16 * q, w);
+              }
+              const float2 s2 =
+                  __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+              l += s2.x + s2.y;
+            }
+          }
+          if (__builtin_expect(!done, 0)) {
+            // Any other page, 16 keys at a time in rolled loops: keys masked, keys
+            // past the query with a bias, scores near their cap.
+            constexpr int kFew = 16;
+            float mx = -INFINITY, mn = INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < kPage; q += kFew) {
+              float sv[kFew];
+              tmem_ld16(s_col + q, sv);
+              tmem_wait_ld();
+              const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
+#pragma unroll
+              for (int k = 0; k < kFew; ++k)
+                if (k >= k_lo && k <= k_hi) {
+                  mx = fmaxf(mx, sv[k]);
+                  mn = fminf(mn, sv[k]);
+                }
+            }
+            int form = kNoCap;
+            if constexpr (kCap) {
+              const float most = mx == -INFINITY ? 0.f : fmaxf(fabsf(mx), fabsf(mn));
+              form = __all_sync(0xffffffffu, most <= row.limit_near)  ? kCapNear
+                     : __all_sync(0xffffffffu, most <= row.limit_mid) ? kCapMid
+                                                                      : kCapFar;
+            }
+            if constexpr (kBias) {
+              mx = -INFINITY;
+#pragma unroll 1
+              for (int q = 0; q < kPage; q += kFew) {
+                float sv[kFew];
+                tmem_ld16(s_col + q, sv);
+                tmem_wait_ld();
+                any_scores<KIND>(sv, row, form, pos0 + q - pos, 0.f);
+                const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
+#pragma unroll
+                for (int k = 0; k < kFew; ++k)
+                  if (k >= k_lo && k <= k_hi) mx = fmaxf(mx, sv[k]);
+              }
+            } else if (mx != -INFINITY) {
+              mx = fmaxf(one_score<KIND>(mx, row, form), one_score<KIND>(mn, row, form));
+            }
+            if (!settle(mx)) {
+              mine = false;
+              break;
+            }
+            const float ref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll 1
+            for (int q = 0; q < kPage; q += kFew) {
+              float sv[kFew];
+              tmem_ld16(s_col + q, sv);
+              tmem_wait_ld();
+              if (q + kFew == kPage) s_read();
+              any_scores<KIND>(sv, row, form, pos0 + q - pos, ref);
+              const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
+              uint32_t w[kFew / 2];
+#pragma unroll
+              for (int j = 0; j < kFew / 2; ++j) {
+                const int k = 2 * j;
+                const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[k]) : 0.f;
+                const float y = k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[k + 1]) : 0.f;
+                l += x + y;
+                w[j] = pack_bf16x2(x, y);
+              }
+              tmem_st8(p_col + q / 2, w);
+            }
+          }
+          // V rows outside the run's key range on a boundary page -> zero (both
+          // tiles' products are issued after this tile's P)
+          if (zeroes) {
+            const int rlo = max(lo_run - pos0, 0), rhi = min(hi_run - pos0, kPage - 1);
+            if (rlo > 0 || rhi < kPage - 1) {
+              if (!all_ok(wait(&v_full[gi % R], (gi / R) & 1))) {
+                mine = false;
+                break;
+              }
+              unsigned char* vt = v_slots + (gi % R) * C::kTileBytes;
+              for (int e = m; e < kPage * (D / 8); e += C::kRows) {
+                const int k = e / (D / 8), ch = e % (D / 8);
+                if (k < rlo || k > rhi)
+                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * kBoxBytes + k * 128 +
+                                            (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_shared();  // the zeros are read by the tensor core
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[sb]);
+        }
+
+        i = i_end;
+        gi = gi_end;
+        // end of run: the O_t row once P V of the last page is done
+        if (mine) {
+          if (all_ok(wait(&o_done[2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1)))
+            tc_fence_after_sync();
+          else
+            mine = false;
+        }
+        {  // the row's sum over both warpgroups' pages, relative to the last reference
+          const int sl = xn & 1;
+          xval[t][sl][h][m] = make_float2(l, m_run);
+          if (named_sync_or(xid, xcount, !mine)) {
+            ok = false;
+            break;
+          }
+          const float2 other = xval[t][sl][1 - h][m];
+          const float m_end = fmaxf(m_run, other.y);
+          if (m_end != -INFINITY)
+            l = l * exp2_approx(m_run - m_end) + other.x * exp2_approx(other.y - m_end);
+          m_run = m_end;
+          ++xn;
+        }
+        float inv = 1.f;
+        float* arow = nullptr;
+        if constexpr (kParts) {
+          // the row's partial over this part's keys, unnormalised (the sink
+          // and the other parts are merged by the combine launch)
+          if (live) {
+            const size_t u = unit_of();
+            if (h == 0) {
+              part_ml[2 * u] = m_run;
+              part_ml[2 * u + 1] = l;
+            }
+            arow = part_acc + u * D + h * (D / 2);
+          }
+        } else if (live) {
+          const float sk = p.sinks ? p.sinks[h0 + g] * kLog2e : -INFINITY;
+          const float mf = fmaxf(m_run, sk);
+          const float scl = exp2_approx(m_run - mf);
+          const float total = fmaf(l, scl, exp2_approx(sk - mf));
+          inv = l == 0.f ? 0.f : scl / total;
+        }
+        uint16_t* orow =
+            p.out + ((size_t)(t_begin + (live ? tl : 0)) * p.hq + h0 + g) * D + h * (D / 2);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {  // this half's O columns
+          float ov[16];
+          tmem_ld16(o_col + 16 * j, ov);
+          tmem_wait_ld();
+          if (!live) continue;
+          if constexpr (kParts) {
+            float4* dst = reinterpret_cast<float4*>(arow + 16 * j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(ov[2 * k] * inv, ov[2 * k + 1] * inv);
+            uint4* dst = reinterpret_cast<uint4*>(orow + 16 * j);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        tc_fence_before_sync();
+      }
+      if (!ok) break;
+      // this item's descriptor is no longer read: free its slot before
+      // waiting for the next item
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_free[d]);
+      have = next_item(seq + 1);
+      ok = !named_sync_or(xid, xcount, !mine);
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, bool kParts, int KIND>
+cudaError_t launch_prefill_mod_kernel(const ModParams& p, const CUtensorMap& k_map,
+                                      const CUtensorMap& v_map, const CUtensorMap& q_map,
+                                      unsigned ctas, int* counter, const int* order, int parts,
+                                      float* part_acc, float* part_ml, cudaStream_t stream) {
+  using C = ModPrefillCfg<D>;
+  auto kern = paged_prefill_mod_kernel<D, kParts, KIND>;
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
+  }
+  return launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kSmemBytes, stream, k_map, v_map,
+                    q_map, p, counter, order, parts, part_acc, part_ml);
+}
+
+// As launch_prefill_umma: `prepared` -- the step's write launch has zeroed the
+// work counter and written the block order; `parts` > 1 -- key parts, merged by
+// a combine launch.
+template <int D, int KIND>
+cudaError_t launch_prefill_mod(const ModParams& p, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, const CUtensorMap& q_map, int sm_count,
+                               bool prepared, int parts, cudaStream_t stream) {
+  using C = ModPrefillCfg<D>;
+  if (parts < 1 || (parts > 1 && (parts > p.max_splits - 1 || p.rows > 65535)))
+    return cudaErrorInvalidValue;
+  if (p.rows == 0) return cudaSuccess;
+  const int tokens = C::kTiles * (C::kRows / p.group);
+  const int n_blocks = (p.rows + tokens - 1) / tokens;
+  int* counter = reinterpret_cast<int*>(p.ws_acc);
+  const int64_t units = (int64_t)n_blocks * p.hkv * parts;
+  // longest first, unless every unit has an SM at once
+  const bool sorted = prepared || units > sm_count;
+  int* order =
+      sorted && p.window == 0 && n_blocks <= kMaxSortedBlocks ? counter + 4 : nullptr;
+  cudaError_t e;
+  if (!prepared) {
+    e = order ? launch_pdl(prefill_block_order_kernel<D, ModScore>, dim3(1),
+                           dim3(block_order_threads(n_blocks)), 0, stream, p, tokens, n_blocks,
+                           counter, order)
+              : cudaMemsetAsync(counter, 0, sizeof(int), stream);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned ctas = (unsigned)(units < sm_count ? units : sm_count);
+  if (parts == 1)
+    return launch_prefill_mod_kernel<D, false, KIND>(p, k_map, v_map, q_map, ctas, counter, order,
+                                                     1, nullptr, nullptr, stream);
+  float* part_acc = prefill_part_acc(p, n_blocks);
+  e = launch_prefill_mod_kernel<D, true, KIND>(p, k_map, v_map, q_map, ctas, counter, order, parts,
+                                               part_acc, p.ws_ml, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_part_combine_kernel<D>, dim3((p.hq + 3) / 4, p.rows), dim3(128), 0,
+                    stream, p, parts, static_cast<const float*>(part_acc),
+                    static_cast<const float*>(p.ws_ml));
+}
+
+}  // namespace pgd

@@ -108,7 +108,7 @@ struct UmmaPrefillCfg {
   static_assert(kSCol + kTiles * kSBufs * kPage <= kTmemCols, "TMEM columns");
   static_assert(RK == RV, "the K and V rings are streamed by one helper");
   static_assert(kSBufs <= RV, "a V slot is freed when S of the page kSBufs later is issued");
-  static_assert(kSmemBytes + 24 * 1024 <= 227 * 1024, "shared memory (dynamic + static)");
+  static_assert(kSmemBytes + 20 * 1024 <= 227 * 1024, "shared memory (dynamic + static)");
 };
 
 // Slack of the lazy running max, in log2 units: P values stay below 2^8.
@@ -162,25 +162,6 @@ struct PrefillItem {
   int run_pg[256], run_last[256];
 };
 
-// With ModScore, also each token's first key and last visible position.
-struct ModItem : PrefillItem {
-  int tok_first[256], tok_hi[256];
-};
-
-template <class Score>
-using ItemOf = typename std::conditional<Score::kMod, ModItem, PrefillItem>::type;
-
-// First and last position that token k of an item sees (run by run, both grow
-// with k).
-__device__ __forceinline__ int item_lo(const PrefillItem& it, int k, int window) {
-  return window > 0 ? max(it.tok_pos[k] - window + 1, 0) : 0;
-}
-__device__ __forceinline__ int item_hi(const PrefillItem& it, int k) { return it.tok_pos[k]; }
-__device__ __forceinline__ int item_lo(const ModItem& it, int k, int window) {
-  return max(window > 0 ? it.tok_pos[k] - window + 1 : 0, it.tok_first[k]);
-}
-__device__ __forceinline__ int item_hi(const ModItem& it, int k) { return it.tok_hi[k]; }
-
 // Page sequence of one item: run by run (inactive and bad runs skipped),
 // pages first..last of each.
 struct ItemCursor {
@@ -201,8 +182,8 @@ __device__ __forceinline__ bool part_pages(const PrefillItem& it, int& first, in
 // kParts: the item is one key part of its pages (kernels built for key
 // parts: each run's range as the producer wrote it in the descriptor);
 // otherwise every page of every run.
-template <bool kParts = false, class Item = PrefillItem>
-__device__ __forceinline__ bool item_next_run(const Item& it, int window, ItemCursor& c) {
+template <bool kParts = false>
+__device__ __forceinline__ bool item_next_run(const PrefillItem& it, int window, ItemCursor& c) {
   for (++c.r; c.r < it.runs; ++c.r) {
     c.rs = c.r == 0 ? 0 : it.run_end[c.r - 1];
     c.re = it.run_end[c.r];
@@ -213,8 +194,9 @@ __device__ __forceinline__ bool item_next_run(const Item& it, int window, ItemCu
       c.last = it.run_last[c.r];
       if (c.pg > c.last) continue;  // no page of this run in the part
     } else {
-      c.pg = item_lo(it, c.rs, window) / kPage;
-      c.last = item_hi(it, c.re - 1) / kPage;
+      const int lo = window > 0 ? max(it.tok_pos[c.rs] - window + 1, 0) : 0;
+      c.pg = lo / kPage;
+      c.last = it.tok_pos[c.re - 1] / kPage;
     }
     return true;
   }
@@ -222,61 +204,24 @@ __device__ __forceinline__ bool item_next_run(const Item& it, int window, ItemCu
 }
 
 // Next page of the item; false at its end.
-template <bool kParts = false, class Item = PrefillItem>
-__device__ __forceinline__ bool item_advance(const Item& it, int window, ItemCursor& c) {
+template <bool kParts = false>
+__device__ __forceinline__ bool item_advance(const PrefillItem& it, int window, ItemCursor& c) {
   if (++c.pg <= c.last) return true;
   return item_next_run<kParts>(it, window, c);
-}
-
-// Raw products of one row with kHalf keys to capped and biased scores in log2
-// units: `rel` is the first key's position less the query's.  Pairs go
-// through the packed fp32 pipe, so a capped score costs about five issue slots
-// and a biased one two.
-template <int N>
-__device__ __forceinline__ void mod_scores(float (&sv)[N], const ModParams& p, float c,
-                                           float nslope, int rel) {
-  if (p.cap_in != 0.f) {
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < N; k += 2) top = fmax3(top, fabsf(sv[k]), fabsf(sv[k + 1]));
-    if (__all_sync(0xffffffffu, top * fabsf(p.cap_in) <= 1.f)) {
-#pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        const float2 v = cap_near2(make_float2(sv[k], sv[k + 1]), p.cap_in, c);
-        sv[k] = v.x;
-        sv[k + 1] = v.y;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k) sv[k] = cap_far(sv[k], p.cap_in, p.cap_out);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) sv[k] *= c;
-  }
-  if (p.slopes) {
-    const float r = (float)rel;
-#pragma unroll
-    for (int k = 0; k < N; ++k) sv[k] = fmaf(nslope, fabsf(r + (float)k), sv[k]);
-  }
 }
 
 // kParts: built for key parts (`parts` units per item, partials to
 // part_acc / part_ml for the combine launch); otherwise parts is 1 and each
 // item's outputs are written directly.  Two builds, so that the direct one
-// carries none of the key-part code.  Score: how scores differ from scale *
-// q . k (paged_score.cuh); with ModScore the tokens of a run also share their
-// first key, and a run's pages are the union of its tokens' visible ranges.
-template <int D, int RK, int RV, bool kParts, class Score = PlainScore>
+// carries none of the key-part code.
+template <int D, int RK, int RV, bool kParts>
 __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
     paged_prefill_umma_kernel(const __grid_constant__ CUtensorMap k_map,
                               const __grid_constant__ CUtensorMap v_map,
-                              const __grid_constant__ CUtensorMap q_map,
-                              const typename Score::Params p, int* item_counter, const int* block_order, int parts,
+                              const __grid_constant__ CUtensorMap q_map, const DecodeParams p,
+                              int* item_counter, const int* block_order, int parts,
                               float* part_acc, float* part_ml) {
   using C = UmmaPrefillCfg<D, RK, RV>;
-  using Item = ItemOf<Score>;
-  constexpr bool kMod = Score::kMod;
   const int G = p.group;
   const int T = C::kRows / G;  // tokens per tile
   const int tokens = C::kTiles * T;
@@ -306,7 +251,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
   uint64_t* fin = item_free + 2;              // [issuer] every MMA it issued done
   uint64_t* q_full = fin + 2;                 // the item's Q rows landed (TMA)
   uint64_t* q_free = q_full + 1;              // the item's S products done: Q may be replaced
-  __shared__ Item items[2];
+  __shared__ PrefillItem items[2];
   __shared__ int y_ring[2][64];  // [K, V producer] tile rows of upcoming pages, by page % 64
   // [tile][slot][half][row]: the values the tile's two warpgroups exchange
   // (row maximum of a page, row sum of a run) at the tile's named barrier
@@ -380,7 +325,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
   // lane) into `ring` (by page number % 64); lane 0 waits for each slot and
   // issues its copy, and with `prefetch` pulls K and V pages into L2 ahead (the
   // token blocks of a request reach each page together).
-  auto stream_item = [&](const Item& it, int kvh, const CUtensorMap* map,
+  auto stream_item = [&](const PrefillItem& it, int kvh, const CUtensorMap* map,
                          unsigned char* slots, uint64_t* full, uint64_t* empty, int* ring, int& i,
                          bool prefetch) -> bool {
     int n_pages = 0;
@@ -439,7 +384,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int d = seq & 1;
-      Item& it = items[d];
+      PrefillItem& it = items[d];
       int j = 0;
       if (lane == 0) j = atomicAdd(item_counter, 1);
       j = __shfl_sync(0xffffffffu, j, 0);
@@ -467,16 +412,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
         if (t < t_end) {
           row = p.row_of ? p.row_of[t] : t;
           pos = p.positions[t];
-          bool bad = row < 0 || row >= p.table_rows || (pos >= 0 && pos / kPage >= p.maxp);
-          if constexpr (kMod) {
-            if (!bad && pos >= 0) {
-              const TokenSpan span = mod_span(p, t, row, pos);
-              bad = span.hi / kPage >= p.maxp;
-              if (!bad && span.lo > span.hi) row = -1;  // sees no key: zeros
-              it.tok_hi[k] = span.hi;
-              it.tok_first[k] = p.first_key ? max(p.first_key[t], 0) : 0;
-            }
-          }
+          const bool bad = row < 0 || row >= p.table_rows || (pos >= 0 && pos / kPage >= p.maxp);
           if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
           if (bad || pos < 0) row = -1;
         }
@@ -494,8 +430,6 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
             brk = k + 1 == tokens || it.tok_row[k + 1] != it.tok_row[k] ||
                   it.tok_pos[k + 1] != it.tok_pos[k] + 1 || it.tok_row[k + 1] < 0 ||
                   it.tok_row[k] < 0;
-          if constexpr (kMod)
-            if (!brk && k < tokens) brk = it.tok_first[k + 1] != it.tok_first[k];
           const unsigned bal = __ballot_sync(0xffffffffu, brk);
           if (brk) it.run_end[r + __popc(bal & ((1u << lane) - 1u))] = k + 1;
           r += __popc(bal);
@@ -518,8 +452,8 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
         const int row = it.tok_row[rs];
         int bad = 0;
         if (row >= 0) {
-          const int first = item_lo(it, rs, p.window) / kPage;
-          const int last = item_hi(it, re - 1) / kPage;
+          const int lo = p.window > 0 ? max(it.tok_pos[rs] - p.window + 1, 0) : 0;
+          const int first = lo / kPage, last = it.tok_pos[re - 1] / kPage;
           for (int pg = first + lane; pg <= last; pg += 32) {
             const int page = page_of(p.table, row, pg, p.maxp);
             if (page < 0 || page >= p.num_pages) bad = 1;
@@ -535,12 +469,8 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
         // each run's pages in this unit's key part, for every role's walk
         for (int r = lane; r < it.runs; r += 32) {
           const int rs = r == 0 ? 0 : it.run_end[r - 1], re = it.run_end[r];
-          // (a run of no row is skipped by every role: its range is of no use)
-          int first = 0, last = 0;
-          if (it.tok_row[rs] >= 0) {
-            first = item_lo(it, rs, p.window) / kPage;
-            last = item_hi(it, re - 1) / kPage;
-          }
+          const int lo = p.window > 0 ? max(it.tok_pos[rs] - p.window + 1, 0) : 0;
+          int first = lo / kPage, last = max(it.tok_pos[re - 1], 0) / kPage;
           part_pages(it, first, last);
           it.run_pg[r] = first;
           it.run_last[r] = last;
@@ -573,7 +503,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
     for (int seq = 0;; ++seq) {
       const int d = seq & 1;
       if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) break;
-      const Item& it = items[d];
+      const PrefillItem& it = items[d];
       if (!it.valid) break;
       if (!stream_item(it, it.kvh, &v_map, v_slots, v_full, v_empty, y_ring[1], iv, false)) break;
       if (lane == 0) mbar_arrive(&item_free[d]);
@@ -592,7 +522,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
       for (int seq = 0; ok; ++seq) {
         const int d = seq & 1;
         if (!wait(&item_ready[d], (seq >> 1) & 1)) break;
-        const Item& it = items[d];
+        const PrefillItem& it = items[d];
         if (!it.valid) break;
         {
           // the item's Q rows by TMA ([token][head] rows of 64 values: the
@@ -665,7 +595,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
       for (int seq = 0; ok; ++seq) {
         const int d = seq & 1;
         if (!wait(&item_ready[d], (seq >> 1) & 1)) break;
-        const Item& it = items[d];
+        const PrefillItem& it = items[d];
         if (!it.valid) break;
         ItemCursor cur{-1, 0, -1, -1, 0, 0};
         bool first = true;  // O restarts with each item
@@ -721,9 +651,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
     int xn = 0;  // exchanges with the other half so far
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = p.q_scale_log2;
-    bool modded = false;  // scores are capped or biased, in log2 units before the softmax
-    if constexpr (kMod) modded = p.cap_in != 0.f || p.slopes != nullptr;
-    const float cc = c > 0.f && !modded ? c : 1.f;
+    const float cc = c > 0.f ? c : 1.f;
     int i = 0;  // page index over all items
     // The tile's two warpgroups exchange values at a named barrier (id 1 +
     // t) that also ORs a failure flag over them, so they leave their loops
@@ -747,7 +675,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
     ok = !named_sync_or(xid, xcount, !mine);
     for (int seq = 0; ok && have; ++seq) {
       const int d = seq & 1;
-      const Item& it = items[d];
+      const PrefillItem& it = items[d];
       const int t_begin = it.t_begin, t_end = it.t_end, h0 = it.kvh * G;
       const bool row_ok = in_tile && t_begin + tl < t_end;
       int rs = 0;
@@ -775,20 +703,10 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
           continue;
         }
         const bool live = row_ok && tl >= rs && tl < re;
-        float nslope = 0.f;  // bias per position of distance, log2 units
-        if constexpr (kMod)
-          if (p.slopes && live) nslope = -p.slopes[h0 + g] * kLog2e;
         const int pos = live ? it.tok_pos[tl] : -1;
-        // keys lo .. hi of this row's token, the union of the run's
-        int lo = p.window > 0 ? pos - p.window + 1 : 0, hi = pos;
-        if constexpr (kMod) {
-          if (live) {
-            lo = item_lo(it, tl, p.window);
-            hi = it.tok_hi[tl];
-          }
-        }
-        const int lo_run = item_lo(it, rs, p.window);
-        const int pos_last = item_hi(it, re - 1);
+        const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+        const int lo_run = p.window > 0 ? max(it.tok_pos[rs] - p.window + 1, 0) : 0;
+        const int pos_last = it.tok_pos[re - 1];
         int first = lo_run / kPage, last = pos_last / kPage;
         if constexpr (kParts) {
           // a key part without pages of this run: the rows' partials are
@@ -820,29 +738,16 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
           tmem_wait_ld();
           // scores stay raw: the scale is folded into the exponent's FMA (for
           // a positive scale; otherwise it is applied here)
-          const int pos0 = pg * kPage;
-          const int pos0h = pos0 + kHalf * h;  // this half's first key
-          const bool all_seen = live && pos0h >= lo && pos0h + kHalf - 1 <= hi;
-          if constexpr (kMod) {
-            if (modded) {
-              if (!all_seen) {  // masked places have no say in how the others are capped
-#pragma unroll
-                for (int k = 0; k < kHalf; ++k)
-                  if (!(live && pos0h + k >= lo && pos0h + k <= hi)) sv[k] = 0.f;
-              }
-              mod_scores(sv, p, c, nslope, pos0h - pos);
-            } else if (!(c > 0.f)) {
-#pragma unroll
-              for (int k = 0; k < kHalf; ++k) sv[k] *= c;
-            }
-          } else if (!(c > 0.f)) {
+          if (!(c > 0.f)) {
 #pragma unroll
             for (int k = 0; k < kHalf; ++k) sv[k] *= c;
           }
-          if (!all_seen) {
+          const int pos0 = pg * kPage;
+          const int pos0h = pos0 + kHalf * h;  // this half's first key
+          if (!(live && pos0h >= lo && pos0h + kHalf - 1 <= pos)) {
 #pragma unroll
             for (int k = 0; k < kHalf; ++k)
-              if (!(live && pos0h + k >= lo && pos0h + k <= hi)) sv[k] = -INFINITY;
+              if (!(live && pos0h + k >= lo && pos0h + k <= pos)) sv[k] = -INFINITY;
           }
           // eight partial maxima: the first 8 scores, then 24 more two at a
           // time (a block of 16 and a last block of 8)
@@ -1291,7 +1196,7 @@ inline float* prefill_part_acc(const DecodeParams& p, int n_blocks) {
 // written the block order (prefill_write_kernel).  `parts` > 1: each item's
 // pages are cut into that many key parts, one work unit each, and a combine
 // launch merges their partials.
-template <int D, int RK, int RV, bool kParts, class Score>
+template <int D, int RK, int RV, bool kParts>
 cudaError_t configure_prefill_umma() {
   using C = UmmaPrefillCfg<D, RK, RV>;
   static std::atomic<bool> configured[64];
@@ -1299,7 +1204,7 @@ cudaError_t configure_prefill_umma() {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(paged_prefill_umma_kernel<D, RK, RV, kParts, Score>,
+    e = cudaFuncSetAttribute(paged_prefill_umma_kernel<D, RK, RV, kParts>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
@@ -1307,8 +1212,8 @@ cudaError_t configure_prefill_umma() {
   return cudaSuccess;
 }
 
-template <int D, int RK, int RV, class Score = PlainScore>
-cudaError_t launch_prefill_umma(const typename Score::Params& p, const CUtensorMap& k_map,
+template <int D, int RK, int RV>
+cudaError_t launch_prefill_umma(const DecodeParams& p, const CUtensorMap& k_map,
                                 const CUtensorMap& v_map, const CUtensorMap& q_map, int sm_count,
                                 bool prepared, int parts, cudaStream_t stream) {
   using C = UmmaPrefillCfg<D, RK, RV>;
@@ -1316,8 +1221,8 @@ cudaError_t launch_prefill_umma(const typename Score::Params& p, const CUtensorM
   // per token
   if (parts < 1 || (parts > 1 && (parts > p.max_splits - 1 || p.rows > 65535)))
     return cudaErrorInvalidValue;
-  cudaError_t e = parts > 1 ? configure_prefill_umma<D, RK, RV, true, Score>()
-                            : configure_prefill_umma<D, RK, RV, false, Score>();
+  cudaError_t e = parts > 1 ? configure_prefill_umma<D, RK, RV, true>()
+                            : configure_prefill_umma<D, RK, RV, false>();
   if (e != cudaSuccess) return e;
   if (p.rows == 0) return cudaSuccess;
   const int tokens = C::kTiles * (C::kRows / p.group);
@@ -1331,8 +1236,8 @@ cudaError_t launch_prefill_umma(const typename Score::Params& p, const CUtensorM
   if (prepared)
     e = cudaSuccess;
   else if (order)
-    e = launch_pdl(prefill_block_order_kernel<D, Score>, dim3(1),
-                   dim3(block_order_threads(n_blocks)), 0, stream, p, tokens, n_blocks, counter, order);
+    e = launch_pdl(prefill_block_order_kernel<D>, dim3(1), dim3(block_order_threads(n_blocks)), 0,
+                   stream, p, tokens, n_blocks, counter, order);
   else
     e = cudaMemsetAsync(counter, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
@@ -1341,11 +1246,11 @@ cudaError_t launch_prefill_umma(const typename Score::Params& p, const CUtensorM
   const int units = items * parts;
   const int ctas = units < sm_count ? units : sm_count;
   if (parts == 1)
-    return launch_pdl(paged_prefill_umma_kernel<D, RK, RV, false, Score>, dim3(ctas),
-                      dim3(C::kThreads), C::kSmemBytes, stream, k_map, v_map, q_map, p, counter,
+    return launch_pdl(paged_prefill_umma_kernel<D, RK, RV, false>, dim3(ctas), dim3(C::kThreads),
+                      C::kSmemBytes, stream, k_map, v_map, q_map, p, counter,
                       static_cast<const int*>(order), 1, part_acc, part_ml);
-  e = launch_pdl(paged_prefill_umma_kernel<D, RK, RV, true, Score>, dim3(ctas),
-                 dim3(C::kThreads), C::kSmemBytes, stream, k_map, v_map, q_map, p, counter,
+  e = launch_pdl(paged_prefill_umma_kernel<D, RK, RV, true>, dim3(ctas), dim3(C::kThreads),
+                 C::kSmemBytes, stream, k_map, v_map, q_map, p, counter,
                  static_cast<const int*>(order), parts, part_acc, part_ml);
   if (e != cudaSuccess) return e;
   return launch_pdl(prefill_part_combine_kernel<D>, dim3((p.hq + 3) / 4, p.rows), dim3(128), 0,

@@ -44,37 +44,31 @@ __device__ __forceinline__ TokenSpan mod_span(const ModParams& p, int b, int row
   return s;
 }
 
-// cap * tanh(x / cap) in log2 units for a raw score s = q . k, with a = scale /
-// cap and c = scale log2 e (so cap log2 e = c / a).
-//   |a s| <= 1: c s P(u), u = (a s)^2, P(u) = tanh(x) / x as a polynomial of
-//   degree 5 in u, fitted here by a minimax exchange on [0, 1]: within 6e-7 of
-//   it, so a score capped at 50 is off by less than 3e-5.  No special function.
-//   beyond: cap (1 - 2 / (1 + 2^(2 a s log2 e))), two special functions,
-//   within 2^-22 of the cap at any argument (also an infinite one).
-// A warp takes the first form when all of its scores allow it: nearly always,
-// scores of trained models staying well inside their cap.
-constexpr float kTanh0 = 0.9999994039535522f, kTanh1 = -0.3332904279232025f,
-                kTanh2 = 0.13281433284282684f, kTanh3 = -0.051605675369501114f,
-                kTanh4 = 0.016743114218115807f, kTanh5 = -0.003067060373723507f;
+// cap * tanh(x / cap) in log2 units for a raw score s = q . k, with t = a s, a =
+// scale / cap, and the cap in log2 units.
+//   |t| <= 1: cap t P(t^2), P(u) = tanh(x) / x at x^2 = u as a polynomial of
+//   degree 5 in u, fitted here by a minimax exchange on [0, 1]: within 6.2e-7
+//   of it, so a score capped at 50 is off by less than 3e-5.
+//   |t| <= 0.3: the same with degree 2, fitted on [0, 0.09], within 1.2e-6.
+//   beyond: cap (1 - 2 / (1 + 2^(2 t log2 e))), two special functions, within
+//   2^-21 of the cap at any argument (also an infinite one).
+// A warp takes the shortest form that all of its scores allow: nearly always
+// the first or second, scores of trained models staying well inside their cap.
+constexpr float kTanhMid = 1.f, kTanhNear = 0.3f;
+constexpr float kMid0 = 0.9999994039535522f, kMid1 = -0.3332904279232025f,
+                kMid2 = 0.13281433284282684f, kMid3 = -0.051605675369501114f,
+                kMid4 = 0.016743114218115807f, kMid5 = -0.003067060373723507f;
+constexpr float kNear0 = 0.9999988675117493f, kNear1 = -0.33310022950172424f,
+                kNear2 = 0.12633946537971497f;
 
-__device__ __forceinline__ float cap_near(float s, float a, float c) {
+__device__ __forceinline__ float cap_mid(float s, float a, float cap_log2) {
   const float t = a * s, u = t * t;
-  float q = fmaf(kTanh5, u, kTanh4);
-  q = fmaf(q, u, kTanh3);
-  q = fmaf(q, u, kTanh2);
-  q = fmaf(q, u, kTanh1);
-  q = fmaf(q, u, kTanh0);
-  return (c * s) * q;
-}
-
-__device__ __forceinline__ float2 cap_near2(float2 s, float a, float c) {
-  const float2 t = __fmul2_rn(make_float2(a, a), s), u = __fmul2_rn(t, t);
-  float2 q = __ffma2_rn(make_float2(kTanh5, kTanh5), u, make_float2(kTanh4, kTanh4));
-  q = __ffma2_rn(q, u, make_float2(kTanh3, kTanh3));
-  q = __ffma2_rn(q, u, make_float2(kTanh2, kTanh2));
-  q = __ffma2_rn(q, u, make_float2(kTanh1, kTanh1));
-  q = __ffma2_rn(q, u, make_float2(kTanh0, kTanh0));
-  return __fmul2_rn(__fmul2_rn(make_float2(c, c), s), q);
+  float q = fmaf(kMid5, u, kMid4);
+  q = fmaf(q, u, kMid3);
+  q = fmaf(q, u, kMid2);
+  q = fmaf(q, u, kMid1);
+  q = fmaf(q, u, kMid0);
+  return (cap_log2 * t) * q;
 }
 
 __device__ __forceinline__ float cap_far(float s, float a, float cap_log2) {

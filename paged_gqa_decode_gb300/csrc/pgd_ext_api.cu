@@ -251,6 +251,7 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   if (kernel == PGD_KERNEL_PREFILL_PAIR) kernel = PGD_KERNEL_PREFILL_UMMA;  // AUTO's only
   const bool tcgen05 = kernel == PGD_KERNEL_PREFILL_UMMA;
   CUtensorMap k_map, v_map, q_map;
+  // the prefill copies a head_dim-128 page tile with one 3-D box
   const int kind = tcgen05 ? kMapWholeTile : kMapBoxes;
   if ((rc = encode_pool_map(&k_map, k_pool, dims, kind)) != PGD_OK) return rc;
   if ((rc = encode_pool_map(&v_map, v_pool, dims, kind)) != PGD_OK) return rc;
@@ -265,10 +266,8 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   }
   cudaError_t e;
   if (tcgen05) {
-    e = dims->head_dim == 64 ? launch_mod_prefill_d64(p, k_map, v_map, q_map, dev->sm_count,
-                                                      prefill_write, parts, st)
-                             : launch_mod_prefill_d128(p, k_map, v_map, q_map, dev->sm_count,
-                                                       prefill_write, parts, st);
+    e = launch_mod_prefill(p, k_map, v_map, q_map, dims->head_dim, dev->sm_count, prefill_write,
+                           parts, st);
   } else {
     const int pages = span_pages(dims, bound);
     const int splits = (pages + pl.pages_per_split - 1) / pl.pages_per_split;

@@ -52,12 +52,9 @@ cudaError_t launch_mod_decode_d64(const ModParams& p, const CUtensorMap& k_map,
 cudaError_t launch_mod_decode_d128(const ModParams& p, const CUtensorMap& k_map,
                                    const CUtensorMap& v_map, int grid_splits, int pages_per_cta,
                                    cudaStream_t stream);
-cudaError_t launch_mod_prefill_d64(const ModParams& p, const CUtensorMap& k_map,
-                                   const CUtensorMap& v_map, const CUtensorMap& q_map,
-                                   int sm_count, bool prepared, int parts, cudaStream_t stream);
-cudaError_t launch_mod_prefill_d128(const ModParams& p, const CUtensorMap& k_map,
-                                    const CUtensorMap& v_map, const CUtensorMap& q_map,
-                                    int sm_count, bool prepared, int parts, cudaStream_t stream);
+cudaError_t launch_mod_prefill(const ModParams& p, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, const CUtensorMap& q_map, int head_dim,
+                               int sm_count, bool prepared, int parts, cudaStream_t stream);
 cudaError_t launch_mod_prefill_write(const ModParams& p, int head_dim, bool umma,
                                      cudaStream_t stream);
 

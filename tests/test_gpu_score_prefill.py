@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import paged_gqa_decode_gb300 as pgd
-from tests.score_side import DEV, Paged, check, i32
+from tests.score_side import DEV, Paged, i32
+from tests.score_side import check as check_score
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,10 @@ def _built():
     __graft_entry__.build()
     yield
     torch.cuda.synchronize()
+
+
+def check(*args, kernel=pgd.KERNEL_PREFILL_UMMA, **kw):
+    check_score(*args, rounded=kernel != pgd.KERNEL_TENSOR_CORE, **kw)
 
 
 def packed(cached, chunks):
@@ -63,7 +68,7 @@ def test_prefill(hq, hkv, d, kw, kernel):
     pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions), sinks,
                                 window, num_kv_heads=hkv, kernel=kernel, out=out, **a)
     assert pgd.get_device_error() == pgd.OK
-    check(out, b, q, rows, positions, scale=d ** -0.5, **c)
+    check(out, b, q, rows, positions, kernel=kernel, scale=d ** -0.5, **c)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(8, 1, 64), (4, 1, 128)])
@@ -108,7 +113,7 @@ def test_step(layout, kernel):
     assert pgd.get_device_error() == pgd.OK
     same = lambda x, y: torch.equal(x.view(torch.int16), y.view(torch.int16))  # noqa: E731
     assert same(b.k_pool, k2) and same(b.v_pool, v2) and same(out, two)
-    check(out, b, q, rows, positions, scale=0.125, **c)
+    check(out, b, q, rows, positions, kernel=kernel, scale=0.125, **c)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -125,7 +130,8 @@ def test_odd_token_orders(kernel):
     out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
                                       num_kv_heads=2, kernel=kernel, **a)
     assert pgd.get_device_error() == pgd.OK
-    check(out, b, q, rows, positions, scale=0.125, softcap=10.0, first=first, prefix=[-4, 60])
+    check(out, b, q, rows, positions, kernel=kernel, scale=0.125, softcap=10.0, first=first,
+          prefix=[-4, 60])
     empty = (positions >= 0) & (first > np.maximum(positions, np.array([-4, 60])[rows] - 1))
     assert empty.any() and not out[torch.from_numpy(empty)].any()
 
@@ -142,7 +148,7 @@ def test_masks_that_leave_nothing(kernel, sinks):
                                       first_key=i32(np.where(positions < 280, 2 ** 31 - 1, 290)))
     assert pgd.get_device_error() == pgd.OK
     first = np.where(positions < 280, 2 ** 31 - 1, 290)
-    check(out, b, q, rows, positions, scale=0.125, softcap=3.0, sinks=s, first=first)
+    check(out, b, q, rows, positions, kernel=kernel, scale=0.125, softcap=3.0, sinks=s, first=first)
     assert not out[:190].any() and out[190:].any()
 
 
@@ -164,7 +170,7 @@ def test_values_in_masked_places(kernel):
                 for n in list(range(lo)) + list(range(hi + 1, 512)):
                     pool[b.table_np[r, n // 64], :, n % 64] = bad
         assert torch.equal(call(), want)
-    check(want, b, q, rows, positions, scale=128 ** -0.5, softcap=6.0, first=first,
+    check(want, b, q, rows, positions, kernel=kernel, scale=128 ** -0.5, softcap=6.0, first=first,
           prefix=[333, 0])
 
 
@@ -179,7 +185,7 @@ def test_scores_far_past_the_cap(kernel, softcap, gain, scale):
     out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
                                       None, 0, scale, num_kv_heads=2, softcap=softcap,
                                       kernel=kernel)
-    check(out, b, q, rows, positions, scale=scale, softcap=softcap)
+    check(out, b, q, rows, positions, kernel=kernel, scale=scale, softcap=softcap)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -198,8 +204,8 @@ def test_bad_entries(kernel):
                                       prefix_len=i32(prefix), kernel=kernel)
     assert pgd.get_device_error() == pgd.EDEVICE_BOUNDS
     good = np.r_[0:35, 40:80]
-    check(out[good], b, q[good], rows[good], positions[good], scale=0.125, softcap=8.0,
-          first=first[good], prefix=prefix)
+    check(out[good], b, q[good], rows[good], positions[good], kernel=kernel, scale=0.125,
+          softcap=8.0, first=first[good], prefix=prefix)
     assert not out[35:40].any() and not out[80:].any()
 
 
@@ -250,11 +256,11 @@ def test_random(seed):
         kw["softcap"] = 4.0
     a, sinks, window, c = mods(kw, b, rows, positions, seed)
     q = b.queries(len(rows))
+    kernel = int(rng.choice(KERNELS))
     out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
-                                      sinks, window, num_kv_heads=hkv,
-                                      kernel=int(rng.choice(KERNELS)), **a)
+                                      sinks, window, num_kv_heads=hkv, kernel=kernel, **a)
     assert pgd.get_device_error() == pgd.OK
-    check(out, b, q, rows, positions, scale=d ** -0.5, **c)
+    check(out, b, q, rows, positions, kernel=kernel, scale=d ** -0.5, **c)
 
 
 def test_refusals():
