@@ -13,20 +13,20 @@
 // tokens of a run share table row and first key and have consecutive
 // positions, and a run is one pass over the pages that its tokens see.
 //
-// What bounds it is the softmax: 64 exponentials a row and page are 256 cycles
-// of a sub-partition's special function unit for each of its four softmax
-// warps, and every trip to TMEM or through a barrier costs hundreds of cycles
-// that only other warps can fill.  So
-//   - the two warpgroups of a tile take its pages in turn, each with S columns
-//     of its own, a whole row of 64 scores to a thread: four independent
-//     warps a sub-partition, in different phases of their pages.  (Warpgroups
-//     that share a page and exchange its maxima at a barrier move in lockstep
-//     and queue at one pipe after the other: 128-key steps in that form
-//     measured 1.5 times slower, with one thread to 128 keys 1.7 times.)
-//   - all that a page needs from the one before is the row's reference m, handed
-//     from warp to warp through shared memory; it rises only when a score
-//     exceeds it by more than 2^8;
-//   - S is read from TMEM once;
+// What bounds it is the softmax: a page's 64 scores a row are 64 exponentials,
+// 256 cycles of a sub-partition's special function unit for each warp, and
+// every trip to TMEM or through a barrier costs hundreds of cycles.  So
+//   - one warpgroup has a tile to itself, a thread to a row and page: no
+//     exchange between threads, and registers for 64 scores and their
+//     polynomials at once (208 a thread).  Two warpgroups to a tile, sharing
+//     each page or taking pages in turn, have 104 and measured 1.3 to 2 times
+//     slower, though twice the warps: what they gain in warps they lose in
+//     registers moved, barriers and instructions fetched;
+//   - each tile has two S buffers: S of the next page is computed under the
+//     softmax of this one;
+//   - S is read from TMEM once, but on pages out of the usual (keys past the
+//     query with a bias, scores near their cap), which go 16 keys at a time in
+//     rolled loops;
 //   - a capped score is a polynomial in s^2 times s plus what the exponent needs
 //     anyway: y = s Q(s^2) + (bias - m), four packed instructions for two keys;
 //   - P is rounded to bf16 once, without a residual product: an output is off
@@ -35,20 +35,18 @@
 //   - a tile without rows of a run (a block that reaches into another row or
 //     document) takes no part in it.
 //
-// Warps (640 threads):
-//   0-15  softmax: tile t has two warpgroups (warps 4t .. and 8 + 4t ..), one
-//         thread per query row in each; warpgroup h takes the tile's pages
-//         i = h mod 2 (and half of the O columns for the store), and zeroes a
-//         boundary page's V rows outside the run's range (the first tile that
-//         takes part).
-//   16    producer: takes items from the counter, lays out their runs (checks
+// Warps (384 threads):
+//   0-7   softmax: tile t is warps 4t .. 4t + 3, a thread per query row; it
+//         zeroes a boundary page's V rows outside the run's range too (the
+//         first tile that takes part).
+//   8     producer: takes items from the counter, lays out their runs (checks
 //         the table, zeroes uncovered outputs), copies Q and streams K pages.
-//   17    S issuer and TMEM owner, 18 P V issuer (one thread each), 19 V pages.
+//   9     S issuer and TMEM owner, 10 P V issuer (one thread each), 11 V pages.
 // Shared memory: K and V rings of page tiles (four each at head_dim 128, eight
 // at 64), Q (two buffers at 64, so that the next item's is there early); 192 KB
-// of both.  TMEM: O_t at t D, then S of (tile, h), 64 columns each; P, 32 columns
-// of bf16 pairs, at head_dim 64 after them (S of the page after next is computed
-// as soon as S is read), at 128 over S (it then waits for P V).
+// of both.  TMEM: O_t at t D, then S of (tile, page mod 2), 64 columns each; P, 32
+// columns of bf16 pairs, at head_dim 64 after them (S of the page after next is
+// computed as soon as S is read), at 128 over S (it then waits for P V).
 // Key parts as in the one-SM kernel.
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
 // roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.
@@ -62,9 +60,9 @@ namespace pgd {
 template <int D>
 struct ModPrefillCfg {
   static constexpr int kRows = 128, kTiles = 2;
-  static constexpr int kSoftmaxWarps = 16;
-  static constexpr int kProducerWarp = 16, kMmaWarp = 17, kPvWarp = 18, kVWarp = 19;
-  static constexpr int kThreads = 640;
+  static constexpr int kSoftmaxWarps = 8;
+  static constexpr int kProducerWarp = 8, kMmaWarp = 9, kPvWarp = 10, kVWarp = 11;
+  static constexpr int kThreads = 384;
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kPage * D * 2;
   static constexpr int kRing = D == 128 ? 4 : 8;
@@ -75,12 +73,12 @@ struct ModPrefillCfg {
   static constexpr int kVOff = kRing * kTileBytes;
   static constexpr int kQOff = 2 * kRing * kTileBytes;
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kNumBars = 4 * kRing + 8 * kTiles + 16 + 4 + 2 * kQBufs + 2;
+  static constexpr int kNumBars = 4 * kRing + 8 * kTiles + 4 + 2 * kQBufs + 2;
   static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr bool kOwnP = D == 64;  // P beside S (else over it)
   static constexpr uint32_t kOCol = 0, kSCol = kTiles * D;
-  // S of (tile t, parity h): kSCol + (2 t + h) kPage; P: kPCol + (2 t + h) kPStride
+  // S of (tile t, page i): kSCol + (2 t + i % 2) kPage; P: kPCol + the same kPStride
   static constexpr uint32_t kPCol = kOwnP ? kSCol + 2 * kTiles * kPage : kSCol;
   static constexpr uint32_t kPStride = kOwnP ? kPage / 2 : kPage;
   static constexpr uint32_t kIdescS = umma_idesc_bf16(128, kPage, 0, 0);
@@ -119,53 +117,49 @@ enum ModKind { kModMask = 0, kModCap = 1, kModBias = 2 };
 //   Q: c = scale log2 e without a cap, else the cap's polynomial with the
 //      powers of a = scale / cap and the cap folded into its coefficients
 //      (near, mid), or cap_far in its place.
-//   A: the bias less m, linear in k where every key is at or before the query.
+//   A: the bias less m, linear in k where every key is at or before the query;
+//      nslope is the bias per position of distance (log2 units, <= 0 usually).
 // On the packed fp32 pipe, two keys at a time, but cap_far and the bias of
 // keys past the query.
-struct ModRow {
-  float c, nslope;  // scale log2 e; bias per position of distance (log2 units, <= 0 usually)
-  float near[3];    // coefficients of the near form
-  float a2;         // a^2, for the mid form
-  float cap_in, cap_out, limit_near, limit_mid;  // |s| up to which a form holds
-};
-
 enum CapForm { kNoCap, kCapNear, kCapMid, kCapFar };
 
-__device__ __forceinline__ float2 scaled2(float2 v, float2 add, const ModRow& r) {
-  return __ffma2_rn(v, make_float2(r.c, r.c), add);
+__device__ __forceinline__ float2 scaled2(float2 v, float2 add, const ModParams& p) {
+  return __ffma2_rn(v, make_float2(p.q_scale_log2, p.q_scale_log2), add);
 }
-__device__ __forceinline__ float2 near2(float2 v, float2 add, const ModRow& r) {
+__device__ __forceinline__ float2 near2(float2 v, float2 add, const ModParams& p) {
   const float2 u = __fmul2_rn(v, v);
-  float2 q = __ffma2_rn(make_float2(r.near[2], r.near[2]), u, make_float2(r.near[1], r.near[1]));
-  q = __ffma2_rn(q, u, make_float2(r.near[0], r.near[0]));
+  float2 q = __ffma2_rn(make_float2(p.near_q[2], p.near_q[2]), u,
+                        make_float2(p.near_q[1], p.near_q[1]));
+  q = __ffma2_rn(q, u, make_float2(p.near_q[0], p.near_q[0]));
   return __ffma2_rn(v, q, add);
 }
-__device__ __forceinline__ float2 mid2(float2 v, float2 add, const ModRow& r) {
-  const float2 u = __fmul2_rn(__fmul2_rn(v, v), make_float2(r.a2, r.a2));
+__device__ __forceinline__ float2 mid2(float2 v, float2 add, const ModParams& p) {
+  const float2 u = __fmul2_rn(__fmul2_rn(v, v), make_float2(p.a2, p.a2));
   float2 q = __ffma2_rn(make_float2(kMid5, kMid5), u, make_float2(kMid4, kMid4));
   q = __ffma2_rn(q, u, make_float2(kMid3, kMid3));
   q = __ffma2_rn(q, u, make_float2(kMid2, kMid2));
   q = __ffma2_rn(q, u, make_float2(kMid1, kMid1));
   q = __ffma2_rn(q, u, make_float2(kMid0, kMid0));
-  return __ffma2_rn(__fmul2_rn(v, make_float2(r.c, r.c)), q, add);
+  return __ffma2_rn(__fmul2_rn(v, make_float2(p.q_scale_log2, p.q_scale_log2)), q, add);
 }
 
-// A page's usual case: near form (or no cap), every key at or before the query
-// where there is a bias.
+// A page's usual case: near form (or no cap), every visible key at or before
+// the query where there is a bias.
 template <int KIND, int N>
-__device__ __forceinline__ void usual_scores(float (&s)[N], const ModRow& r, int rel, float m) {
-  const float b0 = KIND & kModBias ? fmaf(-r.nslope, (float)rel, -m) : -m;
+__device__ __forceinline__ void usual_scores(float (&s)[N], const ModParams& p, float nslope,
+                                             int rel, float m) {
+  const float b0 = KIND & kModBias ? fmaf(-nslope, (float)rel, -m) : -m;
 #pragma unroll
   for (int k = 0; k < N; k += 2) {
     float2 add = make_float2(b0, b0);
     if constexpr (KIND & kModBias)
-      add = __ffma2_rn(make_float2(-r.nslope, -r.nslope), make_float2((float)k, (float)(k + 1)),
+      add = __ffma2_rn(make_float2(-nslope, -nslope), make_float2((float)k, (float)(k + 1)),
                        add);
     float2 v = make_float2(s[k], s[k + 1]);
     if constexpr (KIND & kModCap)
-      v = near2(v, add, r);
+      v = near2(v, add, p);
     else
-      v = scaled2(v, add, r);
+      v = scaled2(v, add, p);
     s[k] = v.x;
     s[k + 1] = v.y;
   }
@@ -173,27 +167,27 @@ __device__ __forceinline__ void usual_scores(float (&s)[N], const ModRow& r, int
 
 // Any case, for few keys at a time.
 template <int KIND, int N>
-__device__ __forceinline__ void any_scores(float (&s)[N], const ModRow& r, int form, int rel,
-                                           float m) {
+__device__ __forceinline__ void any_scores(float (&s)[N], const ModParams& p, float nslope,
+                                           int form, int rel, float m) {
 #pragma unroll
   for (int k = 0; k < N; k += 2) {
     float2 add = make_float2(-m, -m);
     if constexpr (KIND & kModBias) {
-      add.x = fmaf(r.nslope, fabsf((float)(rel + k)), -m);
-      add.y = fmaf(r.nslope, fabsf((float)(rel + k + 1)), -m);
+      add.x = fmaf(nslope, fabsf((float)(rel + k)), -m);
+      add.y = fmaf(nslope, fabsf((float)(rel + k + 1)), -m);
     }
     float2 v = make_float2(s[k], s[k + 1]);
     if constexpr (KIND & kModCap) {
       if (form == kCapNear) {
-        v = near2(v, add, r);
+        v = near2(v, add, p);
       } else if (form == kCapMid) {
-        v = mid2(v, add, r);
+        v = mid2(v, add, p);
       } else {
-        v.x = cap_far(v.x, r.cap_in, r.cap_out) + add.x;
-        v.y = cap_far(v.y, r.cap_in, r.cap_out) + add.y;
+        v.x = cap_far(v.x, p.cap_in, p.cap_out) + add.x;
+        v.y = cap_far(v.y, p.cap_in, p.cap_out) + add.y;
       }
     } else {
-      v = scaled2(v, add, r);
+      v = scaled2(v, add, p);
     }
     s[k] = v.x;
     s[k + 1] = v.y;
@@ -202,9 +196,9 @@ __device__ __forceinline__ void any_scores(float (&s)[N], const ModRow& r, int f
 
 // The score, without a bias, of the raw product s.
 template <int KIND>
-__device__ __forceinline__ float one_score(float s, const ModRow& r, int form) {
-  if constexpr ((KIND & kModCap) == 0) return s * r.c;
-  return form == kCapFar ? cap_far(s, r.cap_in, r.cap_out) : cap_mid(s, r.cap_in, r.cap_out);
+__device__ __forceinline__ float one_score(float s, const ModParams& p, int form) {
+  if constexpr ((KIND & kModCap) == 0) return s * p.q_scale_log2;
+  return form == kCapFar ? cap_far(s, p.cap_in, p.cap_out) : cap_mid(s, p.cap_in, p.cap_out);
 }
 
 // The largest of N values (N a multiple of 16).
@@ -298,21 +292,17 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
   uint64_t* k_empty = k_full + R;          // S of the tiles taking part done
   uint64_t* v_full = k_empty + R;          // V page landed
   uint64_t* v_empty = v_full + R;          // their P V done
-  // [2 tile + parity of the tile's page]:
+  // [2 tile + (the tile's page) % 2]:
   uint64_t* s_full = v_empty + R;              // S of the page in TMEM
   uint64_t* s_free = s_full + 2 * C::kTiles;   // S in the warpgroup's registers
   uint64_t* p_full = s_free + 2 * C::kTiles;   // P in TMEM (O rescaled, V rows zeroed)
   uint64_t* o_done = p_full + 2 * C::kTiles;   // P V of the page done
-  uint64_t* m_set = o_done + 2 * C::kTiles;    // [softmax warp] its rows' reference written
-  uint64_t* item_ready = m_set + 16;           // [item % 2] descriptor written
+  uint64_t* item_ready = o_done + 2 * C::kTiles;  // [item % 2] descriptor written
   uint64_t* item_free = item_ready + 2;        // [item % 2] read for the last time
   uint64_t* q_full = item_free + 2;            // [item % QB] Q landed
   uint64_t* q_free = q_full + QB;              // [item % QB] the item's S products done
   uint64_t* fin = q_free + QB;                 // [issuer] every MMA it issued done
   __shared__ ModItem items[2];
-  __shared__ float m_ref[C::kTiles][C::kRows];  // the rows' references (log2 units)
-  // [tile][slot][warpgroup][row]: row sums and references at the end of a run
-  __shared__ float2 xval[C::kTiles][2][2][C::kRows];
   __shared__ volatile int abort_flag;
   __shared__ uint32_t tmem_slot;
 
@@ -329,7 +319,6 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
       mbar_init(&p_full[b], 4);
       mbar_init(&o_done[b], 1);
     }
-    for (int w = 0; w < C::kSoftmaxWarps; ++w) mbar_init(&m_set[w], 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&item_ready[b], 1);
       mbar_init(&item_free[b], C::kSoftmaxWarps + 3);  // softmax warps, issuers, V producer
@@ -428,9 +417,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
   };
 
   // The softmax warpgroups hold 64 scores a thread: registers from the other
-  // warpgroup (4 x 128 x 104 + 128 x 64 = 640 x 96, the launch's total).
+  // warpgroup (2 x 128 x 208 + 128 x 88 = 384 x 168, the launch's total).
   if (warp >= C::kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == C::kProducerWarp) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
@@ -669,61 +658,25 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax
-    // row; tile; parity h of the tile's pages that this warpgroup takes (and the
-    // half of the O columns that it stores)
-    const int m = tid & 127, t = (tid >> 7) & 1, h = tid >> 8;
-    const int sb = 2 * t + h;
-    int xn = 0;  // runs whose sums were exchanged
+    const int m = tid & 127, t = tid >> 7;  // row; tile
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t s_col = lane_base + C::kSCol + sb * kPage;
-    const uint32_t p_col = lane_base + C::kPCol + sb * C::kPStride;
-    const uint32_t o_row = lane_base + C::kOCol + t * D, o_col = o_row + h * (D / 2);
-    uint64_t* m_mine = &m_set[warp];
-    uint64_t* m_theirs = &m_set[warp ^ 8];  // the other warpgroup's warp on these rows
+    const uint32_t o_col = lane_base + C::kOCol + t * D;
     constexpr bool kCap = (KIND & kModCap) != 0, kBias = (KIND & kModBias) != 0;
-    ModRow row;
-    row.c = p.q_scale_log2;
-    row.nslope = 0.f;
-    {
-      const float a2 = p.cap_in * p.cap_in;
-      row.near[0] = kNear0 * row.c;
-      row.near[1] = kNear1 * row.c * a2;
-      row.near[2] = kNear2 * row.c * a2 * a2;
-      row.a2 = a2;
-      row.cap_in = p.cap_in;
-      row.cap_out = p.cap_out;
-      // where the folded coefficients would leave the normal range, the far
-      // form serves all scores
-      const bool folds = fabsf(p.cap_in) >= 0x1p-16f && fabsf(p.cap_in) <= 0x1p16f &&
-                         fabsf(row.c) >= 0x1p-40f && fabsf(row.c) <= 0x1p40f;
-      row.limit_near = folds ? kTanhNear / fabsf(p.cap_in) : -1.f;
-      row.limit_mid = folds ? kTanhMid / fabsf(p.cap_in) : -1.f;
-    }
     int i = 0, gi = 0;  // this tile's pages, all pages (over all items)
-    // A thread whose wait gave up (`mine` false) carries on to the next
-    // exchange, which ORs the failures, so the tile's threads stop together.
-    bool ok = true, mine = true;
-    const uint32_t xid = 1 + t, xcount = 2 * C::kRows;
+    bool ok = true;
     const int tl = t * T + m / G, g = m % G;  // token of the block, head of the group
     const bool in_tile = m / G < T;
-    auto next_item = [&](int seq) -> bool {
+    for (int seq = 0; ok; ++seq) {
       const int d = seq & 1;
-      if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) {
-        mine = false;
-        return false;
-      }
-      return items[d].valid != 0;
-    };
-    bool have = next_item(0);
-    ok = !named_sync_or(xid, xcount, !mine);
-    for (int seq = 0; ok && have; ++seq) {
-      const int d = seq & 1;
+      if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) break;
       const ModItem& it = items[d];
+      if (!it.valid) break;
       const int t_begin = it.t_begin, h0 = it.kvh * G;
       const bool row_ok = in_tile && t_begin + tl < it.t_end;
-      if constexpr (kBias) row.nslope = -p.slopes[h0 + g] * kLog2e;
+      float nslope = 0.f;
+      if constexpr (kBias) nslope = -p.slopes[h0 + g] * kLog2e;
       int rs = 0, re = 0;
       for (int r = 0; r < it.runs && ok; ++r) {
         rs = re;
@@ -738,7 +691,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           // no pass covers these tokens (their outputs are zeroed, the combine
           // leaves them), or the key part has none of their pages
           if constexpr (kParts) {
-            if (h == 0 && live) {
+            if (live) {
               const size_t u = unit_of();
               part_ml[2 * u] = -INFINITY;
               part_ml[2 * u + 1] = first < 0 ? -1.f : 0.f;
@@ -750,29 +703,30 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           gi += last - first + 1;
           continue;
         }
-        // keys lo .. hi of this row, and of the run, in these pages
-        const int pos = live ? it.tok_pos[tl] : 1 << 30;  // (other rows: behind every key)
+        // keys lo .. hi of this row in these pages; rows of other runs go along
+        // behind every key and unmasked (their P and O stay their own and are
+        // not stored: masking them would cost the run's pages their fast form)
+        const int pos = live ? it.tok_pos[tl] : 1 << 30;
         const int lo = live ? it.lo(tl, p.window) : 0;
-        const int hi = live ? min(it.tok_hi[tl], last * kPage + kPage - 1) : -1;
-        const int lo_run = it.lo(rs, p.window), hi_run = it.tok_hi[re - 1];
-        const bool zeroes = t == 0 || !ModItem::takes_part(0, T, rs, re);
-        float m_run = -INFINITY;  // the reference that l is relative to, log2 units
-        float l = 0.f;            // sum of this thread's pages
-        // this warpgroup's pages of the run; i, gi: their numbers
-        const int i_end = i + (last - first + 1), gi_end = gi + (last - first + 1);
-        const int skip = (i ^ h) & 1;
-        i += skip;
-        gi += skip;
-        for (int pg = first + skip; pg <= last; pg += 2, i += 2, gi += 2) {
+        const int hi = live ? it.tok_hi[tl] : 1 << 30;
+        float m_run = -INFINITY;  // running (lazy) max of the row, log2 units
+        float l = 0.f;            // row sum relative to it
+        for (int pg = first; pg <= last; ++pg, ++i, ++gi) {
+          const int sb = 2 * t + (i & 1);
+          const uint32_t s_col = lane_base + C::kSCol + sb * kPage;
+          const uint32_t p_col = lane_base + C::kPCol + sb * C::kPStride;
           if (!all_ok(wait(&s_full[sb], (i >> 1) & 1))) {
-            mine = false;
+            ok = false;
             break;
           }
           tc_fence_after_sync();
           const int pos0 = pg * kPage;
-          bool usual = pos0 >= lo && pos0 + kPage - 1 <= hi;  // the whole page is seen
-          if constexpr (kBias) usual = usual && pos0 + kPage - 1 <= pos;
-          usual = __all_sync(0xffffffffu, usual);
+          const int k_lo = lo - pos0, k_hi = hi - pos0;  // this row's keys of the page
+          // the usual case (the same for the warp): nothing masked; or masked
+          // keys only, the others' bias linear
+          const bool whole = __all_sync(0xffffffffu, k_lo <= 0 && k_hi >= kPage - 1);
+          const bool usual =
+              !kBias || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos);
 
           auto s_read = [&]() {  // S is in registers: its columns are free
             if constexpr (C::kOwnP) {
@@ -781,48 +735,45 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               if (lane == 0) mbar_arrive(&s_free[sb]);
             }
           };
-          // The row's reference: the page before's, unless this page's maximum
-          // mx exceeds it by the slack; handed on at once.  False: a wait failed.
+          // The row's reference, raised when this page's maximum mx exceeds it by
+          // the slack (O is then rescaled); P of the page may be written after it.
+          // False: a wait failed.
           auto settle = [&](float mx) -> bool {
-            float m_prev = -INFINITY;
-            if (pg > first) {
-              if (!all_ok(wait(m_theirs, ((i - 1) >> 1) & 1))) return false;
-              m_prev = m_ref[t][m];
-            }
-            const float m_new = mx > m_prev + kLazyRescaleLog2 ? mx : m_prev;
-            m_ref[t][m] = m_new;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(m_mine);
-            if (m_new != m_run) {  // (m_run -inf: l is 0)
-              l *= m_run == -INFINITY ? 0.f : exp2_approx(m_run - m_new);
-              m_run = m_new;
-            }
-            if (__builtin_expect(
-                    __any_sync(0xffffffffu, m_new != m_prev && m_prev != -INFINITY), 0)) {
-              // O holds the pages before, once P V of the last of them is done
-              if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) return false;
-              tc_fence_after_sync();
-              const float alpha = m_prev == -INFINITY ? 1.f : exp2_approx(m_prev - m_new);
-#pragma unroll 1
-              for (int j = 0; j < D / 16; ++j) {
-                float ov[16];
-                tmem_ld16(o_row + 16 * j, ov);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) ov[k] *= alpha;
-                tmem_st16(o_row + 16 * j, ov);
-              }
-            }
-            // P V of this warpgroup's page before has read P (P over S: S waited)
+            // P V of the page before last has read P (P over S: S waited for it).
+            // It also puts the wait below at most one phase ahead.
             if (C::kOwnP && i >= 2) {
               if (!all_ok(wait(&o_done[sb], ((i >> 1) - 1) & 1))) return false;
               tc_fence_after_sync();
             }
+            const bool rises = mx > m_run + kLazyRescaleLog2;
+            float alpha = 1.f;
+            if (rises) {
+              alpha = m_run == -INFINITY ? 1.f : exp2_approx(m_run - mx);
+              l *= alpha;  // (0 before the first key)
+              m_run = mx;
+            }
+            if (__builtin_expect(__any_sync(0xffffffffu, alpha != 1.f), 0)) {
+              // O holds the pages before, once P V of the last of them is done
+              if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) return false;
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int j = 0; j < D / 16; ++j) {
+                float ov[16];
+                tmem_ld16(o_col + 16 * j, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) ov[k] *= alpha;
+                tmem_st16(o_col + 16 * j, ov);
+              }
+            }
             return true;
           };
 
-          bool done = false;
-          if (__builtin_expect(usual, 1)) {
+          // A usual page, its 64 scores in registers.  1: done; 0: the scores are
+          // not all within the cap's near form (nothing changed); -1: a wait failed.
+          auto usual_page = [&](auto masked) -> int {
+            constexpr bool kMasked = decltype(masked)::value;
+            auto seen = [&](int k) { return !kMasked || (k >= k_lo && k <= k_hi); };
             float sv[kPage];
 #pragma unroll
             for (int q = 0; q < kPage / 16; ++q)
@@ -830,52 +781,65 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             tmem_wait_ld();
             // the page's maximum: of the products (a score without a bias grows,
             // or falls, with them), or with a bias of the scores
-            float mx = 0.f;
-            done = true;
+            float mx;
             if constexpr (kCap) {
-              const float mn = row_min(sv);
-              mx = row_max(sv);
-              done = __all_sync(0xffffffffu, fmaxf(fabsf(mx), fabsf(mn)) <= row.limit_near);
-              mx = fmaxf(one_score<KIND>(mx, row, kCapNear), one_score<KIND>(mn, row, kCapNear));
-            } else if constexpr (!kBias) {
-              mx = row.c > 0.f ? row_max(sv) * row.c : row_min(sv) * row.c;
+              if constexpr (kMasked) {
+#pragma unroll
+                for (int k = 0; k < kPage; ++k) sv[k] = seen(k) ? sv[k] : 0.f;
+              }
+              const float low = row_min(sv), top = row_max(sv);
+              if (!__all_sync(0xffffffffu,
+                              !live || fmaxf(fabsf(low), fabsf(top)) <= p.limit_near))
+                return 0;
+              mx = fmaxf(one_score<KIND>(top, p, kCapNear), one_score<KIND>(low, p, kCapNear));
             }
-            if (__builtin_expect(done, 1)) {
-              s_read();
-              if constexpr (kBias) {
-                usual_scores<KIND>(sv, row, pos0 - pos, 0.f);
+            s_read();
+            if constexpr (kCap ? kBias || kMasked : true) {
+              // the scores themselves (of all but unmasked capped ones, whose
+              // maximum is had from the products)
+              if constexpr (kBias || kCap || kMasked) usual_scores<KIND>(sv, p, nslope, pos0 - pos, 0.f);
+              if constexpr (kMasked) {
+#pragma unroll
+                for (int k = 0; k < kPage; ++k) sv[k] = seen(k) ? sv[k] : -INFINITY;
+              }
+              if constexpr (kBias || kCap || kMasked)
                 mx = row_max(sv);
-              }
-              if (!settle(mx)) {
-                mine = false;
-                break;
-              }
-              const float ref = m_run == -INFINITY ? 0.f : m_run;
-              if constexpr (!kBias) usual_scores<KIND>(sv, row, 0, ref);
-              float2 sum2[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int q = 0; q < kPage / 32; ++q) {
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  float2 y = make_float2(sv[32 * q + 2 * j], sv[32 * q + 2 * j + 1]);
-                  if constexpr (kBias) y = __fadd2_rn(y, make_float2(-ref, -ref));
-                  const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                  sum2[j & 3] = __fadd2_rn(sum2[j & 3], x);
-                  w[j] = pack_bf16x2(x.x, x.y);
-                }
-                tmem_st16(p_col + 16 * q, w);
-              }
-              const float2 s2 =
-                  __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
-              l += s2.x + s2.y;
+              else
+                mx = p.q_scale_log2 > 0.f ? row_max(sv) * p.q_scale_log2 : row_min(sv) * p.q_scale_log2;
             }
-          }
-          if (__builtin_expect(!done, 0)) {
-            // Any other page, 16 keys at a time in rolled loops: keys masked, keys
-            // past the query with a bias, scores near their cap.
+            if (!settle(mx)) return -1;
+            const float ref = m_run == -INFINITY ? 0.f : m_run;
+            constexpr bool kScored = kBias || kMasked;  // sv holds scores, not products
+            if constexpr (!kScored) usual_scores<KIND>(sv, p, nslope, 0, ref);
+            float2 sum2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < kPage / 32; ++q) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float2 y = make_float2(sv[32 * q + 2 * j], sv[32 * q + 2 * j + 1]);
+                if constexpr (kScored) y = __fadd2_rn(y, make_float2(-ref, -ref));
+                const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                sum2[j & 3] = __fadd2_rn(sum2[j & 3], x);
+                w[j] = pack_bf16x2(x.x, x.y);
+              }
+              tmem_st16(p_col + 16 * q, w);
+            }
+            const float2 s2 =
+                __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+            l += s2.x + s2.y;
+            return 1;
+          };
+          int done = 0;
+          if (__builtin_expect(whole && usual, 1))
+            done = usual_page(std::false_type{});
+          else if (usual)
+            done = usual_page(std::true_type{});
+          if (__builtin_expect(done == 0, 0)) {
+            // Any other page, 16 keys at a time in rolled loops: visible keys past
+            // the query with a bias, scores near their cap.
             constexpr int kFew = 16;
             float mx = -INFINITY, mn = INFINITY;
 #pragma unroll 1
@@ -883,19 +847,19 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               float sv[kFew];
               tmem_ld16(s_col + q, sv);
               tmem_wait_ld();
-              const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
 #pragma unroll
               for (int k = 0; k < kFew; ++k)
-                if (k >= k_lo && k <= k_hi) {
+                if (q + k >= k_lo && q + k <= k_hi) {
                   mx = fmaxf(mx, sv[k]);
                   mn = fminf(mn, sv[k]);
                 }
             }
             int form = kNoCap;
             if constexpr (kCap) {
-              const float most = mx == -INFINITY ? 0.f : fmaxf(fabsf(mx), fabsf(mn));
-              form = __all_sync(0xffffffffu, most <= row.limit_near)  ? kCapNear
-                     : __all_sync(0xffffffffu, most <= row.limit_mid) ? kCapMid
+              const float most =
+                  !live || mx == -INFINITY ? 0.f : fmaxf(fabsf(mx), fabsf(mn));
+              form = __all_sync(0xffffffffu, most <= p.limit_near)  ? kCapNear
+                     : __all_sync(0xffffffffu, most <= p.limit_mid) ? kCapMid
                                                                       : kCapFar;
             }
             if constexpr (kBias) {
@@ -905,19 +869,17 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
                 float sv[kFew];
                 tmem_ld16(s_col + q, sv);
                 tmem_wait_ld();
-                any_scores<KIND>(sv, row, form, pos0 + q - pos, 0.f);
-                const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
+                any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, 0.f);
 #pragma unroll
                 for (int k = 0; k < kFew; ++k)
-                  if (k >= k_lo && k <= k_hi) mx = fmaxf(mx, sv[k]);
+                  if (q + k >= k_lo && q + k <= k_hi) mx = fmaxf(mx, sv[k]);
               }
             } else if (mx != -INFINITY) {
-              mx = fmaxf(one_score<KIND>(mx, row, form), one_score<KIND>(mn, row, form));
+              mx = fmaxf(one_score<KIND>(mx, p, form), one_score<KIND>(mn, p, form));
             }
             if (!settle(mx)) {
-              mine = false;
-              break;
-            }
+              done = -1;
+            } else {
             const float ref = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll 1
             for (int q = 0; q < kPage; q += kFew) {
@@ -925,27 +887,32 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               tmem_ld16(s_col + q, sv);
               tmem_wait_ld();
               if (q + kFew == kPage) s_read();
-              any_scores<KIND>(sv, row, form, pos0 + q - pos, ref);
-              const int k_lo = lo - pos0 - q, k_hi = hi - pos0 - q;
+              any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, ref);
               uint32_t w[kFew / 2];
 #pragma unroll
               for (int j = 0; j < kFew / 2; ++j) {
-                const int k = 2 * j;
-                const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[k]) : 0.f;
-                const float y = k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[k + 1]) : 0.f;
+                const int k = q + 2 * j;
+                const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[2 * j]) : 0.f;
+                const float y = k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[2 * j + 1]) : 0.f;
                 l += x + y;
                 w[j] = pack_bf16x2(x, y);
               }
               tmem_st8(p_col + q / 2, w);
             }
+            }
+          }
+          if (__builtin_expect(done < 0, 0)) {
+            ok = false;
+            break;
           }
           // V rows outside the run's key range on a boundary page -> zero (both
           // tiles' products are issued after this tile's P)
-          if (zeroes) {
-            const int rlo = max(lo_run - pos0, 0), rhi = min(hi_run - pos0, kPage - 1);
+          if ((pg == first || pg == last) && (t == 0 || !ModItem::takes_part(0, T, rs, re))) {
+            const int rlo = max(it.lo(rs, p.window) - pos0, 0);
+            const int rhi = min(it.tok_hi[re - 1] - pos0, kPage - 1);
             if (rlo > 0 || rhi < kPage - 1) {
               if (!all_ok(wait(&v_full[gi % R], (gi / R) & 1))) {
-                mine = false;
+                ok = false;
                 break;
               }
               unsigned char* vt = v_slots + (gi % R) * C::kTileBytes;
@@ -964,29 +931,14 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[sb]);
         }
 
-        i = i_end;
-        gi = gi_end;
+        if (!ok) break;
+
         // end of run: the O_t row once P V of the last page is done
-        if (mine) {
-          if (all_ok(wait(&o_done[2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1)))
-            tc_fence_after_sync();
-          else
-            mine = false;
+        if (!all_ok(wait(&o_done[2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1))) {
+          ok = false;
+          break;
         }
-        {  // the row's sum over both warpgroups' pages, relative to the last reference
-          const int sl = xn & 1;
-          xval[t][sl][h][m] = make_float2(l, m_run);
-          if (named_sync_or(xid, xcount, !mine)) {
-            ok = false;
-            break;
-          }
-          const float2 other = xval[t][sl][1 - h][m];
-          const float m_end = fmaxf(m_run, other.y);
-          if (m_end != -INFINITY)
-            l = l * exp2_approx(m_run - m_end) + other.x * exp2_approx(other.y - m_end);
-          m_run = m_end;
-          ++xn;
-        }
+        tc_fence_after_sync();
         float inv = 1.f;
         float* arow = nullptr;
         if constexpr (kParts) {
@@ -994,50 +946,47 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           // and the other parts are merged by the combine launch)
           if (live) {
             const size_t u = unit_of();
-            if (h == 0) {
-              part_ml[2 * u] = m_run;
-              part_ml[2 * u + 1] = l;
-            }
-            arow = part_acc + u * D + h * (D / 2);
+            part_ml[2 * u] = m_run;
+            part_ml[2 * u + 1] = l;
+            arow = part_acc + u * D;
           }
         } else if (live) {
-          const float sk = p.sinks ? p.sinks[h0 + g] * kLog2e : -INFINITY;
-          const float mf = fmaxf(m_run, sk);
+          const float sink = p.sinks ? p.sinks[h0 + g] * kLog2e : -INFINITY;
+          const float mf = fmaxf(m_run, sink);
           const float scl = exp2_approx(m_run - mf);
-          const float total = fmaf(l, scl, exp2_approx(sk - mf));
+          const float total = fmaf(l, scl, exp2_approx(sink - mf));
           inv = l == 0.f ? 0.f : scl / total;
         }
-        uint16_t* orow =
-            p.out + ((size_t)(t_begin + (live ? tl : 0)) * p.hq + h0 + g) * D + h * (D / 2);
+        uint16_t* orow = p.out + ((size_t)(t_begin + (live ? tl : 0)) * p.hq + h0 + g) * D;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {  // this half's O columns
-          float ov[16];
-          tmem_ld16(o_col + 16 * j, ov);
+        for (int j = 0; j < D / 64; ++j) {
+          float ov[64];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tmem_ld16(o_col + 64 * j + 16 * q, *reinterpret_cast<float(*)[16]>(&ov[16 * q]));
           tmem_wait_ld();
           if (!live) continue;
           if constexpr (kParts) {
-            float4* dst = reinterpret_cast<float4*>(arow + 16 * j);
+            float4* dst = reinterpret_cast<float4*>(arow + 64 * j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 16; ++k)
               dst[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
           } else {
-            uint32_t w[8];
+            uint4* dst = reinterpret_cast<uint4*>(orow + 64 * j);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(ov[2 * k] * inv, ov[2 * k + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(orow + 16 * j);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_uint4(pack_bf16x2(ov[8 * k] * inv, ov[8 * k + 1] * inv),
+                                  pack_bf16x2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                                  pack_bf16x2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv),
+                                  pack_bf16x2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
           }
         }
         tc_fence_before_sync();
       }
       if (!ok) break;
-      // this item's descriptor is no longer read: free its slot before
-      // waiting for the next item
+      // this item's descriptor is no longer read
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_free[d]);
-      have = next_item(seq + 1);
-      ok = !named_sync_or(xid, xcount, !mine);
     }
   }
 

@@ -17,8 +17,12 @@ struct PlainScore {
 };
 
 struct ModParams : DecodeParams {
-  float cap_in;   // scale / softcap (0: no cap)
+  float cap_in;   // a = scale / softcap (0: no cap)
   float cap_out;  // softcap * log2(e): capped scores in log2 units
+  // the polynomial forms of a capped score (cap_near below): coefficients of the
+  // near form with the cap and the powers of a folded in, a^2, and the raw
+  // scores up to which each form holds (-1: not used)
+  float near_q[3], a2, limit_near, limit_mid;
   const float* slopes;       // [Hq] or nullptr
   const int32_t* first_key;  // [rows] or nullptr
   const int32_t* prefix_len; // [table_rows] or nullptr

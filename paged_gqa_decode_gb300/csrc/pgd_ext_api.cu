@@ -238,6 +238,17 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   p.cap_in = capped ? scale / score->softcap : 0.f;
   p.cap_out = capped ? (float)((double)score->softcap * 1.4426950408889634) : 0.f;
   if (capped && (p.cap_in == 0.f || !std::isfinite(p.cap_in))) return PGD_EINVAL;
+  // the forms fold powers of a into their coefficients: where those would leave
+  // the normal range, cap_far serves all scores
+  const float a = std::fabs(p.cap_in), a2 = a * a, c = p.q_scale_log2;
+  const bool folds = a >= 0x1p-16f && a <= 0x1p16f && std::fabs(c) >= 0x1p-40f &&
+                     std::fabs(c) <= 0x1p40f;
+  p.near_q[0] = kNear0 * c;
+  p.near_q[1] = kNear1 * c * a2;
+  p.near_q[2] = kNear2 * c * a2 * a2;
+  p.a2 = a2;
+  p.limit_near = folds ? kTanhNear / a : -1.f;
+  p.limit_mid = folds ? kTanhMid / a : -1.f;
   p.slopes = score->alibi_slopes;
   p.first_key = score->first_key;
   p.prefix_len = score->prefix_len;
