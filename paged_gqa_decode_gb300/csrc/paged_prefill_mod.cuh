@@ -272,6 +272,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
                              float* part_acc, float* part_ml) {
   using C = ModPrefillCfg<D>;
   constexpr int R = C::kRing, QB = C::kQBufs;
+  // With a bias a run's pages are taken last first: the scores then fall from
+  // page to page (usually), and the reference never rises.
+  constexpr bool kBack = (KIND & kModBias) != 0;
   const int G = p.group;
   const int T = C::kRows / G;  // tokens per tile
   const int tokens = C::kTiles * T;
@@ -378,15 +381,17 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
       const int first = it.run_pg[r], last = it.run_last[r];
       if (first < 0 || first > last) continue;
       const int row = it.tok_row[r == 0 ? 0 : it.run_end[r - 1]];
-      auto look_up = [&](int pg0) -> int {
-        if (lane >= 16 || pg0 + lane > last) return 0;
-        return (int)tile_first_row(p.layout, page_of(p.table, row, pg0 + lane, p.maxp), it.kvh,
-                                   p.hkv, p.num_pages, p.maxp);
+      const int pages = last - first + 1;
+      auto look_up = [&](int n0) -> int {
+        if (lane >= 16 || n0 + lane >= pages) return 0;
+        const int pg = kBack ? last - n0 - lane : first + n0 + lane;
+        return (int)tile_first_row(p.layout, page_of(p.table, row, pg, p.maxp), it.kvh, p.hkv,
+                                   p.num_pages, p.maxp);
       };
-      int y_next = look_up(first);
-      for (int pg0 = first; pg0 <= last; pg0 += 16) {
+      int y_next = look_up(0);
+      for (int n0 = 0; n0 < pages; n0 += 16) {
         const int y = y_next;
-        if (is_k && lane < 16 && pg0 + lane <= last && pg0 + lane >= first + R) {
+        if (is_k && lane < 16 && n0 + lane < pages && n0 + lane >= R) {
           if constexpr (D == 128) {
             tma_prefetch_l2_3d(&k_map, 0, y, 0);
             tma_prefetch_l2_3d(&v_map, 0, y, 0);
@@ -395,8 +400,8 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             tma_prefetch_l2_2d(&v_map, 0, y);
           }
         }
-        y_next = look_up(pg0 + 16);
-        for (int j = 0; j < 16 && pg0 + j <= last; ++j, ++i) {
+        y_next = look_up(n0 + 16);
+        for (int j = 0; j < 16 && n0 + j < pages; ++j, ++i) {
           const int yj = __shfl_sync(0xffffffffu, y, j);
           const int s = i % R;
           if (i >= R && !all_ok(wait(&empty[s], ((i / R) - 1) & 1))) return false;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
                                   ModItem::takes_part(1, T, rs, re)};
             rs = re;
             if (first < 0) continue;
-            for (int pg = first; pg <= last && ok; ++pg, ++i) {
+            for (int pg = first; pg <= last && ok; ++pg, ++i) {  // (their number; order: kBack)
               const int s = i % R;
               if (!wait(is_s ? &k_full[s] : &v_full[s], (i / R) & 1)) {
                 ok = false;
@@ -675,8 +680,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
       if (!it.valid) break;
       const int t_begin = it.t_begin, h0 = it.kvh * G;
       const bool row_ok = in_tile && t_begin + tl < it.t_end;
-      float nslope = 0.f;
-      if constexpr (kBias) nslope = -p.slopes[h0 + g] * kLog2e;
+      // (loaded here, needed later)
+      const float slope = kBias ? p.slopes[h0 + g] : 0.f;
+      const float sink = !kParts && p.sinks ? p.sinks[h0 + g] : -INFINITY;
       int rs = 0, re = 0;
       for (int r = 0; r < it.runs && ok; ++r) {
         rs = re;
@@ -709,9 +715,11 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         const int pos = live ? it.tok_pos[tl] : 1 << 30;
         const int lo = live ? it.lo(tl, p.window) : 0;
         const int hi = live ? it.tok_hi[tl] : 1 << 30;
+        const float nslope = -slope * kLog2e;  // bias per position of distance, log2 units
         float m_run = -INFINITY;  // running (lazy) max of the row, log2 units
         float l = 0.f;            // row sum relative to it
-        for (int pg = first; pg <= last; ++pg, ++i, ++gi) {
+        for (int n = 0; n <= last - first; ++n, ++i, ++gi) {
+          const int pg = kBack ? last - n : first + n;
           const int sb = 2 * t + (i & 1);
           const uint32_t s_col = lane_base + C::kSCol + sb * kPage;
           const uint32_t p_col = lane_base + C::kPCol + sb * C::kPStride;
@@ -951,10 +959,10 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             arow = part_acc + u * D;
           }
         } else if (live) {
-          const float sink = p.sinks ? p.sinks[h0 + g] * kLog2e : -INFINITY;
-          const float mf = fmaxf(m_run, sink);
+          const float sk = sink * kLog2e;
+          const float mf = fmaxf(m_run, sk);
           const float scl = exp2_approx(m_run - mf);
-          const float total = fmaf(l, scl, exp2_approx(sink - mf));
+          const float total = fmaf(l, scl, exp2_approx(sk - mf));
           inv = l == 0.f ? 0.f : scl / total;
         }
         uint16_t* orow = p.out + ((size_t)(t_begin + (live ? tl : 0)) * p.hq + h0 + g) * D;
