@@ -13,6 +13,11 @@
 // tokens of a run share table row and first key and have consecutive
 // positions, and a run is one pass over the pages that its tokens see.
 //
+// With a bias a run's pages are taken last first: the nearest keys, usually the
+// largest scores, come early, and the running maximum of a softmax in one pass
+// hardly rises after them.  Taken first to last every page raised it and O was
+// rescaled each time: 14 heads of 64 over 4000 positions 895 us, so 712.
+//
 // What bounds it is the softmax: a page's 64 scores a row are 64 exponentials,
 // 256 cycles of a sub-partition's special function unit for each warp, and
 // every trip to TMEM or through a barrier costs hundreds of cycles.  So
@@ -48,6 +53,16 @@
 // columns of bf16 pairs, at head_dim 64 after them (S of the page after next is
 // computed as soon as S is read), at 128 over S (it then waits for P V).
 // Key parts as in the one-SM kernel.
+//
+// Measured (heads of 128, window 4096, eight chunks of 1024 tokens behind 7168,
+// 4.3e11 multiply-adds of two): 309 us capped, 845 TFLOP/s (270 us without cap
+// and bias; the one-SM kernel takes 334 us for those, 569 with the cap built into
+// it); one such chunk 102 us.  The tensor cores are active for 40 % of the time,
+// an instruction is issued in 44 % of the cycles, and the rest are each warp's own
+// waits from one step of a page to the next.  Tried and left out: reading the
+// next page's S while this one's exponentials run (311 us); scalar instead of
+// packed arithmetic for the cap (438 us where packed took 403).
+//
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
 // roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.
 #pragma once
@@ -462,8 +477,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           mbar_arrive_expect_tx(&q_full[qb], C::kTiles * C::kBoxes * T * G * 128);
           for (int t = 0; t < C::kTiles; ++t)
             for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_3d(q_smem + qb * C::kQBytes + t * C::kQTileBytes + bx * C::kQBoxBytes, &q_map,
-                          64 * bx, kvh * G, t_begin + t * T, &q_full[qb]);
+              tma_load_3d(
+                  q_smem + qb * C::kQBytes + t * C::kQTileBytes + bx * C::kQBoxBytes, &q_map,
+                  64 * bx, kvh * G, t_begin + t * T, &q_full[qb]);
         }
         // tokens: bad ones are reported, and left out of every run with those
         // that see no key (their outputs are zeroed below)
@@ -549,8 +565,8 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             const int tl = rs + e / per_token;
             if (t_begin + tl >= t_end) continue;
             const int g = (e / (D / 8)) % G, ch = e % (D / 8);
-            reinterpret_cast<uint4*>(p.out + ((size_t)(t_begin + tl) * p.hq + kvh * G + g) * D)[ch] =
-                make_uint4(0u, 0u, 0u, 0u);
+            uint16_t* o = p.out + ((size_t)(t_begin + tl) * p.hq + kvh * G + g) * D;
+            reinterpret_cast<uint4*>(o)[ch] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         __syncwarp();
@@ -789,6 +805,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             tmem_wait_ld();
             // the page's maximum: of the products (a score without a bias grows,
             // or falls, with them), or with a bias of the scores
+            constexpr bool kScored = kBias || kMasked;
             float mx;
             if constexpr (kCap) {
               if constexpr (kMasked) {
@@ -802,22 +819,18 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               mx = fmaxf(one_score<KIND>(top, p, kCapNear), one_score<KIND>(low, p, kCapNear));
             }
             s_read();
-            if constexpr (kCap ? kBias || kMasked : true) {
-              // the scores themselves (of all but unmasked capped ones, whose
-              // maximum is had from the products)
-              if constexpr (kBias || kCap || kMasked) usual_scores<KIND>(sv, p, nslope, pos0 - pos, 0.f);
+            if constexpr (kScored) {  // sv: scores in place of the products
+              usual_scores<KIND>(sv, p, nslope, pos0 - pos, 0.f);
               if constexpr (kMasked) {
 #pragma unroll
                 for (int k = 0; k < kPage; ++k) sv[k] = seen(k) ? sv[k] : -INFINITY;
               }
-              if constexpr (kBias || kCap || kMasked)
-                mx = row_max(sv);
-              else
-                mx = p.q_scale_log2 > 0.f ? row_max(sv) * p.q_scale_log2 : row_min(sv) * p.q_scale_log2;
+              mx = row_max(sv);
+            } else if constexpr (!kCap) {
+              mx = p.q_scale_log2 * (p.q_scale_log2 > 0.f ? row_max(sv) : row_min(sv));
             }
             if (!settle(mx)) return -1;
             const float ref = m_run == -INFINITY ? 0.f : m_run;
-            constexpr bool kScored = kBias || kMasked;  // sv holds scores, not products
             if constexpr (!kScored) usual_scores<KIND>(sv, p, nslope, 0, ref);
             float2 sum2[4];
 #pragma unroll
@@ -888,25 +901,26 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             if (!settle(mx)) {
               done = -1;
             } else {
-            const float ref = m_run == -INFINITY ? 0.f : m_run;
+              const float ref = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll 1
-            for (int q = 0; q < kPage; q += kFew) {
-              float sv[kFew];
-              tmem_ld16(s_col + q, sv);
-              tmem_wait_ld();
-              if (q + kFew == kPage) s_read();
-              any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, ref);
-              uint32_t w[kFew / 2];
+              for (int q = 0; q < kPage; q += kFew) {
+                float sv[kFew];
+                tmem_ld16(s_col + q, sv);
+                tmem_wait_ld();
+                if (q + kFew == kPage) s_read();
+                any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, ref);
+                uint32_t w[kFew / 2];
 #pragma unroll
-              for (int j = 0; j < kFew / 2; ++j) {
-                const int k = q + 2 * j;
-                const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[2 * j]) : 0.f;
-                const float y = k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[2 * j + 1]) : 0.f;
-                l += x + y;
-                w[j] = pack_bf16x2(x, y);
+                for (int j = 0; j < kFew / 2; ++j) {
+                  const int k = q + 2 * j;
+                  const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[2 * j]) : 0.f;
+                  const float y =
+                      k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[2 * j + 1]) : 0.f;
+                  l += x + y;
+                  w[j] = pack_bf16x2(x, y);
+                }
+                tmem_st8(p_col + q / 2, w);
               }
-              tmem_st8(p_col + q / 2, w);
-            }
             }
           }
           if (__builtin_expect(done < 0, 0)) {

@@ -172,3 +172,92 @@ def test_rotary_append_python_checks():
     with pytest.raises(ValueError, match="CUDA"):
         pgd.rotary_append_paged(None, b(2, 1, 64), b(2, 1, 64), torch.zeros(2, dtype=torch.int32),
                                 b(1, 1, 64, 64), b(1, 1, 64, 64), rotary=pgd.Rotary(64, 1e4))
+
+
+# ----------------------------------------------------------------- attention
+
+def _dims(**kw):
+    return pgd.make_dims(**dict(dict(rows=2, num_q_heads=4, num_kv_heads=2, head_dim=64,
+                                     num_pages=4, max_pages_per_row=2), **kw))
+
+
+def _attend(ext, prefill, dims=None, score=None, **kw):
+    """A call whose arguments would all do but for kw; tensors are places in a host buffer."""
+    buf = ctypes.create_string_buffer(8192)
+    at = (ctypes.addressof(buf) + 15) & ~15
+    s = dict(softcap=30.0, alibi_slopes=None, first_key=None, prefix_len=None)
+    s.update({k: (at + v[1] if isinstance(v, tuple) else v) for k, v in (score or {}).items()})
+    args = dict(q=at, k_new=None, v_new=None, k_pool=at + 1024, v_pool=at + 2048, table=at + 3072)
+    if prefill:
+        args["rows"] = at + 3200
+    args.update(positions=at + 3300, sinks=None, window=0, scale=0.125, out=at + 4096,
+                workspace=at + 5120, workspace_bytes=0)
+    opts = pgd.DecodeOptions(**kw.pop("opts", {}))
+    d = dims or _dims()
+    table_rows = kw.pop("table_rows", 2)
+    given = kw.pop("given", True)
+    args.update({k: (at + v[1] if isinstance(v, tuple) else v) for k, v in kw.items()})
+    head = [ctypes.byref(d) if dims is not False else None]
+    if prefill:
+        head.append(table_rows)
+    call = ext.pgdx_paged_prefill if prefill else ext.pgdx_paged_decode
+    return call(*head, ctypes.byref(pgd.Score(**s)) if given else None, *args.values(),
+                ctypes.byref(opts), None)
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(k_pool=None), dict(v_pool=None), dict(positions=None), dict(out=None),
+    dict(table=None), dict(q=("at", 8)), dict(k_pool=("at", 1032)), dict(out=("at", 4098)),
+    dict(k_new=("at", 0)), dict(v_new=("at", 0)),             # one of the two alone
+    dict(k_new=("at", 4), v_new=("at", 0)),
+    dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(given=False),
+    dict(score=dict(softcap=float("nan"))), dict(score=dict(softcap=float("inf"))),
+    dict(score=dict(alibi_slopes=("at", 3))), dict(score=dict(first_key=("at", 2))),
+    dict(opts=dict(kernel=-1)), dict(opts=dict(kernel=6)),
+])
+def test_attention_refuses(ext, prefill, kw):
+    assert _attend(ext, prefill, **dict(kw)) == pgd.EINVAL
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_attention_refuses_dims(ext, prefill):
+    assert _attend(ext, prefill, dims=False) == pgd.EINVAL
+    assert _attend(ext, prefill, dims=_dims(rows=-1)) == pgd.EINVAL
+    assert _attend(ext, prefill, dims=_dims(num_q_heads=5)) == pgd.EINVAL
+    assert _attend(ext, prefill, dims=_dims(head_dim=96)) == pgd.EUNSUPPORTED
+    pages32 = _dims()
+    pages32.page_size = 32
+    assert _attend(ext, prefill, dims=pages32) == pgd.EUNSUPPORTED
+    assert _attend(ext, prefill, dims=_dims(num_pages=2 ** 25)) == pgd.EUNSUPPORTED
+    # dense rows without a pool for each
+    assert _attend(ext, prefill, dims=_dims(layout=pgd.ROW_MAJOR, num_pages=2),
+                   table=None) == pgd.EINVAL
+    assert _attend(ext, prefill, dims=_dims(rows=0), q=None, out=None) == pgd.OK
+
+
+def test_attention_refuses_the_other_calls_kernels(ext):
+    for kernel in (pgd.KERNEL_CUDA_CORE, pgd.KERNEL_PREFILL_TILED, pgd.KERNEL_PREFILL_PAIR):
+        for prefill in (False, True):
+            assert _attend(ext, prefill, opts=dict(kernel=kernel)) == pgd.EUNSUPPORTED
+    assert _attend(ext, False, opts=dict(kernel=pgd.KERNEL_PREFILL_UMMA)) == pgd.EINVAL
+
+
+def test_decode_refuses_a_prefix_and_prefill_a_missing_map(ext):
+    assert _attend(ext, False, score=dict(prefix_len=("at", 0))) == pgd.EINVAL
+    assert _attend(ext, True, score=dict(prefix_len=("at", 2))) == pgd.EINVAL
+    assert _attend(ext, True, rows=None) == pgd.EINVAL
+    assert _attend(ext, True, table_rows=0) == pgd.EINVAL
+    assert _attend(ext, True, table_rows=-3) == pgd.EINVAL
+
+
+def test_attention_python_checks():
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)     # noqa: E731
+    with pytest.raises(ValueError, match="CUDA"):
+        pgd.paged_decode_attention(b(2, 4, 64), b(4, 2, 64, 64), b(4, 2, 64, 64), i(2, 2), i(2),
+                                   num_kv_heads=2, softcap=30.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        pgd.paged_prefill_attention(b(2, 4, 64), b(4, 2, 64, 64), b(4, 2, 64, 64), i(2, 2), i(2),
+                                    i(2), num_kv_heads=2, alibi_slopes=torch.zeros(4))
