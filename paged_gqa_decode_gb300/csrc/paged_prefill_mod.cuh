@@ -16,7 +16,7 @@
 // With a bias a run's pages are taken last first: the nearest keys, usually the
 // largest scores, come early, and the running maximum of a softmax in one pass
 // hardly rises after them.  Taken first to last every page raised it and O was
-// rescaled each time: 14 heads of 64 over 4000 positions 895 us, so 712.
+// rescaled each time: 895 us, so 712, for 64 heads of 64 over 4000 positions.
 //
 // What bounds it is the softmax: a page's 64 scores a row are 64 exponentials,
 // 256 cycles of a sub-partition's special function unit for each warp, and
@@ -33,7 +33,15 @@
 //     query with a bias, scores near their cap), which go 16 keys at a time in
 //     rolled loops;
 //   - a capped score is a polynomial in s^2 times s plus what the exponent needs
-//     anyway: y = s Q(s^2) + (bias - m), four packed instructions for two keys;
+//     anyway: y = s Q(s^2) - m, four packed instructions for two keys;
+//   - a bias is linear in the key up to the query: 16 keys against the first of
+//     them from registers that last the run, the blocks' own offsets from the
+//     reference in the subtraction that is there anyway (the whole bias per pair
+//     of keys from constants: 712 us, so 650, on 64 heads of 64 over 4000
+//     positions);
+//   - masked keys are taken out 16 at a time, only where a row of the warp has
+//     one (64 selects on every boundary page, in a copy of the page code: 113 us,
+//     so 92, for prompts of documents with a prefix and a window);
 //   - P is rounded to bf16 once, without a residual product: an output is off
 //     by at most 2^-8 sum_j p_j |v_j| and typically by as much again as its own
 //     rounding to bf16; the row sums take the unrounded values;
@@ -54,14 +62,15 @@
 // computed as soon as S is read), at 128 over S (it then waits for P V).
 // Key parts as in the one-SM kernel.
 //
-// Measured (heads of 128, window 4096, eight chunks of 1024 tokens behind 7168,
-// 4.3e11 multiply-adds of two): 309 us capped, 845 TFLOP/s (270 us without cap
-// and bias; the one-SM kernel takes 334 us for those, 569 with the cap built into
-// it); one such chunk 102 us.  The tensor cores are active for 40 % of the time,
+// Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
+// up to 8192, 2.6e11 operations): 290 us capped, 902 TFLOP/s (the one-SM kernel
+// takes 334 us for them without a cap, 569 with the cap built into it); one chunk
+// behind 8000 positions 99 us.  The tensor cores are active for 40 % of the time,
 // an instruction is issued in 44 % of the cycles, and the rest are each warp's own
 // waits from one step of a page to the next.  Tried and left out: reading the
-// next page's S while this one's exponentials run (311 us); scalar instead of
-// packed arithmetic for the cap (438 us where packed took 403).
+// next page's S while this one's exponentials run (311 us, of 309 without); P in
+// columns of its own and one S buffer a tile at head_dim 128 (317 us, of 309);
+// scalar instead of packed arithmetic for the cap (438 us where packed took 403).
 //
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
 // roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.
@@ -158,26 +167,10 @@ __device__ __forceinline__ float2 mid2(float2 v, float2 add, const ModParams& p)
   return __ffma2_rn(__fmul2_rn(v, make_float2(p.q_scale_log2, p.q_scale_log2)), q, add);
 }
 
-// A page's usual case: near form (or no cap), every visible key at or before
-// the query where there is a bias.
-template <int KIND, int N>
-__device__ __forceinline__ void usual_scores(float (&s)[N], const ModParams& p, float nslope,
-                                             int rel, float m) {
-  const float b0 = KIND & kModBias ? fmaf(-nslope, (float)rel, -m) : -m;
-#pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    float2 add = make_float2(b0, b0);
-    if constexpr (KIND & kModBias)
-      add = __ffma2_rn(make_float2(-nslope, -nslope), make_float2((float)k, (float)(k + 1)),
-                       add);
-    float2 v = make_float2(s[k], s[k + 1]);
-    if constexpr (KIND & kModCap)
-      v = near2(v, add, p);
-    else
-      v = scaled2(v, add, p);
-    s[k] = v.x;
-    s[k + 1] = v.y;
-  }
+// Usual scores, a cap's near form or none: y = s Q(s^2) + add.
+template <int KIND>
+__device__ __forceinline__ float2 usual2(float2 v, float2 add, const ModParams& p) {
+  return (KIND & kModCap) ? near2(v, add, p) : scaled2(v, add, p);
 }
 
 // Any case, for few keys at a time.
@@ -731,7 +724,17 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         const int pos = live ? it.tok_pos[tl] : 1 << 30;
         const int lo = live ? it.lo(tl, p.window) : 0;
         const int hi = live ? it.tok_hi[tl] : 1 << 30;
+        // the keys that every row of the warp sees; whether one sees keys past itself
+        const int lo_all = __reduce_max_sync(0xffffffffu, lo);
+        const int hi_all = __reduce_min_sync(0xffffffffu, hi);
+        const bool ahead = kBias && __any_sync(0xffffffffu, hi > pos);
         const float nslope = -slope * kLog2e;  // bias per position of distance, log2 units
+        float2 step[8];  // bias of 16 keys against the first of them
+        if constexpr (kBias) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            step[j] = make_float2(-nslope * (float)(2 * j), -nslope * (float)(2 * j + 1));
+        }
         float m_run = -INFINITY;  // running (lazy) max of the row, log2 units
         float l = 0.f;            // row sum relative to it
         for (int n = 0; n <= last - first; ++n, ++i, ++gi) {
@@ -746,11 +749,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           tc_fence_after_sync();
           const int pos0 = pg * kPage;
           const int k_lo = lo - pos0, k_hi = hi - pos0;  // this row's keys of the page
-          // the usual case (the same for the warp): nothing masked; or masked
-          // keys only, the others' bias linear
-          const bool whole = __all_sync(0xffffffffu, k_lo <= 0 && k_hi >= kPage - 1);
+          // the usual case (the same for the warp): the bias is linear in the key
           const bool usual =
-              !kBias || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos);
+              !ahead || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos);
 
           auto s_read = [&]() {  // S is in registers: its columns are free
             if constexpr (C::kOwnP) {
@@ -795,43 +796,68 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
 
           // A usual page, its 64 scores in registers.  1: done; 0: the scores are
           // not all within the cap's near form (nothing changed); -1: a wait failed.
-          auto usual_page = [&](auto masked) -> int {
-            constexpr bool kMasked = decltype(masked)::value;
-            auto seen = [&](int k) { return !kMasked || (k >= k_lo && k <= k_hi); };
+          auto usual_page = [&]() -> int {
+            // masks 16 keys at a time, and only where some row of the warp has one:
+            // most boundary pages are cut in one or two of their four blocks
+            const bool whole = pos0 >= lo_all && pos0 + kPage - 1 <= hi_all;
             float sv[kPage];
+            auto mask_to = [&](float value) {
+#pragma unroll
+              for (int q = 0; q < kPage; q += 16)
+                if (pos0 + q < lo_all || pos0 + q + 15 > hi_all) {
+#pragma unroll
+                  for (int k = q; k < q + 16; ++k)
+                    sv[k] = k >= k_lo && k <= k_hi ? sv[k] : value;
+                }
+            };
 #pragma unroll
             for (int q = 0; q < kPage / 16; ++q)
               tmem_ld16(s_col + 16 * q, *reinterpret_cast<float(*)[16]>(&sv[16 * q]));
             tmem_wait_ld();
             // the page's maximum: of the products (a score without a bias grows,
-            // or falls, with them), or with a bias of the scores
-            constexpr bool kScored = kBias || kMasked;
-            float mx;
+            // or falls, with them; max and min pass over a NaN), or with a bias of
+            // the scores
+            float mx = -INFINITY;
+            if constexpr (kCap || !kBias) {
+              if (!whole) mask_to(__int_as_float(0x7fffffff));
+            }
             if constexpr (kCap) {
-              if constexpr (kMasked) {
-#pragma unroll
-                for (int k = 0; k < kPage; ++k) sv[k] = seen(k) ? sv[k] : 0.f;
-              }
               const float low = row_min(sv), top = row_max(sv);
               if (!__all_sync(0xffffffffu,
-                              !live || fmaxf(fabsf(low), fabsf(top)) <= p.limit_near))
+                              !live || !(fmaxf(fabsf(low), fabsf(top)) > p.limit_near)))
                 return 0;
               mx = fmaxf(one_score<KIND>(top, p, kCapNear), one_score<KIND>(low, p, kCapNear));
             }
             s_read();
-            if constexpr (kScored) {  // sv: scores in place of the products
-              usual_scores<KIND>(sv, p, nslope, pos0 - pos, 0.f);
-              if constexpr (kMasked) {
+            if constexpr (kBias) {
+              // each block of 16 against the bias of its first key
 #pragma unroll
-                for (int k = 0; k < kPage; ++k) sv[k] = seen(k) ? sv[k] : -INFINITY;
+              for (int k = 0; k < kPage; k += 2) {
+                const float2 y = usual2<KIND>(make_float2(sv[k], sv[k + 1]), step[k / 2 % 8], p);
+                sv[k] = y.x;
+                sv[k + 1] = y.y;
               }
-              mx = row_max(sv);
+              if (!whole) mask_to(-INFINITY);
+              mx = -INFINITY;
+#pragma unroll
+              for (int q = 0; q < kPage; q += 16)
+                mx = fmaxf(mx, fmaf(-nslope, (float)(pos0 + q - pos),
+                                    row_max(*reinterpret_cast<float(*)[16]>(&sv[q]))));
             } else if constexpr (!kCap) {
               mx = p.q_scale_log2 * (p.q_scale_log2 > 0.f ? row_max(sv) : row_min(sv));
             }
             if (!settle(mx)) return -1;
             const float ref = m_run == -INFINITY ? 0.f : m_run;
-            if constexpr (!kScored) usual_scores<KIND>(sv, p, nslope, 0, ref);
+            if constexpr (!kBias) {
+#pragma unroll
+              for (int k = 0; k < kPage; k += 2) {
+                const float2 y =
+                    usual2<KIND>(make_float2(sv[k], sv[k + 1]), make_float2(-ref, -ref), p);
+                sv[k] = y.x;
+                sv[k + 1] = y.y;
+              }
+              if (!whole) mask_to(-INFINITY);
+            }
             float2 sum2[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
@@ -840,8 +866,12 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                float2 y = make_float2(sv[32 * q + 2 * j], sv[32 * q + 2 * j + 1]);
-                if constexpr (kScored) y = __fadd2_rn(y, make_float2(-ref, -ref));
+                const int k = 32 * q + 2 * j;
+                float2 y = make_float2(sv[k], sv[k + 1]);
+                if constexpr (kBias) {
+                  const float b = fmaf(-nslope, (float)(pos0 + k / 16 * 16 - pos), -ref);
+                  y = __fadd2_rn(y, make_float2(b, b));
+                }
                 const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                 sum2[j & 3] = __fadd2_rn(sum2[j & 3], x);
                 w[j] = pack_bf16x2(x.x, x.y);
@@ -854,10 +884,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             return 1;
           };
           int done = 0;
-          if (__builtin_expect(whole && usual, 1))
-            done = usual_page(std::false_type{});
-          else if (usual)
-            done = usual_page(std::true_type{});
+          if (__builtin_expect(usual, 1)) done = usual_page();
           if (__builtin_expect(done == 0, 0)) {
             // Any other page, 16 keys at a time in rolled loops: visible keys past
             // the query with a bias, scores near their cap.
