@@ -19,8 +19,9 @@
 // rescaled each time: 895 us, so 712, for 64 heads of 64 over 4000 positions.
 //
 // What bounds it is the softmax: a page's 64 scores a row are 64 exponentials,
-// 256 cycles of a sub-partition's special function unit for each warp, and
-// every trip to TMEM or through a barrier costs hundreds of cycles.  So
+// 256 cycles of a sub-partition's special function unit for each warp, with
+// about 300 other instructions, and every trip to TMEM or through a barrier costs
+// hundreds of cycles.  So
 //   - one warpgroup has a tile to itself, a thread to a row and page: no
 //     exchange between threads, and registers for 64 scores and their
 //     polynomials at once (208 a thread).  Two warpgroups to a tile, sharing
@@ -29,11 +30,19 @@
 //     registers moved, barriers and instructions fetched;
 //   - each tile has two S buffers: S of the next page is computed under the
 //     softmax of this one;
-//   - S is read from TMEM once, but on pages out of the usual (keys past the
-//     query with a bias, scores near their cap), which go 16 keys at a time in
-//     rolled loops;
+//   - a page is tried with the reference (the running maximum) as it is, a cap's
+//     polynomial for small scores and a bias linear in the key, and what that
+//     needs is looked at when the exponentials are there: no maximum to wait for
+//     before them.  Where it did not hold for a row of the warp -- a run's first
+//     page, a larger score, keys past the query with a bias -- S, still in TMEM,
+//     is read again and the page taken in full (with the maximum first on every
+//     page: 275 us, so 265, on the chunks below, before the issuers' last form;
+//     507 us, so 421, with 64 heads of 64);
+//   - capped scores without a bias lie within the cap: their reference is 0 and
+//     stays it (caps to 52);
 //   - a capped score is a polynomial in s^2 times s plus what the exponent needs
-//     anyway: y = s Q(s^2) - m, four packed instructions for two keys;
+//     anyway: y = s Q(s^2) - m, four packed instructions for two keys, and the
+//     largest s^2 tells whether it served;
 //   - a bias is linear in the key up to the query: 16 keys against the first of
 //     them from registers that last the run, the blocks' own offsets from the
 //     reference in the subtraction that is there anyway (the whole bias per pair
@@ -49,28 +58,31 @@
 //     document) takes no part in it.
 //
 // Warps (384 threads):
-//   0-7   softmax: tile t is warps 4t .. 4t + 3, a thread per query row; it
-//         zeroes a boundary page's V rows outside the run's range too (the
-//         first tile that takes part).
+//   0-7   softmax: tile t is warps 4t .. 4t + 3, a thread per query row.
 //   8     producer: takes items from the counter, lays out their runs (checks
 //         the table, zeroes uncovered outputs), copies Q and streams K pages.
-//   9     S issuer and TMEM owner, 10 P V issuer (one thread each), 11 V pages.
+//   9     S issuer and TMEM owner.  10 P V issuer; it zeroes a boundary page's V
+//         rows outside the run's range (while the softmax of the page runs).
+//   11    V pages.
 // Shared memory: K and V rings of page tiles (four each at head_dim 128, eight
 // at 64), Q (two buffers at 64, so that the next item's is there early); 192 KB
 // of both.  TMEM: O_t at t D, then S of (tile, page mod 2), 64 columns each; P, 32
-// columns of bf16 pairs, at head_dim 64 after them (S of the page after next is
-// computed as soon as S is read), at 128 over S (it then waits for P V).
+// columns of bf16 pairs, over the first half of its S, so S of the page after next
+// waits for P V.  (P in columns of its own, S free once read and tried pages kept
+// in registers: 274 us, of 265; 474 of 421 at head_dim 64.)
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
-// up to 8192, 2.6e11 operations): 290 us capped, 902 TFLOP/s (the one-SM kernel
+// up to 8192, 2.6e11 operations): 246 us capped, 1064 TFLOP/s (the one-SM kernel
 // takes 334 us for them without a cap, 569 with the cap built into it); one chunk
-// behind 8000 positions 99 us.  The tensor cores are active for 40 % of the time,
-// an instruction is issued in 44 % of the cycles, and the rest are each warp's own
-// waits from one step of a page to the next.  Tried and left out: reading the
-// next page's S while this one's exponentials run (311 us, of 309 without); P in
-// columns of its own and one S buffer a tile at head_dim 128 (317 us, of 309);
-// scalar instead of packed arithmetic for the cap (438 us where packed took 403).
+// behind 8000 positions 89 us; prompts of documents with prefix, window and bias
+// 90 us.  A page takes about 1900 cycles: 1000 of the softmax warps' work (two
+// share a sub-partition), 1280 of the tensor cores at head_dim 128 (640 at 64),
+// and the way from P through P V and the next S back to the softmax.  Tried and
+// left out: reading the next page's S while this one's exponentials run (311 us,
+// of 309 then); polynomial and exponentials interleaved 16 keys at a time (272 us,
+// of 246; but 382 of 426 for capped heads of 64); polling instead of suspended
+// waits (the same); scalar instead of packed arithmetic for the cap (438 of 403).
 //
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
 // roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.
@@ -97,20 +109,15 @@ struct ModPrefillCfg {
   static constexpr int kVOff = kRing * kTileBytes;
   static constexpr int kQOff = 2 * kRing * kTileBytes;
   static constexpr int kBarOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kNumBars = 4 * kRing + 8 * kTiles + 4 + 2 * kQBufs + 2;
+  static constexpr int kNumBars = 4 * kRing + 6 * kTiles + 4 + 2 * kQBufs + 2;
   static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr bool kOwnP = D == 64;  // P beside S (else over it)
   static constexpr uint32_t kOCol = 0, kSCol = kTiles * D;
-  // S of (tile t, page i): kSCol + (2 t + i % 2) kPage; P: kPCol + the same kPStride
-  static constexpr uint32_t kPCol = kOwnP ? kSCol + 2 * kTiles * kPage : kSCol;
-  static constexpr uint32_t kPStride = kOwnP ? kPage / 2 : kPage;
+  // S of (tile t, page i): kSCol + (2 t + i % 2) kPage; P, bf16 pairs, over its first half
   static constexpr uint32_t kIdescS = umma_idesc_bf16(128, kPage, 0, 0);
   static constexpr uint32_t kIdescPV = umma_idesc_bf16(128, D, 0, 1);
   static_assert(D == 64 || D == 128, "head_dim");
-  static_assert(kPCol + 3 * kPStride + kPage / 2 <= kTmemCols &&
-                    kSCol + 2 * kTiles * kPage <= kTmemCols,
-                "TMEM columns");
+  static_assert(kSCol + 2 * kTiles * kPage <= kTmemCols, "TMEM columns");
   static_assert(kSmemBytes + 24 * 1024 <= 227 * 1024, "shared memory (dynamic + static)");
 };
 
@@ -150,8 +157,9 @@ enum CapForm { kNoCap, kCapNear, kCapMid, kCapFar };
 __device__ __forceinline__ float2 scaled2(float2 v, float2 add, const ModParams& p) {
   return __ffma2_rn(v, make_float2(p.q_scale_log2, p.q_scale_log2), add);
 }
-__device__ __forceinline__ float2 near2(float2 v, float2 add, const ModParams& p) {
+__device__ __forceinline__ float2 near2(float2 v, float2 add, const ModParams& p, float* most) {
   const float2 u = __fmul2_rn(v, v);
+  if (most) *most = fmax3(*most, u.x, u.y);
   float2 q = __ffma2_rn(make_float2(p.near_q[2], p.near_q[2]), u,
                         make_float2(p.near_q[1], p.near_q[1]));
   q = __ffma2_rn(q, u, make_float2(p.near_q[0], p.near_q[0]));
@@ -168,37 +176,42 @@ __device__ __forceinline__ float2 mid2(float2 v, float2 add, const ModParams& p)
 }
 
 // Usual scores, a cap's near form or none: y = s Q(s^2) + add.
+// With a cap, *most becomes at least s^2.
 template <int KIND>
-__device__ __forceinline__ float2 usual2(float2 v, float2 add, const ModParams& p) {
-  return (KIND & kModCap) ? near2(v, add, p) : scaled2(v, add, p);
+__device__ __forceinline__ float2 usual2(float2 v, float2 add, const ModParams& p, float* most) {
+  return (KIND & kModCap) ? near2(v, add, p, most) : scaled2(v, add, p);
 }
 
-// Any case, for few keys at a time.
+// Any other: scores past a cap's near form, or with the bias of keys on both sides
+// of the query (N of them, the first at rel from it), less m.
 template <int KIND, int N>
 __device__ __forceinline__ void any_scores(float (&s)[N], const ModParams& p, float nslope,
-                                           int form, int rel, float m) {
+                                           int form, float rel, float m) {
+  auto each = [&](auto score) {
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    float2 add = make_float2(-m, -m);
-    if constexpr (KIND & kModBias) {
-      add.x = fmaf(nslope, fabsf((float)(rel + k)), -m);
-      add.y = fmaf(nslope, fabsf((float)(rel + k + 1)), -m);
-    }
-    float2 v = make_float2(s[k], s[k + 1]);
-    if constexpr (KIND & kModCap) {
-      if (form == kCapNear) {
-        v = near2(v, add, p);
-      } else if (form == kCapMid) {
-        v = mid2(v, add, p);
-      } else {
-        v.x = cap_far(v.x, p.cap_in, p.cap_out) + add.x;
-        v.y = cap_far(v.y, p.cap_in, p.cap_out) + add.y;
+    for (int k = 0; k < N; k += 2) {
+      float2 add = make_float2(-m, -m);
+      if constexpr (KIND & kModBias) {
+        add.x = fmaf(nslope, fabsf(rel + (float)k), -m);
+        add.y = fmaf(nslope, fabsf(rel + (float)(k + 1)), -m);
       }
-    } else {
-      v = scaled2(v, add, p);
+      const float2 y = score(make_float2(s[k], s[k + 1]), add);
+      s[k] = y.x;
+      s[k + 1] = y.y;
     }
-    s[k] = v.x;
-    s[k + 1] = v.y;
+  };
+  if constexpr (KIND & kModCap) {
+    if (form == kCapFar)
+      each([&](float2 v, float2 add) {
+        return make_float2(cap_far(v.x, p.cap_in, p.cap_out) + add.x,
+                           cap_far(v.y, p.cap_in, p.cap_out) + add.y);
+      });
+    else if (form == kCapMid)
+      each([&](float2 v, float2 add) { return mid2(v, add, p); });
+    else
+      each([&](float2 v, float2 add) { return near2(v, add, p, nullptr); });
+  } else {
+    each([&](float2 v, float2 add) { return scaled2(v, add, p); });
   }
 }
 
@@ -260,12 +273,15 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
   }
 }
 
-// 8 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+// True for one lane of a converged warp, always the same one.  The compiler knows
+// that what it guards runs in one thread of a warp with uniform control, and keeps
+// the descriptors of MMAs in uniform registers (as `lane == 0` it does not).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // kParts: built for key parts (`parts` units per item, partials to
@@ -305,8 +321,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
   uint64_t* v_empty = v_full + R;          // their P V done
   // [2 tile + (the tile's page) % 2]:
   uint64_t* s_full = v_empty + R;              // S of the page in TMEM
-  uint64_t* s_free = s_full + 2 * C::kTiles;   // S in the warpgroup's registers
-  uint64_t* p_full = s_free + 2 * C::kTiles;   // P in TMEM (O rescaled, V rows zeroed)
+  uint64_t* p_full = s_full + 2 * C::kTiles;   // P in its place (O rescaled)
   uint64_t* o_done = p_full + 2 * C::kTiles;   // P V of the page done
   uint64_t* item_ready = o_done + 2 * C::kTiles;  // [item % 2] descriptor written
   uint64_t* item_free = item_ready + 2;        // [item % 2] read for the last time
@@ -326,8 +341,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
     }
     for (int b = 0; b < 2 * C::kTiles; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], 4);  // the warpgroup's warps
-      mbar_init(&p_full[b], 4);
+      mbar_init(&p_full[b], 4);  // the warpgroup's warps
       mbar_init(&o_done[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -582,93 +596,141 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(&item_free[d]);
       }
       drain(v_full, iv);
-    } else if (warp == C::kMmaWarp || warp == C::kPvWarp) {
-      // ------------------------------------------------------------ issuers
-      if (lane == 0) {
-        const bool is_s = warp == C::kMmaWarp;
-        const uint32_t k_addr = smem_addr(k_slots), v_addr = smem_addr(v_slots);
-        int i = 0;                    // page over all items
-        int it_[C::kTiles] = {0, 0};  // pages that each tile took part in
-        bool issued = false, ok = true;
-        for (int seq = 0; ok; ++seq) {
-          const int d = seq & 1, qb = seq % QB;
-          if (!wait(&item_ready[d], (seq >> 1) & 1)) break;
-          const ModItem& it = items[d];
-          if (!it.valid) break;
-          if (is_s && !wait(&q_full[qb], (seq / QB) & 1)) break;
-          const uint32_t q_addr = smem_addr(q_smem + qb * C::kQBytes);
-          int rs = 0;
-          for (int r = 0; r < it.runs && ok; ++r) {
-            const int first = it.run_pg[r], last = it.run_last[r], re = it.run_end[r];
-            const bool part[2] = {ModItem::takes_part(0, T, rs, re),
-                                  ModItem::takes_part(1, T, rs, re)};
-            rs = re;
-            if (first < 0) continue;
-            for (int pg = first; pg <= last && ok; ++pg, ++i) {  // (their number; order: kBack)
-              const int s = i % R;
-              if (!wait(is_s ? &k_full[s] : &v_full[s], (i / R) & 1)) {
+    } else if (warp == C::kMmaWarp) {
+      // ------------------------------------------------------------ S issuer
+      // (What it and the P V issuer do between a barrier and the products it allows
+      // is on every tile's path.  Both wait as whole warps and issue under
+      // elect_lane: 249 us where one thread of S and lane 0 of P V took 261, and
+      // 473 of 595 at head_dim 64 without cap or bias.)
+      const uint32_t k_addr = smem_addr(k_slots);
+      int i = 0;                    // page over all items
+      int it_[C::kTiles] = {0, 0};  // pages that each tile took part in
+      bool ok = true;
+      for (int seq = 0; ok; ++seq) {
+        const int d = seq & 1, qb = seq % QB;
+        if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) break;
+        const ModItem& it = items[d];
+        if (!it.valid) break;
+        if (!all_ok(wait(&q_full[qb], (seq / QB) & 1))) break;
+        const uint32_t q_addr = smem_addr(q_smem + qb * C::kQBytes);
+        int rs = 0;
+        for (int r = 0; r < it.runs && ok; ++r) {
+          const int first = it.run_pg[r], last = it.run_last[r], re = it.run_end[r];
+          const bool part[2] = {ModItem::takes_part(0, T, rs, re),
+                                ModItem::takes_part(1, T, rs, re)};
+          rs = re;
+          if (first < 0) continue;
+          for (int n = 0; n <= last - first && ok; ++n, ++i) {
+            const int s = i % R;
+            if (!all_ok(wait(&k_full[s], (i / R) & 1))) {
+              ok = false;
+              break;
+            }
+            const uint64_t kd = umma_desc_sw128(k_addr + s * C::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+              if (!part[t]) continue;
+              const int m = it_[t]++, b = 2 * t + (m & 1);
+              // the columns are free: P V of the tile's page before last is done
+              if (m >= 2 && !all_ok(wait(&o_done[b], ((m >> 1) - 1) & 1))) {
                 ok = false;
                 break;
               }
-              if (is_s) {
-                const uint64_t kd = umma_desc_sw128(k_addr + s * C::kTileBytes, 16, 1024);
+              tc_fence_after_sync();
+              const uint64_t qd = umma_desc_sw128(q_addr + t * C::kQTileBytes, 16, 1024);
+              if (elect_lane()) {
 #pragma unroll
-                for (int t = 0; t < C::kTiles; ++t) {
-                  if (!part[t]) continue;
-                  const int n = it_[t], b = 2 * t + (n & 1);
-                  // the columns are free: S of the tile's page before last is
-                  // in registers, or, with P over S, its P V is done
-                  if (n >= 2 &&
-                      !wait(C::kOwnP ? &s_free[b] : &o_done[b], ((n >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after_sync();
-                  const uint64_t qd = umma_desc_sw128(q_addr + t * C::kQTileBytes, 16, 1024);
-#pragma unroll
-                  for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + C::kSCol + b * kPage,
-                              umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
-                              umma_desc_advance(kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32),
-                              C::kIdescS, kk > 0);
-                  issued = true;
-                  umma_commit(&s_full[b]);
-                  it_[t] = n + 1;
-                }
-                if (ok) umma_commit(&k_empty[s]);
-              } else {
-                const uint64_t vd = umma_desc_sw128(v_addr + s * C::kTileBytes, kBoxBytes, 1024);
-#pragma unroll
-                for (int t = 0; t < C::kTiles; ++t) {
-                  if (!part[t]) continue;
-                  const int n = it_[t], b = 2 * t + (n & 1);
-                  if (!wait(&p_full[b], (n >> 1) & 1)) {
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after_sync();
-                  const uint32_t pa = tmem + C::kPCol + b * C::kPStride;
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16_tmem_a(tmem + C::kOCol + t * D, pa + 8 * kk,
-                                     umma_desc_advance(vd, kk * 2048), C::kIdescPV,
-                                     !(pg == first && kk == 0));
-                  issued = true;
-                  umma_commit(&o_done[b]);
-                  it_[t] = n + 1;
-                }
-                if (ok) umma_commit(&v_empty[s]);
+                for (int kk = 0; kk < D / 16; ++kk)
+                  umma_bf16(tmem + C::kSCol + b * kPage,
+                            umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
+                            umma_desc_advance(kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32),
+                            C::kIdescS, kk > 0);
+                umma_commit(&s_full[b]);
               }
             }
+            if (ok && elect_lane()) umma_commit(&k_empty[s]);
           }
-          if (ok && is_s) umma_commit(&q_free[qb]);
-          if (ok) mbar_arrive(&item_free[d]);
         }
-        // every MMA this thread issued completes before TMEM is freed
-        if (issued) {
-          umma_commit(&fin[is_s ? 0 : 1]);
-          mbar_wait_bounded(&fin[is_s ? 0 : 1], 0, p.err);
+        if (ok && elect_lane()) {
+          umma_commit(&q_free[qb]);
+          mbar_arrive(&item_free[d]);
         }
+      }
+      // every MMA this thread issued completes before TMEM is freed
+      if (it_[0] + it_[1] > 0 && elect_lane()) {
+        umma_commit(&fin[0]);
+        mbar_wait_bounded(&fin[0], 0, p.err);
+      }
+    } else if (warp == C::kPvWarp) {
+      // ------------------------------------------------------------ P V issuer
+      // (the whole warp zeroes boundary pages, one lane issues)
+      const uint32_t v_addr = smem_addr(v_slots);
+      int i = 0;                    // page over all items
+      int it_[C::kTiles] = {0, 0};  // pages that each tile took part in
+      bool ok = true;
+      for (int seq = 0; ok; ++seq) {
+        const int d = seq & 1;
+        if (!all_ok(wait(&item_ready[d], (seq >> 1) & 1))) break;
+        const ModItem& it = items[d];
+        if (!it.valid) break;
+        int rs = 0;
+        for (int r = 0; r < it.runs && ok; ++r) {
+          const int first = it.run_pg[r], last = it.run_last[r], re = it.run_end[r];
+          const bool part[2] = {ModItem::takes_part(0, T, rs, re),
+                                ModItem::takes_part(1, T, rs, re)};
+          // keys that the run's rows see (V of the others is zeroed)
+          const int lo = first < 0 ? 0 : it.lo(rs, p.window), hi = it.tok_hi[re - 1];
+          rs = re;
+          if (first < 0) continue;
+          for (int n = 0; n <= last - first && ok; ++n, ++i) {
+            const int s = i % R;
+            if (!all_ok(wait(&v_full[s], (i / R) & 1))) {
+              ok = false;
+              break;
+            }
+            const int pos0 = (kBack ? last - n : first + n) * kPage;
+            const int rlo = lo - pos0, rhi = hi - pos0;
+            if (rlo > 0 || rhi < kPage - 1) {  // a boundary page
+              unsigned char* vt = v_slots + s * C::kTileBytes;
+              for (int e = lane; e < kPage * (D / 8); e += 32) {
+                const int k = e / (D / 8), ch = e % (D / 8);
+                if (k < rlo || k > rhi)
+                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * kBoxBytes + k * 128 +
+                                            (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_shared();  // the zeros are read by the tensor core
+              __syncwarp();
+            }
+            const uint64_t vd = umma_desc_sw128(v_addr + s * C::kTileBytes, kBoxBytes, 1024);
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+              if (!part[t]) continue;
+              const int m = it_[t]++, b = 2 * t + (m & 1);
+              if (!all_ok(wait(&p_full[b], (m >> 1) & 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+              const uint32_t pa = tmem + C::kSCol + b * kPage;
+              if (elect_lane()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_tmem_a(tmem + C::kOCol + t * D, pa + 8 * kk,
+                                   umma_desc_advance(vd, kk * 2048), C::kIdescPV,
+                                   !(n == 0 && kk == 0));
+                umma_commit(&o_done[b]);
+              }
+            }
+            if (ok && elect_lane()) umma_commit(&v_empty[s]);
+          }
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&item_free[d]);
+      }
+      // every MMA this warp issued completes before TMEM is freed
+      if (it_[0] + it_[1] > 0 && elect_lane()) {
+        umma_commit(&fin[1]);
+        mbar_wait_bounded(&fin[1], 0, p.err);
       }
     }
   } else {
@@ -678,7 +740,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_col = lane_base + C::kOCol + t * D;
     constexpr bool kCap = (KIND & kModCap) != 0, kBias = (KIND & kModBias) != 0;
-    int i = 0, gi = 0;  // this tile's pages, all pages (over all items)
+    int i = 0;  // this tile's pages (over all items)
     bool ok = true;
     const int tl = t * T + m / G, g = m % G;  // token of the block, head of the group
     const bool in_tile = m / G < T;
@@ -714,10 +776,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           }
           continue;
         }
-        if (!ModItem::takes_part(t, T, rs, re)) {
-          gi += last - first + 1;
-          continue;
-        }
+        if (!ModItem::takes_part(t, T, rs, re)) continue;
         // keys lo .. hi of this row in these pages; rows of other runs go along
         // behind every key and unmasked (their P and O stay their own and are
         // not stored: masking them would cost the run's pages their fast form)
@@ -735,13 +794,12 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           for (int j = 0; j < 8; ++j)
             step[j] = make_float2(-nslope * (float)(2 * j), -nslope * (float)(2 * j + 1));
         }
-        float m_run = -INFINITY;  // running (lazy) max of the row, log2 units
+        float m_run = p.ref_log2;  // the row's reference (its lazy maximum), log2 units
         float l = 0.f;            // row sum relative to it
-        for (int n = 0; n <= last - first; ++n, ++i, ++gi) {
+        for (int n = 0; n <= last - first; ++n, ++i) {
           const int pg = kBack ? last - n : first + n;
           const int sb = 2 * t + (i & 1);
           const uint32_t s_col = lane_base + C::kSCol + sb * kPage;
-          const uint32_t p_col = lane_base + C::kPCol + sb * C::kPStride;
           if (!all_ok(wait(&s_full[sb], (i >> 1) & 1))) {
             ok = false;
             break;
@@ -749,37 +807,146 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           tc_fence_after_sync();
           const int pos0 = pg * kPage;
           const int k_lo = lo - pos0, k_hi = hi - pos0;  // this row's keys of the page
-          // the usual case (the same for the warp): the bias is linear in the key
-          const bool usual =
+          // The page is tried as a usual one first: a cap's near form or none, a bias
+          // linear in the key, the reference as it is.  Whether that held is known
+          // when the exponentials are; if not for a row of the warp, S, still in
+          // place, is read again and taken in full.
+          const bool linear =
               !ahead || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos);
-
-          auto s_read = [&]() {  // S is in registers: its columns are free
-            if constexpr (C::kOwnP) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&s_free[sb]);
+          float sv[kPage];
+          auto read_s = [&]() {
+#pragma unroll
+            for (int q = 0; q < kPage / 16; ++q)
+              tmem_ld16(s_col + 16 * q, *reinterpret_cast<float(*)[16]>(&sv[16 * q]));
+            tmem_wait_ld();
+          };
+          // Masks go 16 keys at a time, and only where some row of the warp has one:
+          // most boundary pages are cut in one or two of their four blocks.
+          const bool whole = pos0 >= lo_all && pos0 + kPage - 1 <= hi_all;
+          auto mask_to = [&](float value) {
+#pragma unroll
+            for (int q = 0; q < kPage; q += 16)
+              if (pos0 + q < lo_all || pos0 + q + 15 > hi_all) {
+#pragma unroll
+                for (int k = q; k < q + 16; ++k) sv[k] = k >= k_lo && k <= k_hi ? sv[k] : value;
+              }
+          };
+          // Usual scores: less ref, or with a bias each block of 16 against the bias
+          // of its first key, block_bias (then less ref).
+          float most[4];
+          auto usual_scores = [&](float ref) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPage; k += 2) {
+              const float2 y =
+                  usual2<KIND>(make_float2(sv[k], sv[k + 1]),
+                               kBias ? step[k / 2 % 8] : make_float2(-ref, -ref), p,
+                               &most[k / 2 % 4]);
+              sv[k] = y.x;
+              sv[k + 1] = y.y;
             }
           };
-          // The row's reference, raised when this page's maximum mx exceeds it by
-          // the slack (O is then rescaled); P of the page may be written after it.
-          // False: a wait failed.
-          auto settle = [&](float mx) -> bool {
-            // P V of the page before last has read P (P over S: S waited for it).
-            // It also puts the wait below at most one phase ahead.
-            if (C::kOwnP && i >= 2) {
-              if (!all_ok(wait(&o_done[sb], ((i >> 1) - 1) & 1))) return false;
-              tc_fence_after_sync();
+          const float rel = (float)(pos0 - pos);
+          auto block_bias = [&](int q, float ref) {
+            return fmaf(-nslope, rel + (float)(16 * q), -ref);
+          };
+          auto usual_top = [&](float ref) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kPage / 16; ++q)
+              top = fmaxf(top, block_bias(q, ref) +
+                                   row_max(*reinterpret_cast<float(*)[16]>(&sv[16 * q])));
+            return top;
+          };
+          // P = exp2(sv + block's offset) to w; their sum
+          uint32_t w[kPage / 2];
+          auto exps = [&](auto offset) -> float {
+            float2 sum2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kPage; k += 2) {
+              float2 y = make_float2(sv[k], sv[k + 1]);
+              if constexpr (kBias) y = __fadd2_rn(y, offset(k / 16));
+              const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              sum2[k / 2 & 3] = __fadd2_rn(sum2[k / 2 & 3], x);
+              w[k / 2] = pack_bf16x2(x.x, x.y);
             }
-            const bool rises = mx > m_run + kLazyRescaleLog2;
+            const float2 s2 =
+                __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+            return s2.x + s2.y;
+          };
+          bool done = false;
+          if (__builtin_expect(linear && __all_sync(0xffffffffu, !live || m_run != -INFINITY), 1)) {
+            read_s();
+            if (kCap && !whole) mask_to(__int_as_float(0x7fffffff));  // (max passes over NaN)
+            const float ref = m_run == -INFINITY ? 0.f : m_run;
+            usual_scores(ref);
+            const float most2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+            if (!whole) mask_to(-INFINITY);
+            // the largest score less the reference, or a bound of it
+            float top;
+            if constexpr (kBias) {
+              top = usual_top(ref);
+            } else if constexpr (kCap) {
+              top = -ref;  // (a first reference that is never raised: nothing to bound)
+              if (p.slack_log2 < INFINITY)
+                top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
+            } else {
+              top = row_max(sv);
+            }
+            const float sum = exps([&](int q) {
+              const float b = block_bias(q, ref);
+              return make_float2(b, b);
+            });
+            const bool held =
+                !live || (!(top > p.slack_log2) && (!kCap || !(most2 > p.limit_near2)));
+            done = __all_sync(0xffffffffu, held);
+            if (done) l += sum;
+          }
+          if (__builtin_expect(!done, 0)) {
+            read_s();
+            // The cap's form for the warp's largest product, and the page's maximum:
+            // of the products (a score without a bias grows, or falls, with them; max
+            // and min pass over a NaN), or with a bias of the scores.
+            int form = kNoCap;
+            float mx = -INFINITY;
+            if ((kCap || !kBias) && !whole) mask_to(__int_as_float(0x7fffffff));
+            if constexpr (kCap) {
+              const float low = row_min(sv), top = row_max(sv);
+              const float most = live ? fmaxf(fabsf(low), fabsf(top)) : 0.f;
+              form = !__any_sync(0xffffffffu, most > p.limit_near)  ? kCapNear
+                     : !__any_sync(0xffffffffu, most > p.limit_mid) ? kCapMid
+                                                                    : kCapFar;
+              if constexpr (!kBias)
+                mx = fmaxf(one_score<KIND>(top, p, form), one_score<KIND>(low, p, form));
+            } else if constexpr (!kBias) {
+              mx = p.q_scale_log2 * (p.q_scale_log2 > 0.f ? row_max(sv) : row_min(sv));
+            }
+            const bool usual = linear && form <= kCapNear;
+            if constexpr (kBias) {
+              if (usual)
+                usual_scores(0.f);
+              else
+                any_scores<KIND>(sv, p, nslope, form, rel, 0.f);
+              if (!whole) mask_to(-INFINITY);
+              mx = usual ? usual_top(0.f) : row_max(sv);
+            }
+            // the row's reference, raised when the maximum exceeds it by the slack
+            // (O is then rescaled)
             float alpha = 1.f;
-            if (rises) {
+            if (mx > m_run + p.slack_log2) {
               alpha = m_run == -INFINITY ? 1.f : exp2_approx(m_run - mx);
               l *= alpha;  // (0 before the first key)
               m_run = mx;
             }
-            if (__builtin_expect(__any_sync(0xffffffffu, alpha != 1.f), 0)) {
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds the pages before, once P V of the last of them is done
-              if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) return false;
+              if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) {
+                ok = false;
+                break;
+              }
               tc_fence_after_sync();
 #pragma unroll 1
               for (int j = 0; j < D / 16; ++j) {
@@ -791,189 +958,19 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
                 tmem_st16(o_col + 16 * j, ov);
               }
             }
-            return true;
-          };
-
-          // A usual page, its 64 scores in registers.  1: done; 0: the scores are
-          // not all within the cap's near form (nothing changed); -1: a wait failed.
-          auto usual_page = [&]() -> int {
-            // masks 16 keys at a time, and only where some row of the warp has one:
-            // most boundary pages are cut in one or two of their four blocks
-            const bool whole = pos0 >= lo_all && pos0 + kPage - 1 <= hi_all;
-            float sv[kPage];
-            auto mask_to = [&](float value) {
-#pragma unroll
-              for (int q = 0; q < kPage; q += 16)
-                if (pos0 + q < lo_all || pos0 + q + 15 > hi_all) {
-#pragma unroll
-                  for (int k = q; k < q + 16; ++k)
-                    sv[k] = k >= k_lo && k <= k_hi ? sv[k] : value;
-                }
-            };
-#pragma unroll
-            for (int q = 0; q < kPage / 16; ++q)
-              tmem_ld16(s_col + 16 * q, *reinterpret_cast<float(*)[16]>(&sv[16 * q]));
-            tmem_wait_ld();
-            // the page's maximum: of the products (a score without a bias grows,
-            // or falls, with them; max and min pass over a NaN), or with a bias of
-            // the scores
-            float mx = -INFINITY;
-            if constexpr (kCap || !kBias) {
-              if (!whole) mask_to(__int_as_float(0x7fffffff));
-            }
-            if constexpr (kCap) {
-              const float low = row_min(sv), top = row_max(sv);
-              if (!__all_sync(0xffffffffu,
-                              !live || !(fmaxf(fabsf(low), fabsf(top)) > p.limit_near)))
-                return 0;
-              mx = fmaxf(one_score<KIND>(top, p, kCapNear), one_score<KIND>(low, p, kCapNear));
-            }
-            s_read();
-            if constexpr (kBias) {
-              // each block of 16 against the bias of its first key
-#pragma unroll
-              for (int k = 0; k < kPage; k += 2) {
-                const float2 y = usual2<KIND>(make_float2(sv[k], sv[k + 1]), step[k / 2 % 8], p);
-                sv[k] = y.x;
-                sv[k + 1] = y.y;
-              }
-              if (!whole) mask_to(-INFINITY);
-              mx = -INFINITY;
-#pragma unroll
-              for (int q = 0; q < kPage; q += 16)
-                mx = fmaxf(mx, fmaf(-nslope, (float)(pos0 + q - pos),
-                                    row_max(*reinterpret_cast<float(*)[16]>(&sv[q]))));
-            } else if constexpr (!kCap) {
-              mx = p.q_scale_log2 * (p.q_scale_log2 > 0.f ? row_max(sv) : row_min(sv));
-            }
-            if (!settle(mx)) return -1;
             const float ref = m_run == -INFINITY ? 0.f : m_run;
             if constexpr (!kBias) {
-#pragma unroll
-              for (int k = 0; k < kPage; k += 2) {
-                const float2 y =
-                    usual2<KIND>(make_float2(sv[k], sv[k + 1]), make_float2(-ref, -ref), p);
-                sv[k] = y.x;
-                sv[k + 1] = y.y;
-              }
+              any_scores<KIND>(sv, p, nslope, form, 0.f, ref);
               if (!whole) mask_to(-INFINITY);
             }
-            float2 sum2[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int q = 0; q < kPage / 32; ++q) {
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int k = 32 * q + 2 * j;
-                float2 y = make_float2(sv[k], sv[k + 1]);
-                if constexpr (kBias) {
-                  const float b = fmaf(-nslope, (float)(pos0 + k / 16 * 16 - pos), -ref);
-                  y = __fadd2_rn(y, make_float2(b, b));
-                }
-                const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                sum2[j & 3] = __fadd2_rn(sum2[j & 3], x);
-                w[j] = pack_bf16x2(x.x, x.y);
-              }
-              tmem_st16(p_col + 16 * q, w);
-            }
-            const float2 s2 =
-                __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
-            l += s2.x + s2.y;
-            return 1;
-          };
-          int done = 0;
-          if (__builtin_expect(usual, 1)) done = usual_page();
-          if (__builtin_expect(done == 0, 0)) {
-            // Any other page, 16 keys at a time in rolled loops: visible keys past
-            // the query with a bias, scores near their cap.
-            constexpr int kFew = 16;
-            float mx = -INFINITY, mn = INFINITY;
-#pragma unroll 1
-            for (int q = 0; q < kPage; q += kFew) {
-              float sv[kFew];
-              tmem_ld16(s_col + q, sv);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < kFew; ++k)
-                if (q + k >= k_lo && q + k <= k_hi) {
-                  mx = fmaxf(mx, sv[k]);
-                  mn = fminf(mn, sv[k]);
-                }
-            }
-            int form = kNoCap;
-            if constexpr (kCap) {
-              const float most =
-                  !live || mx == -INFINITY ? 0.f : fmaxf(fabsf(mx), fabsf(mn));
-              form = __all_sync(0xffffffffu, most <= p.limit_near)  ? kCapNear
-                     : __all_sync(0xffffffffu, most <= p.limit_mid) ? kCapMid
-                                                                      : kCapFar;
-            }
-            if constexpr (kBias) {
-              mx = -INFINITY;
-#pragma unroll 1
-              for (int q = 0; q < kPage; q += kFew) {
-                float sv[kFew];
-                tmem_ld16(s_col + q, sv);
-                tmem_wait_ld();
-                any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, 0.f);
-#pragma unroll
-                for (int k = 0; k < kFew; ++k)
-                  if (q + k >= k_lo && q + k <= k_hi) mx = fmaxf(mx, sv[k]);
-              }
-            } else if (mx != -INFINITY) {
-              mx = fmaxf(one_score<KIND>(mx, p, form), one_score<KIND>(mn, p, form));
-            }
-            if (!settle(mx)) {
-              done = -1;
-            } else {
-              const float ref = m_run == -INFINITY ? 0.f : m_run;
-#pragma unroll 1
-              for (int q = 0; q < kPage; q += kFew) {
-                float sv[kFew];
-                tmem_ld16(s_col + q, sv);
-                tmem_wait_ld();
-                if (q + kFew == kPage) s_read();
-                any_scores<KIND>(sv, p, nslope, form, pos0 + q - pos, ref);
-                uint32_t w[kFew / 2];
-#pragma unroll
-                for (int j = 0; j < kFew / 2; ++j) {
-                  const int k = q + 2 * j;
-                  const float x = k >= k_lo && k <= k_hi ? exp2_approx(sv[2 * j]) : 0.f;
-                  const float y =
-                      k + 1 >= k_lo && k + 1 <= k_hi ? exp2_approx(sv[2 * j + 1]) : 0.f;
-                  l += x + y;
-                  w[j] = pack_bf16x2(x, y);
-                }
-                tmem_st8(p_col + q / 2, w);
-              }
-            }
+            l += exps([&](int q) {
+              const float b = usual ? block_bias(q, ref) : -ref;
+              return make_float2(b, b);
+            });
           }
-          if (__builtin_expect(done < 0, 0)) {
-            ok = false;
-            break;
-          }
-          // V rows outside the run's key range on a boundary page -> zero (both
-          // tiles' products are issued after this tile's P)
-          if ((pg == first || pg == last) && (t == 0 || !ModItem::takes_part(0, T, rs, re))) {
-            const int rlo = max(it.lo(rs, p.window) - pos0, 0);
-            const int rhi = min(it.tok_hi[re - 1] - pos0, kPage - 1);
-            if (rlo > 0 || rhi < kPage - 1) {
-              if (!all_ok(wait(&v_full[gi % R], (gi / R) & 1))) {
-                ok = false;
-                break;
-              }
-              unsigned char* vt = v_slots + (gi % R) * C::kTileBytes;
-              for (int e = m; e < kPage * (D / 8); e += C::kRows) {
-                const int k = e / (D / 8), ch = e % (D / 8);
-                if (k < rlo || k > rhi)
-                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * kBoxBytes + k * 128 +
-                                            (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_shared();  // the zeros are read by the tensor core
-            }
-          }
+#pragma unroll
+          for (int q = 0; q < kPage / 32; ++q)
+            tmem_st16(s_col + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&w[16 * q]));
           tmem_wait_st();
           tc_fence_before_sync();
           __syncwarp();

@@ -23,6 +23,9 @@ struct ModParams : DecodeParams {
   // near form with the cap and the powers of a folded in, a^2, and the raw
   // scores up to which each form holds (-1: not used)
   float near_q[3], a2, limit_near, limit_mid;
+  // tcgen05 prefill: a row's first reference (log2 units; -inf: its first page's
+  // maximum), and by how much a score may exceed the reference before it is raised
+  float ref_log2, slack_log2, limit_near2;  // (limit_near's square, with its sign)
   const float* slopes;       // [Hq] or nullptr
   const int32_t* first_key;  // [rows] or nullptr
   const int32_t* prefix_len; // [table_rows] or nullptr
