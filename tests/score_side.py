@@ -12,7 +12,10 @@ rounding 2^-23 of it (at most 2^-16 at scores of 2^7), the bf16 head and
 residual 2^-16, the sums' additions (a few hundred of 2^-24 in a row) 2^-16:
 together under 2^-14.  The tcgen05 prefill rounds each weight to bf16 in the
 product with V (half a step, 2^-8 of it), not in the row sums: sum_j p_j |v_j|
-times that more.  The result is rounded to bf16 once: 2^-8 of it."""
+times that more.  The result is rounded to bf16 once: 2^-8 of it, or, below 2^-126,
+where bf16 values are 2^-133 apart, 2^-134.  A weight below 2^-126 of the
+denominator's largest term is no normal fp32 number and may be taken as zero:
+2^-126 sum_j |v_j|."""
 from __future__ import annotations
 
 import numpy as np
@@ -100,7 +103,11 @@ def check(got, batch, q, rows, positions, *, scale, softcap=0.0, what="", rounde
     weight = 2 * d * 2.0 ** -24 * size + softcap * 2.0 ** -20 + far * 2.0 ** -22 + 2.0 ** -14
     if rounded:
         weight = weight + 2.0 ** -9        # (twice the weights' error is taken below)
-    bound = (2 * weight * mass) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(want)
+    bound = (2 * weight * mass) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(want) + 2.0 ** -134
+    group = batch.hq // batch.hkv
+    v_sums = [np.repeat(np.abs(v).sum(axis=1), group, axis=0) for v in batch.v_rows]
+    at_row = [r if 0 <= r < len(v_sums) else 0 for r in rows]
+    bound = bound + 2.0 ** -126 * np.stack([v_sums[r] for r in at_row])
     g = got.double().cpu().numpy()
     assert np.all(np.isfinite(g)), f"{what}: non-finite output"
     excess = np.abs(g - want) - bound

@@ -276,3 +276,80 @@ def test_refusals():
         with pytest.raises(pgd.PgdError) as e:
             call(prefix_len=i32([3]), kernel=kernel)
         assert e.value.status == pgd.EUNSUPPORTED
+
+
+def ramp(b, gains):
+    """Keys of each row times a gain per position (rounded to bf16 again)."""
+    for r, n in enumerate(b.lengths):
+        k = torch.from_numpy(b.k_rows[r]).transpose(0, 1) * torch.as_tensor(gains[:n])[:, None, None]
+        k = k.bfloat16()
+        b.k_rows[r] = k.transpose(0, 1).double().numpy()
+        b.write(b.k_pool, [r] * n, range(n), k.to(DEV))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_AUTO, pgd.KERNEL_PREFILL_UMMA])
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(docs=10000), dict(softcap=50.0), dict(softcap=53.0), dict(softcap=300.0),
+    dict(slopes=-0.05), dict(slopes=0.05), dict(softcap=70.0, slopes=-0.02)], ids=str)
+def test_scores_that_grow(hq, hkv, d, kernel, falling, kw):
+    """Scores that grow, or fall, from page to page by more than a row's reference allows:
+    every page raises it, or (a reference that stays) the caps' forms change on the way."""
+    b = Paged(12, [1100, 700], hq, hkv, d)
+    gains = np.linspace(0.2, 12.0, 1100)
+    ramp(b, gains[::-1].copy() if falling else gains)
+    rows, positions = packed([1020, 640], [80, 60])
+    q = b.queries(140)
+    softcap = kw.get("softcap", 0.0)
+    slopes = torch.full((hq,), kw["slopes"], device=DEV) if "slopes" in kw else None
+    first = positions // kw["docs"] if "docs" in kw else None
+    out = pgd.paged_prefill_attention(
+        q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions), num_kv_heads=hkv,
+        kernel=kernel, softcap=softcap, alibi_slopes=slopes,
+        first_key=None if first is None else i32(first))
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, scale=d ** -0.5, softcap=softcap, slopes=slopes, first=first)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("softcap", [1.0, 50.0, 52.6, 52.8, 100.0, 1000.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_all_scores_at_one_end_of_the_cap(hq, hkv, d, softcap, sign, sinks):
+    """Every score near -cap (or cap): weights far from 1 against a reference that stays;
+    values of 2^20 with them."""
+    b = Paged(13, [300, 65], hq, hkv, d, scale_v=2.0 ** 20)
+    ramp(b, np.ones(300))
+    for r, n in enumerate(b.lengths):
+        k = (torch.from_numpy(b.k_rows[r]).abs() + 0.5).bfloat16()
+        b.k_rows[r] = k.double().numpy()
+        b.write(b.k_pool, [r] * n, range(n), k.transpose(0, 1).to(DEV))
+    rows, positions = packed([200, 0], [100, 65])
+    q = b.queries(165).abs() + 0.25
+    scale = sign * softcap / d                    # products of about 1.3 d: well past the cap
+    s = torch.linspace(-60.0, 60.0, hq, device=DEV) if sinks else None
+    out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                      s, 0, scale, num_kv_heads=hkv, softcap=softcap,
+                                      kernel=pgd.KERNEL_PREFILL_UMMA)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, scale=scale, softcap=softcap, sinks=s)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_one_row_of_nan(kernel):
+    """A token's own NaN (or infinite) query reaches its own outputs only."""
+    b = Paged(14, [300], 16, 2, 64)
+    rows, positions = packed([100], [200])
+    q = b.queries(200)
+    args = (b.k_pool, b.v_pool, b.table, i32(rows), i32(positions))
+    kw = dict(num_kv_heads=2, softcap=9.0, alibi_slopes=torch.full((16,), 0.1, device=DEV),
+              kernel=kernel)
+    want = pgd.paged_prefill_attention(q, *args, **kw)
+    bad = q.clone()
+    bad[77], bad[150, 3] = float("nan"), float("inf")
+    got = pgd.paged_prefill_attention(bad, *args, **kw)
+    same = torch.ones(200, 16, dtype=torch.bool, device=DEV)
+    same[77], same[150, 3] = False, False
+    assert torch.equal(got[same], want[same])
+    assert torch.isnan(got[77]).all()
