@@ -782,12 +782,18 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
             or (free_head is not None and free_head.numel() != 1):
         raise ValueError("inconsistent shapes")
     sizes = (num_tokens, num_tokens, num_tokens, requests + 1, requests, 1)
+    whole = None
     with _on_device(dev):
-        if out is None:  # one allocation, cut into the plan's arrays
+        if out is None:  # one allocation, cut into the plan's arrays after the launch
             if num_tokens < 0:
                 raise ValueError("num_tokens must be >= 0")
-            whole = table.new_empty(3 * num_tokens + 2 * requests + 2)
-            out = PagePlan(*torch.unsafe_split_with_sizes(whole, sizes))
+            whole = torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
+                                device=table.device)
+            at = whole.data_ptr()
+            starts = at + 12 * num_tokens
+            lengths = starts + 4 * (requests + 1)
+            ptrs = (at, at + 4 * num_tokens, at + 8 * num_tokens, starts, lengths,
+                    lengths + 4 * requests)
         else:
             if _check_cuda(*out) != dev:
                 raise ValueError("all tensors must be on one device")
@@ -795,14 +801,15 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
                 _dtype(t, torch.int32, n)
                 if t.shape != (size,):
                     raise ValueError(f"out.{n} must have {size} entries")
-        rows, positions, slots, starts, lengths, head = out
+            ptrs = [t.data_ptr() for t in out]
         rc = load_extension().pgdx_assign_pages(
             requests, width, num_pages, num_tokens, table.data_ptr(), cached.data_ptr(),
             new_tokens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], _ptr(free_head),
-            rows.data_ptr(), positions.data_ptr(), slots.data_ptr(), starts.data_ptr(),
-            lengths.data_ptr(), head.data_ptr(), _stream_handle(stream))
+            *ptrs, _stream_handle(stream))
     if rc != OK:
         raise PgdError(rc, "assign_pages")
+    if whole is not None:
+        out = PagePlan(*torch.unsafe_split_with_sizes(whole, sizes))
     return out
 
 
