@@ -73,10 +73,10 @@
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
-// up to 8192, 2.6e11 operations): 246 us capped, 1064 TFLOP/s (the one-SM kernel
+// up to 8192, 2.6e11 operations): 245 us capped, 1068 TFLOP/s (the one-SM kernel
 // takes 334 us for them without a cap, 569 with the cap built into it); one chunk
-// behind 8000 positions 89 us; prompts of documents with prefix, window and bias
-// 90 us.  A page takes about 1900 cycles: 1000 of the softmax warps' work (two
+// behind 8000 positions 90 us; prompts of documents with prefix, window and bias
+// 89 us.  A page takes about 1900 cycles: 1000 of the softmax warps' work (two
 // share a sub-partition), 1280 of the tensor cores at head_dim 128 (640 at 64),
 // and the way from P through P V and the next S back to the softmax.  Tried and
 // left out: reading the next page's S while this one's exponentials run (311 us,
@@ -796,6 +796,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         }
         float m_run = p.ref_log2;  // the row's reference (its lazy maximum), log2 units
         float l = 0.f;            // row sum relative to it
+        bool begun = p.ref_log2 != -INFINITY;  // every live row of the warp has one
         for (int n = 0; n <= last - first; ++n, ++i) {
           const int pg = kBack ? last - n : first + n;
           const int sb = 2 * t + (i & 1);
@@ -878,10 +879,10 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             return s2.x + s2.y;
           };
           bool done = false;
-          if (__builtin_expect(linear && __all_sync(0xffffffffu, !live || m_run != -INFINITY), 1)) {
+          if (__builtin_expect(linear && begun, 1)) {
             read_s();
             if (kCap && !whole) mask_to(__int_as_float(0x7fffffff));  // (max passes over NaN)
-            const float ref = m_run == -INFINITY ? 0.f : m_run;
+            const float ref = m_run;  // (of a row that is not live, perhaps -inf)
             usual_scores(ref);
             const float most2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
             if (!whole) mask_to(-INFINITY);
@@ -941,6 +942,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               l *= alpha;  // (0 before the first key)
               m_run = mx;
             }
+            begun = __all_sync(0xffffffffu, !live || m_run != -INFINITY);
             if (__any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds the pages before, once P V of the last of them is done
               if (!all_ok(wait(&o_done[sb ^ 1], ((i - 1) >> 1) & 1))) {
