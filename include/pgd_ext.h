@@ -196,6 +196,10 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * in the pools (or written by this step).  opts->kernel: AUTO (PREFILL_UMMA
  * when the tokens average at least 8 a table row, with key parts for few
  * items; else per token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).
+ * PREFILL_UMMA rounds each weight to bf16 once (TENSOR_CORE, per token, carries
+ * its residual too), and with a softcap up to 52 and no bias multiplies V by
+ * weights up to 2^76 before it divides: |V| up to 2^31 stays in range over a
+ * million keys.
  */
 PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
                                const void* q, const void* k_new, const void* v_new, void* k_pool,
