@@ -156,7 +156,9 @@ PGD_API int pgdx_rotary_append(const pgd_dims* dims, const pgdx_rotary* rotary, 
  *   x_j = softcap * tanh(scale q . k_j / softcap)   (softcap > 0; else scale q . k_j)
  *         - alibi_slopes[h] * |n - j|               (alibi_slopes not NULL)
  * for the keys j with lo <= j <= hi, where hi = max(n, prefix_len - 1) and
- * lo = max(0, first_key, n - window + 1 with a window).  The sinks join the
+ * lo = max(0, first_key, n - window + 1 with a window).  A softcap above 2^50 |scale|
+ * is refused (PGD_EUNSUPPORTED), one so small that scale / softcap overflows or
+ * above 2^126 too (PGD_EINVAL); slopes are finite and at most 2^90.  The sinks join the
  * denominator as they are, neither capped nor biased.  A token that sees no
  * key (first_key > hi) gives zeros.
  * K may hold anything at positions that a token does not see.  So may V, except

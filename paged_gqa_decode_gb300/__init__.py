@@ -206,6 +206,14 @@ def _on_device(index: int):
     return _no_switch if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
+def _used_on(t: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor:
+    """A tensor made here for a call on `stream`: its memory is not handed out again
+    before the call is done with it, whatever happens to the tensor."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -383,12 +391,12 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
     lib = load_library()
     with _on_device(dev):
         if out is None:
-            out = torch.empty_like(q)
+            out = _used_on(torch.empty_like(q), stream)
         elif out.shape != q.shape or out.dtype != torch.bfloat16:
             raise ValueError("out must be bf16 shaped like q")
         if workspace is None:  # (one that is given is checked by the call)
             need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
         tail = (_ptr(table), _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                 ctypes.byref(opts), _stream_handle(stream))
@@ -565,12 +573,12 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
     lib = load_library()
     with _on_device(dev):
         if out is None:
-            out = torch.empty_like(q)
+            out = _used_on(torch.empty_like(q), stream)
         elif out.shape != q.shape or out.dtype != torch.bfloat16:
             raise ValueError("out must be bf16 shaped like q")
         if workspace is None:  # (one that is given is checked by the call)
             need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
         ws = (_ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
               ctypes.byref(opts), _stream_handle(stream))
         tail = (_ptr(table), _ptr(rows), _ptr(positions), _ptr(sinks), int(window),
@@ -694,10 +702,10 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
     lib = load_library()
     with _on_device(dev):
         if out is None:
-            out = torch.empty_like(q)
+            out = _used_on(torch.empty_like(q), stream)
         if workspace is None:  # (one that is given is checked by the call)
             need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
         tail = (None, _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                 ctypes.byref(opts), _stream_handle(stream))
@@ -787,8 +795,8 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
         if out is None:  # one allocation, cut into the plan's arrays after the launch
             if num_tokens < 0:
                 raise ValueError("num_tokens must be >= 0")
-            whole = torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
-                                device=table.device)
+            whole = _used_on(torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
+                                         device=table.device), stream)
             at = whole.data_ptr()
             starts = at + 12 * num_tokens
             lengths = starts + 4 * (requests + 1)
@@ -909,7 +917,7 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
                      max_pages_per_row=width, layout=layout)
     with _on_device(dev):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            q_out = _used_on(torch.empty(q.shape, dtype=torch.bfloat16, device=dev), stream)
         rc = load_extension().pgdx_rotary_append(
             ctypes.byref(dims), ctypes.byref(rotary.plan), _ptr(q),
             0 if q is None else _token_stride(q, "q"), _ptr(q_out), _ptr(k_new),

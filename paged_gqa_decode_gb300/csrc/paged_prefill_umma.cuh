@@ -1147,7 +1147,7 @@ __global__ void __launch_bounds__(128) prefill_part_combine_kernel(const DecodeP
   bool covered = true;
   for (int s = 0; s < parts; ++s) {
     const float ms = part_ml[2 * (u0 + s)], ls = part_ml[2 * (u0 + s) + 1];
-    covered = covered && ls >= 0.f;
+    covered = covered && !(ls < 0.f);  // (NaN: the row's own, written below)
     mx = fmaxf(mx, ms);
   }
   if (!covered) return;

@@ -226,6 +226,14 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   if (asked != PGD_KERNEL_AUTO && asked != PGD_KERNEL_TENSOR_CORE &&
       asked != PGD_KERNEL_PREFILL_UMMA)
     return PGD_EUNSUPPORTED;
+  if (!std::isfinite(scale)) return PGD_EINVAL;
+  const bool capped = score->softcap > 0.f && scale != 0.f;  // a zero score is its own cap
+  if (capped) {
+    const float ratio = std::fabs(scale / score->softcap);
+    // (a cap that far above the scores: cap_far's error of 2^-21 of it swamps them)
+    if (ratio < 0x1p-50f) return PGD_EUNSUPPORTED;
+    if (!std::isfinite(ratio) || score->softcap > 0x1p126f) return PGD_EINVAL;
+  }
   if (dims->rows == 0) return PGD_OK;
   DeviceInfo* dev = nullptr;
   Plan pl;
@@ -234,21 +242,18 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
                               window, scale, out, workspace, workspace_size, opts, k_new, v_new,
                               &dev, &pl, &p)) != PGD_OK)
     return rc;
-  const bool capped = score->softcap > 0.f && scale != 0.f;  // a zero score is its own cap
   p.cap_in = capped ? scale / score->softcap : 0.f;
   p.cap_out = capped ? (float)((double)score->softcap * 1.4426950408889634) : 0.f;
-  if (capped && (p.cap_in == 0.f || !std::isfinite(p.cap_in))) return PGD_EINVAL;
-  // the forms fold powers of a into their coefficients: where those would leave
-  // the normal range, cap_far serves all scores
   const float a = std::fabs(p.cap_in), a2 = a * a, c = p.q_scale_log2;
-  const bool folds = a >= 0x1p-16f && a <= 0x1p16f && std::fabs(c) >= 0x1p-40f &&
-                     std::fabs(c) <= 0x1p40f;
   p.near_q[0] = kNear0 * c;
   p.near_q[1] = kNear1 * c * a2;
   p.near_q[2] = kNear2 * c * a2 * a2;
   p.a2 = a2;
-  p.limit_near = folds ? kTanhNear / a : -1.f;
-  p.limit_mid = folds ? kTanhMid / a : -1.f;
+  // The prefill's forms fold powers of a into their coefficients: each serves only
+  // while those are normal numbers.
+  const auto normal = [](float x) { return std::fabs(x) >= 0x1p-120f && std::fabs(x) <= 0x1p120f; };
+  p.limit_near = normal(p.near_q[2]) && normal(c) ? kTanhNear / a : -1.f;
+  p.limit_mid = normal(a2) ? kTanhMid / a : -1.f;
   p.limit_near2 = p.limit_near * fabsf(p.limit_near);
   // Capped scores without a bias stay within the cap, cap_out in log2 units: up
   // to 76 the prefill takes weights 2^score against a reference of 0 (2^96 for

@@ -244,6 +244,14 @@ def test_attention_refuses_the_other_calls_kernels(ext):
     assert _attend(ext, False, opts=dict(kernel=pgd.KERNEL_PREFILL_UMMA)) == pgd.EINVAL
 
 
+@pytest.mark.parametrize("prefill", [False, True])
+def test_attention_refuses_caps_out_of_range(ext, prefill):
+    assert _attend(ext, prefill, score=dict(softcap=1e16)) == pgd.EUNSUPPORTED
+    assert _attend(ext, prefill, score=dict(softcap=3e38), scale=1e-30) == pgd.EUNSUPPORTED
+    assert _attend(ext, prefill, score=dict(softcap=1e-30), scale=1e10) == pgd.EINVAL
+    assert _attend(ext, prefill, score=dict(softcap=3e38), scale=1e30) == pgd.EINVAL
+
+
 def test_decode_refuses_a_prefix_and_prefill_a_missing_map(ext):
     assert _attend(ext, False, score=dict(prefix_len=("at", 0))) == pgd.EINVAL
     assert _attend(ext, True, score=dict(prefix_len=("at", 2))) == pgd.EINVAL

@@ -248,3 +248,14 @@ def test_refusals():
     with pytest.raises(pgd.PgdError) as e:
         call(softcap=5.0, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == pgd.EWORKSPACE
+
+
+@pytest.mark.parametrize("softcap", [1e4, 1e6, 4e8, 1e12])
+def test_a_cap_far_above_the_scores(softcap):
+    """Scores up to s differ from uncapped ones by s^3 / (3 softcap^2): here by less than 1e-6."""
+    b = Paged(21, [300, 65], 8, 2, 64)
+    q = b.queries(2)
+    out = pgd.paged_decode_attention(q, b.k_pool, b.v_pool, b.table, i32([299, 64]),
+                                     num_kv_heads=2, softcap=softcap)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, [0, 1], [299, 64], scale=0.125)

@@ -353,3 +353,50 @@ def test_one_row_of_nan(kernel):
     same[77], same[150, 3] = False, False
     assert torch.equal(got[same], want[same])
     assert torch.isnan(got[77]).all()
+
+
+def test_a_nan_row_in_key_parts():
+    """As above where the keys are cut into parts: the row's outputs are NaN, not left over."""
+    b = Paged(15, [2570], 4, 1, 128)
+    rows, positions = packed([2500], [70])
+    q = b.queries(70)
+    q[33] = float("nan")
+    out = torch.full_like(q, 7.0)
+    pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                num_kv_heads=1, softcap=20.0, out=out)
+    assert pgd.get_device_error() == pgd.OK
+    good = np.r_[0:33, 34:70]
+    check(out[good], b, q[good], rows[good], positions[good], scale=128 ** -0.5, softcap=20.0)
+    assert torch.isnan(out[33]).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap", [1e4, 1e6, 4e8, 1e12])
+def test_a_cap_far_above_the_scores(kernel, d, softcap):
+    """Scores up to s differ from uncapped ones by s^3 / (3 softcap^2): here by less than 1e-6."""
+    b = Paged(16, [300, 65], 8, 2, d)
+    rows, positions = packed([200, 0], [100, 65])
+    q = b.queries(165)
+    out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                      num_kv_heads=2, softcap=softcap, kernel=kernel)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, kernel=kernel, scale=d ** -0.5)
+
+
+def test_scratch_on_a_side_stream():
+    """A call's own workspace is not handed out while the call runs on another stream."""
+    b = Paged(17, [3000], 8, 2, 64)
+    rows, positions = packed([2900], [100])
+    q = b.queries(100)
+    args = (b.k_pool, b.v_pool, b.table, i32(rows), i32(positions))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(pgd.paged_prefill_attention(q, *args, num_kv_heads=2, softcap=9.0, stream=side))
+        for size in (1 << 20, 1 << 22, 1 << 23):          # (would take the block if it were free)
+            torch.full((size,), float("nan"), device=DEV)
+    torch.cuda.synchronize()
+    check(outs[0], b, q, rows, positions, scale=0.125, softcap=9.0)
+    assert all(torch.equal(o, outs[0]) for o in outs)

@@ -158,3 +158,60 @@ def test_decode_steps_after_a_prompt():
         s.lengths.copy_(s.plan.lengths)
         s.head.copy_(s.plan.free_head)
         s.expect([1, 1, 1])
+
+
+def test_a_pool_past_32_bits():
+    """Pages whose values lie past 2^31 of the pools (4.7 GB each): appended, decoded, and
+    read by a prompt; pools are left uninitialised but for the row's pages."""
+    hq, hkv, d, pages = 32, 8, 128, 36000
+    k_pool = torch.empty(pages, hkv, 64, d, dtype=torch.bfloat16, device=DEV)
+    v_pool = torch.empty_like(k_pool)
+    table = i32([[pages - 1, 3, pages - 3]])
+    gen = torch.Generator().manual_seed(5)
+    n = 170
+    x = torch.randn(n, hq + 2 * hkv, d, generator=gen).bfloat16().to(DEV)
+    rotary = pgd.Rotary(d, 1e4)
+    pos, rows = i32(np.arange(n)), i32(np.zeros(n))
+    q = pgd.rotary_append_paged(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, k_pool, v_pool,
+                                rotary=rotary, table=table, rows=rows)
+    out = pgd.paged_prefill_attention(q, k_pool, v_pool, table, rows, pos, num_kv_heads=hkv,
+                                      softcap=30.0)
+    one = pgd.paged_decode_attention(q[-1:].contiguous(), k_pool, v_pool, table, i32([n - 1]),
+                                     num_kv_heads=hkv, softcap=30.0)
+    assert pgd.get_device_error() == pgd.OK
+    # the same in a small pool
+    small = (torch.empty(4, hkv, 64, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k2, v2 = small
+    t2 = i32([[2, 0, 1]])
+    q2 = pgd.rotary_append_paged(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, k2, v2,
+                                 rotary=rotary, table=t2, rows=rows)
+    out2 = pgd.paged_prefill_attention(q2, k2, v2, t2, rows, pos, num_kv_heads=hkv, softcap=30.0)
+    one2 = pgd.paged_decode_attention(q2[-1:].contiguous(), k2, v2, t2, i32([n - 1]),
+                                      num_kv_heads=hkv, softcap=30.0)
+    assert torch.equal(q, q2) and torch.equal(out, out2) and torch.equal(one, one2)
+    assert torch.equal(k_pool[pages - 1], k2[2]) and torch.equal(v_pool[pages - 3, :, :42],
+                                                                 v2[1, :, :42])
+
+
+def test_two_calls_at_once():
+    """Two steps on two streams, each with tensors of its own, against each alone."""
+    def make(seed):
+        s = Serving(16, 2, 64, requests=2, width=20, pages=48, tokens=900, kw=dict(softcap=25.0),
+                    seed=seed)
+        s.feed([500, 380])
+        return s
+    alone = make(1), make(2)
+    for s in alone:
+        s.enqueue()
+    torch.cuda.synchronize()
+    both = make(1), make(2)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s, stream in zip(both, streams):
+        with torch.cuda.stream(stream):
+            s.enqueue()
+    torch.cuda.synchronize()
+    assert pgd.get_device_error() == pgd.OK
+    for a, b in zip(alone, both):
+        assert torch.equal(a.out, b.out) and torch.equal(a.table, b.table)
+        b.expect([500, 380])
