@@ -889,23 +889,33 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             return s2.x + s2.y;
           };
           bool done = false;
-          // Capped heads of 64, pages without masks: block by block, the polynomial of
-          // one under the exponentials of the one before (375 us, of 425 with all of
-          // the page's polynomials first; heads of 128 take 272 so, of 246, and with a
-          // bias 536 of 518).
-          constexpr bool kInterleaved = D == 64 && KIND == kModCap;
-          if (kInterleaved && whole && begun) {
+          // Capped scores have a stretch of code of their own for pages without masks
+          // (one chunk: 83 us, of 90; with a bias it costs more instruction fetches
+          // than it saves, 98 of 89 us for prompts of documents).  At head_dim 64 it
+          // goes block by block, the polynomial of one under the exponentials of the
+          // one before (358 us, of 425); at 128 all polynomials go first (241 us, of 274:
+          // the two warps of a sub-partition then share its pipes better).
+          constexpr bool kStraight = KIND == kModCap;
+          if (kStraight && whole && begun) {
             read_s();
             const float ref = m_run;
+            if constexpr (D == 64) {
 #pragma unroll
-            for (int q = 0; q < kPage / 16; ++q) {
-              usual_block(q, ref);
-              exp_block(q, 0.f);
+              for (int q = 0; q < kPage / 16; ++q) {
+                usual_block(q, ref);
+                exp_block(q, 0.f);
+              }
+            } else {
+              usual_scores(ref);
             }
             const float most2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-            float top = -ref;
+            float top = -ref;  // (a first reference that is never raised: nothing to bound)
             if (p.slack_log2 < INFINITY)
               top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
+            if constexpr (D == 128) {
+#pragma unroll
+              for (int q = 0; q < kPage / 16; ++q) exp_block(q, 0.f);
+            }
             const bool held = !live || (!(top > p.slack_log2) && !(most2 > p.limit_near2));
             done = __all_sync(0xffffffffu, held);
             if (done) l += page_sum();
@@ -921,7 +931,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             if constexpr (kBias) {
               top = usual_top(ref);
             } else if constexpr (kCap) {
-              top = -ref;  // (a first reference that is never raised: nothing to bound)
+              top = -ref;  // (as above)
               if (p.slack_log2 < INFINITY)
                 top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
             } else {
