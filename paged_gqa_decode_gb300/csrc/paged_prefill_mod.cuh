@@ -73,15 +73,16 @@
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
-// up to 8192, 2.6e11 operations): 245 us capped, 1068 TFLOP/s (the one-SM kernel
-// takes 334 us for them without a cap, 569 with the cap built into it); one chunk
-// behind 8000 positions 90 us; prompts of documents with prefix, window and bias
+// up to 8192, 2.6e11 operations): 241 us capped, 1084 TFLOP/s, 231 without a cap,
+// 276 with cap and bias (the one-SM kernel takes 334 us without a cap, 569 with
+// the cap built into it); 64 / 8 heads of 64: 358 capped, 299 without.  One chunk
+// behind 8000 positions 83 us; prompts of documents with prefix, window and bias
 // 89 us.  A page takes about 1900 cycles: 1000 of the softmax warps' work (two
 // share a sub-partition), 1280 of the tensor cores at head_dim 128 (640 at 64),
 // and the way from P through P V and the next S back to the softmax.  Tried and
 // left out: reading the next page's S while this one's exponentials run (311 us,
-// of 309 then); polynomial and exponentials interleaved 16 keys at a time (272 us,
-// of 246; but 382 of 426 for capped heads of 64); polling instead of suspended
+// of 309 then); a first reference from the raw products instead of the full path
+// on a run's first page (252 of 246, 106 of 89); polling instead of suspended
 // waits (the same); scalar instead of packed arithmetic for the cap (438 of 403).
 //
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
