@@ -19,6 +19,8 @@ namespace pgd {
 // of a place or page by binary search.  The places are shared out once for the
 // whole pass, so consecutive threads write consecutive tokens.  Sums are 64-bit
 // (the lengths are the caller's; only their clipped values are stored).
+// Bound by latency: 64 requests of a token each take 5.8 us, 500 with 27 008
+// tokens 6.5 us, 4099 with 131 072 tokens 10.7 us (1.7 MB, 0.25 us of bytes).
 constexpr int kAssignThreads = 1024;
 constexpr int kAssignItems = 4;
 constexpr int kAssignChunk = kAssignThreads * kAssignItems;
@@ -258,7 +260,10 @@ __device__ __forceinline__ void turn_adjacent(uint32_t* w, const float4& c, cons
 // head, as all of v's do.  A thread's units are a multiple of D / 16 apart, so
 // it needs the same eight frequencies for all of them.  Bound by memory: a
 // thread has its (nearly always only) unit in flight while the token's
-// position, slot and angles are found.
+// position, slot and angles are found.  4096 tokens of 32 / 8 heads of 128 take
+// 19.5 us (101 MB, 5.1 TB/s; 25.5 us with the values loaded after the position),
+// 16 001 out of a fused projection of 64 / 8 heads of 64 52.2 us (328 MB, 6.3 TB/s;
+// 83.5 us so).
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(512, 4) rotary_append_kernel(const RotaryParams p) {
   constexpr int kUnits = D / 16;

@@ -187,7 +187,7 @@ def _attend(ext, prefill, dims=None, score=None, **kw):
     at = (ctypes.addressof(buf) + 15) & ~15
     s = dict(softcap=30.0, alibi_slopes=None, first_key=None, prefix_len=None)
     s.update({k: (at + v[1] if isinstance(v, tuple) else v) for k, v in (score or {}).items()})
-    args = dict(q=at, k_new=None, v_new=None, k_pool=at + 1024, v_pool=at + 2048, table=at + 3072)
+    args = dict(q=at, k_new=None, v_new=None, k_pool=at + 1024, v_pool=at + 2048, table=at + 3136)
     if prefill:
         args["rows"] = at + 3200
     args.update(positions=at + 3300, sinks=None, window=0, scale=0.125, out=at + 4096,
