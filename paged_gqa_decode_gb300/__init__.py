@@ -186,14 +186,20 @@ def status_string(status: int) -> str:
     return load_library().pgd_status_string(status).decode()
 
 
+# A small call's kernel runs for a few microseconds, and its checks here cost as
+# much: these go straight to what torch.cuda's functions call (CUDA tensors
+# exist by then, so CUDA is initialised).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
-def _stream_handle(stream: torch.cuda.Stream | None) -> int:
+def _stream_handle(stream: torch.cuda.Stream | None, device: int | None = None) -> int:
+    """`device`: the current one, where the caller knows it."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:  # the current stream's handle, without a Stream object for it
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -224,14 +230,15 @@ def _check_cuda(*tensors: torch.Tensor | None) -> int | None:
     device = None
     for t in tensors:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError("paged_gqa_decode_gb300 runs on CUDA tensors only")
+            index = t.get_device()
+            if index != device:
+                if not t.is_cuda:
+                    raise ValueError("paged_gqa_decode_gb300 runs on CUDA tensors only")
+                if device is not None:
+                    raise ValueError("all tensors must be on one device")
+                device = index
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
-            if device is None:
-                device = t.get_device()
-            elif t.get_device() != device:
-                raise ValueError("all tensors must be on one device")
     return device
 
 
@@ -244,6 +251,31 @@ def make_dims(*, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int, 
               max_pages_per_row: int, layout: int = PAGE_MAJOR) -> Dims:
     return Dims(rows, num_q_heads, num_kv_heads, head_dim, PAGE_SIZE, num_pages,
                 max_pages_per_row, layout)
+
+
+_dims_kept: dict[tuple, Dims] = {}
+_opts_kept: dict[tuple, DecodeOptions] = {}
+
+
+def _dims_of(*sizes: int) -> Dims:
+    """make_dims of (rows, q heads, kv heads, head_dim, pages, max pages per row, layout), the
+    struct kept for the next call of these sizes (it is only read)."""
+    dims = _dims_kept.get(sizes)
+    if dims is None:
+        if len(_dims_kept) >= 1024:
+            _dims_kept.clear()
+        dims = _dims_kept[sizes] = Dims(*sizes[:4], PAGE_SIZE, *sizes[4:])
+    return dims
+
+
+def _opts_of(pages_per_split: int, kernel: int) -> DecodeOptions:
+    key = (pages_per_split, kernel)
+    opts = _opts_kept.get(key)
+    if opts is None:
+        if len(_opts_kept) >= 64:
+            _opts_kept.clear()
+        opts = _opts_kept[key] = DecodeOptions(pages_per_split, kernel)
+    return opts
 
 
 def _pool_pages(pool: torch.Tensor, kv_heads: int, head_dim: int) -> int:
@@ -350,13 +382,12 @@ def _check_score(score, dev, rows, hq, table_rows) -> Score:
     softcap, slopes, first_key, prefix_len = score
     if not math.isfinite(softcap) or softcap < 0.0:
         raise ValueError("softcap must be finite and >= 0 (0: none)")
-    other = _check_cuda(slopes, first_key, prefix_len)
-    if other is not None and other != dev:
-        raise ValueError("all tensors must be on one device")
-    for t, n, dtype, size in ((slopes, "alibi_slopes", torch.float32, hq),
-                              (first_key, "first_key", torch.int32, rows),
-                              (prefix_len, "prefix_len", torch.int32, table_rows)):
+    for t, n, dtype, size in ((slopes, "alibi_slopes", _F32, hq),
+                              (first_key, "first_key", _I32, rows),
+                              (prefix_len, "prefix_len", _I32, table_rows)):
         if t is not None:
+            if _check_cuda(t) != dev:
+                raise ValueError("all tensors must be on one device")
             _dtype(t, dtype, n)
             if t.shape != (size,):
                 raise ValueError(f"{n} must have {size} entries")
@@ -366,11 +397,18 @@ def _check_score(score, dev, rows, hq, table_rows) -> Score:
 def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
             num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream, score=None):
     dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, out, workspace)
-    _dtype(q, torch.bfloat16, "q")
-    _dtype(k_pool, torch.bfloat16, "k_pool")
-    _dtype(v_pool, torch.bfloat16, "v_pool")
-    _dtype(table, torch.int32, "table")
-    _dtype(positions, torch.int32, "positions")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
+                           num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
+                           score)
+    if not (q.dtype is k_pool.dtype is v_pool.dtype is _BF16
+            and table.dtype is positions.dtype is _I32):
+        _dtype(q, torch.bfloat16, "q")
+        _dtype(k_pool, torch.bfloat16, "k_pool")
+        _dtype(v_pool, torch.bfloat16, "v_pool")
+        _dtype(table, torch.int32, "table")
+        _dtype(positions, torch.int32, "positions")
     if sinks is not None:
         _dtype(sinks, torch.float32, "sinks")
     rows, hq, d = q.shape
@@ -384,36 +422,34 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
             raise ValueError("k_new and v_new must be [R, Hkv, D]")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dims = make_dims(rows=rows, num_q_heads=hq, num_kv_heads=num_kv_heads, head_dim=d,
-                     num_pages=_pool_pages(k_pool, num_kv_heads, d),
-                     max_pages_per_row=table.shape[1], layout=layout)
-    opts = DecodeOptions(pages_per_split, kernel)
+    dims = ctypes.byref(_dims_of(rows, hq, num_kv_heads, d, _pool_pages(k_pool, num_kv_heads, d),
+                                 table.shape[1], layout))
+    opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
-    with _on_device(dev):
-        if out is None:
-            out = _used_on(torch.empty_like(q), stream)
-        elif out.shape != q.shape or out.dtype != torch.bfloat16:
-            raise ValueError("out must be bf16 shaped like q")
-        if workspace is None:  # (one that is given is checked by the call)
-            need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
-        tail = (_ptr(table), _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
-                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                ctypes.byref(opts), _stream_handle(stream))
-        if score is not None:
-            mod = _check_score(score, dev, rows, hq, rows)
-            rc = load_extension().pgdx_paged_decode(
-                ctypes.byref(dims), ctypes.byref(mod), _ptr(q), _ptr(k_new), _ptr(v_new),
-                _ptr(k_pool), _ptr(v_pool), *tail)
-            what = "paged_decode_attention" if k_new is None else "paged_decode_step"
-        elif k_new is None:
-            rc = lib.pgd_paged_decode_attention(ctypes.byref(dims), _ptr(q), _ptr(k_pool),
-                                                _ptr(v_pool), *tail)
-            what = "paged_decode_attention"
-        else:
-            rc = lib.pgd_paged_decode_step(ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                           _ptr(k_pool), _ptr(v_pool), *tail)
-            what = "paged_decode_step"
+    if out is None:
+        out = _used_on(torch.empty_like(q), stream)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16 shaped like q")
+    if workspace is None:  # (one that is given is checked by the call)
+        need = lib.pgd_paged_decode_workspace_bytes(dims, opts)
+        workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+    tail = (table.data_ptr(), positions.data_ptr(), _ptr(sinks), int(window), float(scale),
+            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, opts,
+            _stream_handle(stream, dev))
+    if score is not None:
+        mod = _check_score(score, dev, rows, hq, rows)
+        rc = load_extension().pgdx_paged_decode(
+            dims, ctypes.byref(mod), q.data_ptr(), _ptr(k_new), _ptr(v_new), k_pool.data_ptr(),
+            v_pool.data_ptr(), *tail)
+        what = "paged_decode_attention" if k_new is None else "paged_decode_step"
+    elif k_new is None:
+        rc = lib.pgd_paged_decode_attention(dims, q.data_ptr(), k_pool.data_ptr(),
+                                            v_pool.data_ptr(), *tail)
+        what = "paged_decode_attention"
+    else:
+        rc = lib.pgd_paged_decode_step(dims, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                       k_pool.data_ptr(), v_pool.data_ptr(), *tail)
+        what = "paged_decode_step"
     if rc != OK:
         raise PgdError(rc, what)
     return out
@@ -545,12 +581,19 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
     step = k_new is not None
     dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, out,
                       workspace)
-    _dtype(q, torch.bfloat16, "q")
-    _dtype(k_pool, torch.bfloat16, "k_pool")
-    _dtype(v_pool, torch.bfloat16, "v_pool")
-    _dtype(table, torch.int32, "table")
-    _dtype(rows, torch.int32, "rows")
-    _dtype(positions, torch.int32, "positions")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, window,
+                            scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,
+                            stream, score)
+    if not (q.dtype is k_pool.dtype is v_pool.dtype is _BF16
+            and table.dtype is rows.dtype is positions.dtype is _I32):
+        _dtype(q, torch.bfloat16, "q")
+        _dtype(k_pool, torch.bfloat16, "k_pool")
+        _dtype(v_pool, torch.bfloat16, "v_pool")
+        _dtype(table, torch.int32, "table")
+        _dtype(rows, torch.int32, "rows")
+        _dtype(positions, torch.int32, "positions")
     if sinks is not None:
         _dtype(sinks, torch.float32, "sinks")
     tokens, hq, d = q.shape
@@ -566,35 +609,33 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
             raise ValueError("k_new and v_new are bf16 [P, Hkv, D]")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dims = make_dims(rows=tokens, num_q_heads=hq, num_kv_heads=num_kv_heads, head_dim=d,
-                     num_pages=_pool_pages(k_pool, num_kv_heads, d),
-                     max_pages_per_row=table.shape[1], layout=layout)
-    opts = DecodeOptions(pages_per_split, kernel)
+    table_rows = table.shape[0]
+    dims = ctypes.byref(_dims_of(tokens, hq, num_kv_heads, d,
+                                 _pool_pages(k_pool, num_kv_heads, d), table.shape[1], layout))
+    opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
-    with _on_device(dev):
-        if out is None:
-            out = _used_on(torch.empty_like(q), stream)
-        elif out.shape != q.shape or out.dtype != torch.bfloat16:
-            raise ValueError("out must be bf16 shaped like q")
-        if workspace is None:  # (one that is given is checked by the call)
-            need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
-        ws = (_ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-              ctypes.byref(opts), _stream_handle(stream))
-        tail = (_ptr(table), _ptr(rows), _ptr(positions), _ptr(sinks), int(window),
-                float(scale))
-        if score is not None:
-            mod = _check_score(score, dev, tokens, hq, table.shape[0])
-            rc = load_extension().pgdx_paged_prefill(
-                ctypes.byref(dims), table.shape[0], ctypes.byref(mod), _ptr(q), _ptr(k_new),
-                _ptr(v_new), _ptr(k_pool), _ptr(v_pool), *tail, *ws)
-        elif step:
-            rc = lib.pgd_paged_prefill_step(ctypes.byref(dims), table.shape[0], _ptr(q),
-                                            _ptr(k_new), _ptr(v_new), _ptr(k_pool),
-                                            _ptr(v_pool), *tail, *ws)
-        else:
-            rc = lib.pgd_paged_prefill_attention(ctypes.byref(dims), table.shape[0], _ptr(q),
-                                                 _ptr(k_pool), _ptr(v_pool), *tail, *ws)
+    if out is None:
+        out = _used_on(torch.empty_like(q), stream)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16 shaped like q")
+    if workspace is None:  # (one that is given is checked by the call)
+        need = lib.pgd_paged_decode_workspace_bytes(dims, opts)
+        workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+    tail = (table.data_ptr(), rows.data_ptr(), positions.data_ptr(), _ptr(sinks), int(window),
+            float(scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, opts,
+            _stream_handle(stream, dev))
+    if score is not None:
+        mod = _check_score(score, dev, tokens, hq, table_rows)
+        rc = load_extension().pgdx_paged_prefill(
+            dims, table_rows, ctypes.byref(mod), q.data_ptr(), _ptr(k_new), _ptr(v_new),
+            k_pool.data_ptr(), v_pool.data_ptr(), *tail)
+    elif step:
+        rc = lib.pgd_paged_prefill_step(dims, table_rows, q.data_ptr(), k_new.data_ptr(),
+                                        v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                        *tail)
+    else:
+        rc = lib.pgd_paged_prefill_attention(dims, table_rows, q.data_ptr(), k_pool.data_ptr(),
+                                             v_pool.data_ptr(), *tail)
     if rc != OK:
         raise PgdError(rc, "paged_prefill_step" if step else "paged_prefill_attention")
     return out
@@ -781,39 +822,44 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
     num_pages: the pool's pages.  Requests that do not fit are left out and
     reported (get_device_error: EDEVICE_BOUNDS).  ``out`` reuses a plan."""
     dev = _check_cuda(table, cached, new_tokens, free_pages, free_head)
-    for t, n in ((table, "table"), (cached, "cached"), (new_tokens, "new_tokens"),
-                 (free_pages, "free_pages"), (free_head, "free_head")):
-        if t is not None and t.dtype != torch.int32:
-            _dtype(t, torch.int32, n)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return assign_pages(table, cached, new_tokens, free_pages, num_tokens=num_tokens,
+                                num_pages=num_pages, free_head=free_head, out=out, stream=stream)
+    if not (table.dtype is cached.dtype is new_tokens.dtype is free_pages.dtype is _I32
+            and (free_head is None or free_head.dtype is _I32)):
+        for t, n in ((table, "table"), (cached, "cached"), (new_tokens, "new_tokens"),
+                     (free_pages, "free_pages"), (free_head, "free_head")):
+            if t is not None:
+                _dtype(t, torch.int32, n)
     requests, width = table.shape if table.dim() == 2 else (-1, 0)
     if cached.shape != (requests,) or new_tokens.shape != (requests,) or free_pages.dim() != 1 \
             or (free_head is not None and free_head.numel() != 1):
         raise ValueError("inconsistent shapes")
     sizes = (num_tokens, num_tokens, num_tokens, requests + 1, requests, 1)
     whole = None
-    with _on_device(dev):
-        if out is None:  # one allocation, cut into the plan's arrays after the launch
-            if num_tokens < 0:
-                raise ValueError("num_tokens must be >= 0")
-            whole = _used_on(torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
-                                         device=table.device), stream)
-            at = whole.data_ptr()
-            starts = at + 12 * num_tokens
-            lengths = starts + 4 * (requests + 1)
-            ptrs = (at, at + 4 * num_tokens, at + 8 * num_tokens, starts, lengths,
-                    lengths + 4 * requests)
-        else:
-            if _check_cuda(*out) != dev:
-                raise ValueError("all tensors must be on one device")
-            for t, n, size in zip(out, PagePlan._fields, sizes):
-                _dtype(t, torch.int32, n)
-                if t.shape != (size,):
-                    raise ValueError(f"out.{n} must have {size} entries")
-            ptrs = [t.data_ptr() for t in out]
-        rc = load_extension().pgdx_assign_pages(
-            requests, width, num_pages, num_tokens, table.data_ptr(), cached.data_ptr(),
-            new_tokens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], _ptr(free_head),
-            *ptrs, _stream_handle(stream))
+    if out is None:  # one allocation, cut into the plan's arrays after the launch
+        if num_tokens < 0:
+            raise ValueError("num_tokens must be >= 0")
+        whole = _used_on(torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
+                                     device=table.device), stream)
+        at = whole.data_ptr()
+        starts = at + 12 * num_tokens
+        lengths = starts + 4 * (requests + 1)
+        ptrs = (at, at + 4 * num_tokens, at + 8 * num_tokens, starts, lengths,
+                lengths + 4 * requests)
+    else:
+        if _check_cuda(*out) != dev:
+            raise ValueError("all tensors must be on one device")
+        for t, n, size in zip(out, PagePlan._fields, sizes):
+            _dtype(t, torch.int32, n)
+            if t.shape != (size,):
+                raise ValueError(f"out.{n} must have {size} entries")
+        ptrs = [t.data_ptr() for t in out]
+    rc = load_extension().pgdx_assign_pages(
+        requests, width, num_pages, num_tokens, table.data_ptr(), cached.data_ptr(),
+        new_tokens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], _ptr(free_head),
+        *ptrs, _stream_handle(stream, dev))
     if rc != OK:
         raise PgdError(rc, "assign_pages")
     if whole is not None:
@@ -883,17 +929,25 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     too.  With ROW_MAJOR pools the table may be None (then max_pages_per_row,
     and with rows table_rows, give its shape)."""
     dev = _check_cuda(positions, k_pool, v_pool, slots, table, rows, q_out)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return rotary_append_paged(
+                q, k_new, v_new, positions, k_pool, v_pool, rotary=rotary, slots=slots, table=table,
+                rows=rows, table_rows=table_rows, layout=layout,
+                max_pages_per_row=max_pages_per_row, q_out=q_out, stream=stream)
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         if t is not None:
             if t.get_device() != dev:
                 raise ValueError("all tensors must be on one CUDA device")
             if t.dim() != 3:
                 raise ValueError(f"{n} must be [P, heads, D]")
-            _dtype(t, torch.bfloat16, n)
-    _dtype(k_pool, torch.bfloat16, "k_pool")
-    _dtype(v_pool, torch.bfloat16, "v_pool")
+            if t.dtype is not _BF16:
+                _dtype(t, torch.bfloat16, n)
+    if not k_pool.dtype is v_pool.dtype is _BF16:
+        _dtype(k_pool, torch.bfloat16, "k_pool")
+        _dtype(v_pool, torch.bfloat16, "v_pool")
     for t, n in ((positions, "positions"), (slots, "slots"), (table, "table"), (rows, "rows")):
-        if t is not None:
+        if t is not None and t.dtype is not _I32:
             _dtype(t, torch.int32, n)
     tokens, hkv, d = k_new.shape
     if v_new.shape != k_new.shape or positions.shape != (tokens,) or k_pool.shape != v_pool.shape \
@@ -912,18 +966,16 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
             raise ValueError("q_out must be shaped like q")
     width = table.shape[1] if table is not None else (max_pages_per_row or 1)
     count = table.shape[0] if table is not None else (table_rows or 0)
-    dims = make_dims(rows=tokens, num_q_heads=q.shape[1] if q is not None else hkv,
-                     num_kv_heads=hkv, head_dim=d, num_pages=_pool_pages(k_pool, hkv, d),
-                     max_pages_per_row=width, layout=layout)
-    with _on_device(dev):
-        if q is not None and q_out is None:
-            q_out = _used_on(torch.empty(q.shape, dtype=torch.bfloat16, device=dev), stream)
-        rc = load_extension().pgdx_rotary_append(
-            ctypes.byref(dims), ctypes.byref(rotary.plan), _ptr(q),
-            0 if q is None else _token_stride(q, "q"), _ptr(q_out), _ptr(k_new),
-            _token_stride(k_new, "k_new"), _ptr(v_new), _token_stride(v_new, "v_new"),
-            _ptr(table), count, _ptr(rows), _ptr(positions), _ptr(slots), _ptr(k_pool),
-            _ptr(v_pool), _stream_handle(stream))
+    dims = _dims_of(tokens, q.shape[1] if q is not None else hkv, hkv, d,
+                    _pool_pages(k_pool, hkv, d), width, layout)
+    if q is not None and q_out is None:
+        q_out = _used_on(torch.empty(q.shape, dtype=torch.bfloat16, device=dev), stream)
+    rc = load_extension().pgdx_rotary_append(
+        ctypes.byref(dims), ctypes.byref(rotary.plan), _ptr(q),
+        0 if q is None else _token_stride(q, "q"), _ptr(q_out), k_new.data_ptr(),
+        _token_stride(k_new, "k_new"), v_new.data_ptr(), _token_stride(v_new, "v_new"),
+        _ptr(table), count, _ptr(rows), positions.data_ptr(), _ptr(slots), k_pool.data_ptr(),
+        v_pool.data_ptr(), _stream_handle(stream, dev))
     if rc != OK:
         raise PgdError(rc, "rotary_append_paged")
     return q_out
