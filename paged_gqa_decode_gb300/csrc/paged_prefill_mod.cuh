@@ -491,38 +491,37 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         }
         // tokens: bad ones are reported, and left out of every run with those
         // that see no key (their outputs are zeroed below)
-        for (int k = lane; k < tokens; k += 32) {
+        const int count = t_end - t_begin;
+        for (int k = lane; k < count; k += 32) {
           const int t = t_begin + k;
-          int row = -1, pos = -1, first = 0, hi = -1;
-          if (t < t_end) {
-            row = p.row_of[t];
-            pos = p.positions[t];
-            bool bad = row < 0 || row >= p.table_rows || (pos >= 0 && pos / kPage >= p.maxp);
-            if (!bad && pos >= 0) {
-              const TokenSpan span = mod_span(p, t, row, pos);
-              hi = span.hi;
-              first = p.first_key ? max(p.first_key[t], 0) : 0;
-              bad = hi / kPage >= p.maxp;
-              if (span.lo > hi) row = -1;
-            }
-            if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
-            if (bad || pos < 0) row = -1;
+          int row = p.row_of[t], first = 0, hi = -1;
+          const int pos = p.positions[t];
+          bool bad = row < 0 || row >= p.table_rows || (pos >= 0 && pos / kPage >= p.maxp);
+          if (!bad && pos >= 0) {
+            const TokenSpan span = mod_span(p, t, row, pos);
+            hi = span.hi;
+            first = p.first_key ? max(p.first_key[t], 0) : 0;
+            bad = hi / kPage >= p.maxp;
+            if (span.lo > hi) row = -1;
           }
+          if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+          if (bad || pos < 0) row = -1;
           it.tok_row[k] = row;
           it.tok_pos[k] = pos;
           it.tok_first[k] = first;
           it.tok_hi[k] = hi;
         }
         __syncwarp();
-        // runs: token k ends one when k + 1 starts another (or is past the end)
+        // runs: token k ends one when k + 1 starts another (or is past the end);
+        // tokens left out in a row are one
         int runs = 0;
-        for (int k0 = 0; k0 < tokens; k0 += 32) {
+        for (int k0 = 0; k0 < count; k0 += 32) {
           const int k = k0 + lane;
           bool brk = false;
-          if (k < tokens)
-            brk = k + 1 == tokens || it.tok_row[k + 1] != it.tok_row[k] ||
-                  it.tok_pos[k + 1] != it.tok_pos[k] + 1 || it.tok_row[k] < 0 ||
-                  it.tok_first[k + 1] != it.tok_first[k];
+          if (k < count)
+            brk = k + 1 == count || it.tok_row[k + 1] != it.tok_row[k] ||
+                  (it.tok_row[k] >= 0 && (it.tok_pos[k + 1] != it.tok_pos[k] + 1 ||
+                                          it.tok_first[k + 1] != it.tok_first[k]));
           const unsigned bal = __ballot_sync(0xffffffffu, brk);
           if (brk) it.run_end[runs + __popc(bal & ((1u << lane) - 1u))] = k + 1;
           runs += __popc(bal);
@@ -571,7 +570,6 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           const int per_token = G * (D / 8);
           for (int e = lane; e < (re - rs) * per_token; e += 32) {
             const int tl = rs + e / per_token;
-            if (t_begin + tl >= t_end) continue;
             const int g = (e / (D / 8)) % G, ch = e % (D / 8);
             uint16_t* o = p.out + ((size_t)(t_begin + tl) * p.hq + kvh * G + g) * D;
             reinterpret_cast<uint4*>(o)[ch] = make_uint4(0u, 0u, 0u, 0u);
