@@ -196,8 +196,9 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * more positions than the table row holds is a device error
  * (PGD_EDEVICE_BOUNDS, the row's tokens give zeros); the prefix's keys must be
  * in the pools (or written by this step).  opts->kernel: AUTO (PREFILL_UMMA
- * when the tokens average at least 8 a table row, with key parts for few
- * items; else per token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).
+ * when the tokens average at least 8 a table row and there is more to do than
+ * some 14 us of the per-token kernel, with key parts for few items; else per
+ * token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).
  * PREFILL_UMMA rounds each weight to bf16 once (TENSOR_CORE, per token, carries
  * its residual too), and with a softcap up to 52 and no bias multiplies V by
  * weights up to 2^76 before it divides: |V| up to 2^31 stays in range over a

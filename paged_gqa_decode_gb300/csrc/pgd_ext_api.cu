@@ -274,6 +274,15 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
                            bound)) != PGD_OK)
     return rc;
   if (kernel == PGD_KERNEL_PREFILL_PAIR) kernel = PGD_KERNEL_PREFILL_UMMA;  // AUTO's only
+  // AUTO takes a prefill of little work token by token: that costs about 5 us and
+  // 4 + 2.2 pages ns for each token and kv head (pages: the most that one may
+  // span), the tcgen05 kernel 12 us at least.  156 tokens over 800 positions with 2
+  // kv heads 17 us so, 27 in blocks; 9 tokens over 1660 with 8 heads 6 and 12; 178
+  // tokens, 2 heads, window 12, 7 and 17; but 274, 8 heads, window 6, 21 and 23, and
+  // 372, window 64, 27 and 18.5.
+  if (asked == PGD_KERNEL_AUTO && kernel == PGD_KERNEL_PREFILL_UMMA &&
+      (double)dims->rows * dims->num_kv_heads * (4.0 + 2.2 * span_pages(dims, bound)) < 14000.0)
+    kernel = PGD_KERNEL_TENSOR_CORE;
   const bool tcgen05 = kernel == PGD_KERNEL_PREFILL_UMMA;
   CUtensorMap k_map, v_map, q_map;
   // the prefill copies a head_dim-128 page tile with one 3-D box

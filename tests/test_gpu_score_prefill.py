@@ -75,12 +75,12 @@ def test_prefill(hq, hkv, d, kw, kernel):
 @pytest.mark.parametrize("kw", MODS, ids=str)
 def test_key_parts(hq, hkv, d, kw):
     """Few items over a long cached prefix: AUTO cuts them into key parts."""
-    cached, chunks = [2500], [70]
+    cached, chunks = [2370], [200]
     b = Paged(2, [2570], hq, hkv, d)
     rows, positions = packed(cached, chunks)
     kw = dict(kw)
     if "docs" in kw:
-        kw["docs"] = 2520
+        kw["docs"] = 2450
     a, sinks, window, c = mods(kw, b, rows, positions)
     q = b.queries(len(rows))
     out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
@@ -299,8 +299,8 @@ def test_scores_that_grow(hq, hkv, d, kernel, falling, kw):
     b = Paged(12, [1100, 700], hq, hkv, d)
     gains = np.linspace(0.2, 12.0, 1100)
     ramp(b, gains[::-1].copy() if falling else gains)
-    rows, positions = packed([1020, 640], [80, 60])
-    q = b.queries(140)
+    rows, positions = packed([900, 560], [200, 140])
+    q = b.queries(340)
     softcap = kw.get("softcap", 0.0)
     slopes = torch.full((hq,), kw["slopes"], device=DEV) if "slopes" in kw else None
     first = positions // kw["docs"] if "docs" in kw else None
@@ -358,14 +358,14 @@ def test_one_row_of_nan(kernel):
 def test_a_nan_row_in_key_parts():
     """As above where the keys are cut into parts: the row's outputs are NaN, not left over."""
     b = Paged(15, [2570], 4, 1, 128)
-    rows, positions = packed([2500], [70])
-    q = b.queries(70)
+    rows, positions = packed([2370], [200])
+    q = b.queries(200)
     q[33] = float("nan")
     out = torch.full_like(q, 7.0)
     pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
                                 num_kv_heads=1, softcap=20.0, out=out)
     assert pgd.get_device_error() == pgd.OK
-    good = np.r_[0:33, 34:70]
+    good = np.r_[0:33, 34:200]
     check(out[good], b, q[good], rows[good], positions[good], scale=128 ** -0.5, softcap=20.0)
     assert torch.isnan(out[33]).all()
 

@@ -27,8 +27,9 @@ def _built():
 
 
 class Serving:
-    def __init__(self, hq, hkv, d, requests, width, pages, tokens, kw, seed):
-        self.hq, self.hkv, self.d, self.kw = hq, hkv, d, kw
+    def __init__(self, hq, hkv, d, requests, width, pages, tokens, kw, seed,
+                 kernel=pgd.KERNEL_AUTO):
+        self.hq, self.hkv, self.d, self.kw, self.kernel = hq, hkv, d, kw, kernel
         self.gen = torch.Generator().manual_seed(seed)
         self.tokens, self.pages = tokens, pages
         self.table = torch.zeros(requests, width, dtype=torch.int32, device=DEV)
@@ -67,7 +68,8 @@ class Serving:
             self.q, self.k_pool, self.v_pool, self.table, self.plan.rows, self.plan.positions,
             None, self.kw.get("window", 0), num_kv_heads=hkv, out=self.out, workspace=self.work,
             softcap=self.kw.get("softcap", 0.0),
-            alibi_slopes=self.slopes if self.kw.get("alibi") else None, prefix_len=self.prefix)
+            alibi_slopes=self.slopes if self.kw.get("alibi") else None, prefix_len=self.prefix,
+            kernel=self.kernel)
         self.lengths.copy_(self.plan.lengths)
         self.head.copy_(self.plan.free_head)
 
@@ -121,8 +123,10 @@ PASSES = [[70, 0, 3, 129], [1, 64, 1, 1], [1, 1, 61, 1], [0, 1, 1, 200], [1, 1, 
 @pytest.mark.parametrize("hq,hkv,d", [(14, 2, 64), (8, 2, 128)])
 @pytest.mark.parametrize("kw", [dict(softcap=30.0), dict(alibi=True), dict(softcap=20.0, window=90)])
 @pytest.mark.parametrize("captured", [False, True])
-def test_passes(hq, hkv, d, kw, captured):
-    s = Serving(hq, hkv, d, requests=4, width=8, pages=24, tokens=256, kw=kw, seed=hq)
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_AUTO, pgd.KERNEL_PREFILL_UMMA])
+def test_passes(hq, hkv, d, kw, captured, kernel):
+    s = Serving(hq, hkv, d, requests=4, width=8, pages=24, tokens=256, kw=kw, seed=hq,
+                kernel=kernel)
     s.prefix.copy_(i32([0, 0, 0, 40]))
     run = s.enqueue
     if captured:
