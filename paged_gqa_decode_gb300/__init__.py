@@ -318,8 +318,9 @@ def paged_decode_workspace_bytes(dims: Dims, pages_per_split: int = 0) -> int:
 def attention_kernel_count(dims: Dims, table_rows: int = 0, window: int = 0,
                            pages_per_split: int = 0, kernel: int = KERNEL_AUTO) -> int:
     """Kernels one paged_decode_attention (table_rows 0) or
-    paged_prefill_attention (table_rows > 0) call with these arguments
-    launches on the current device."""
+    paged_prefill_attention (table_rows > 0) call with these arguments (and
+    none of softcap, alibi_slopes, first_key, prefix_len) launches on the
+    current device."""
     opts = DecodeOptions(pages_per_split, kernel)
     count = ctypes.c_int32(0)
     rc = load_library().pgd_attention_kernel_count(ctypes.byref(dims), int(table_rows),
