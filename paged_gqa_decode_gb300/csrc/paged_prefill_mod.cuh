@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         const ModItem& it = items[d];
         if (!it.valid) break;
         if (!stream_item(it, false, iv)) break;
+        __syncwarp();  // every lane is done with the descriptor (trailing runs without pages)
         if (lane == 0) mbar_arrive(&item_free[d]);
       }
       drain(v_full, iv);

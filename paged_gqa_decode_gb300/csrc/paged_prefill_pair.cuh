@@ -439,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       const PrefillItem& it = items[d];
       if (!it.valid) break;
       if (!stream_item(it, it.kvh, y_ring[1], iv, false)) break;
+      __syncwarp();  // every lane is done with the descriptor
       if (lane == 0) mbar_arrive(&item_free[d]);
     }
     if (lane == 0)

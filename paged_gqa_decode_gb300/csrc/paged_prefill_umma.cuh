@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(UmmaPrefillCfg<D, RK, RV>::kThreads, 1)
       const PrefillItem& it = items[d];
       if (!it.valid) break;
       if (!stream_item(it, it.kvh, &v_map, v_slots, v_full, v_empty, y_ring[1], iv, false)) break;
+      __syncwarp();  // every lane is done with the descriptor
       if (lane == 0) mbar_arrive(&item_free[d]);
     }
     if (lane == 0)
