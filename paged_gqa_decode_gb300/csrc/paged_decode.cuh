@@ -827,7 +827,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, STAGES, Consumer, WARPS>::kThread
 // out = sum_i acc_i 2^(m_i - M) / L, written as bf16 to o.  Partial i is
 // (m, l) at ml + i * ml_stride and acc at ac + i * ac_stride (ac already
 // offset to this lane's dims).  A partial marked l < 0 (skipped for a bad
-// table entry or an abandoned wait) zeroes the output.
+// table entry or an abandoned wait) zeroes the output; one of l = NaN (a NaN
+// score, which the maxima pass over) makes it NaN, as in a row of one split.
 // One warp; lane l owns dims [D/32 * l, D/32 * (l + 1)).  The partials'
 // (m, l) are read 32 at a time, one per lane, together with the first
 // kEarly accumulators, so the merge costs about one round trip to L2; the
@@ -844,17 +845,19 @@ __device__ __forceinline__ void merge_partials(const float* ml, int ml_stride, c
   for (int k = 0; k < kEarly; ++k)
     if (k < nsplit) early[k] = *reinterpret_cast<const Vec*>(ac + (size_t)k * ac_stride);
   float mx = sk;
-  bool skipped = false;
+  bool skipped = false, nan = false;
   for (int base = 0; base < nsplit; base += 32) {
     const int i = base + lane;
     const float2 mli = i < nsplit ? *reinterpret_cast<const float2*>(ml + (size_t)i * ml_stride)
                                   : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, warp_max(mli.x));
     skipped |= __any_sync(0xffffffffu, mli.y < 0.f);
+    nan |= __any_sync(0xffffffffu, mli.y != mli.y);
   }
-  if (skipped || mx == -INFINITY) {
+  if (skipped || nan || mx == -INFINITY) {
+    const uint16_t v = nan && !skipped ? 0x7fff : 0;
 #pragma unroll
-    for (int j = 0; j < kDims; ++j) o[j] = 0;
+    for (int j = 0; j < kDims; ++j) o[j] = v;
     return;
   }
   float res[kDims];

@@ -1123,9 +1123,11 @@ cudaError_t launch_prefill_write_for(const typename Score::Params& p, bool umma,
 //   out = sum_s O_s 2^(m_s - M) / L,
 // the split softmax of the attention step over all of the token's keys, the
 // sink in the denominator only (GPT-OSS 20B model files, src/attention.linnet,
-// SinkAttention).  A part without keys (m = -inf) adds nothing; a token whose
-// partial carries l < 0 was covered by no pass, and its output, already
-// zeroed, is left.  One warp per (token, query head), 32 lanes over D.
+// SinkAttention).  A part without keys (l = 0) adds nothing; a part of NaN
+// scores has l = NaN (and m = -inf, maxima passing over NaN), and the output is
+// NaN, as where the keys are not cut; a token whose partial carries l < 0 was
+// covered by no pass, and its output, already zeroed, is left.  One warp per
+// (token, query head), 32 lanes over D.
 template <int D>
 __global__ void __launch_bounds__(128) prefill_part_combine_kernel(const DecodeParams p,
                                                                    int parts,
@@ -1157,23 +1159,21 @@ __global__ void __launch_bounds__(128) prefill_part_combine_kernel(const DecodeP
 #pragma unroll
   for (int j = 0; j < kDims; ++j) acc[j] = 0.f;
   float total = 0.f;
-  if (mx != -INFINITY) {
-    if (sk != -INFINITY) total = exp2_approx(sk - mx);
-    for (int s = 0; s < parts; ++s) {
-      const float ms = part_ml[2 * (u0 + s)];
-      if (ms == -INFINITY) continue;
-      const float w = exp2_approx(ms - mx);
-      total = fmaf(part_ml[2 * (u0 + s) + 1], w, total);
-      const float* a = part_acc + (u0 + s) * D + lane * kDims;
+  if (sk != -INFINITY) total = exp2_approx(sk - mx);
+  for (int s = 0; s < parts; ++s) {
+    const float ls = part_ml[2 * (u0 + s) + 1];
+    if (ls == 0.f) continue;  // no keys
+    const float w = exp2_approx(part_ml[2 * (u0 + s)] - mx);
+    total = fmaf(ls, w, total);
+    const float* a = part_acc + (u0 + s) * D + lane * kDims;
 #pragma unroll
-      for (int j = 0; j < kDims; j += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(a + j);
-        acc[j] = fmaf(v.x, w, acc[j]);
-        acc[j + 1] = fmaf(v.y, w, acc[j + 1]);
-      }
+    for (int j = 0; j < kDims; j += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(a + j);
+      acc[j] = fmaf(v.x, w, acc[j]);
+      acc[j + 1] = fmaf(v.y, w, acc[j + 1]);
     }
   }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;  // (no key seen: zeros)
   uint32_t w2[kDims / 2];
 #pragma unroll
   for (int j = 0; j < kDims / 2; ++j) w2[j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);

@@ -53,3 +53,64 @@ def test_many_items_that_end_in_runs_without_pages(hq, hkv, d, softcap, kernel):
     check(out, b, q, rows, positions, scale=d ** -0.5, softcap=softcap, first=first, rounded=True)
 
 
+def slopes_of(hq):
+    return torch.exp2(-8.0 * torch.arange(1, hq + 1) / hq).to(DEV)
+
+
+KINDS = [dict(), dict(first=True), dict(alibi=True), dict(softcap=20.0), dict(softcap=100.0),
+         dict(softcap=100.0, alibi=True)]
+
+
+def of_kind(kw, hq, tokens):
+    """Arguments of a call and of the check (no modification: the plain call)."""
+    a = dict(softcap=kw.get("softcap", 0.0), alibi_slopes=slopes_of(hq) if kw.get("alibi") else None,
+             first_key=i32([1] * tokens) if kw.get("first") else None)
+    return a, dict(softcap=a["softcap"], slopes=a["alibi_slopes"], first=a["first_key"])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", KINDS, ids=str)
+@pytest.mark.parametrize("with_sinks", [False, True])
+def test_a_nan_query_in_prefill_cut_into_key_parts(d, kw, with_sinks):
+    """As in calls that are not cut: NaN for that token's heads, nothing else changed."""
+    b = Paged(15, [2570], 4, 1, d)
+    rows, positions = packed([2370], [200])
+    q = b.queries(200)
+    q[33], q[150, 2] = float("nan"), float("nan")
+    a, c = of_kind(kw, 4, 200)
+    sinks = torch.zeros(4, device=DEV) if with_sinks else None
+    out = torch.full_like(q, 7.0)
+    pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions), sinks,
+                                num_kv_heads=1, out=out, **a)
+    assert pgd.get_device_error() == pgd.OK
+    assert torch.isnan(out[33]).all() and torch.isnan(out[150, 2]).all()
+    assert torch.isfinite(out[150, [0, 1, 3]]).all()
+    good = np.r_[0:33, 34:150, 151:200]
+    if c["first"] is not None:
+        c["first"] = c["first"][good]
+    check(out[good], b, q[good], rows[good], positions[good], scale=d ** -0.5, sinks=sinks,
+          rounded=True, **c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", KINDS, ids=str)
+@pytest.mark.parametrize("with_sinks", [False, True])
+@pytest.mark.parametrize("pages_per_split", [0, 5])
+def test_a_nan_query_in_decode_cut_into_splits(d, kw, with_sinks, pages_per_split):
+    contexts = [2049, 2300, 64]
+    b = Paged(16, contexts, 8, 2, d)
+    positions = [n - 1 for n in contexts]
+    q = b.queries(3)
+    q[0], q[1, 5] = float("nan"), float("nan")
+    a, c = of_kind(kw, 8, 3)
+    sinks = torch.zeros(8, device=DEV) if with_sinks else None
+    out = pgd.paged_decode_attention(q, b.k_pool, b.v_pool, b.table, i32(positions), sinks,
+                                     num_kv_heads=2, pages_per_split=pages_per_split, **a)
+    assert pgd.get_device_error() == pgd.OK
+    assert torch.isnan(out[0]).all() and torch.isnan(out[1, 5]).all()
+    assert torch.isfinite(out[1, [0, 1, 2, 3, 4, 6, 7]]).all()
+    if c["first"] is not None:
+        c["first"] = c["first"][2:]
+    check(out[2:], b, q[2:], [2], positions[2:], scale=d ** -0.5, sinks=sinks, **c)
+
+
