@@ -212,11 +212,22 @@ def _on_device(index: int):
     return _no_switch if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _used_on(t: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor:
-    """A tensor made here for a call on `stream`: its memory is not handed out again
-    before the call is done with it, whatever happens to the tensor."""
+def _scratch(size: tuple, dtype: torch.dtype, device: int,
+             stream: torch.cuda.Stream | None) -> torch.Tensor:
+    """Memory for a call on `stream`: out of that stream's own pool, so that nothing that
+    runs elsewhere still uses it and nothing gets it before the call is done with it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
+def _result(size: tuple, dtype: torch.dtype, device: int,
+            stream: torch.cuda.Stream | None) -> torch.Tensor:
+    """_scratch that the caller gets: it may be used on the current stream later on."""
+    t = _scratch(size, dtype, device, stream)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -428,12 +439,12 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
     opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
     if out is None:
-        out = _used_on(torch.empty_like(q), stream)
+        out = _result(q.shape, _BF16, dev, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16:
         raise ValueError("out must be bf16 shaped like q")
     if workspace is None:  # (one that is given is checked by the call)
         need = lib.pgd_paged_decode_workspace_bytes(dims, opts)
-        workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+        workspace = _scratch((max(need, 16),), torch.uint8, dev, stream)
     tail = (table.data_ptr(), positions.data_ptr(), _ptr(sinks), int(window), float(scale),
             out.data_ptr(), workspace.data_ptr(), workspace.nbytes, opts,
             _stream_handle(stream, dev))
@@ -503,7 +514,7 @@ def page_slots(table: torch.Tensor, positions: torch.Tensor, rows: torch.Tensor 
     dims = make_dims(rows=tokens, num_q_heads=1, num_kv_heads=1, head_dim=64,
                      num_pages=num_pages, max_pages_per_row=table.shape[1])
     with _on_device(dev):
-        slots = torch.empty(tokens, dtype=torch.int32, device=dev)
+        slots = _result((tokens,), _I32, dev, stream)
         rc = load_library().pgd_page_slots(ctypes.byref(dims), table.shape[0], _ptr(table),
                                            _ptr(rows), _ptr(positions), _ptr(slots),
                                            _stream_handle(stream))
@@ -616,12 +627,12 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
     opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
     if out is None:
-        out = _used_on(torch.empty_like(q), stream)
+        out = _result(q.shape, _BF16, dev, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16:
         raise ValueError("out must be bf16 shaped like q")
     if workspace is None:  # (one that is given is checked by the call)
         need = lib.pgd_paged_decode_workspace_bytes(dims, opts)
-        workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+        workspace = _scratch((max(need, 16),), torch.uint8, dev, stream)
     tail = (table.data_ptr(), rows.data_ptr(), positions.data_ptr(), _ptr(sinks), int(window),
             float(scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, opts,
             _stream_handle(stream, dev))
@@ -744,10 +755,10 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
     lib = load_library()
     with _on_device(dev):
         if out is None:
-            out = _used_on(torch.empty_like(q), stream)
+            out = _result(q.shape, _BF16, dev, stream)
         if workspace is None:  # (one that is given is checked by the call)
             need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
-            workspace = _used_on(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+            workspace = _scratch((max(need, 16),), torch.uint8, dev, stream)
         tail = (None, _ptr(positions), _ptr(sinks), int(window), float(scale), _ptr(out),
                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                 ctypes.byref(opts), _stream_handle(stream))
@@ -842,8 +853,7 @@ def assign_pages(table: torch.Tensor, cached: torch.Tensor, new_tokens: torch.Te
     if out is None:  # one allocation, cut into the plan's arrays after the launch
         if num_tokens < 0:
             raise ValueError("num_tokens must be >= 0")
-        whole = _used_on(torch.empty(3 * num_tokens + 2 * requests + 2, dtype=torch.int32,
-                                     device=table.device), stream)
+        whole = _result((3 * num_tokens + 2 * requests + 2,), _I32, dev, stream)
         at = whole.data_ptr()
         starts = at + 12 * num_tokens
         lengths = starts + 4 * (requests + 1)
@@ -970,7 +980,7 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     dims = _dims_of(tokens, q.shape[1] if q is not None else hkv, hkv, d,
                     _pool_pages(k_pool, hkv, d), width, layout)
     if q is not None and q_out is None:
-        q_out = _used_on(torch.empty(q.shape, dtype=torch.bfloat16, device=dev), stream)
+        q_out = _result(q.shape, _BF16, dev, stream)
     rc = load_extension().pgdx_rotary_append(
         ctypes.byref(dims), ctypes.byref(rotary.plan), _ptr(q),
         0 if q is None else _token_stride(q, "q"), _ptr(q_out), k_new.data_ptr(),
