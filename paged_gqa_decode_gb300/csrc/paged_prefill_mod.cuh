@@ -274,6 +274,14 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
   }
 }
 
+// Slopes to which a bias is taken in its linear form.  That adds up to 15 slope log2 e
+// to a score and takes it off again: two roundings, 2^-23 of 15 slope in natural
+// units, below 2^-17 up to here (from 1e6 on nothing of the score would be left).  A
+// warp with a steeper row takes every page in full, key by key, where the nearest
+// key's bias is exact: 186 us to this slope and 251 past it (8 chunks of 512 behind up
+// to 4000, 64 / 8 heads of 64), 255 and 278 (32 / 8 heads of 128, up to 8192).
+constexpr float kSteepSlope = 4.f;
+
 // True for one lane of a converged warp, always the same one.  The compiler knows
 // that what it guards runs in one thread of a warp with uniform control, and keeps
 // the descriptors of MMAs in uniform registers (as `lane == 0` it does not).
@@ -787,6 +795,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
         const int lo_all = __reduce_max_sync(0xffffffffu, lo);
         const int hi_all = __reduce_min_sync(0xffffffffu, hi);
         const bool ahead = kBias && __any_sync(0xffffffffu, hi > pos);
+        const bool steep = kBias && __any_sync(0xffffffffu, live && fabsf(slope) > kSteepSlope);
         const float nslope = -slope * kLog2e;  // bias per position of distance, log2 units
         float2 step[8];  // bias of 16 keys against the first of them
         if constexpr (kBias) {
@@ -813,7 +822,8 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           // when the exponentials are; if not for a row of the warp, S, still in
           // place, is read again and taken in full.
           const bool linear =
-              !ahead || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos);
+              !steep &&
+              (!ahead || __all_sync(0xffffffffu, pos0 + min(k_hi, kPage - 1) <= pos));
           float sv[kPage];
           auto read_s = [&]() {
 #pragma unroll

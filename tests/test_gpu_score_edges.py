@@ -114,3 +114,54 @@ def test_a_nan_query_in_decode_cut_into_splits(d, kw, with_sinks, pages_per_spli
     check(out[2:], b, q[2:], [2], positions[2:], scale=d ** -0.5, sinks=sinks, **c)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (4, 1, 128)])
+@pytest.mark.parametrize("slope", [1e2, 1e4, 1e6, 1e8, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(prefix=120)], ids=str)
+@pytest.mark.parametrize("cut", [False, True])
+def test_steep_slopes(hq, hkv, d, slope, kw, cut):
+    """Slopes that leave a token its own key alone: out = v_n / (1 + e^(sink - x_n)), whatever
+    n mod 16 is."""
+    cached, chunk = (2370, 200) if cut else (40, 90)
+    b = Paged(18, [cached + chunk], hq, hkv, d)
+    rows, positions = packed([cached], [chunk])
+    q = b.queries(chunk)
+    sinks = torch.linspace(-2.0, 2.0, hq, device=DEV)
+    softcap = kw.get("softcap", 0.0)
+    out = pgd.paged_prefill_attention(
+        q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions), sinks, num_kv_heads=hkv,
+        softcap=softcap, alibi_slopes=torch.full((hq,), slope, device=DEV),
+        prefix_len=i32([kw["prefix"]]) if "prefix" in kw else None,
+        kernel=pgd.KERNEL_AUTO if cut else UMMA)
+    assert pgd.get_device_error() == pgd.OK
+    group = hq // hkv
+    k = np.repeat(b.k_rows[0][:, positions], group, axis=0).transpose(1, 0, 2)
+    v = np.repeat(b.v_rows[0][:, positions], group, axis=0).transpose(1, 0, 2)
+    qd = q.double().cpu().numpy()
+    x, size = ((qd * k).sum(-1) * d ** -0.5, np.abs(qd * k).sum(-1) * d ** -0.5)
+    if softcap:
+        x = softcap * np.tanh(x / softcap)
+    want = v / (1.0 + np.exp(sinks.double().cpu().numpy() - x))[..., None]
+    # the weights' errors of score_side; the key's own bias is zero and no other key has weight
+    weight = (2 * d * 2.0 ** -24 * size + softcap * 2.0 ** -20 + 2.0 ** -14)[..., None]
+    bound = 2 * weight * np.abs(want) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(want)
+    excess = np.abs(out.double().cpu().numpy() - want) - bound
+    assert excess.max() <= 0, (excess.max(), np.unravel_index(np.argmax(excess), excess.shape))
+
+
+@pytest.mark.parametrize("slope", [3.0, 3.9, 4.1, 60.0, -0.3, -5.0])
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_TENSOR_CORE, UMMA])
+def test_slopes_on_both_sides_of_the_linear_form(slope, kernel):
+    """A slope per head, some heads of a tile steep and some not."""
+    b = Paged(19, [300, 200], 16, 2, 64)
+    rows, positions = packed([150, 0], [150, 200])
+    q = b.queries(350)
+    slopes = torch.linspace(slope, slope / 7, 16, device=DEV)
+    sinks = torch.zeros(16, device=DEV)
+    out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                      sinks, num_kv_heads=2, alibi_slopes=slopes,
+                                      prefix_len=i32([260, 0]), kernel=kernel)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, scale=0.125, slopes=slopes, prefix=[260, 0], sinks=sinks,
+          rounded=True)
+
+
