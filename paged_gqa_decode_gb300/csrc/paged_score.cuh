@@ -45,7 +45,7 @@ struct TokenSpan {
 __device__ __forceinline__ TokenSpan mod_span(const ModParams& p, int b, int row, int n) {
   TokenSpan s;
   s.hi = n;
-  if (p.prefix_len) s.hi = max(n, p.prefix_len[row] - 1);
+  if (p.prefix_len) s.hi = max(n, max(p.prefix_len[row], 0) - 1);  // (-2^31 - 1 wraps)
   s.lo = p.window > 0 ? max(n - p.window + 1, 0) : 0;
   if (p.first_key) s.lo = max(s.lo, p.first_key[b]);
   return s;

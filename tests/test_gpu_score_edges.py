@@ -165,3 +165,18 @@ def test_slopes_on_both_sides_of_the_linear_form(slope, kernel):
           rounded=True)
 
 
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_AUTO, pgd.KERNEL_TENSOR_CORE, UMMA])
+def test_prefix_lengths_that_mean_none(kernel):
+    """Lengths of 0 and less, down to the end of int32, are no prefix."""
+    b = Paged(20, [100] * 5, 8, 2, 64)
+    rows, positions = packed([20] * 5, [80] * 5)
+    q = b.queries(400)
+    args = (q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions))
+    kw = dict(num_kv_heads=2, softcap=20.0, kernel=kernel)
+    prefix = [0, -1, -2 ** 31, -2 ** 31 + 1, -2 ** 31]
+    out = pgd.paged_prefill_attention(*args, prefix_len=i32(prefix), **kw)
+    assert pgd.get_device_error() == pgd.OK
+    assert torch.equal(out, pgd.paged_prefill_attention(*args, **kw))
+    check(out, b, q, rows, positions, scale=0.125, softcap=20.0, rounded=True)
+
+
