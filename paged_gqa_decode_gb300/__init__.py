@@ -474,7 +474,8 @@ def rope_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.
                       stream: torch.cuda.Stream | None = None) -> None:
     """rope_rows + append: rotates q (bf16 [R, Hq, D], in place) and k_new at
     positions[b] (base theta), writes rotated k and v into the pools at each
-    row's slot (from the table, or the explicit slots)."""
+    row's slot (from the table, or the explicit slots).  With ROW_MAJOR pools and
+    no table, max_pages_per_row says how many pages a row has (None: one)."""
     dev = _check_cuda(q, k_new, v_new, table, positions, slots, k_pool, v_pool)
     for t, n in ((k_new, "k_new"), (v_new, "v_new"), (k_pool, "k_pool"), (v_pool, "v_pool")):
         _dtype(t, torch.bfloat16, n)
@@ -525,8 +526,11 @@ def page_slots(table: torch.Tensor, positions: torch.Tensor, rows: torch.Tensor 
 
 def kv_write_slots(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
                    k_pool: torch.Tensor, v_pool: torch.Tensor, *, layout: int = PAGE_MAJOR,
+                   max_pages_per_row: int = 1,
                    stream: torch.cuda.Stream | None = None) -> None:
-    """Writes token p's key and value (bf16 [P, Hkv, D]) at pool position slots[p]."""
+    """Writes token p's key and value (bf16 [P, Hkv, D]) at pool position slots[p].
+    With ROW_MAJOR pools slots do not say how many pages a row has:
+    max_pages_per_row does (MaxSeq / 64)."""
     dev = _check_cuda(k_new, v_new, slots, k_pool, v_pool)
     for t, n in ((k_new, "k_new"), (v_new, "v_new"), (k_pool, "k_pool"), (v_pool, "v_pool")):
         _dtype(t, torch.bfloat16, n)
@@ -535,7 +539,8 @@ def kv_write_slots(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor
     if v_new.shape != k_new.shape or slots.shape != (tokens,) or k_pool.shape != v_pool.shape:
         raise ValueError("inconsistent shapes")
     dims = make_dims(rows=tokens, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d,
-                     num_pages=_pool_pages(k_pool, hkv, d), max_pages_per_row=1, layout=layout)
+                     num_pages=_pool_pages(k_pool, hkv, d), max_pages_per_row=max_pages_per_row,
+                     layout=layout)
     with _on_device(dev):
         rc = load_library().pgd_kv_write_slots(ctypes.byref(dims), _ptr(k_new), _ptr(v_new),
                                                _ptr(slots), _ptr(k_pool), _ptr(v_pool),
@@ -937,8 +942,9 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     token stride of their own (a multiple of 8 values).  Returns the rotated q:
     q_out if given (q itself for in place), else a new contiguous tensor.
     Tokens with a negative position or slot are left alone, their q_out rows
-    too.  With ROW_MAJOR pools the table may be None (then max_pages_per_row,
-    and with rows table_rows, give its shape)."""
+    too.  With ROW_MAJOR pools the table may be None: max_pages_per_row then
+    says how many pages a row has (with slots too), and with rows table_rows
+    how many rows there are."""
     dev = _check_cuda(positions, k_pool, v_pool, slots, table, rows, q_out)
     if _current_device() != dev:
         with torch.cuda.device(dev):
@@ -975,7 +981,10 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
         _dtype(q_out, torch.bfloat16, "q_out")
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
-    width = table.shape[1] if table is not None else (max_pages_per_row or 1)
+    if layout == ROW_MAJOR and table is None and max_pages_per_row is None:
+        raise ValueError("ROW_MAJOR pools without a table need max_pages_per_row")
+    width = table.shape[1] if table is not None else \
+        1 if max_pages_per_row is None else max_pages_per_row
     count = table.shape[0] if table is not None else (table_rows or 0)
     dims = _dims_of(tokens, q.shape[1] if q is not None else hkv, hkv, d,
                     _pool_pages(k_pool, hkv, d), width, layout)
