@@ -180,7 +180,8 @@ typedef struct {
  * pgd_paged_decode_step (both given) with the scores of *score.  Arguments,
  * workspace (pgd_paged_decode_workspace_bytes), results and device errors as
  * there; with a step, the new token is appended whether or not its row sees
- * it.  opts->kernel: AUTO or TENSOR_CORE (else PGD_EUNSUPPORTED).
+ * it.  opts->kernel: AUTO or TENSOR_CORE (else PGD_EUNSUPPORTED).  At most 65535
+ * rows and kv heads (the grid's limit; else PGD_EUNSUPPORTED).
  * score->prefix_len must be NULL.
  */
 PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, const void* q,
@@ -198,7 +199,8 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * in the pools (or written by this step).  opts->kernel: AUTO (PREFILL_UMMA
  * when the tokens average at least 8 a table row and there is more to do than
  * some 14 us of the per-token kernel, with key parts for few items; else per
- * token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).
+ * token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).  TENSOR_CORE takes
+ * at most 65535 tokens and kv heads (else PGD_EUNSUPPORTED); AUTO takes more in blocks.
  * PREFILL_UMMA rounds each weight to bf16 once (TENSOR_CORE, per token, carries
  * its residual too), and with a softcap up to 52 and no bias multiplies V by
  * weights up to 2^76 before it divides: |V| up to 2^31 stays in range over a

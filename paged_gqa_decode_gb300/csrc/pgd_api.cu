@@ -204,6 +204,10 @@ static int decode_impl(const pgd_dims* dims, int32_t table_rows, const int32_t* 
   const int grid_splits = (grid_pages + pl.pages_per_split - 1) / pl.pages_per_split;
   const int pages_per_cta = grid_pages < pl.pages_per_split ? grid_pages : pl.pages_per_split;
   const bool short_rows = short_row_kernel(dims, window, opts, kernel, dev->sm_count);
+  const bool split = kernel == PGD_KERNEL_TENSOR_CORE || kernel == PGD_KERNEL_CUDA_CORE ||
+                     (kernel == PGD_KERNEL_AUTO && !short_rows &&
+                      !(window > 0 && window <= kMaxWindowKernel));
+  if (split && !per_token_fits(dims)) return PGD_EUNSUPPORTED;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // prefill step: the tokens' K and V are written by a launch of their own

@@ -235,6 +235,9 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
     if (!std::isfinite(ratio) || score->softcap > 0x1p126f) return PGD_EINVAL;
   }
   if (dims->rows == 0) return PGD_OK;
+  // (AUTO takes a prefill of more tokens in blocks)
+  if (!per_token_fits(dims) && (!prefill || asked == PGD_KERNEL_TENSOR_CORE))
+    return PGD_EUNSUPPORTED;
   DeviceInfo* dev = nullptr;
   Plan pl;
   ModParams p;
@@ -273,14 +276,15 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   if ((rc = resolve_kernel(dims, table_rows, prefill, opts, &kernel, dev->sm_count, &parts,
                            bound)) != PGD_OK)
     return rc;
-  if (kernel == PGD_KERNEL_PREFILL_PAIR) kernel = PGD_KERNEL_PREFILL_UMMA;  // AUTO's only
+  if (kernel == PGD_KERNEL_PREFILL_PAIR || (prefill && !per_token_fits(dims)))
+    kernel = PGD_KERNEL_PREFILL_UMMA;  // (the pair: AUTO's only)
   // AUTO takes a prefill of little work token by token: that costs about 5 us and
   // 4 + 2.2 pages ns for each token and kv head (pages: the most that one may
   // span), the tcgen05 kernel 12 us at least.  156 tokens over 800 positions with 2
   // kv heads 17 us so, 27 in blocks; 9 tokens over 1660 with 8 heads 6 and 12; 178
   // tokens, 2 heads, window 12, 7 and 17; but 274, 8 heads, window 6, 21 and 23, and
   // 372, window 64, 27 and 18.5.
-  if (asked == PGD_KERNEL_AUTO && kernel == PGD_KERNEL_PREFILL_UMMA &&
+  if (asked == PGD_KERNEL_AUTO && kernel == PGD_KERNEL_PREFILL_UMMA && per_token_fits(dims) &&
       (double)dims->rows * dims->num_kv_heads * (4.0 + 2.2 * span_pages(dims, bound)) < 14000.0)
     kernel = PGD_KERNEL_TENSOR_CORE;
   const bool tcgen05 = kernel == PGD_KERNEL_PREFILL_UMMA;

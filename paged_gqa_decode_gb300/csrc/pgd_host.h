@@ -132,6 +132,13 @@ size_t workspace_bytes(const pgd_dims* d, const Plan& pl) {
   return (size_t)d->rows * d->num_q_heads * pl.max_splits * (d->head_dim + 2) * sizeof(float);
 }
 
+// Whether the per-token split kernel's grid, (splits, kv heads, rows), holds the
+// call: the last two stop at 65535.
+constexpr int kMaxGridYZ = 65535;
+bool per_token_fits(const pgd_dims* d) {
+  return d->rows <= kMaxGridYZ && d->num_kv_heads <= kMaxGridYZ;
+}
+
 // The kernel a call runs: opts->kernel, or for AUTO the per-token split
 // kernel, except that prefill with tokens in runs goes to a tcgen05 kernel:
 // the one-SM kernel, with key parts (`key_parts` > 1) when its work items
@@ -156,8 +163,11 @@ int resolve_kernel(const pgd_dims* dims, int32_t table_rows, bool prefill,
   // pair of SMs per item (measured on GB300: key parts 41-99 us against
   // 43-109 us for pairs on one Mistral-shaped chunk of 256-512 tokens; with
   // 128 items, pairs 102 us against 96-98 us for one SM per item).
+  // More tokens than the split kernel's grid holds go to blocks whatever they are.
   int parts = 1;
-  if (prefill && k == PGD_KERNEL_AUTO && dims->rows >= 8ll * table_rows) {
+  const bool window_kernel = window > 0 && window <= kMaxWindowKernel;
+  if (prefill && k == PGD_KERNEL_AUTO &&
+      (dims->rows >= 8ll * table_rows || (!per_token_fits(dims) && !window_kernel))) {
     k = PGD_KERNEL_PREFILL_UMMA;
     const int group = dims->num_q_heads / dims->num_kv_heads;
     const int64_t block = 2 * (128 / group);  // tokens per work item

@@ -180,3 +180,44 @@ def test_prefix_lengths_that_mean_none(kernel):
     check(out, b, q, rows, positions, scale=0.125, softcap=20.0, rounded=True)
 
 
+MANY = 65_600  # tokens: more than a grid's third dimension
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_more_tokens_than_the_per_token_grid_holds(softcap):
+    """AUTO takes them in blocks, few to a table row as they are."""
+    b = Paged(24, [200] * 64, 1, 1, 64)
+    count = MANY // 4
+    rows = np.repeat(np.arange(count), 4)
+    positions = np.tile([17, 64, 130, 199], count)
+    table = b.table.repeat(count // 64 + 1, 1)[:count].contiguous()
+    q = b.queries(MANY)
+    out = torch.full_like(q, float("nan"))
+    pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, table, i32(rows), i32(positions),
+                                num_kv_heads=1, softcap=softcap, out=out)
+    assert pgd.get_device_error() == pgd.OK
+    assert torch.isfinite(out).all()
+    some = np.r_[0:300, 65_500:MANY]
+    check(out[some], b, q[some], rows[some] % 64, positions[some], scale=0.125, softcap=softcap,
+          rounded=True)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_refused_calls_of_many_tokens_leave_the_pools(softcap):
+    b = Paged(25, [64], 1, 1, 64)
+    b.k_pool.zero_(), b.v_pool.zero_()
+    q = b.queries(MANY)
+    n, rows = i32(np.zeros(MANY)), i32(np.zeros(MANY))
+    kw = dict(num_kv_heads=1, softcap=softcap)
+    with pytest.raises(pgd.PgdError) as e:
+        pgd.paged_prefill_step(q, q, q, b.k_pool, b.v_pool, b.table, rows, n,
+                               kernel=pgd.KERNEL_TENSOR_CORE, **kw)
+    assert e.value.status == pgd.EUNSUPPORTED
+    many = b.table.repeat(MANY, 1)
+    with pytest.raises(pgd.PgdError) as e:
+        pgd.paged_decode_step(q, q, q, b.k_pool, b.v_pool, many, n, **kw)
+    assert e.value.status == pgd.EUNSUPPORTED
+    torch.cuda.synchronize()
+    assert not b.k_pool.any() and not b.v_pool.any() and pgd.get_device_error() == pgd.OK
+
+
