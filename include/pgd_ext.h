@@ -78,7 +78,7 @@ PGD_API int pgdx_assign_pages(int32_t requests, int32_t max_pages_per_row, int32
 enum {
   PGDX_ROTARY_NONE = 0,
   PGDX_ROTARY_LINEAR = 1, /* f_i / factor */
-  PGDX_ROTARY_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) for theta */
+  PGDX_ROTARY_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) for theta (finite) */
   PGDX_ROTARY_YARN = 3,   /* f_i (1 - r_i) + f_i / factor r_i, the ramp r_i = clamp((i - a) /
                              (b - a), 0, 1) from pair a, which turns beta_fast times over
                              original_positions, to pair b, which turns beta_slow times

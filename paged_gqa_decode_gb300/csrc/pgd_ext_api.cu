@@ -102,6 +102,7 @@ int pgdx_rotary_init(const pgdx_rotary_config* c, pgdx_rotary* out) {
   const double two_pi = 6.283185307179586476925286766559;
   double theta = c->theta, factor = c->attention_factor;
   if (kind == PGDX_ROTARY_NTK) theta *= std::pow(c->factor, (double)rd / (rd - 2));
+  if (!std::isfinite(theta)) return PGD_EINVAL;
   const double log_theta = std::log(theta);
   double a = 0.0, b = 0.0;
   if (kind == PGDX_ROTARY_YARN) {

@@ -37,3 +37,11 @@ def test_more_than_the_per_token_grid_holds_is_refused(ext, dims):
         assert attend(ext, True, kernel, **dims) in (pgd.ECUDA, pgd.EWORKSPACE)
     fewer = {k: 65535 for k in dims}
     assert attend(ext, False, pgd.KERNEL_AUTO, **fewer) in (pgd.ECUDA, pgd.EWORKSPACE)
+
+
+def test_a_scaled_base_past_the_range_of_doubles_is_refused():
+    for theta, factor in ((1e300, 1e10), (1e10, 1e300)):
+        with pytest.raises(pgd.PgdError) as e:
+            pgd.Rotary(64, theta, scaling="ntk", factor=factor)
+        assert e.value.status == pgd.EINVAL
+    assert pgd.Rotary(64, 1e10, scaling="ntk", factor=1e4).plan.turns[0] > 0
