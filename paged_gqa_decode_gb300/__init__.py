@@ -761,6 +761,8 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
     with _on_device(dev):
         if out is None:
             out = _result(q.shape, _BF16, dev, stream)
+        elif out.shape != q.shape or out.dtype != torch.bfloat16:
+            raise ValueError("out must be bf16 shaped like q")
         if workspace is None:  # (one that is given is checked by the call)
             need = lib.pgd_paged_decode_workspace_bytes(ctypes.byref(dims), ctypes.byref(opts))
             workspace = _scratch((max(need, 16),), torch.uint8, dev, stream)

@@ -221,3 +221,18 @@ def test_refused_calls_of_many_tokens_leave_the_pools(softcap):
     assert not b.k_pool.any() and not b.v_pool.any() and pgd.get_device_error() == pgd.OK
 
 
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("softcap", [0.0, 9.0])
+def test_dense_rows_check_their_output(step, softcap):
+    cache = [torch.zeros(2, 2, 64, 64, device=DEV).bfloat16() for _ in range(2)]
+    q, n = torch.ones(2, 8, 64, device=DEV).bfloat16(), i32([3, 5])
+    k = torch.ones(2, 2, 64, device=DEV).bfloat16()
+    for out in (q[:1].clone(), q.float(), q.view(2, 64, 8)):
+        with pytest.raises(ValueError, match="out"):
+            if step:
+                pgd.decode_rows_step(q, k, k, *cache, n, softcap=softcap, out=out)
+            else:
+                pgd.decode_rows_attention(q, *cache, n, softcap=softcap, out=out)
+    assert not cache[0].any()
+
+
