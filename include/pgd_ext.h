@@ -129,7 +129,8 @@ PGD_API int pgdx_rotary_init(const pgdx_rotary_config* config, pgdx_rotary* rota
  *                leave q out (num_q_heads is then not used).
  *   q            bf16 [P] rows of [Hq][D] at q_stride values apart, or NULL.
  *   q_out        bf16 [P][Hq][D] contiguous; may be q itself when q_stride ==
- *                Hq * D (in place), and must not overlap it otherwise.
+ *                Hq * D (in place), and must not overlap it otherwise, nor k_new
+ *                or v_new.
  *   k_new, v_new bf16 [P] rows of [Hkv][D] at k_stride, v_stride values apart
  *                (views of one fused projection: strides of (Hq + 2 Hkv) * D).
  *                Strides are multiples of 8 values and at least a row long.

@@ -15,6 +15,17 @@ bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
   return x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
 }
 
+// Whether a token's `row` values of the bf16 tensor x (rows of them, `stride` values
+// apart, stride >= row) share a byte with the `n` values at y.
+bool rows_overlap(const void* x, int64_t rows, int64_t stride, int64_t row, const void* y,
+                  int64_t n) {
+  // in values: the first row that ends past y, against y's end
+  const int64_t at = ((int64_t)reinterpret_cast<uintptr_t>(y) -
+                      (int64_t)reinterpret_cast<uintptr_t>(x)) / 2;  // (both 16-byte aligned)
+  const int64_t first = at < row ? 0 : (at - row) / stride + 1;
+  return first < rows && first * stride < at + n;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -175,6 +186,10 @@ int pgdx_rotary_append(const pgd_dims* dims, const pgdx_rotary* rotary, const vo
     const uintptr_t x_end = x + 2 * ((uintptr_t)(dims->rows - 1) * q_stride + q_row);
     const uintptr_t y_end = y + 2 * (uintptr_t)dims->rows * q_row;
     if (x == y ? q_stride != q_row : (x < y_end && y < x_end)) return PGD_EINVAL;
+    // k and v are read while q_out is written
+    if (rows_overlap(k_new, dims->rows, k_stride, kv_row, q_out, dims->rows * q_row) ||
+        rows_overlap(v_new, dims->rows, v_stride, kv_row, q_out, dims->rows * q_row))
+      return PGD_EINVAL;
   }
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev)) != PGD_OK) return rc;

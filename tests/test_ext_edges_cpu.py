@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import paged_gqa_decode_gb300 as pgd
 
@@ -45,3 +46,41 @@ def test_a_scaled_base_past_the_range_of_doubles_is_refused():
             pgd.Rotary(64, theta, scaling="ntk", factor=factor)
         assert e.value.status == pgd.EINVAL
     assert pgd.Rotary(64, 1e10, scaling="ntk", factor=1e4).plan.turns[0] > 0
+
+
+def rotate(ext, *, rows, k_at, v_at, k_stride, v_stride, q_out):
+    """4 query and 2 kv heads of 64 (rows of 256 and 128 values); places in bytes of one buffer."""
+    buf = ctypes.create_string_buffer(1 << 16)
+    at = (ctypes.addressof(buf) + 15) & ~15
+    d = pgd.make_dims(rows=rows, num_q_heads=4, num_kv_heads=2, head_dim=64, num_pages=4,
+                      max_pages_per_row=2)
+    far = at + 40000
+    return ext.pgdx_rotary_append(ctypes.byref(d), ctypes.byref(pgd.Rotary(64, 1e4).plan),
+                                  far, 256, at + q_out, at + k_at, k_stride, at + v_at, v_stride,
+                                  at, 2, None, at, None, at, at, None)
+
+
+# k rows of 128 values: bytes [k_at + 2 i k_stride, + 256)
+@pytest.mark.parametrize("rows,k_at,k_stride,q_out,hit", [
+    (2, 4096, 128, 2048, False),      # q_out [2048, 3072) before k
+    (2, 4096, 128, 3088, True),       # reaches k's first row by 16 bytes
+    (2, 4096, 128, 3072, False),      # ends where k begins
+    (2, 4096, 128, 4592, True),       # k's last 16 bytes
+    (2, 4096, 128, 4608, False),      # k ends where it begins
+    (2, 4096, 1024, 4352, False),     # in the gap between k's rows: [4352, 5376) of [4352, 6144)
+    (2, 4096, 1024, 5120, False),
+    (2, 4096, 1024, 5136, True),      # reaches the second row
+    (2, 4096, 1024, 4336, True),      # the first row's end
+    (2, 4096, 1024, 6384, True),      # the second row's end
+    (2, 4096, 1024, 6400, False),
+    (1, 4096, 1024, 4352, False),     # a fused projection of one token: q, k, v in a row
+    (3, 0, 128, 512, True),
+])
+def test_rotary_append_refuses_a_q_out_over_k_or_v(ext, rows, k_at, k_stride, q_out, hit):
+    kw = dict(rows=rows, q_out=q_out)
+    for call in (dict(k_at=k_at, k_stride=k_stride, v_at=30000, v_stride=128),
+                 dict(v_at=k_at, v_stride=k_stride, k_at=30000, k_stride=128)):
+        if hit:
+            assert rotate(ext, **call, **kw) == pgd.EINVAL
+        elif not torch.cuda.is_available():  # (with a device it would be launched)
+            assert rotate(ext, **call, **kw) == pgd.ECUDA
