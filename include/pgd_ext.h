@@ -202,10 +202,9 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * some 14 us of the per-token kernel, with key parts for few items; else per
  * token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).  TENSOR_CORE takes
  * at most 65535 tokens and kv heads (else PGD_EUNSUPPORTED); AUTO takes more in blocks.
- * PREFILL_UMMA rounds each weight to bf16 once (TENSOR_CORE, per token, carries
- * its residual too), and with a softcap up to 52 and no bias multiplies V by
- * weights up to 2^76 before it divides: |V| up to 2^31 stays in range over a
- * million keys.
+ * Both take weights as a bf16 head and residual.  PREFILL_UMMA, with a softcap up
+ * to 52 and no bias, multiplies V by weights up to 2^76 before it divides: |V| up
+ * to 2^31 stays in range over a million keys.
  */
 PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
                                const void* q, const void* k_new, const void* v_new, void* k_pool,

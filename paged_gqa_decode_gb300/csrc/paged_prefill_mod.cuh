@@ -51,9 +51,10 @@
 //   - masked keys are taken out 16 at a time, only where a row of the warp has
 //     one (64 selects on every boundary page, in a copy of the page code: 113 us,
 //     so 92, for prompts of documents with a prefix and a window);
-//   - P is rounded to bf16 once, without a residual product: an output is off
-//     by at most 2^-8 sum_j p_j |v_j| and typically by as much again as its own
-//     rounding to bf16; the row sums take the unrounded values;
+//   - P is a bf16 head and residual, as in the other attention kernels, and P V two
+//     chains of products: rounded to bf16 once an output would be off by as much
+//     again as by its own rounding (0.0024 of the outputs' norm, of 0.0017), for
+//     289 us in place of 239 with a cap and 273 of 232 without on the chunks below;
 //   - a tile without rows of a run (a block that reaches into another row or
 //     document) takes no part in it.
 //
@@ -66,10 +67,11 @@
 //   11    V pages.
 // Shared memory: K and V rings of page tiles (four each at head_dim 128, eight
 // at 64), Q (two buffers at 64, so that the next item's is there early); 192 KB
-// of both.  TMEM: O_t at t D, then S of (tile, page mod 2), 64 columns each; P, 32
-// columns of bf16 pairs, over the first half of its S, so S of the page after next
-// waits for P V.  (P in columns of its own, S free once read and tried pages kept
-// in registers: 274 us, of 265; 474 of 421 at head_dim 64.)
+// of both.  TMEM: O_t at t D, then S of (tile, page mod 2), 64 columns each; P's
+// heads, 32 columns of bf16 pairs, over the first half of its S and its residuals over
+// the second, so S of the page after next waits for P V.  (With heads alone, P in
+// columns of its own, S free once read and tried pages kept in registers: 274 us, of
+// 265; 474 of 421 at head_dim 64.)
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
@@ -114,7 +116,7 @@ struct ModPrefillCfg {
   static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 0, kSCol = kTiles * D;
-  // S of (tile t, page i): kSCol + (2 t + i % 2) kPage; P, bf16 pairs, over its first half
+  // S of (tile t, page i): kSCol + (2 t + i % 2) kPage; P over it, bf16 pairs: heads, residuals
   static constexpr uint32_t kIdescS = umma_idesc_bf16(128, kPage, 0, 0);
   static constexpr uint32_t kIdescPV = umma_idesc_bf16(128, D, 0, 1);
   static_assert(D == 64 || D == 128, "head_dim");
@@ -722,9 +724,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               const uint32_t pa = tmem + C::kSCol + b * kPage;
               if (elect_lane()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                for (int kk = 0; kk < 8; ++kk)  // P's heads, then its residuals
                   umma_bf16_tmem_a(tmem + C::kOCol + t * D, pa + 8 * kk,
-                                   umma_desc_advance(vd, kk * 2048), C::kIdescPV,
+                                   umma_desc_advance(vd, (kk & 3) * 2048), C::kIdescPV,
                                    !(n == 0 && kk == 0));
                 umma_commit(&o_done[b]);
               }
@@ -876,8 +878,9 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
                                    row_max(*reinterpret_cast<float(*)[16]>(&sv[16 * q])));
             return top;
           };
-          // P = exp2(scores + offset) of a block, to w; added to the sums
-          uint32_t w[kPage / 2];
+          // P = exp2(scores + offset) of a block, as bf16 heads to w and residuals to
+          // wl; added to the sums
+          uint32_t w[kPage / 2], wl[kPage / 2];
           float2 sum2[4];
           auto exp_block = [&](int q, float offset) {
             if (q == 0) {
@@ -890,7 +893,11 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               if constexpr (kBias) y = __fadd2_rn(y, make_float2(offset, offset));
               const float2 x = make_float2(exp2_approx(y.x), exp2_approx(y.y));
               sum2[k / 2 & 3] = __fadd2_rn(sum2[k / 2 & 3], x);
-              w[k / 2] = pack_bf16x2(x.x, x.y);
+              const uint32_t h = pack_bf16x2(x.x, x.y);
+              const float2 r = __ffma2_rn(make_float2(bf16_lo(h), bf16_hi(h)),
+                                          make_float2(-1.f, -1.f), x);
+              w[k / 2] = h;
+              wl[k / 2] = pack_bf16x2(r.x, r.y);
             }
           };
           auto page_sum = [&]() {
@@ -900,32 +907,23 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
           };
           bool done = false;
           // Capped scores have a stretch of code of their own for pages without masks
-          // (one chunk: 83 us, of 90; with a bias it costs more instruction fetches
-          // than it saves, 98 of 89 us for prompts of documents).  At head_dim 64 it
-          // goes block by block, the polynomial of one under the exponentials of the
-          // one before (358 us, of 425); at 128 all polynomials go first (241 us, of 274:
-          // the two warps of a sub-partition then share its pipes better).
+          // (one chunk: 95 us, of 105; with a bias it cost more instruction fetches
+          // than it saved, 98 of 89 us for prompts of documents).  It goes block by block,
+          // the polynomial of one under the exponentials of the one before (289 us on
+          // the header's chunks; 302 with all polynomials first).
           constexpr bool kStraight = KIND == kModCap;
           if (kStraight && whole && begun) {
             read_s();
             const float ref = m_run;
-            if constexpr (D == 64) {
 #pragma unroll
-              for (int q = 0; q < kPage / 16; ++q) {
-                usual_block(q, ref);
-                exp_block(q, 0.f);
-              }
-            } else {
-              usual_scores(ref);
+            for (int q = 0; q < kPage / 16; ++q) {
+              usual_block(q, ref);
+              exp_block(q, 0.f);
             }
             const float most2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
             float top = -ref;  // (a first reference that is never raised: nothing to bound)
             if (p.slack_log2 < INFINITY)
               top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
-            if constexpr (D == 128) {
-#pragma unroll
-              for (int q = 0; q < kPage / 16; ++q) exp_block(q, 0.f);
-            }
             const bool held = !live || (!(top > p.slack_log2) && !(most2 > p.limit_near2));
             done = __all_sync(0xffffffffu, held);
             if (done) l += page_sum();
@@ -1019,8 +1017,10 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
             l += page_sum();
           }
 #pragma unroll
-          for (int q = 0; q < kPage / 32; ++q)
+          for (int q = 0; q < kPage / 32; ++q) {
             tmem_st16(s_col + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&w[16 * q]));
+            tmem_st16(s_col + kPage / 2 + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&wl[16 * q]));
+          }
           tmem_wait_st();
           tc_fence_before_sync();
           __syncwarp();

@@ -236,3 +236,22 @@ def test_dense_rows_check_their_output(step, softcap):
     assert not cache[0].any()
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("kw", [dict(first=True), dict(softcap=50.0), dict(alibi=True),
+                                dict(softcap=50.0, alibi=True)], ids=str)
+@pytest.mark.parametrize("cut", [False, True])
+def test_prefill_carries_the_weights_residual(hq, hkv, d, kw, cut):
+    """The bound of the framework's other attention kernels, whose weights are a bf16 head and
+    residual: outputs near cancellation err by far less than a rounded weight would make them."""
+    cached, chunks = ([2370], [140]) if cut else ([0, 5, 300], [40, 70, 45])
+    b = Paged(21, np.add(cached, chunks), hq, hkv, d)
+    rows, positions = packed(cached, chunks)
+    q = b.queries(len(rows))
+    a, c = of_kind(kw, hq, len(rows))
+    out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                      num_kv_heads=hkv, kernel=pgd.KERNEL_AUTO if cut else UMMA,
+                                      **a)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, scale=d ** -0.5, **c)
+
+
