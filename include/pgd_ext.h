@@ -202,9 +202,10 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * some 14 us of the per-token kernel, with key parts for few items; else per
  * token), TENSOR_CORE or PREFILL_UMMA (else PGD_EUNSUPPORTED).  TENSOR_CORE takes
  * at most 65535 tokens and kv heads (else PGD_EUNSUPPORTED); AUTO takes more in blocks.
- * Both take weights as a bf16 head and residual.  PREFILL_UMMA, with a softcap up
- * to 52 and no bias, multiplies V by weights up to 2^76 before it divides: |V| up
- * to 2^31 stays in range over a million keys.
+ * Both take weights as a bf16 head and residual, against a reference near the
+ * row's maximum: PREFILL_UMMA multiplies V by weights up to 2^24 before it divides
+ * (softcap up to 52 without a bias; else 2^8), so |V| up to 2^83 stays in range over
+ * a million keys.
  */
 PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
                                const void* q, const void* k_new, const void* v_new, void* k_pool,

@@ -38,8 +38,8 @@
 //     is read again and the page taken in full (with the maximum first on every
 //     page: 275 us, so 265, on the chunks below, before the issuers' last form;
 //     507 us, so 421, with 64 heads of 64);
-//   - capped scores without a bias lie within the cap: their reference is 0 and
-//     stays it (caps to 52);
+//   - capped scores without a bias lie within the cap: their reference is 0 to
+//     begin with, and scores in the cap's near form never raise it (caps to 52);
 //   - a capped score is a polynomial in s^2 times s plus what the exponent needs
 //     anyway: y = s Q(s^2) - m, four packed instructions for two keys, and the
 //     largest s^2 tells whether it served;
@@ -921,9 +921,8 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               exp_block(q, 0.f);
             }
             const float most2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-            float top = -ref;  // (a first reference that is never raised: nothing to bound)
-            if (p.slack_log2 < INFINITY)
-              top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
+            float top = -ref;  // (where near scores fit: nothing to bound)
+            if (!p.near_fits) top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
             const bool held = !live || (!(top > p.slack_log2) && !(most2 > p.limit_near2));
             done = __all_sync(0xffffffffu, held);
             if (done) l += page_sum();
@@ -940,8 +939,7 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               top = usual_top(ref);
             } else if constexpr (kCap) {
               top = -ref;  // (as above)
-              if (p.slack_log2 < INFINITY)
-                top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
+              if (!p.near_fits) top = fmaf(sqrtf(most2), fabsf(p.q_scale_log2), -ref);
             } else {
               top = row_max(sv);
             }
@@ -981,10 +979,10 @@ __global__ void __launch_bounds__(ModPrefillCfg<D>::kThreads, 1)
               mx = usual ? usual_top(0.f) : row_max(sv);
             }
             // the row's reference, raised when the maximum exceeds it by the slack
-            // (O is then rescaled)
+            // (O is then rescaled; a run's first page finds none)
             float alpha = 1.f;
             if (mx > m_run + p.slack_log2) {
-              alpha = m_run == -INFINITY ? 1.f : exp2_approx(m_run - mx);
+              alpha = m_run == -INFINITY || n == 0 ? 1.f : exp2_approx(m_run - mx);
               l *= alpha;  // (0 before the first key)
               m_run = mx;
             }

@@ -24,8 +24,10 @@ struct ModParams : DecodeParams {
   // scores up to which each form holds (-1: not used)
   float near_q[3], a2, limit_near, limit_mid;
   // tcgen05 prefill: a row's first reference (log2 units; -inf: its first page's
-  // maximum), and by how much a score may exceed the reference before it is raised
+  // maximum), by how much a score may exceed the reference before it is raised, and
+  // whether scores in the cap's near form never do
   float ref_log2, slack_log2, limit_near2;  // (limit_near's square, with its sign)
+  bool near_fits;
   const float* slopes;       // [Hq] or nullptr
   const int32_t* first_key;  // [rows] or nullptr
   const int32_t* prefix_len; // [table_rows] or nullptr

@@ -274,14 +274,16 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   p.limit_near = normal(p.near_q[2]) && normal(c) ? kTanhNear / a : -1.f;
   p.limit_mid = normal(a2) ? kTanhMid / a : -1.f;
   p.limit_near2 = p.limit_near * fabsf(p.limit_near);
-  // Capped scores without a bias stay within the cap, cap_out in log2 units: up
-  // to 76 the prefill takes weights 2^score against a reference of 0 (2^96 for
-  // 2^20 keys at the cap, so |V| up to 2^31 is safe; 2^-76 for keys at the cap's
-  // other end).  Others take the row's maximum, raised when a score exceeds it by
-  // more than 2^8 (each raise is a pass over the row's outputs).
-  const bool fixed = capped && !score->alibi_slopes && p.cap_out <= 76.f;
-  p.ref_log2 = fixed ? 0.f : -INFINITY;
-  p.slack_log2 = fixed ? INFINITY : 8.f;
+  // A row's reference is its first maximum, raised when a score exceeds it by more
+  // than 2^8 (each raise is a pass over the row's outputs).  Capped scores without a
+  // bias stay within the cap, cap_out in log2 units: up to 76 their reference is 0 to
+  // begin with, weights no less than 2^-76, and is raised past 2^24, which a score in
+  // the cap's near form (0.3 of 76) does not reach, so that pages in that form need no
+  // look at it.  Weights up to 2^24 of 2^20 keys leave |V| up to 2^83 in range.
+  p.near_fits = capped && !score->alibi_slopes && p.cap_out <= 76.f;
+  static_assert(kTanhNear * 76.f < 24.f, "near scores within the slack");
+  p.ref_log2 = p.near_fits ? 0.f : -INFINITY;
+  p.slack_log2 = p.near_fits ? 24.f : 8.f;
   p.slopes = score->alibi_slopes;
   p.first_key = score->first_key;
   p.prefix_len = score->prefix_len;

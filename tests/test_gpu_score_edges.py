@@ -255,3 +255,28 @@ def test_prefill_carries_the_weights_residual(hq, hkv, d, kw, cut):
     check(out, b, q, rows, positions, scale=d ** -0.5, **c)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap", [20.0, 50.0, 52.6, 53.0])
+@pytest.mark.parametrize("log2_v", [-30, 40, 80])
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_TENSOR_CORE, UMMA])
+def test_capped_scores_with_values_of_any_size(d, softcap, log2_v, far, kernel):
+    """Scores as they come, or (far) all near the cap, where weights are at their largest."""
+    b = Paged(22, [400, 65], 8, 2, d, scale_v=2.0 ** log2_v)
+    if far:
+        for r, n in enumerate(b.lengths):
+            k = (torch.from_numpy(b.k_rows[r]).abs() + 0.5).bfloat16()
+            b.k_rows[r] = k.double().numpy()
+            b.write(b.k_pool, [r] * n, range(n), k.transpose(0, 1).to(DEV))
+    rows, positions = packed([200, 0], [200, 65])
+    q = b.queries(265)
+    if far:
+        q = q.abs() + 0.25
+    scale = softcap / d if far else d ** -0.5
+    out = pgd.paged_prefill_attention(q, b.k_pool, b.v_pool, b.table, i32(rows), i32(positions),
+                                      None, 0, scale, num_kv_heads=2, softcap=softcap,
+                                      kernel=kernel)
+    assert pgd.get_device_error() == pgd.OK
+    check(out, b, q, rows, positions, scale=scale, softcap=softcap, rounded=True)
+
+
