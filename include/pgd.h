@@ -184,7 +184,8 @@ PGD_API int pgd_page_slots(const pgd_dims* dims, int32_t table_rows, const int32
  * kv_write_slots -- prefill's write_tokens at caller-given places (Mistral 7B
  * Instruct v0.3 model files, src/attention.linnet, prefill_paged: each
  * packed prompt token is written at its place in the pool, `slots`).
- *   dims->rows    P tokens; dims->max_pages_per_row is not used.
+ *   dims->rows    P tokens; dims->max_pages_per_row is the pages of a dense row with
+ *                 PGD_ROW_MAJOR, and not used otherwise.
  *   k_new, v_new  bf16 [P][Hkv][D].
  *   slots         int32 [P]: pool position slot = page * 64 + offset, the
  *                 same numbering page_slots produces; < 0: padding, skipped.

@@ -206,6 +206,10 @@ PGD_API int pgdx_paged_decode(const pgd_dims* dims, const pgdx_score* score, con
  * row's maximum: PREFILL_UMMA multiplies V by weights up to 2^24 before it divides
  * (softcap up to 52 without a bias; else 2^8), so |V| up to 2^83 stays in range over
  * a million keys.
+ * A token's result may change in its last bits with the tokens beside it in the pass
+ * (its weights by 2^-20 of the softcap, or 2^-16, relative): AUTO's kernel and key parts
+ * go by the call's sizes, and the 32 (token, head) rows of a PREFILL_UMMA warp choose
+ * the forms of the cap and of the bias together.  Equal calls give equal bits.
  */
 PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_score* score,
                                const void* q, const void* k_new, const void* v_new, void* k_pool,
