@@ -60,20 +60,20 @@ def rotate(ext, *, rows, k_at, v_at, k_stride, v_stride, q_out):
                                   at, 2, None, at, None, at, at, None)
 
 
-# k rows of 128 values: bytes [k_at + 2 i k_stride, + 256)
+# q_out is 1024 bytes of two tokens; k rows of 128 values: bytes [k_at + 2 i k_stride, + 256)
 @pytest.mark.parametrize("rows,k_at,k_stride,q_out,hit", [
-    (2, 4096, 128, 2048, False),      # q_out [2048, 3072) before k
-    (2, 4096, 128, 3088, True),       # reaches k's first row by 16 bytes
-    (2, 4096, 128, 3072, False),      # ends where k begins
-    (2, 4096, 128, 4592, True),       # k's last 16 bytes
-    (2, 4096, 128, 4608, False),      # k ends where it begins
-    (2, 4096, 1024, 4352, False),     # in the gap between k's rows: [4352, 5376) of [4352, 6144)
-    (2, 4096, 1024, 5120, False),
-    (2, 4096, 1024, 5136, True),      # reaches the second row
-    (2, 4096, 1024, 4336, True),      # the first row's end
-    (2, 4096, 1024, 6384, True),      # the second row's end
-    (2, 4096, 1024, 6400, False),
-    (1, 4096, 1024, 4352, False),     # a fused projection of one token: q, k, v in a row
+    (2, 6144, 128, 2048, False),      # q_out far before k
+    (2, 6144, 128, 5136, True),       # reaches k's first row by 16 bytes
+    (2, 6144, 128, 5120, False),      # ends where k begins
+    (2, 6144, 128, 6640, True),       # k's last 16 bytes
+    (2, 6144, 128, 6656, False),      # k ends where it begins
+    (2, 6144, 1024, 6400, False),     # in the gap between k's rows, from 6400 to 8192
+    (2, 6144, 1024, 7168, False),
+    (2, 6144, 1024, 7184, True),      # reaches the second row
+    (2, 6144, 1024, 6384, True),      # the first row's end
+    (2, 6144, 1024, 8432, True),      # the second row's end
+    (2, 6144, 1024, 8448, False),
+    (1, 6144, 1024, 6400, False),     # a fused projection of one token: q, k, v in a row
     (3, 0, 128, 512, True),
 ])
 def test_rotary_append_refuses_a_q_out_over_k_or_v(ext, rows, k_at, k_stride, q_out, hit):
