@@ -62,7 +62,9 @@ typedef struct CUstream_st* pgd_stream_t;
 enum {
   PGD_OK = 0,
   PGD_EINVAL = 1,          /* NULL pointer, bad shape, misaligned pointer */
-  PGD_EUNSUPPORTED = 2,    /* head_dim not 64/128, page_size not 64, group > 8 */
+  PGD_EUNSUPPORTED = 2,    /* head_dim not 64/128, page_size not 64, group > 8; more than
+                              65535 rows or kv heads for the per-token split kernel (AUTO
+                              takes a prefill of so many tokens in blocks) */
   PGD_ECUDA = 3,           /* a CUDA runtime or driver call failed */
   PGD_EDEVICE_BOUNDS = 4,  /* device: table entry or position out of range */
   PGD_EDEVICE_TIMEOUT = 5, /* device: a pipeline wait gave up (bounded waits) */

@@ -439,7 +439,7 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
     opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
     if out is None:
-        out = _result(q.shape, _BF16, dev, stream)
+        out = torch.empty_like(q) if stream is None else _result(q.shape, _BF16, dev, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16:
         raise ValueError("out must be bf16 shaped like q")
     if workspace is None:  # (one that is given is checked by the call)
@@ -632,7 +632,7 @@ def _prefill(q, k_new, v_new, k_pool, v_pool, table, rows, positions, sinks, win
     opts = ctypes.byref(_opts_of(pages_per_split, kernel))
     lib = load_library()
     if out is None:
-        out = _result(q.shape, _BF16, dev, stream)
+        out = torch.empty_like(q) if stream is None else _result(q.shape, _BF16, dev, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16:
         raise ValueError("out must be bf16 shaped like q")
     if workspace is None:  # (one that is given is checked by the call)
@@ -760,7 +760,7 @@ def _decode_rows(q, k_new, v_new, cache_k, cache_v, positions, sinks, window, sc
     lib = load_library()
     with _on_device(dev):
         if out is None:
-            out = _result(q.shape, _BF16, dev, stream)
+            out = torch.empty_like(q) if stream is None else _result(q.shape, _BF16, dev, stream)
         elif out.shape != q.shape or out.dtype != torch.bfloat16:
             raise ValueError("out must be bf16 shaped like q")
         if workspace is None:  # (one that is given is checked by the call)

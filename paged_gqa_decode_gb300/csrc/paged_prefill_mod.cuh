@@ -36,8 +36,8 @@
 //     before them.  Where it did not hold for a row of the warp -- a run's first
 //     page, a larger score, keys past the query with a bias -- S, still in TMEM,
 //     is read again and the page taken in full (with the maximum first on every
-//     page: 275 us, so 265, on the chunks below, before the issuers' last form;
-//     507 us, so 421, with 64 heads of 64);
+//     page: 275 us, so 265, on the chunks below, before the issuers' last form and
+//     the residual; 507 us, so 421, with 64 heads of 64);
 //   - capped scores without a bias lie within the cap: their reference is 0 to
 //     begin with, and scores in the cap's near form never raise it (caps to 52);
 //   - a capped score is a polynomial in s^2 times s plus what the exponent needs
@@ -75,17 +75,20 @@
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
-// up to 8192, 2.6e11 operations): 241 us capped, 1084 TFLOP/s, 231 without a cap,
-// 276 with cap and bias (the one-SM kernel takes 334 us without a cap, 569 with
-// the cap built into it); 64 / 8 heads of 64: 358 capped, 299 without.  One chunk
-// behind 8000 positions 83 us; prompts of documents with prefix, window and bias
-// 89 us.  A page takes about 1900 cycles: 1000 of the softmax warps' work (two
-// share a sub-partition), 1280 of the tensor cores at head_dim 128 (640 at 64),
-// and the way from P through P V and the next S back to the softmax.  Tried and
-// left out: reading the next page's S while this one's exponentials run (311 us,
-// of 309 then); a first reference from the raw products instead of the full path
-// on a run's first page (252 of 246, 106 of 89); polling instead of suspended
-// waits (the same); scalar instead of packed arithmetic for the cap (438 of 403).
+// up to 8192, 2.6e11 operations): 289 us capped, 904 TFLOP/s (310 after seconds of
+// it, at the clocks the power limit then leaves), 273 without a cap, 280 with a bias,
+// 306 with both (the one-SM kernel takes 334 us without a cap, 569 with the cap built
+// into it); 64 / 8 heads of 64 behind up to 4000: 248 capped, 206 without, 224 with a
+// bias, 297 with both.  One chunk behind 8000 positions 95 us; prompts of documents
+// with prefix, window and bias 100 us.  A page takes about 2300 cycles: 1790 of the
+// tensor cores at head_dim 128 (48 a product of S, 64 of P V, 0.29 of it the
+// residual's; ncu: active for 65 % of the cycles), fewer at 64; instructions
+// issued in 49 %; and the way from P through P V and the next S back to the softmax.
+// Tried and left out, with P rounded once (16-21 % faster then): reading the next
+// page's S while this one's exponentials run (311 us, of 309 then); a first reference
+// from the raw products instead of the full path on a run's first page (252 of 246,
+// 106 of 89); polling instead of suspended waits (the same); scalar instead of packed
+// arithmetic for the cap (438 of 403).
 //
 // Every wait is bounded; a timeout records PGD_EDEVICE_TIMEOUT, stops all
 // roles, drains in-flight copies and MMAs and frees TMEM before the CTA exits.

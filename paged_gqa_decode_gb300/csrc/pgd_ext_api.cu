@@ -297,11 +297,12 @@ static int attention_impl(const pgd_dims* dims, int32_t table_rows, const int32_
   if (kernel == PGD_KERNEL_PREFILL_PAIR || (prefill && !per_token_fits(dims)))
     kernel = PGD_KERNEL_PREFILL_UMMA;  // (the pair: AUTO's only)
   // AUTO takes a prefill of little work token by token: that costs about 5 us and
-  // 4 + 2.2 pages ns for each token and kv head (pages: the most that one may
-  // span), the tcgen05 kernel 12 us at least.  156 tokens over 800 positions with 2
-  // kv heads 17 us so, 27 in blocks; 9 tokens over 1660 with 8 heads 6 and 12; 178
-  // tokens, 2 heads, window 12, 7 and 17; but 274, 8 heads, window 6, 21 and 23, and
-  // 372, window 64, 27 and 18.5.
+  // 4 + 2.2 pages ns for each token and kv head (pages: the most that one may span;
+  // the width of the table, so that a short context in a wide one stays with the
+  // blocks), the tcgen05 kernel 12 us at least.  On tables as wide as the context: 156
+  // tokens over 800 positions with 2 kv heads 17 us so, 27 in blocks; 9 tokens over
+  // 1660 with 8 heads 6 and 12; 178 tokens, 2 heads, window 12, 7 and 17; but 274, 8
+  // heads, window 6, 21 and 23, and 372, window 64, 27 and 18.5.
   if (asked == PGD_KERNEL_AUTO && kernel == PGD_KERNEL_PREFILL_UMMA && per_token_fits(dims) &&
       (double)dims->rows * dims->num_kv_heads * (4.0 + 2.2 * span_pages(dims, bound)) < 14000.0)
     kernel = PGD_KERNEL_TENSOR_CORE;
