@@ -1,9 +1,9 @@
 // Decode kernels for modified scores (paged_score.cuh) at one head_dim: the
 // split kernel of paged_decode.cuh with the tensor-core consumer, its ring no
 // deeper than the pages a split can stream.  As that bound by the copies of K and
-// V: 64 rows of 512 to 4096 positions, 64 / 8 heads of 64, capped, 55.5 us (303 MB,
-// 5.5 TB/s; 53.7 us uncapped), 64 rows of 1024 to 16384, 32 / 8 heads of 128, with a
-// bias and documents, 189 us (1.25 GB, 6.6 TB/s).
+// V: 64 rows of 512 to 4096 positions, 64 / 8 heads of 64, capped, 55.5-57 us (303 MB,
+// 5.4 TB/s; 53.7 us uncapped), 64 rows of 1024 to 16384, 32 / 8 heads of 128, with a
+// bias and documents, 189-193 us (1.25 GB, 6.5 TB/s).
 #pragma once
 
 #include "paged_decode.cuh"
