@@ -75,7 +75,7 @@
 // Key parts as in the one-SM kernel.
 //
 // Measured (32 / 8 heads of 128, eight prompt chunks of up to 512 tokens behind
-// up to 8192, 2.6e11 operations): 289 us capped, 904 TFLOP/s (310 after seconds of
+// up to 8192, 2.6e11 operations): 289 us capped, 904 TFLOP/s (315 after seconds of
 // it, at the clocks the power limit then leaves), 273 without a cap, 280 with a bias,
 // 306 with both (the one-SM kernel takes 334 us without a cap, 569 with the cap built
 // into it); 64 / 8 heads of 64 behind up to 4000: 248 capped, 206 without, 224 with a
