@@ -8,7 +8,12 @@
  *     the head, scaled frequencies) on q and k, fused with the paged append;
  *   - pgdx_paged_decode, pgdx_paged_prefill: the attention of pgd.h with a
  *     tanh score cap, a distance bias, a first visible key per token
- *     (documents) and, for prefill, a bidirectional prefix.
+ *     (documents) and, for prefill, a bidirectional prefix;
+ *   - pgdx_fork_rows, pgdx_copy_pages, pgdx_compact_pages: table rows that
+ *     share pages -- forked, reordered (beam search), cut back and released
+ *     over reference counts -- page copies, and the pool's compaction;
+ *   - pgdx_shared_decode: decode attention of rows that share their first
+ *     pages, which are read once for all of them.
  *
  * The conventions are those of pgd.h: its types, dims, options, status codes,
  * layouts, alignment (16 bytes for bf16 tensors and the workspace; int32 and
@@ -217,6 +222,122 @@ PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const p
                                const int32_t* positions, const float* sinks, int32_t window,
                                float scale, void* out, void* workspace, size_t workspace_bytes,
                                const pgd_decode_options* opts, pgd_stream_t stream);
+
+/*
+ * fork_rows -- makes each table row a copy of an old row (its parent), cut to the
+ * positions it keeps, over reference-counted pages: forks (parents[r] = the
+ * row forked), beam search's reordering (any map), releases (parents[r] = -1) and
+ * cuts (keep) in one call.
+ *   rows         R in 0 .. 12288; max_pages_per_row: W, R * W <= 2^30.
+ *   table        int32 [R][W], read and rewritten in place: row i's first
+ *                ceil(lengths[i] / 64) entries are its pages.
+ *   lengths      int32 [R]: positions of each row in the cache.
+ *   parents      int32 [R]: the old row that row r continues, or -1: row r gets none.
+ *   keep         int32 [R]: row r keeps its parent's first keep[r] positions (all
+ *                of them if it has fewer; below 0: none), or NULL: all.
+ *   shares       int32 [num_pages], read and written: how many rows hold each page
+ *                beyond the first (0: held once, or free; pgdx_assign_pages hands
+ *                out free pages, whose shares are 0).
+ *   free_pages   int32 [num_free], free_head: the list as for pgdx_assign_pages, here
+ *                read and written: pages are taken from index *free_head on and
+ *                given back below it.
+ * Row r gets the length n = min(lengths[parent], keep) and the parent's first
+ * ceil(n / 64) entries (entries past them stay as they are).  Shares follow.
+ * Pages that no row holds any more are given back, first of all, in the order
+ * of the old entries (row by row) that held them first: to indices *free_head - their
+ * count .. *free_head - 1.  Then a last page in part use (n % 64 != 0) becomes the
+ * row's own, for its next positions to be written there: where all that hold the
+ * page hold it so, the lowest row keeps it; each other row takes the next free
+ * page, in row order, and leaves the copy to pgdx_copy_pages:
+ *   sources, targets, counts  int32 [R]: row r's page to copy from and to and its
+ *                positions in use (n % 64), or -1, -1, 0.
+ *   new_lengths  int32 [R]: n.
+ *   free_head_out  int32 [1]: the list's next page afterwards.
+ * Outputs must not overlap each other or an input (table, shares and free_pages
+ * count as outputs).
+ * Device errors (PGD_EDEVICE_BOUNDS): a length outside [0, 64 W] (taken as 0); a parent
+ * outside [-1, R) (taken as -1); an entry outside the pool (its page is not
+ * counted); a page given back more often than held; no page, or one outside the pool,
+ * for a last page's copy, or a last page outside the pool: the row loses that page, its
+ * new length is rounded down to whole pages; a *free_head outside [0, num_free]: nothing is taken
+ * or given back; a list with too few places below *free_head: the pages without one are lost to it.
+ */
+PGD_API int pgdx_fork_rows(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
+                           int32_t* table, const int32_t* lengths, const int32_t* parents,
+                           const int32_t* keep, int32_t* shares, int32_t* free_pages,
+                           int32_t num_free, const int32_t* free_head, int32_t* new_lengths,
+                           int32_t* sources, int32_t* targets, int32_t* counts,
+                           int32_t* free_head_out, pgd_stream_t stream);
+
+/*
+ * copy_pages -- copies the first counts[i] positions of page sources[i] to page
+ * targets[i], for all kv heads, in the K and V pools of each layer.
+ *   dims         num_kv_heads, head_dim, num_pages and layout (PAGE_MAJOR or HEAD_MAJOR,
+ *                else PGD_EUNSUPPORTED) of every pool; the rest is not used but checked.
+ *   layers       L >= 0; k_pools, v_pools: host arrays of L device pointers.
+ *   copies       n >= 0; sources, targets, counts: int32 [n]; counts NULL: 64.
+ * A negative source or target: no copy.  A page that is a target must not be named
+ * by another copy (pgdx_fork_rows' and pgdx_compact_pages' copies never are).
+ * Device errors: a page outside the pool or a count outside [0, 64]
+ * (PGD_EDEVICE_BOUNDS): that copy is left out.
+ */
+PGD_API int pgdx_copy_pages(const pgd_dims* dims, int32_t layers, void* const* k_pools,
+                            void* const* v_pools, int32_t copies, const int32_t* sources,
+                            const int32_t* targets, const int32_t* counts, pgd_stream_t stream);
+
+/*
+ * compact_pages -- moves held pages to the lowest free ones: with k counting from
+ * 0, the k-th highest page held by a row goes to the k-th lowest page listed as
+ * free, as long as that is lower and k < max_moves.  Pages neither held nor listed
+ * stay as they are.
+ *   table, lengths, shares, free_pages, free_head: as for pgdx_fork_rows; every row that
+ *                holds pages is in the table.
+ *   new_table    int32 [R][W]: the table with the pages' new names (entries past a row's
+ *                pages copied); new_shares int32 [num_pages]; new_free int32
+ *                [num_free]: from *free_head on the free pages, lowest first,
+ *                before it copied.  Each may be its input.
+ *   sources, targets  int32 [max_moves]: the copies, for pgdx_copy_pages; -1 past the last.
+ *   end          int32 [1]: 1 + the highest page held afterwards (0: none).
+ *   workspace    pgdx_compact_workspace_bytes(num_pages) bytes.
+ * Otherwise outputs must not overlap each other or an input.
+ * Device errors (PGD_EDEVICE_BOUNDS; nothing is moved then): a length outside [0, 64 W], an
+ * entry or a listed page outside the pool, a page listed twice or both listed and
+ * held, a *free_head outside [0, num_free].
+ */
+PGD_API size_t pgdx_compact_workspace_bytes(int32_t num_pages);
+PGD_API int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
+                               const int32_t* table, const int32_t* lengths,
+                               const int32_t* shares, const int32_t* free_pages, int32_t num_free,
+                               const int32_t* free_head, int32_t max_moves, int32_t* new_table,
+                               int32_t* new_shares, int32_t* new_free, int32_t* sources,
+                               int32_t* targets, int32_t* end, void* workspace,
+                               size_t workspace_bytes, pgd_stream_t stream);
+
+/*
+ * shared_decode -- pgd_paged_decode_attention (k_new and v_new NULL) or
+ * pgd_paged_decode_step (both given), full attention, for rows in groups that share
+ * their first pages: the rows b of group g, group_starts[g] <= b < group_starts[g + 1],
+ * hold the same first group_pages[g] pages, which are read once for all of them (out of
+ * the table row of group_starts[g], or of another of its rows).
+ *   groups       S in 0 .. 8192; group_starts int32 [S + 1], not decreasing, in [0, rows];
+ *                group_pages int32 [S].  Rows in no group are read on their own.
+ *   dims         rows at most 65535; layout PAGE_MAJOR or HEAD_MAJOR (else PGD_EUNSUPPORTED).
+ *   workspace    pgdx_shared_decode_workspace_bytes(dims, groups) bytes (0 for dims or groups
+ *                that the call refuses).
+ * Everything else, inactive rows among it, as there.  Device errors
+ * (PGD_EDEVICE_BOUNDS, the rows concerned give zeros, a step leaves them unwritten): starts
+ * that decrease or lie outside (all rows), group_pages outside [0, max_pages_per_row] (its
+ * rows), a row whose position is beyond its table or in its group's pages, a page outside
+ * the pool.  A step writes its rows' keys and values to pages of their own: two rows must
+ * not hold the page of their positions together.
+ */
+PGD_API size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups);
+PGD_API int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* group_starts,
+                               const int32_t* group_pages, const void* q, const void* k_new,
+                               const void* v_new, void* k_pool, void* v_pool,
+                               const int32_t* table, const int32_t* positions, const float* sinks,
+                               float scale, void* out, void* workspace, size_t workspace_bytes,
+                               pgd_stream_t stream);
 
 /* As pgd_get_device_error, for this library's error word. */
 PGD_API int pgdx_get_device_error(pgd_stream_t stream);

@@ -24,7 +24,14 @@ Entry points (same names as the C ABI, without the ``pgd_`` / ``pgdx_`` prefix):
 - decode, prefill and their steps take ``softcap`` (tanh score cap),
   ``alibi_slopes`` (distance bias), ``first_key`` (documents) and, for prefill,
   ``prefix_len`` (bidirectional prefixes); without them they are libpgd's.
-- ``paged_decode_workspace_bytes``, ``get_device_error``.
+- ``fork_rows``: table rows forked, reordered (beam search), cut back and
+  released over reference-counted pages; ``copy_pages``: the copies it leaves to
+  make, in all layers' pools; ``compact_pages``: held pages moved to the pool's
+  lower end.
+- decode and its step take ``group_starts`` and ``group_pages``: rows that share
+  their first pages, which are read once for all of them.
+- ``paged_decode_workspace_bytes``, ``shared_decode_workspace_bytes``,
+  ``get_device_error``.
 """
 from __future__ import annotations
 
@@ -174,10 +181,22 @@ def load_extension(path: str | None = None) -> ctypes.CDLL:
                 tail = [i32, ctypes.c_float, vp, vp, ctypes.c_size_t, opts_p, vp]
                 lib.pgdx_paged_decode.argtypes = [dims_p, score_p] + [vp] * 8 + tail
                 lib.pgdx_paged_prefill.argtypes = [dims_p, i32, score_p] + [vp] * 9 + tail
+                size = ctypes.c_size_t
+                lib.pgdx_fork_rows.argtypes = [i32] * 3 + [vp] * 6 + [i32] + [vp] * 7
+                lib.pgdx_copy_pages.argtypes = [dims_p, i32, vp, vp, i32, vp, vp, vp, vp]
+                lib.pgdx_compact_workspace_bytes.argtypes = [i32]
+                lib.pgdx_compact_pages.argtypes = [i32] * 3 + [vp] * 4 + [i32, vp, i32] + \
+                    [vp] * 7 + [size, vp]
+                lib.pgdx_shared_decode_workspace_bytes.argtypes = [dims_p, i32]
+                lib.pgdx_shared_decode.argtypes = [dims_p, i32] + [vp] * 10 + \
+                    [ctypes.c_float, vp, vp, size, vp]
                 lib.pgdx_get_device_error.argtypes = [vp]
                 for name in ("assign_pages", "rotary_init", "rotary_append", "paged_decode",
-                             "paged_prefill", "get_device_error"):
+                             "paged_prefill", "fork_rows", "copy_pages", "compact_pages",
+                             "shared_decode", "get_device_error"):
                     getattr(lib, "pgdx_" + name).restype = ctypes.c_int
+                for name in ("compact", "shared_decode"):
+                    getattr(lib, f"pgdx_{name}_workspace_bytes").restype = size
                 _ext = lib
     return _ext
 
@@ -351,6 +370,8 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
                            kernel: int = KERNEL_AUTO, softcap: float = 0.0,
                            alibi_slopes: torch.Tensor | None = None,
                            first_key: torch.Tensor | None = None,
+                           group_starts: torch.Tensor | None = None,
+                           group_pages: torch.Tensor | None = None,
                            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Grouped-query decode attention of each row over its pages.
 
@@ -358,8 +379,16 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     table: int32 [R, max_pages]; positions: int32 [R]; sinks: fp32 [Hq] or
     None; window <= 0 for full attention.  softcap > 0: scores softcap *
     tanh(scale q.k / softcap); alibi_slopes (fp32 [Hq]): less slope * distance;
-    first_key (int32 [R]): row b sees positions from first_key[b] on.  Returns
-    bf16 [R, Hq, D]."""
+    first_key (int32 [R]): row b sees positions from first_key[b] on.
+    group_starts (int32 [S + 1]) and group_pages (int32 [S]): rows group_starts[g] ..
+    group_starts[g + 1] - 1 hold the same first group_pages[g] pages, which are read
+    once for all of them (full attention, none of the above; a workspace of
+    shared_decode_workspace_bytes).  Returns bf16 [R, Hq, D]."""
+    if group_starts is not None or group_pages is not None:
+        return _shared_decode(q, None, None, k_pool, v_pool, table, positions, sinks, window,
+                              scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,
+                              stream, _score(softcap, alibi_slopes, first_key), group_starts,
+                              group_pages)
     return _decode(q, None, None, k_pool, v_pool, table, positions, sinks, window, scale,
                    num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
                    _score(softcap, alibi_slopes, first_key))
@@ -374,10 +403,17 @@ def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                       kernel: int = KERNEL_AUTO, softcap: float = 0.0,
                       alibi_slopes: torch.Tensor | None = None,
                       first_key: torch.Tensor | None = None,
+                      group_starts: torch.Tensor | None = None,
+                      group_pages: torch.Tensor | None = None,
                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """kv_append_paged then paged_decode_attention in one launch: each row's
     new K/V (bf16 [R, Hkv, D]) goes to its slot in the pools and the row
     attends over its pages, the new token included."""
+    if group_starts is not None or group_pages is not None:
+        return _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window,
+                              scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,
+                              stream, _score(softcap, alibi_slopes, first_key), group_starts,
+                              group_pages)
     return _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
                    num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream,
                    _score(softcap, alibi_slopes, first_key))
@@ -462,6 +498,71 @@ def _decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, sc
         rc = lib.pgd_paged_decode_step(dims, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                                        k_pool.data_ptr(), v_pool.data_ptr(), *tail)
         what = "paged_decode_step"
+    if rc != OK:
+        raise PgdError(rc, what)
+    return out
+
+
+def shared_decode_workspace_bytes(dims: Dims, groups: int) -> int:
+    """Workspace of a decode call of these dims with group_starts of groups + 1 entries."""
+    return load_extension().pgdx_shared_decode_workspace_bytes(ctypes.byref(dims), groups)
+
+
+def _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window, scale,
+                   num_kv_heads, layout, out, workspace, pages_per_split, kernel, stream, score,
+                   group_starts, group_pages):
+    if group_starts is None or group_pages is None:
+        raise ValueError("group_starts and group_pages go together")
+    if window > 0 or score is not None:
+        raise ValueError("group_starts: full attention, without softcap, alibi_slopes or first_key")
+    if pages_per_split > 0 or kernel != KERNEL_AUTO:
+        raise ValueError("group_starts: the split and the kernel are the library's")
+    dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, out, workspace,
+                      group_starts, group_pages)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window,
+                                  scale, num_kv_heads, layout, out, workspace, pages_per_split,
+                                  kernel, stream, score, group_starts, group_pages)
+    if not (q.dtype is k_pool.dtype is v_pool.dtype is _BF16 and table.dtype is positions.dtype
+            is group_starts.dtype is group_pages.dtype is _I32):
+        for t, n in ((q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool")):
+            _dtype(t, torch.bfloat16, n)
+        for t, n in ((table, "table"), (positions, "positions"), (group_starts, "group_starts"),
+                     (group_pages, "group_pages")):
+            _dtype(t, torch.int32, n)
+    if sinks is not None:
+        _dtype(sinks, torch.float32, "sinks")
+    rows, hq, d = q.shape
+    if positions.shape != (rows,) or table.dim() != 2 or table.shape[0] != rows \
+            or k_pool.shape != v_pool.shape or (sinks is not None and sinks.shape != (hq,)):
+        raise ValueError("inconsistent shapes")
+    groups = group_pages.shape[0] if group_pages.dim() == 1 else -1
+    if groups < 0 or group_starts.shape != (groups + 1,):
+        raise ValueError("group_pages must be [S] and group_starts [S + 1]")
+    what = "paged_decode_attention" if k_new is None else "paged_decode_step"
+    if k_new is not None:
+        _dtype(k_new, torch.bfloat16, "k_new")
+        _dtype(v_new, torch.bfloat16, "v_new")
+        if k_new.shape != (rows, num_kv_heads, d) or v_new.shape != k_new.shape:
+            raise ValueError("k_new and v_new must be [R, Hkv, D]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dims = ctypes.byref(_dims_of(rows, hq, num_kv_heads, d, _pool_pages(k_pool, num_kv_heads, d),
+                                 table.shape[1], layout))
+    lib = load_extension()
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _result(q.shape, _BF16, dev, stream)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16 shaped like q")
+    if workspace is None:  # (one that is given is checked by the call)
+        need = lib.pgdx_shared_decode_workspace_bytes(dims, groups)
+        workspace = _scratch((max(need, 16),), torch.uint8, dev, stream)
+    rc = lib.pgdx_shared_decode(
+        dims, groups, group_starts.data_ptr(), group_pages.data_ptr(), q.data_ptr(), _ptr(k_new),
+        _ptr(v_new), k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(), positions.data_ptr(),
+        _ptr(sinks), float(scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream_handle(stream, dev))
     if rc != OK:
         raise PgdError(rc, what)
     return out
@@ -1001,3 +1102,185 @@ def rotary_append_paged(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torc
     if rc != OK:
         raise PgdError(rc, "rotary_append_paged")
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# Pages that several rows hold (libpgd_ext).
+
+class ForkPlan(NamedTuple):
+    """What fork_rows makes, int32 on the GPU: the rows' lengths; per row the page
+    to copy from, the page to copy to and the positions to copy (-1, -1, 0: none),
+    as copy_pages takes them; the index of the next free page."""
+    lengths: torch.Tensor
+    sources: torch.Tensor
+    targets: torch.Tensor
+    counts: torch.Tensor
+    free_head: torch.Tensor
+
+
+class CompactPlan(NamedTuple):
+    """What compact_pages makes, int32 on the GPU: the table, shares and free pages
+    under the pages' new names; the copies (-1 past the last) as copy_pages takes them;
+    1 + the highest page held."""
+    table: torch.Tensor
+    shares: torch.Tensor
+    free_pages: torch.Tensor
+    sources: torch.Tensor
+    targets: torch.Tensor
+    end: torch.Tensor
+
+
+def _int32(*tensors) -> None:
+    for t, name in tensors:
+        if t is not None and t.dtype is not _I32:
+            _dtype(t, torch.int32, name)
+
+
+def _plan_ptrs(out, sizes, dev) -> list[int]:
+    if _check_cuda(*out) != dev:
+        raise ValueError("all tensors must be on one device")
+    for t, n, size in zip(out, out._fields, sizes):
+        _dtype(t, torch.int32, n)
+        if t.shape != size:
+            raise ValueError(f"out.{n} must be {list(size)}")
+    return [t.data_ptr() for t in out]
+
+
+def fork_rows(table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor,
+              shares: torch.Tensor, free_pages: torch.Tensor, *,
+              free_head: torch.Tensor | None = None, keep: torch.Tensor | None = None,
+              out: ForkPlan | None = None, stream: torch.cuda.Stream | None = None) -> ForkPlan:
+    """Makes each row a copy of an old row, over pages that rows share.
+
+    table: int32 [R, W], rewritten in place; lengths: int32 [R], positions in the
+    cache; parents: int32 [R], the old row that each row continues (itself: as it
+    was; -1: none, its pages are given back); shares: int32 [pages], how many rows hold
+    each page beyond the first, kept up to date in place; free_pages: int32 [F] with
+    the next page at free_head (int32 [1] or None for 0), as for assign_pages, in
+    place: pages that no row holds any more come back below it, copies of last
+    pages in part use are taken from it.  keep (int32 [R]): row r keeps at most its
+    parent's first keep[r] positions.  The copies themselves are copy_pages'.  ``out``
+    reuses a plan (its tensors must be none of the inputs)."""
+    dev = _check_cuda(table, lengths, parents, shares, free_pages, free_head, keep)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fork_rows(table, lengths, parents, shares, free_pages, free_head=free_head,
+                             keep=keep, out=out, stream=stream)
+    _int32((table, "table"), (lengths, "lengths"), (parents, "parents"), (shares, "shares"),
+           (free_pages, "free_pages"), (free_head, "free_head"), (keep, "keep"))
+    rows, width = table.shape if table.dim() == 2 else (-1, 0)
+    if lengths.shape != (rows,) or parents.shape != (rows,) or shares.dim() != 1 \
+            or free_pages.dim() != 1 or (free_head is not None and free_head.numel() != 1) \
+            or (keep is not None and keep.shape != (rows,)):
+        raise ValueError("inconsistent shapes")
+    whole = None
+    if out is None:  # one allocation, cut into the plan's arrays after the launch
+        whole = _result((4 * rows + 1,), _I32, dev, stream)
+        ptrs = [whole.data_ptr() + 4 * rows * k for k in range(5)]
+    else:
+        ptrs = _plan_ptrs(out, ((rows,),) * 4 + ((1,),), dev)
+    rc = load_extension().pgdx_fork_rows(
+        rows, width, shares.shape[0], table.data_ptr(), lengths.data_ptr(), parents.data_ptr(),
+        _ptr(keep), shares.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
+        _ptr(free_head), *ptrs, _stream_handle(stream, dev))
+    if rc != OK:
+        raise PgdError(rc, "fork_rows")
+    if whole is not None:
+        out = ForkPlan(*torch.unsafe_split_with_sizes(whole, (rows, rows, rows, rows, 1)))
+    return out
+
+
+def copy_pages(k_pools: torch.Tensor | list[torch.Tensor], v_pools: torch.Tensor |
+               list[torch.Tensor], sources: torch.Tensor, targets: torch.Tensor,
+               counts: torch.Tensor | None = None, *, num_kv_heads: int, head_dim: int,
+               layout: int = PAGE_MAJOR, stream: torch.cuda.Stream | None = None) -> None:
+    """Copies the first counts[i] positions (None: all) of page sources[i] to page
+    targets[i] (int32 [n]; negative: no copy) in the K and V pools, bf16 in ``layout``,
+    of one layer or, as lists, of several."""
+    if isinstance(k_pools, torch.Tensor):
+        k_pools = [k_pools]
+    if isinstance(v_pools, torch.Tensor):
+        v_pools = [v_pools]
+    if len(k_pools) != len(v_pools):
+        raise ValueError("k_pools and v_pools must be of the same layers")
+    dev = _check_cuda(sources, targets, counts, *k_pools, *v_pools)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return copy_pages(k_pools, v_pools, sources, targets, counts,
+                              num_kv_heads=num_kv_heads, head_dim=head_dim, layout=layout,
+                              stream=stream)
+    _int32((sources, "sources"), (targets, "targets"), (counts, "counts"))
+    if sources.dim() != 1 or targets.shape != sources.shape \
+            or (counts is not None and counts.shape != sources.shape):
+        raise ValueError("sources, targets and counts must be [n]")
+    layers = len(k_pools)
+    if layers == 0:
+        return
+    shape = k_pools[0].shape
+    for name, pools in (("k_pools", k_pools), ("v_pools", v_pools)):
+        for pool in pools:
+            if pool.dtype is not _BF16:
+                _dtype(pool, torch.bfloat16, name)
+            if pool.shape != shape:
+                raise ValueError("the pools must have one shape")
+    dims = _dims_of(sources.shape[0], num_kv_heads, num_kv_heads, head_dim,
+                    _pool_pages(k_pools[0], num_kv_heads, head_dim), 1, layout)
+    at = ctypes.c_void_p * layers
+    rc = load_extension().pgdx_copy_pages(
+        ctypes.byref(dims), layers, at(*[t.data_ptr() for t in k_pools]),
+        at(*[t.data_ptr() for t in v_pools]), sources.shape[0], sources.data_ptr(),
+        targets.data_ptr(), _ptr(counts), _stream_handle(stream, dev))
+    if rc != OK:
+        raise PgdError(rc, "copy_pages")
+
+
+def compact_pages(table: torch.Tensor, lengths: torch.Tensor, shares: torch.Tensor,
+                  free_pages: torch.Tensor, *, free_head: torch.Tensor | None = None,
+                  max_moves: int | None = None, out: CompactPlan | None = None,
+                  stream: torch.cuda.Stream | None = None) -> CompactPlan:
+    """Gives held pages the names of lower free ones: the highest page goes to the
+    lowest free one and so on, at most max_moves of them (None: half of the pool, all
+    there can be).  The arguments are fork_rows'; nothing is changed in place unless ``out``
+    names the inputs as its table, shares and free_pages.  The copies themselves are
+    copy_pages'."""
+    dev = _check_cuda(table, lengths, shares, free_pages, free_head)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return compact_pages(table, lengths, shares, free_pages, free_head=free_head,
+                                 max_moves=max_moves, out=out, stream=stream)
+    _int32((table, "table"), (lengths, "lengths"), (shares, "shares"),
+           (free_pages, "free_pages"), (free_head, "free_head"))
+    rows, width = table.shape if table.dim() == 2 else (-1, 0)
+    if lengths.shape != (rows,) or shares.dim() != 1 or free_pages.dim() != 1 \
+            or (free_head is not None and free_head.numel() != 1):
+        raise ValueError("inconsistent shapes")
+    pages, listed = shares.shape[0], free_pages.shape[0]
+    if max_moves is None:
+        max_moves = pages // 2
+    if max_moves < 0:
+        raise ValueError("max_moves must be >= 0")
+    lib = load_extension()
+    sizes = (rows * width, pages, listed, max_moves, max_moves, 1)
+    whole = None
+    if out is None:  # one allocation, the workspace (16-byte aligned) at its front
+        need = (lib.pgdx_compact_workspace_bytes(pages) + 15) // 16 * 4
+        whole = _result((need + sum(sizes),), _I32, dev, stream)
+        ptrs, at = [], whole.data_ptr() + 4 * need
+        for size in sizes:
+            ptrs.append(at)
+            at += 4 * size
+        workspace = whole
+    else:
+        ptrs = _plan_ptrs(out, ((rows, width),) + tuple((n,) for n in sizes[1:]), dev)
+        need = (lib.pgdx_compact_workspace_bytes(pages) + 15) // 16 * 4
+        workspace = _scratch((max(need, 4),), _I32, dev, stream)
+    rc = lib.pgdx_compact_pages(
+        rows, width, pages, table.data_ptr(), lengths.data_ptr(), shares.data_ptr(),
+        free_pages.data_ptr(), listed, _ptr(free_head), max_moves, *ptrs, workspace.data_ptr(),
+        4 * need, _stream_handle(stream, dev))
+    if rc != OK:
+        raise PgdError(rc, "compact_pages")
+    if whole is not None:
+        parts = torch.unsafe_split_with_sizes(whole, (need,) + sizes)
+        out = CompactPlan(parts[1].view(rows, width), *parts[2:])
+    return out

@@ -21,7 +21,8 @@ EXT_LIB = os.path.join(BUILD, "libpgd_ext.so")
 SOURCES = ["pgd_api.cu", "kv_append.cu", "paged_decode_d64.cu", "paged_decode_d128.cu",
            "paged_prefill.cu", "paged_prefill_umma.cu", "paged_prefill_umma_d64.cu",
            "paged_prefill_pair.cu"]
-EXT_SOURCES = ["pgd_ext_api.cu", "batch_ops.cu", "mod_decode_d64.cu", "mod_decode_d128.cu",
+EXT_SOURCES = ["pgd_ext_api.cu", "batch_ops.cu", "page_ops.cu", "shared_decode_d64.cu",
+               "shared_decode_d128.cu", "mod_decode_d64.cu", "mod_decode_d128.cu",
                "mod_prefill.cu"] + [f"mod_prefill_d{d}_{kind}.cu" for d in (64, 128)
                                     for kind in ("mask", "cap", "bias", "cap_bias")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -28,6 +28,58 @@ bool rows_overlap(const void* x, int64_t rows, int64_t stride, int64_t row, cons
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// An int32 array of a call.
+struct Array {
+  const int32_t* at;
+  int64_t n;
+};
+
+// Whether an array is misaligned, or an output overlaps an input or another output.
+template <int NI, int NO>
+bool arrays_clash(const Array (&in)[NI], const Array (&out)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    if (!aligned4(out[i].at)) return true;
+    for (const Array& a : in)
+      if (!aligned4(a.at) || overlap(out[i].at, out[i].n, a.at, a.n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].at, out[i].n, out[j].at, out[j].n)) return true;
+  }
+  return false;
+}
+
+// Sizes of a table and a pool whose positions and slots are int32.
+int check_table(int32_t rows, int32_t width, int32_t num_pages) {
+  if (rows < 0 || width <= 0 || num_pages <= 0) return PGD_EINVAL;
+  if ((int64_t)width * kPageSize > (int64_t)INT32_MAX ||
+      (int64_t)num_pages * kPageSize > (int64_t)INT32_MAX)
+    return PGD_EUNSUPPORTED;
+  return PGD_OK;
+}
+
+// Where shared_decode's workspace keeps what; the total.
+struct SharedLayout {
+  size_t ml, off, group, bytes;
+};
+SharedLayout shared_layout(const pgd_dims* d, int32_t groups) {
+  const size_t parts =
+      2 * (size_t)d->rows * d->num_q_heads + 256 * (size_t)kMaxSharedCtas;
+  SharedLayout l;
+  l.ml = parts * d->head_dim * sizeof(float);
+  l.off = l.ml + parts * 2 * sizeof(float);
+  l.group = l.off + ((size_t)groups + d->rows + 1) * sizeof(int64_t);
+  l.bytes = l.group + (size_t)d->rows * sizeof(int32_t);
+  return l;
+}
+
+int check_shared(const pgd_dims* d, int32_t groups) {
+  const int rc = check_dims(d);
+  if (rc != PGD_OK) return rc;
+  if (groups < 0) return PGD_EINVAL;
+  if (groups > kMaxSharedGroups || d->rows > kMaxGridYZ || d->layout == PGD_ROW_MAJOR)
+    return PGD_EUNSUPPORTED;
+  return PGD_OK;
+}
+
 }  // namespace
 }  // namespace pgd
 
@@ -358,6 +410,210 @@ int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const pgdx_scor
   return attention_impl(dims, table_rows, rows, score, q, k_new, v_new, k_pool, v_pool, table,
                         positions, sinks, window, scale, out, workspace, workspace_size, opts,
                         stream);
+}
+
+int pgdx_fork_rows(int32_t rows, int32_t max_pages_per_row, int32_t num_pages, int32_t* table,
+                   const int32_t* lengths, const int32_t* parents, const int32_t* keep,
+                   int32_t* shares, int32_t* free_pages, int32_t num_free,
+                   const int32_t* free_head, int32_t* new_lengths, int32_t* sources,
+                   int32_t* targets, int32_t* counts, int32_t* free_head_out,
+                   pgd_stream_t stream) {
+  int rc = check_table(rows, max_pages_per_row, num_pages);
+  if (rc != PGD_OK) return rc;
+  if (num_free < 0 || !shares || !free_head_out || (num_free > 0 && !free_pages))
+    return PGD_EINVAL;
+  if (rows > 0 && (!table || !lengths || !parents || !new_lengths || !sources || !targets ||
+                   !counts))
+    return PGD_EINVAL;
+  const int64_t entries = (int64_t)rows * max_pages_per_row;
+  const Array in[] = {{lengths, rows}, {parents, rows}, {keep, rows}, {free_head, 1}};
+  const Array out[] = {{table, entries}, {shares, num_pages}, {free_pages, num_free},
+                       {new_lengths, rows}, {sources, rows}, {targets, rows}, {counts, rows},
+                       {free_head_out, 1}};
+  if (arrays_clash(in, out)) return PGD_EINVAL;
+  if (rows > kMaxForkRows || entries > (1 << 30)) return PGD_EUNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev)) != PGD_OK) return rc;
+  ForkParams p;
+  p.table = table;
+  p.lengths = lengths;
+  p.parents = parents;
+  p.keep = keep;
+  p.shares = shares;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.new_lengths = new_lengths;
+  p.sources = sources;
+  p.targets = targets;
+  p.counts = counts;
+  p.free_head_out = free_head_out;
+  p.err = dev->err;
+  p.rows = rows;
+  p.width = max_pages_per_row;
+  p.num_pages = num_pages;
+  p.num_free = num_free;
+  return launch_fork_rows(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PGD_OK
+                                                                                    : PGD_ECUDA;
+}
+
+int pgdx_copy_pages(const pgd_dims* dims, int32_t layers, void* const* k_pools,
+                    void* const* v_pools, int32_t copies, const int32_t* sources,
+                    const int32_t* targets, const int32_t* counts, pgd_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != PGD_OK) return rc;
+  if (layers < 0 || copies < 0) return PGD_EINVAL;
+  if (dims->layout == PGD_ROW_MAJOR) return PGD_EUNSUPPORTED;
+  if (layers == 0 || copies == 0) return PGD_OK;
+  if (!k_pools || !v_pools || !sources || !targets) return PGD_EINVAL;
+  if (!aligned4(sources) || !aligned4(targets) || !aligned4(counts)) return PGD_EINVAL;
+  for (int32_t i = 0; i < layers; ++i)
+    if (!k_pools[i] || !v_pools[i] || !aligned16(k_pools[i]) || !aligned16(v_pools[i]))
+      return PGD_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev)) != PGD_OK) return rc;
+  CopyParams p;
+  p.sources = sources;
+  p.targets = targets;
+  p.counts = counts;
+  p.err = dev->err;
+  p.copies = copies;
+  p.hkv = dims->num_kv_heads;
+  p.num_pages = dims->num_pages;
+  p.layout = dims->layout;
+  for (int32_t first = 0; first < layers; first += kMaxCopyPools / 2) {
+    p.pools = 0;
+    for (int32_t i = first; i < layers && p.pools < kMaxCopyPools; ++i) {
+      p.pool[p.pools++] = k_pools[i];
+      p.pool[p.pools++] = v_pools[i];
+    }
+    if (launch_copy_pages(p, dims->head_dim, dev->sm_count,
+                          reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return PGD_ECUDA;
+  }
+  return PGD_OK;
+}
+
+size_t pgdx_compact_workspace_bytes(int32_t num_pages) {
+  if (num_pages <= 0) return 0;
+  return ((size_t)(((int64_t)num_pages + 31) / 32) * 2 + 1) * sizeof(uint32_t);
+}
+
+int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
+                       const int32_t* table, const int32_t* lengths, const int32_t* shares,
+                       const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                       int32_t max_moves, int32_t* new_table, int32_t* new_shares,
+                       int32_t* new_free, int32_t* sources, int32_t* targets, int32_t* end,
+                       void* workspace, size_t workspace_size, pgd_stream_t stream) {
+  int rc = check_table(rows, max_pages_per_row, num_pages);
+  if (rc != PGD_OK) return rc;
+  if (num_free < 0 || max_moves < 0 || !shares || !new_shares || !end) return PGD_EINVAL;
+  if (rows > 0 && (!table || !lengths || !new_table)) return PGD_EINVAL;
+  if (num_free > 0 && (!free_pages || !new_free)) return PGD_EINVAL;
+  if (max_moves > 0 && (!sources || !targets)) return PGD_EINVAL;
+  const int64_t entries = (int64_t)rows * max_pages_per_row;
+  if (workspace_size < pgdx_compact_workspace_bytes(num_pages)) return PGD_EWORKSPACE;
+  if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
+  // an output that is its input is in place
+  const Array in[] = {{lengths, rows},
+                      {free_head, 1},
+                      {table, table == new_table ? 0 : entries},
+                      {shares, shares == new_shares ? 0 : num_pages},
+                      {free_pages, free_pages == new_free ? 0 : num_free}};
+  const Array out[] = {{new_table, entries}, {new_shares, num_pages}, {new_free, num_free},
+                       {sources, max_moves}, {targets, max_moves}, {end, 1},
+                       {static_cast<int32_t*>(workspace),
+                        (int64_t)(pgdx_compact_workspace_bytes(num_pages) / 4)}};
+  if (arrays_clash(in, out)) return PGD_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev)) != PGD_OK) return rc;
+  CompactParams p;
+  p.table = table;
+  p.lengths = lengths;
+  p.shares = shares;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.new_table = new_table;
+  p.new_shares = new_shares;
+  p.new_free = new_free;
+  p.sources = sources;
+  p.targets = targets;
+  p.end = end;
+  p.bits = static_cast<uint32_t*>(workspace);
+  p.err = dev->err;
+  p.rows = rows;
+  p.width = max_pages_per_row;
+  p.num_pages = num_pages;
+  p.num_free = num_free;
+  p.max_moves = max_moves;
+  return launch_compact_pages(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PGD_OK
+             : PGD_ECUDA;
+}
+
+size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups) {
+  return check_shared(dims, groups) == PGD_OK ? shared_layout(dims, groups).bytes : 0;
+}
+
+int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* group_starts,
+                       const int32_t* group_pages, const void* q, const void* k_new,
+                       const void* v_new, void* k_pool, void* v_pool, const int32_t* table,
+                       const int32_t* positions, const float* sinks, float scale, void* out,
+                       void* workspace, size_t workspace_size, pgd_stream_t stream) {
+  int rc = check_shared(dims, groups);
+  if (rc != PGD_OK) return rc;
+  if (!std::isfinite(scale)) return PGD_EINVAL;
+  if (dims->rows == 0) return PGD_OK;
+  if (!q || !k_pool || !v_pool || !table || !positions || !out) return PGD_EINVAL;
+  if (groups > 0 && (!group_starts || !group_pages)) return PGD_EINVAL;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
+      !aligned4(group_starts) || !aligned4(group_pages))
+    return PGD_EINVAL;
+  if ((k_new == nullptr) != (v_new == nullptr) ||
+      (k_new && (!aligned16(k_new) || !aligned16(v_new))))
+    return PGD_EINVAL;
+  const SharedLayout l = shared_layout(dims, groups);
+  if (workspace_size < l.bytes) return PGD_EWORKSPACE;
+  if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev)) != PGD_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  SharedParams p;
+  p.table = table;
+  p.positions = positions;
+  p.starts = group_starts;
+  p.pages = group_pages;
+  p.sinks = sinks;
+  p.out = static_cast<uint16_t*>(out);
+  p.part_acc = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + l.ml);
+  p.item_off = reinterpret_cast<int64_t*>(ws + l.off);
+  p.row_group = reinterpret_cast<int32_t*>(ws + l.group);
+  p.err = dev->err;
+  p.rows = dims->rows;
+  p.groups = groups;
+  p.hq = dims->num_q_heads;
+  p.hkv = dims->num_kv_heads;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.maxp = dims->max_pages_per_row;
+  p.num_pages = dims->num_pages;
+  p.layout = dims->layout;
+  p.min_units = 16;
+  p.q_scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.k_pool = static_cast<uint16_t*>(k_pool);
+  p.v_pool = static_cast<uint16_t*>(v_pool);
+  CUtensorMap k_map, v_map, q_map, q_small_map;
+  if ((rc = encode_pool_map(&k_map, k_pool, dims, kMapWholeTile)) != PGD_OK) return rc;
+  if ((rc = encode_pool_map(&v_map, v_pool, dims, kMapWholeTile)) != PGD_OK) return rc;
+  if ((rc = encode_q_map(&q_map, q, dims)) != PGD_OK) return rc;
+  if ((rc = encode_q_map(&q_small_map, q, dims, 1)) != PGD_OK) return rc;
+  const int ctas = dev->sm_count < kMaxSharedCtas ? dev->sm_count : kMaxSharedCtas;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      dims->head_dim == 64 ? launch_shared_d64(p, k_map, v_map, q_map, q_small_map, ctas, st)
+                           : launch_shared_d128(p, k_map, v_map, q_map, q_small_map, ctas, st);
+  return e == cudaSuccess ? PGD_OK : PGD_ECUDA;
 }
 
 int pgdx_get_device_error(pgd_stream_t stream) {

@@ -43,6 +43,86 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary_append(const RotaryParams& p, int head_dim, cudaStream_t stream);
 
+struct ForkParams {
+  int32_t* table;  // [rows][width], rewritten in place
+  const int32_t* lengths;
+  const int32_t* parents;
+  const int32_t* keep;  // or nullptr
+  int32_t* shares;      // [num_pages]
+  int32_t* free_pages;
+  const int32_t* free_head;  // nullptr: 0
+  int32_t* new_lengths;
+  int32_t* sources;
+  int32_t* targets;
+  int32_t* counts;
+  int32_t* free_head_out;
+  unsigned int* err;
+  int rows, width, num_pages, num_free;
+  int slab_columns;  // (the launcher's)
+};
+constexpr int kMaxForkRows = 12288;  // three words a row and a column of them in shared memory
+cudaError_t launch_fork_rows(const ForkParams& p, cudaStream_t stream);
+
+constexpr int kMaxCopyPools = 128;  // of one launch
+struct CopyParams {
+  const int32_t* sources;
+  const int32_t* targets;
+  const int32_t* counts;  // or nullptr: whole pages
+  unsigned int* err;
+  int copies, pools, hkv, num_pages, layout;
+  void* pool[kMaxCopyPools];
+};
+cudaError_t launch_copy_pages(const CopyParams& p, int head_dim, int sm_count,
+                              cudaStream_t stream);
+
+struct CompactParams {
+  const int32_t* table;  // [rows][width]
+  const int32_t* lengths;
+  const int32_t* shares;
+  const int32_t* free_pages;
+  const int32_t* free_head;  // nullptr: 0
+  int32_t* new_table;        // each may be its input
+  int32_t* new_shares;
+  int32_t* new_free;
+  int32_t* sources;  // [max_moves]
+  int32_t* targets;
+  int32_t* end;
+  uint32_t* bits;  // workspace: two bitmaps over the pool and a flag
+  unsigned int* err;
+  int rows, width, num_pages, num_free, max_moves;
+  int step;  // (the launcher's)
+};
+cudaError_t launch_compact_pages(const CompactParams& p, cudaStream_t stream);
+
+constexpr int kMaxSharedGroups = 8192;  // two words a group in shared memory
+constexpr int kMaxSharedCtas = 160;
+struct SharedParams {
+  const int32_t* table;
+  const int32_t* positions;
+  const int32_t* starts;  // [groups + 1]
+  const int32_t* pages;   // [groups]
+  const float* sinks;     // or nullptr
+  uint16_t* out;
+  float* part_acc;     // [2 rows hq + 256 CTAs][D]
+  float* part_ml;      // (m, l) of each
+  int64_t* item_off;   // [groups + rows + 1]
+  int32_t* row_group;  // [rows]
+  unsigned int* err;
+  int rows, groups, hq, hkv, group, maxp, num_pages, layout;
+  int64_t min_units;   // least weight of a CTA's range
+  float q_scale_log2;
+  const uint16_t* k_new;  // or nullptr
+  const uint16_t* v_new;
+  uint16_t* k_pool;
+  uint16_t* v_pool;
+};
+cudaError_t launch_shared_d64(const SharedParams& p, const CUtensorMap& k_map,
+                              const CUtensorMap& v_map, const CUtensorMap& q_map,
+                              const CUtensorMap& q_small_map, int ctas, cudaStream_t stream);
+cudaError_t launch_shared_d128(const SharedParams& p, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, const CUtensorMap& q_map,
+                               const CUtensorMap& q_small_map, int ctas, cudaStream_t stream);
+
 // Attention with the scores of ModParams: the split decode (and its combine),
 // the tcgen05 prefill (and its block order or key-part combine), and the
 // prefill step's write, as their namesakes in pgd_internal.h.

@@ -1,0 +1,343 @@
+"""Decode over shared pages against the plain 64-bit attention of each row over its own
+table entries, within the bound of page_side."""
+import numpy as np
+import pytest
+import torch
+
+import paged_gqa_decode_gb300 as pgd
+from tests import page_side as side
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+    torch.cuda.synchronize()
+
+
+def dev(a, dtype=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=dtype)).to(DEV)
+
+
+class Batch:
+    """Groups of rows over shared pages.  groups: (rows, shared pages) in order, with
+    shared None for rows in no group (at the start or the end only); own: positions of
+    each row's own (0: an inactive row).  Pool positions out of use hold NaN."""
+
+    def __init__(self, seed, groups, own, hq, hkv, d, layout=pgd.PAGE_MAJOR, width=None,
+                 scale_k=1.0):
+        rng = np.random.default_rng(seed)
+        self.hq, self.hkv, self.d, self.layout = hq, hkv, d, layout
+        rows = len(own)
+        own = np.asarray(own)
+        shared = np.concatenate([np.full(n, p or 0) for n, p in groups]).astype(int)
+        need = side.pages_of(own)
+        self.positions = np.where(own > 0, shared * 64 + own - 1, -1)
+        self.width = width or max(1, int((shared + need).max()))
+        self.pages = int(need.sum()) + sum(p or 0 for _, p in groups) + 3
+        order = list(rng.permutation(self.pages))
+        self.table = np.full((rows, self.width), 2 ** 30)       # entries out of use: any value
+        self.starts, self.shared, b = [], [], 0
+        for n, p in groups:
+            if p is not None:
+                if not self.starts:
+                    self.starts.append(b)
+                self.starts.append(b + n)
+                self.shared.append(p)
+                pages = [order.pop() for _ in range(p)]
+                self.table[b:b + n, :p] = pages
+            for r in range(b, b + n):
+                for e in range(need[r]):
+                    self.table[r, shared[r] + e] = order.pop()
+            b += n
+        assert b == rows
+        g = torch.Generator().manual_seed(seed)
+        shape = (self.pages, hkv, 64, d)
+        self.k = (torch.randn(shape, generator=g) * scale_k).bfloat16()
+        self.v = torch.randn(shape, generator=g).bfloat16()
+        used = np.zeros((self.pages, 64), dtype=bool)
+        for r, n in enumerate(self.positions):
+            for s in range(0, n + 1, 64):
+                used[self.table[r, s // 64], :min(64, n + 1 - s)] = True
+        gone = torch.from_numpy(~used)
+        for pool in (self.k, self.v):
+            pool.permute(0, 2, 1, 3)[gone] = float("nan")
+        self.q = torch.randn(rows, hq, d, generator=g).bfloat16()
+        self.gen = g
+        self.k_pool, self.v_pool = self.lay(self.k), self.lay(self.v)
+
+    def lay(self, pool):
+        return (pool if self.layout == pgd.PAGE_MAJOR else pool.transpose(0, 1)).contiguous().to(DEV)
+
+    def want(self, scale, sinks=None):
+        host = lambda t: t.double().numpy()  # noqa: E731
+        return side.attention(host(self.q), host(self.k), host(self.v), self.table,
+                              self.positions, scale, sinks)
+
+    def call(self, k_new=None, v_new=None, **kw):
+        args = (dev(self.table), dev(self.positions))
+        kw = dict(dict(num_kv_heads=self.hkv, layout=self.layout, group_starts=dev(self.starts or [0]),
+                       group_pages=dev(self.shared)), **kw)
+        if k_new is None:
+            return pgd.paged_decode_attention(self.q.to(DEV), self.k_pool, self.v_pool, *args, **kw)
+        return pgd.paged_decode_step(self.q.to(DEV), k_new, v_new, self.k_pool, self.v_pool, *args,
+                                     **kw)
+
+    def check(self, scale=None, sinks=None, status=pgd.OK, bad=(), **kw):
+        out = self.call(scale=scale, sinks=None if sinks is None else dev(sinks, np.float32), **kw)
+        assert pgd.get_device_error() == status
+        self.compare(out, scale or self.d ** -0.5, sinks, bad)
+        return out
+
+    def compare(self, out, scale, sinks=None, bad=()):
+        want, mass, size, every = self.want(scale, sinks)
+        for b in bad:
+            want[b] = 0
+        limit = side.bound(want, mass, size, every, self.d)
+        got = out.double().cpu().numpy()
+        assert np.all(np.isfinite(got)), "non-finite output"
+        excess = np.abs(got - want) - limit
+        at = np.unravel_index(np.argmax(excess), excess.shape)
+        assert excess.max() <= 0, f"at {at}: {got[at]} for {want[at]}, bound {limit[at]}"
+
+
+HEADS = [(14, 2, 64), (64, 8, 64), (32, 8, 128), (8, 8, 128), (16, 8, 64), (3, 1, 128), (6, 2, 128),
+         (5, 1, 64)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("layout", [pgd.PAGE_MAJOR, pgd.HEAD_MAJOR])
+def test_groups_of_all_sizes(hq, hkv, d, layout):
+    rng = np.random.default_rng(hq + d)
+    groups = [(2, None), (4, 5), (1, 3), (17, 2), (0, 4), (70, 1), (3, 0), (5, 7), (2, None)]
+    rows = sum(n for n, _ in groups)
+    own = rng.integers(1, 200, rows)
+    own[::9] = rng.integers(1, 3, len(own[::9]))
+    own[5], own[7], own[40] = 64, 65, 0
+    b = Batch(1, groups, own, hq, hkv, d, layout)
+    b.check()
+    b.check(sinks=rng.normal(size=hq))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(14, 2, 64), (32, 8, 128)])
+def test_one_token_and_one_page(hq, hkv, d):
+    for groups, own in (([(1, 1)], [1]), ([(1, 0)], [1]), ([(1, None)], [1]), ([(2, 1)], [64, 1]),
+                        ([(4, 4)], [1, 30, 2, 40]), ([(3, 2)], [0, 0, 0]), ([(3, 2)], [0, 5, 0])):
+        Batch(2, groups, own, hq, hkv, d).check()
+
+
+def test_no_groups():
+    Batch(3, [(9, None)], np.arange(1, 900, 100), 32, 8, 128).check(sinks=np.zeros(32))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 64), (32, 8, 128), (14, 2, 64)])
+def test_long_prefix_under_many_rows(hq, hkv, d):
+    rng = np.random.default_rng(4)
+    Batch(4, [(150, 40)], rng.integers(1, 300, 150), hq, hkv, d).check(sinks=rng.normal(size=hq))
+
+
+def test_long_prefix_under_few_rows():
+    Batch(5, [(3, 900), (2, 1)], [1, 100, 64, 3, 500], 16, 8, 64).check()
+
+
+def test_long_own_parts():
+    Batch(6, [(2, 3), (3, None)], [9000, 1, 20000, 7, 12345], 32, 8, 128).check()
+
+
+def test_many_small_groups():
+    rng = np.random.default_rng(7)
+    groups = [(int(n), int(p)) for n, p in zip(rng.integers(0, 5, 150), rng.integers(0, 9, 150))]
+    Batch(7, groups, rng.integers(0, 150, sum(n for n, _ in groups)), 16, 8, 64).check()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1.0, 3.0])
+def test_scales(scale):
+    b = Batch(8, [(5, 6), (3, None)], [1, 70, 128, 5, 200, 3, 64, 90], 32, 8, 128)
+    out = b.call(scale=scale)
+    b.compare(out, scale)
+
+
+def test_scores_that_rise_and_fall_over_the_pages():
+    """The running maximum is raised again and again, in the shared pages and after them."""
+    for rising in (True, False):
+        b = Batch(9, [(6, 30), (2, None)], [500, 1, 64, 300, 90, 70, 2000, 1], 32, 8, 128)
+        key = b.k.float().numpy()
+        for r, n in enumerate(b.positions):
+            for j in range(n // 64 + 1):
+                far = j if rising else n // 64 - j
+                key[b.table[r, j], :, :, 0] = 4.0 * far
+        b.k = torch.from_numpy(key).bfloat16()
+        gone = torch.isnan(b.v)
+        b.k[gone] = float("nan")
+        b.k_pool = b.lay(b.k)
+        b.q[:, :, 0] = 8.0
+        b.check()
+
+
+def test_equal_keys_give_the_mean():
+    b = Batch(10, [(40, 10)], [64] * 40, 8, 8, 128)
+    b.q[:] = 0
+    b.check()
+
+
+def test_a_row_of_nan_stays_in_its_row():
+    b = Batch(11, [(70, 3), (1, None)], [30] * 71, 32, 8, 128)
+    b.q[33, 5] = float("nan")
+    out = b.call()
+    assert pgd.get_device_error() == pgd.OK
+    assert bool(torch.isnan(out[33, 5]).all())
+    got = out.clone()
+    got[33, 5] = 0
+    b.q[33, 5] = 0
+    want, mass, size, every = b.want(128 ** -0.5)
+    want[33, 5] = 0
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= side.bound(want, mass, size, every, 128))
+
+
+@pytest.mark.parametrize("hq,hkv,d,layout", [(14, 2, 64, pgd.PAGE_MAJOR), (32, 8, 128, pgd.HEAD_MAJOR),
+                                             (8, 8, 128, pgd.PAGE_MAJOR)])
+def test_step_appends_first(hq, hkv, d, layout):
+    own = [1, 64, 65, 128, 2, 0, 300, 1, 63]
+    b = Batch(12, [(7, 4), (2, None)], own, hq, hkv, d, layout)
+    k_new, v_new = (torch.randn(9, hkv, d, generator=b.gen).bfloat16() for _ in range(2))
+    for r, n in enumerate(b.positions):
+        page, s = (b.table[r, n // 64], n % 64) if n >= 0 else (0, 0)
+        if n >= 0:
+            b.k[page, :, s], b.v[page, :, s] = k_new[r], v_new[r]
+    # the pools still hold other values at the new positions
+    out = b.call(k_new.to(DEV), v_new.to(DEV))
+    assert pgd.get_device_error() == pgd.OK
+    b.compare(out, d ** -0.5)
+    for pool, host in ((b.k_pool, b.k), (b.v_pool, b.v)):
+        assert torch.equal(pool.view(torch.int16), b.lay(host).view(torch.int16))
+
+
+def test_the_same_as_without_groups():
+    """Grouped and ungrouped calls agree within two roundings and the bound's."""
+    b = Batch(13, [(20, 9), (4, 2)], np.arange(1, 25) * 7, 64, 8, 64)
+    b.check()
+    plain = pgd.paged_decode_attention(b.q.to(DEV), b.k_pool, b.v_pool, dev(np.where(
+        b.table < b.pages, b.table, 0)), dev(b.positions), num_kv_heads=8)
+    b.compare(plain, 64 ** -0.5)
+
+
+def test_equal_calls_give_equal_bits():
+    b = Batch(14, [(50, 20), (9, 3)], np.arange(1, 60) * 5, 32, 8, 128)
+    outs = [b.call() for _ in range(3)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# ----------------------------------------------------------------- device errors
+
+def test_a_page_outside_the_pool():
+    b = Batch(15, [(4, 6), (3, 2), (2, None)], [90] * 9, 32, 8, 128)
+    b.table[4:7, 1] = b.pages                     # of the second group
+    b.table[1, 7] = -1                            # of row 1's own pages
+    args = dict(status=pgd.EDEVICE_BOUNDS, bad=(1, 4, 5, 6))
+    keep, b.want = b.want, None
+    good = Batch(15, [(4, 6), (3, 2), (2, None)], [90] * 9, 32, 8, 128)
+    b.want = good.want
+    b.check(**args)
+    b.want = keep
+
+
+def test_rows_beyond_their_table_or_in_their_groups_pages():
+    b = Batch(16, [(4, 3), (2, None)], [90] * 6, 32, 8, 128)
+    good = b.want
+    true = b.positions.copy()
+    b.positions = true.copy()
+    b.positions[1] = b.width * 64                 # beyond the table
+    b.positions[2] = 3 * 64 - 1                   # in the shared pages
+
+    def want(scale, sinks=None):
+        at, b.positions = b.positions, true
+        r = good(scale, sinks)
+        b.positions = at
+        return r
+    b.want = want
+    b.check(status=pgd.EDEVICE_BOUNDS, bad=(1, 2))
+
+
+@pytest.mark.parametrize("starts,pages,bad", [
+    ([0, 4, 3, 6], [3, 3, 3], range(6)),           # decreasing
+    ([0, 4, 6, 7], [3, 0, 0], range(6)),           # past the rows
+    ([-1, 4, 4, 6], [3, 0, 0], range(6)),
+    ([0, 4, 5, 6], [3, -1, 0], [4]),
+    ([0, 4, 5, 6], [3, 0, 1000], [5]),
+])
+def test_bad_groups(starts, pages, bad):
+    b = Batch(17, [(4, 3), (2, None)], [90] * 6, 32, 8, 128)
+    b.starts, b.shared = starts, pages
+    b.check(status=pgd.EDEVICE_BOUNDS, bad=bad)
+
+
+def test_refusals():
+    b = Batch(18, [(4, 3)], [90] * 4, 32, 8, 128)
+    with pytest.raises(ValueError, match="together"):
+        b.call(group_pages=None)
+    for kw in (dict(window=64), dict(softcap=30.0), dict(first_key=dev([0] * 4)),
+               dict(alibi_slopes=torch.zeros(32, device=DEV))):
+        with pytest.raises(ValueError, match="full attention"):
+            b.call(**kw)
+    for kw in (dict(pages_per_split=4), dict(kernel=pgd.KERNEL_CUDA_CORE)):
+        with pytest.raises(ValueError, match="library's"):
+            b.call(**kw)
+    with pytest.raises(ValueError, match=r"\[S"):
+        b.call(group_starts=dev([0, 2, 4]))
+    with pytest.raises(ValueError, match="int32"):
+        b.call(group_pages=dev([3]).long())
+    with pytest.raises(pgd.PgdError) as e:
+        b.call(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    assert e.value.status == pgd.EWORKSPACE
+    with pytest.raises(pgd.PgdError) as e:
+        b.call(layout=pgd.ROW_MAJOR)
+    assert e.value.status in (pgd.EUNSUPPORTED, pgd.EINVAL)
+    assert pgd.get_device_error() == pgd.OK
+
+
+def test_captured_with_changing_groups():
+    """One graph, replayed over other tables, positions, groups and values."""
+    rows, hq, hkv, d, pages, width = 24, 32, 8, 128, 400, 30
+    t = torch.zeros(rows, width, dtype=torch.int32, device=DEV)
+    n, starts, shared = (torch.zeros(k, dtype=torch.int32, device=DEV) for k in (rows, 4, 3))
+    q = torch.zeros(rows, hq, d, dtype=torch.bfloat16, device=DEV)
+    kp, vp = (torch.zeros(pages, hkv, 64, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = torch.empty_like(q)
+    call = lambda: pgd.paged_decode_attention(  # noqa: E731
+        q, kp, vp, t, n, num_kv_heads=hkv, out=out, group_starts=starts, group_pages=shared)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    rng = np.random.default_rng(19)
+    for step in range(4):
+        cut = np.sort(rng.integers(0, rows + 1, 2))
+        groups = [(int(cut[0]), 5), (int(cut[1] - cut[0]), int(rng.integers(0, 12))),
+                  (int(rows - cut[1]), 1)]
+        b = Batch(20 + step, groups, rng.integers(0, 400, rows), hq, hkv, d, width=width)
+        t.copy_(dev(b.table))
+        n.copy_(dev(b.positions))
+        starts.copy_(dev(b.starts))
+        shared.copy_(dev(b.shared))
+        q.copy_(b.q)
+        kp[:b.pages], vp[:b.pages] = b.k_pool, b.v_pool
+        graph.replay()
+        assert pgd.get_device_error() == pgd.OK
+        b.compare(out, d ** -0.5)
+
+
+def test_on_a_side_stream():
+    b = Batch(21, [(30, 8)], np.arange(1, 31) * 9, 64, 8, 64)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    outs = [b.call(stream=stream) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(stream)
+    assert pgd.get_device_error(stream) == pgd.OK
+    for out in outs:
+        b.compare(out, 64 ** -0.5)
