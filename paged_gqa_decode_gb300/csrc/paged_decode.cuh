@@ -115,6 +115,10 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 
 // ------------------------------------------------------------------ consumers
 
+struct NoHook {
+  __device__ void operator()() const {}
+};
+
 // Tensor-core consumer: one warp, whole pages, group padded to 8 heads.
 // Fragment ownership (m16n8k16): lane = 4 * gid + tig.  Score tile t covers
 // page rows 16t..16t+15; the lane holds rows 16t + gid (+8) of heads 2tig and
@@ -214,9 +218,12 @@ struct MmaConsumer {
 
   // One page (NT = 4: 64 rows), or NT / 4 of one (the window kernel's
   // 32-row slices): kt is the shared address of its K rows, vt_ptr its V
-  // rows, valid rows [rlo, rhi].  Returns true if it wrote zeros into V.
-  template <int NT = 4>
-  __device__ bool page(uint32_t kt, unsigned char* vt_ptr, int rlo, int rhi, int lane) {
+  // rows, valid rows [rlo, rhi].  Returns true if it wrote zeros into V.  k_done is
+  // called once the K rows are read, v_ready before the V rows are: it then has
+  // to write the zeros itself.
+  template <int NT = 4, class KDone = NoHook, class VReady = NoHook>
+  __device__ bool page(uint32_t kt, unsigned char* vt_ptr, int rlo, int rhi, int lane,
+                       KDone k_done = KDone(), VReady v_ready = VReady()) {
     static_assert(NT == 2 || NT == 4, "row tiles");
     const uint32_t vt = smem_addr(vt_ptr);
     float s[NT][4];
@@ -232,6 +239,7 @@ struct MmaConsumer {
         ldsm_x4(kt + (kk >> 2) * kBoxBytes + t * 2048 + off_k[kk & 3], a0, a1, a2, a3);
         mma_bf16(s[t], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
       }
+    k_done();
 
     const bool full = rlo == 0 && rhi == 16 * NT - 1;
     if constexpr (Score::kMod) {
@@ -306,7 +314,8 @@ struct MmaConsumer {
       o[mt][3] *= al1;
     }
 
-    if (!full) {  // zero the V rows outside [rlo, rhi]
+    v_ready();
+    if (std::is_same<VReady, NoHook>::value && !full) {  // zero the V rows outside [rlo, rhi]
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int half = 0; half < NT / 2; ++half) {

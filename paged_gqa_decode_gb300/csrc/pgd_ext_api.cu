@@ -58,16 +58,17 @@ int check_table(int32_t rows, int32_t width, int32_t num_pages) {
 
 // Where shared_decode's workspace keeps what; the total.
 struct SharedLayout {
-  size_t ml, off, group, bytes;
+  size_t ml, off, bytes;
 };
 SharedLayout shared_layout(const pgd_dims* d, int32_t groups) {
-  const size_t parts =
-      2 * (size_t)d->rows * d->num_q_heads + 256 * (size_t)kMaxSharedCtas;
+  // one a (row, head) for the shared pages, eight for its own (of an even count of heads)
+  const size_t group = d->num_q_heads / d->num_kv_heads;
+  const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + 8 * ((group + 1) & ~size_t(1))) +
+                       256 * (size_t)kMaxSharedCtas;
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);
   l.off = l.ml + parts * 2 * sizeof(float);
-  l.group = l.off + ((size_t)groups + d->rows + 1) * sizeof(int64_t);
-  l.bytes = l.group + (size_t)d->rows * sizeof(int32_t);
+  l.bytes = l.off + ((size_t)groups + d->rows + 1) * sizeof(int64_t);
   return l;
 }
 
@@ -578,6 +579,7 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   if ((rc = current_device(&dev)) != PGD_OK) return rc;
   char* ws = static_cast<char*>(workspace);
   SharedParams p;
+  p.q = static_cast<const uint16_t*>(q);
   p.table = table;
   p.positions = positions;
   p.starts = group_starts;
@@ -587,7 +589,6 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.part_acc = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + l.ml);
   p.item_off = reinterpret_cast<int64_t*>(ws + l.off);
-  p.row_group = reinterpret_cast<int32_t*>(ws + l.group);
   p.err = dev->err;
   p.rows = dims->rows;
   p.groups = groups;
@@ -597,22 +598,22 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.maxp = dims->max_pages_per_row;
   p.num_pages = dims->num_pages;
   p.layout = dims->layout;
-  p.min_units = 16;
+  p.min_units = 24;
   p.q_scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.k_new = static_cast<const uint16_t*>(k_new);
   p.v_new = static_cast<const uint16_t*>(v_new);
   p.k_pool = static_cast<uint16_t*>(k_pool);
   p.v_pool = static_cast<uint16_t*>(v_pool);
-  CUtensorMap k_map, v_map, q_map, q_small_map;
+  CUtensorMap k_map, v_map, q_map;
   if ((rc = encode_pool_map(&k_map, k_pool, dims, kMapWholeTile)) != PGD_OK) return rc;
   if ((rc = encode_pool_map(&v_map, v_pool, dims, kMapWholeTile)) != PGD_OK) return rc;
   if ((rc = encode_q_map(&q_map, q, dims)) != PGD_OK) return rc;
-  if ((rc = encode_q_map(&q_small_map, q, dims, 1)) != PGD_OK) return rc;
-  const int ctas = dev->sm_count < kMaxSharedCtas ? dev->sm_count : kMaxSharedCtas;
+  // (an even number: pairs)
+  const int ctas = (dev->sm_count < kMaxSharedCtas ? dev->sm_count : kMaxSharedCtas) & ~1;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dims->head_dim == 64 ? launch_shared_d64(p, k_map, v_map, q_map, q_small_map, ctas, st)
-                           : launch_shared_d128(p, k_map, v_map, q_map, q_small_map, ctas, st);
+      dims->head_dim == 64 ? launch_shared_d64(p, k_map, v_map, q_map, ctas, st)
+                           : launch_shared_d128(p, k_map, v_map, q_map, ctas, st);
   return e == cudaSuccess ? PGD_OK : PGD_ECUDA;
 }
 

@@ -97,16 +97,16 @@ cudaError_t launch_compact_pages(const CompactParams& p, cudaStream_t stream);
 constexpr int kMaxSharedGroups = 8192;  // two words a group in shared memory
 constexpr int kMaxSharedCtas = 160;
 struct SharedParams {
+  const uint16_t* q;
   const int32_t* table;
   const int32_t* positions;
   const int32_t* starts;  // [groups + 1]
   const int32_t* pages;   // [groups]
   const float* sinks;     // or nullptr
   uint16_t* out;
-  float* part_acc;     // [2 rows hq + 256 CTAs][D]
+  float* part_acc;     // D values of each partial
   float* part_ml;      // (m, l) of each
   int64_t* item_off;   // [groups + rows + 1]
-  int32_t* row_group;  // [rows]
   unsigned int* err;
   int rows, groups, hq, hkv, group, maxp, num_pages, layout;
   int64_t min_units;   // least weight of a CTA's range
@@ -117,11 +117,11 @@ struct SharedParams {
   uint16_t* v_pool;
 };
 cudaError_t launch_shared_d64(const SharedParams& p, const CUtensorMap& k_map,
-                              const CUtensorMap& v_map, const CUtensorMap& q_map,
-                              const CUtensorMap& q_small_map, int ctas, cudaStream_t stream);
+                              const CUtensorMap& v_map, const CUtensorMap& q_map, int ctas,
+                              cudaStream_t stream);
 cudaError_t launch_shared_d128(const SharedParams& p, const CUtensorMap& k_map,
-                               const CUtensorMap& v_map, const CUtensorMap& q_map,
-                               const CUtensorMap& q_small_map, int ctas, cudaStream_t stream);
+                              const CUtensorMap& v_map, const CUtensorMap& q_map, int ctas,
+                              cudaStream_t stream);
 
 // Attention with the scores of ModParams: the split decode (and its combine),
 // the tcgen05 prefill (and its block order or key-part combine), and the

@@ -273,16 +273,15 @@ bool load_encode() {
 // tokens) with boxes of 64 x group x (128 / group): one box is one half of a
 // query tile's rows (token-major, head-minor), 128-byte swizzled -- the
 // layout the tcgen05 prefill's S products read.  Tokens past the end read
-// as zeros.  `box_tokens`: tokens of a box instead.
-int encode_q_map(CUtensorMap* map, const void* q, const pgd_dims* d, int box_tokens = 0) {
+// as zeros.
+int encode_q_map(CUtensorMap* map, const void* q, const pgd_dims* d) {
   if (!load_encode()) return PGD_ECUDA;
   const int group = d->num_q_heads / d->num_kv_heads;
-  if (box_tokens == 0) box_tokens = 128 / group;
   const cuuint64_t dims3[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->num_q_heads,
                                (cuuint64_t)d->rows};
   const cuuint64_t strides3[2] = {(cuuint64_t)d->head_dim * 2,
                                   (cuuint64_t)d->num_q_heads * d->head_dim * 2};
-  const cuuint32_t box3[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
+  const cuuint32_t box3[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
   const cuuint32_t elem3[3] = {1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims3,
                         strides3, box3, elem3, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -15,23 +15,27 @@
 // Work items.  (group, block of 2 x 128 / G rows, kv head) over the shared
 // pages: two query tiles of 128 (row, head) pairs, one per TMEM lane, that
 // share each K and V page; one tile where a block's rows fit it.  (row, kv head)
-// over the row's own pages: one tile of G live lanes -- tensor time of a page
-// (384 cycles at head_dim 128) is half of what an SM's share of the HBM
-// bandwidth takes for its bytes, so the empty lanes cost nothing.
-// All items' pages form one sequence, cut into near-equal ranges, one a CTA
-// (one CTA per SM): no CTA ends early, whatever the groups' and rows' lengths.
-// A CTA's range covers the end of one item, whole items, the start of another;
-// each such segment leaves partials (m, l, o), which the combine launch joins.
-// Segments walk a staircase (each next one is of the next item or the next
-// CTA), so segment (item, cta) keeps its partials at
-//   [live lanes of the items before] + 256 * cta + lane
-// without a table.  Offsets: every CTA sums the items' weights itself (two
-// barriers, 1.5 us, less than a launch); CTA 0 leaves them for the combine.
+// over the row's own pages: G query heads, on mma.sync (MmaConsumer of
+// paged_decode.cuh), eight warps taking pages in turn -- a tile of tcgen05 would
+// have G of 128 lanes in use and one warp's exponentials to wait for on every
+// page (measured so: a page of 16 KB in 0.8 us, its share of HBM 0.37).
+// All items' pages form one sequence, cut into ranges of near-equal weight, one
+// a CTA (one CTA per SM): no CTA ends early, whatever the groups' and rows'
+// lengths.  A CTA's range covers the end of one item, whole items, the start of
+// another; each such segment leaves partials (m, l, o), which the combine launch
+// joins.  Segments walk a staircase (each next one is of the next item or the
+// next CTA), so segment (item, cta) keeps its partials at
+//   [partials of the items before] + 256 * cta + its own
+// without a table: a block's, one per lane, then a row's, one per head from each of
+// the eight warps that had a page (a merge of the warps cost 2 us a segment, the
+// partials 6 % of the pages' bytes, in L2).  Offsets: every CTA sums the items' weights itself (two
+// barriers, less than a launch); CTA 0 leaves them for the combine.
 //
 // Roles of a CTA (384 threads): warps 0-3 and 4-7 softmax of tile 0 and 1, one
-// thread a TMEM lane (one-tile items alternate between the tiles, so that one's
-// end overlaps the next one's pages); warp 8 producer (segments, Q, K and V by
-// TMA, the step's append); warp 9 issues S = Q K^T, warp 10 O += P V:
+// thread a TMEM lane (one-tile blocks alternate between the tiles, so that one's
+// end overlaps the next one's pages), and the own pages' consumers; warp 8 lays
+// out the segments and copies Q and K (TMA; and appends the step's key and value),
+// warp 11 copies V; warp 9 issues S = Q K^T, warp 10 O += P V:
 //   S into one of a tile's two buffers of 64 columns, P over it as a bf16 head
 //   and residual (weights to 2^-17, as in every attention kernel here), O in
 //   TMEM, rescaled only when a row's maximum rises by more than 2^8.
@@ -51,59 +55,64 @@ struct SharedCfg {
   static constexpr int kLanes = 128;  // (row, head) pairs of a tile
   static constexpr int kTiles = 2;
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kProducerWarp = 8, kSWarp = 9, kPvWarp = 10;
+  static constexpr int kProducerWarp = 8, kSWarp = 9, kPvWarp = 10, kVWarp = 11;
   static constexpr int kThreads = 384;
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kPage * D * 2;
   static constexpr int kStages = STAGES;
   static constexpr int kQBoxBytes = kLanes * 128;
   static constexpr int kQTileBytes = kBoxes * kQBoxBytes;
-  static constexpr int kSegs = 4;  // segment descriptors in flight
-  // Q of a row's own pages: its G heads alone, 8 lanes a box; the products read
-  // 128 lanes from there, whatever follows it (lanes that no one reads)
-  static constexpr int kSmallQBytes = kBoxes * 1024;
-  static constexpr int kQOff = 0;
-  static constexpr int kSmallQOff = kTiles * kQTileBytes;
-  static constexpr int kStageOff = kSmallQOff + kSegs * kSmallQBytes;
+  // segments in flight: a short one's round (its row's q, its pages, its products) takes 6 us
+  static constexpr int kSegs = 16;
+  static constexpr int kStageOff = kTiles * kQTileBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kBarOff = kStageOff + STAGES * kStageBytes;
-  static constexpr int kNumBars = 4 * STAGES + 3 * kTiles * 2 + 3 * kSegs + kTiles + 2;
+  static constexpr int kNumBars = 4 * STAGES + 3 * kTiles * 2 + 2 * kSegs + 2 * kTiles + 2;
   static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kSCol = kTiles * D;
   static constexpr uint32_t kIdescS = umma_idesc_bf16(128, kPage, 0, 0);
   static constexpr uint32_t kIdescPV = umma_idesc_bf16(128, D, 0, 1);
   static_assert(kSCol + kTiles * 2 * kPage <= kTmemCols, "TMEM columns");
-  static_assert(kSmallQOff + (kSegs - 1) * kSmallQBytes + (kBoxes - 1) * 1024 + kQBoxBytes <=
-                    kBarOff,
-                "a small Q's product stays in the CTA's shared memory");
   static_assert((2 * kMaxSharedGroups + 1) * 4 <= STAGES * kStageBytes, "groups in the stages");
-  static_assert(kSmemBytes + 4096 <= 227 * 1024, "shared memory");
+  static_assert(kSmemBytes + kSegs * 32 + 448 <= 227 * 1024, "shared memory (dynamic + static)");
+  static_assert((2 * kMaxSharedGroups + 1) * 4 + kThreads * 16 <= STAGES * kStageBytes,
+                "the list of items behind them");
 };
 
-// Weight of a page in the cut: two tiles' products and exponentials take longer
-// than the page's bytes, one tile's do not.
-constexpr int kWeightOne = 4, kWeightTwo = 7;
+// Weights in the cut, in about 0.1 us: a page of a block of one or two tiles (two
+// tiles' products and exponentials take longer than the page's bytes), a page of
+// a row's own, and what a (block or row, kv head) costs besides.
+constexpr int kUnitOne = 7, kUnitTwo = 13, kUnitOwn = 7;
+constexpr int kFixedBlock = 25, kFixedOwn = 4;
 
 // A run of pages of one item, as the producer lays it out for the other roles.
-struct SharedSeg {
-  int valid;            // 0: no more
-  int tiles, tile;      // one tile: which
-  int q_tile;           // first Q tile; -1: the small Q of the descriptor's slot
-  int row0, rows, kvh;  // rows of the block
-  int pages;            // 0: a page outside the pool, nothing is read
-  int rhi;              // last visible position of the last page
+struct alignas(16) SharedSeg {
   long long part;       // first partial
+  int pages;            // 0: a page outside the pool, nothing is read
+  int row0, kvh, rows;  // rows of the block
+  int what;             // the fields below (0: no more)
+  int pad;
+  __device__ static int fields(bool own, int tiles, int tile, int q_tile, int rhi) {
+    return 1 | (own ? 2 : 0) | tiles << 2 | tile << 4 | q_tile << 5 | rhi << 8;
+  }
+  __device__ bool own() const { return what & 2; }    // a row's own pages
+  __device__ int tiles() const { return what >> 2 & 3; }
+  __device__ int tile() const { return what >> 4 & 1; }    // a block of one tile: which
+  __device__ int q_tile() const { return what >> 5 & 1; }  // its first Q tile
+  __device__ int rhi() const { return what >> 8; }  // last visible position of the last page
 };
+static_assert(sizeof(SharedSeg) == 32, "counted in SharedCfg");
 
 // An entry of the list: a group's shared pages, or a row's own.
 struct SharedItem {
-  long long weight;  // of all its (block, kv head) pairs
-  int pages, first;  // of one pair; the first one's place in the table row
-  int unit;          // a page's weight
+  int pages, first;  // of one (block, kv head); the first one's place in the table row
+  int unit, fixed;   // a page's weight, and a (block, kv head)'s besides
   int count;         // blocks
   int n;             // own pages: the row's position
   bool bad;
+  __device__ long long pair() const { return fixed + (long long)pages * unit; }
+  __device__ long long weight(int hkv) const { return pages > 0 ? count * hkv * pair() : 0; }
 };
 
 __device__ __forceinline__ SharedItem shared_group(const SharedParams& p, int s, int e,
@@ -115,23 +124,28 @@ __device__ __forceinline__ SharedItem shared_group(const SharedParams& p, int s,
   it.first = 0;
   it.n = 0;
   it.count = (e - s + block - 1) / block;
-  it.unit = e - s > tile ? kWeightTwo : kWeightOne;
-  it.weight = (long long)it.count * p.hkv * it.pages * it.unit;
+  it.unit = e - s > tile ? kUnitTwo : kUnitOne;
+  it.fixed = kFixedBlock;
   return it;
 }
 
-// `shared`: pages of the row's group (0: in none).
-__device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int b, int shared) {
+// A row at position n; `shared`: pages of its group (0: in none).
+__device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, int shared) {
   SharedItem it;
-  it.n = p.positions[b];
+  it.n = n;
   it.bad = shared < 0 || shared > p.maxp ||
            (it.n >= 0 && (it.n / kPage >= p.maxp || it.n / kPage < shared));
   it.first = shared;
   it.pages = it.n < 0 || it.bad ? 0 : it.n / kPage + 1 - shared;
   it.count = 1;
-  it.unit = kWeightOne;
-  it.weight = (long long)p.hkv * it.pages * it.unit;
+  it.unit = kUnitOwn;
+  it.fixed = kFixedOwn;
   return it;
+}
+
+// a / b of weights, a >= 0, b > 0 (64-bit division is a hundred instructions).
+__device__ __forceinline__ long long shared_divide(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // The last g of 0 .. groups with starts[g] <= b, -1: none.  Rows of g = -1 and
@@ -148,15 +162,57 @@ __device__ __forceinline__ int shared_find(const int* starts, int groups, int b)
   return lo;
 }
 
+// The number of copies issued, as one warp leaves it for the others: what was written
+// before it is seen with it.
+__device__ __forceinline__ void shared_store_count(int* at, int n) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_addr(at)), "r"(n) : "memory");
+}
+__device__ __forceinline__ int shared_load_count(const int* at) {
+  int n;
+  asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(n) : "r"(smem_addr(at)) : "memory");
+  return n;
+}
+
+// Waits until more than n copies are issued, or the n of `total` (-1: not known yet),
+// and returns how many are; -1 where it gives up (as mbar_wait_abortable).  A consumer's wait
+// comes before its wait for the copy itself, whose parity it would take for the
+// round's before if it came a round early.
+__device__ __forceinline__ int shared_wait_count(const int* issued, const int* total, int n,
+                                                 unsigned int* err, volatile int* abort) {
+  int c = shared_load_count(issued);
+  if (c > n) return c;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (total != nullptr && shared_load_count(total) == n) return n;
+    __nanosleep(20);
+    c = shared_load_count(issued);
+    if (c > n) return c;
+    if ((it & 63u) == 0u) {
+      if (*abort) return -1;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        record_error(err, PGD_EDEVICE_TIMEOUT);
+        *abort = 1;
+        return -1;
+      }
+    }
+  }
+}
+
+struct SharedScore {
+  using Params = SharedParams;
+  static constexpr bool kMod = false;
+};
+
 template <int D, int STAGES>
 __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     shared_decode_kernel(const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map,
-                         const __grid_constant__ CUtensorMap q_map,
-                         const __grid_constant__ CUtensorMap q_small_map, const SharedParams p) {
+                         const __grid_constant__ CUtensorMap q_map, const SharedParams p) {
   using C = SharedCfg<D, STAGES>;
   const int G = p.group;
   const int T = C::kLanes / G;  // rows of a tile
+  const int Gp = (G + 1) & ~1;  // heads of a row's partial
+  const long long own_part = (long long)p.rows * p.hq;  // the rows' partials come after the blocks'
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
@@ -164,7 +220,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* q_smem = base;
-  unsigned char* q_small = base + C::kSmallQOff;
   unsigned char* stages = base + C::kStageOff;
   uint64_t* k_full = reinterpret_cast<uint64_t*>(base + C::kBarOff);
   uint64_t* k_empty = k_full + STAGES;
@@ -175,16 +230,20 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   uint64_t* o_done = p_full + 4;           // P V of it done
   uint64_t* seg_ready = o_done + 4;        // [slot] descriptor written
   uint64_t* seg_free = seg_ready + C::kSegs;
-  uint64_t* q_full = seg_free + C::kSegs;  // [slot] the segment's Q landed
-  uint64_t* q_free = q_full + C::kSegs;    // [Q tile] its segment's S products done
+  uint64_t* q_full = seg_free + C::kSegs;  // [block % 2] its Q landed
+  uint64_t* q_free = q_full + 2;           // [Q tile] its block's S products done
   uint64_t* fin = q_free + C::kTiles;      // [issuer] all its products done
   __shared__ SharedSeg segs[C::kSegs];
   __shared__ volatile int abort_flag;
   __shared__ uint32_t tmem_slot;
   __shared__ long long warp_sum[C::kThreads / 32];
   __shared__ long long start_rem;
-  __shared__ int start_item, start_group;
-  __shared__ int y_ring[32];
+  __shared__ int start_item;
+  // tile rows of the pages by page % 64 (K is never that far ahead of V: a page's
+  // consumer needs both, and eight or so are at work), how many copies are issued, and
+  // of how many K copies in all (-1: not known yet)
+  __shared__ int y_ring[64];
+  __shared__ int k_issued, v_issued, k_total;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -201,13 +260,17 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     for (int i = 0; i < C::kSegs; ++i) {
       mbar_init(&seg_ready[i], 1);
       mbar_init(&seg_free[i], 2 + C::kSoftmaxWarps);
-      mbar_init(&q_full[i], 1);
     }
-    for (int i = 0; i < C::kTiles; ++i) mbar_init(&q_free[i], 1);
+    for (int i = 0; i < C::kTiles; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+    }
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     mbar_init_fence();
     abort_flag = 0;
+    k_issued = v_issued = 0;
+    k_total = -1;
     start_item = -1;
   }
   if (warp == C::kSWarp) tmem_alloc(&tmem_slot, C::kTmemCols);
@@ -222,9 +285,15 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   // ---------------------------------------------------------------- the cut
   const int S = p.groups, items = S + p.rows;
   long long Q, u0, u1;  // units a CTA, this one's range
+  // pages, first page, first row, end or position of each item, where every thread has one
+  int4* list = reinterpret_cast<int4*>(base + C::kBarOff) - C::kThreads;  // (the last stage's end)
   {
     int* g_start = reinterpret_cast<int*>(stages);  // [S + 1], then pages [S]
     int* g_pages = g_start + S + 1;
+    // thread i sums a run of the list
+    const int run = (items + C::kThreads - 1) / C::kThreads;
+    const int i0 = min(tid * run, items), i1 = min(i0 + run, items);
+    const int n_mine = run == 1 && tid >= S && tid < items ? p.positions[tid - S] : -1;
     bool unsorted = false;
     for (int g = tid; S > 0 && g <= S; g += C::kThreads) {
       const int s = p.starts[g], before = g > 0 ? p.starts[g - 1] : 0;
@@ -239,16 +308,20 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         return shared_group(p, g_start[i], g_start[i + 1], g_pages[i]);
       }
       g = S > 0 ? shared_find(g_start, S, i - S) : -1;
-      return shared_row(p, i - S, g >= 0 && g < S ? g_pages[g] : 0);
+      return shared_row(p, run == 1 ? n_mine : p.positions[i - S],
+                        g >= 0 && g < S ? g_pages[g] : 0);
     };
-    // thread i sums a run of the list
-    const int run = (items + C::kThreads - 1) / C::kThreads;
-    const int i0 = min(tid * run, items), i1 = min(i0 + run, items);
     long long sum = 0;
+    int g_mine = -1;
+    bool bad_mine = unsorted;
     if (!unsorted)
       for (int i = i0; i < i1; ++i) {
-        int g;
-        sum += item_at(i, g).weight;
+        const SharedItem it = item_at(i, g_mine);
+        sum += it.weight(p.hkv);
+        bad_mine = it.bad;
+        if (run == 1)  // the producer's list
+          list[i] = i < S ? make_int4(it.pages, 0, g_start[i], g_start[i + 1])
+                          : make_int4(it.pages, it.first, i - S, it.n);
       }
     long long incl = sum;
 #pragma unroll
@@ -264,7 +337,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (w < warp) at += warp_sum[w];
       total += warp_sum[w];
     }
-    Q = (total + ctas - 1) / ctas;
+    Q = shared_divide(total + ctas - 1, ctas);
     if (Q < p.min_units) Q = p.min_units;
     u0 = min(Q * cta, total);
     u1 = min(u0 + Q, total);
@@ -274,22 +347,23 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     }
     if (cta == 0 || (at <= u0 && u0 < at + sum)) {
       for (int i = i0; i < i1; ++i) {
-        int g = -1;
-        SharedItem it;
-        it.weight = 0;
-        it.bad = true;
-        if (!unsorted) it = item_at(i, g);
-        if (cta == 0) {  // for the combine; without pages: -1, bad -2
-          p.item_off[i] = it.weight > 0 ? at : (it.bad ? -2 : -1);
-          if (i >= S) p.row_group[i - S] = g < S ? g : -1;
-          if (it.bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+        int g = g_mine;
+        long long weight = sum;
+        bool bad = bad_mine;
+        if (run > 1 && !unsorted) {
+          const SharedItem it = item_at(i, g);
+          weight = it.weight(p.hkv);
+          bad = it.bad;
         }
-        if (at <= u0 && u0 < at + it.weight && u0 < u1) {
+        if (cta == 0) {  // for the combine; -1: no pages
+          p.item_off[i] = weight > 0 ? at : -1;
+          if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+        }
+        if (at <= u0 && u0 < at + weight && u0 < u1) {
           start_item = i;
-          start_group = g;
           start_rem = u0 - at;
         }
-        at += it.weight;
+        at += weight;
       }
     }
   }
@@ -307,7 +381,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
       prefetch_tensormap(&q_map);
-      prefetch_tensormap(&q_small_map);
     }
     auto load_tile = [&](unsigned char* dst, const CUtensorMap* map, int y, uint64_t* bar) {
       if constexpr (D == 128)
@@ -315,78 +388,127 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       else
         tma_load_2d(dst, map, 0, y, bar);
     };
-    int kn = 0, vn = 0;       // K and V copies issued
-    int seq = 0, qn = 0;      // segments laid out, and with their Q issued
+    int kn = 0, ks = 0;       // K copies issued, the next one's stage
+    uint32_t kph = 1;         // parity of the stage's last round (the first waits for none)
+    int seq = 0;              // segments laid out
+    int blocks_seen = 0;      // blocks' segments
     int q_next = 0;           // Q tile of the next one-tile block
-    int q_used[2] = {0, 0};   // segments that took each Q tile
-    int tile_next = 0;        // tile of the next one-tile segment
+    int q_used0 = 0, q_used1 = 0;  // segments that took each Q tile
+    int tile_next = 0;        // tile of the next one-tile block
     bool ok = true;
-    // The pages of this segment: descriptor, Q, the step's append, then K and V.
-    auto segment = [&](const SharedItem& it, bool own, int row0, int rows, int kvh, int pg0,
-                       int pg1) -> bool {
+    const bool page_major = p.layout == PGD_PAGE_MAJOR;
+    const int y_page = (page_major ? p.hkv : 1) * kPage;     // tile rows from page to page
+    const int y_head = (page_major ? 1 : p.num_pages) * kPage;  // and from head to head
+    // a row's own pages: the first 32 and whether all are in the pool, kept from
+    // head to head, and the next row's first 32, loaded meanwhile
+    int row_seen = -1, row_id = 0, next_row = -1, next_id = 0;
+    bool row_bad = false;
+    auto in_pool = [&](int id) { return id >= 0 && id < p.num_pages; };
+    auto describe = [&](long long part, int pages, int row0, int kvh, int rows, int what) -> bool {
       const int d = seq % C::kSegs;
-      SharedSeg& sg = segs[d];
       if (seq >= C::kSegs && !all_ok(wait(&seg_free[d], (seq / C::kSegs - 1) & 1))) return false;
-      const int count = pg1 - pg0;
-      const int32_t* trow = p.table + (size_t)row0 * p.maxp + it.first + pg0;
-      bool bad = false;
-      for (int k = lane; k < count; k += 32) bad |= trow[k] < 0 || trow[k] >= p.num_pages;
-      bad = __any_sync(0xffffffffu, bad);
-      const int tiles = rows > T ? 2 : 1;
-      const int q_tile = own ? -1 : tiles == 2 ? 0 : q_next;
       if (lane == 0) {
-        sg.valid = 1;
-        sg.tiles = tiles;
-        sg.tile = tiles == 2 ? 0 : tile_next;
-        sg.q_tile = q_tile;
-        sg.row0 = row0;
-        sg.rows = rows;
-        sg.kvh = kvh;
-        sg.pages = bad ? 0 : count;
-        sg.rhi = own && pg1 == it.pages ? it.n % kPage : kPage - 1;
-        // live lanes of the items before: the groups', then the rows' own
-        sg.part = 256ll * cta + (long long)row0 * p.hq + (long long)kvh * rows * G +
-                  (own ? (long long)p.rows * p.hq : 0ll);
-        if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+        int4* at = reinterpret_cast<int4*>(&segs[d]);
+        at[0] = make_int4((int)part, (int)(part >> 32), pages, row0);
+        at[1] = make_int4(kvh, rows, what, 0);
         mbar_arrive(&seg_ready[d]);
       }
-      __syncwarp();
       ++seq;
+      return true;
+    };
+    auto copy_k = [&](int y) -> bool {
+      if (kn >= STAGES && !all_ok(wait(&k_empty[ks], kph))) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+        load_tile(stages + ks * C::kStageBytes, &k_map, y, &k_full[ks]);
+        y_ring[kn & 63] = y;
+        shared_store_count(&k_issued, kn + 1);
+      }
+      ++kn;
+      if (++ks == STAGES) {
+        ks = 0;
+        kph ^= 1;
+      }
+      return true;
+    };
+    // Pages 0 .. count - 1 at trow, 32 ids at a time (the first 32 in `id`), one a lane.
+    auto copy_pages = [&](const int32_t* trow, int id, int count, int y0) -> bool {
+      for (int k = 0;;) {
+        const int n = min(count - k, 32);
+        const int ahead = k + 32 + lane < count ? trow[k + 32 + lane] : 0;
+        for (int j = 0; j < n; ++j)
+          if (!copy_k(__shfl_sync(0xffffffffu, id, j) * y_page + y0)) return false;
+        k += n;
+        if (k >= count) return true;
+        id = ahead;
+      }
+    };
+    // Pages pg0 .. pg1 - 1 of a block's shared ones.
+    auto block_segment = [&](int row0, int rows, int kvh, int pg0, int pg1) -> bool {
+      const int count = pg1 - pg0;
+      const int32_t* trow = p.table + (size_t)row0 * p.maxp + pg0;
+      const int id = lane < count ? trow[lane] : 0;
+      bool bad = lane < count && !in_pool(id);
+      for (int k = lane + 32; k < count; k += 32) bad |= !in_pool(trow[k]);
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad && lane == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
+      const int tiles = rows > T ? 2 : 1;
+      const int q_tile = tiles == 2 ? 0 : q_next;
+      // (partials of the items before: one a lane)
+      if (!describe(256ll * cta + (long long)row0 * p.hq + (long long)kvh * rows * G,
+                    bad ? 0 : count, row0, kvh, rows,
+                    SharedSeg::fields(false, tiles, tiles == 2 ? 0 : tile_next, q_tile, kPage - 1)))
+        return false;
+      if (bad) return true;
       if (tiles == 1) tile_next ^= 1;
-      if (bad) {
-        if (lane == 0) mbar_arrive(&q_full[d]);
-        qn = seq;
+      // Q, once the products that read its tiles are done
+      if (q_tile == 0) {
+        if (q_used0 > 0 && !all_ok(wait(&q_free[0], (q_used0 - 1) & 1))) return false;
+        ++q_used0;
+      }
+      if (q_tile + tiles == 2) {
+        if (q_used1 > 0 && !all_ok(wait(&q_free[1], (q_used1 - 1) & 1))) return false;
+        ++q_used1;
+      }
+      q_next = tiles == 2 ? 0 : q_next ^ 1;
+      if (lane == 0) {
+        uint64_t* full = &q_full[blocks_seen & 1];
+        mbar_arrive_expect_tx(full, tiles * C::kBoxes * T * G * 128);
+        for (int t = 0; t < tiles; ++t)
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_3d(q_smem + (q_tile + t) * C::kQTileBytes + bx * C::kQBoxBytes, &q_map,
+                        64 * bx, kvh * G, row0 + t * T, full);
+      }
+      ++blocks_seen;
+      return copy_pages(trow, id, count, kvh * y_head);
+    };
+    // Pages pg0 .. pg1 - 1 of a row's own, `pages` from place `first` of its table row on.
+    auto row_segment = [&](int row, int kvh, int first, int pages, int n, int pg0,
+                           int pg1) -> bool {
+      const int32_t* trow = p.table + (size_t)row * p.maxp + first;
+      if (row_seen != row) {
+        row_seen = row;
+        row_id = next_row == row ? next_id : lane < pages ? trow[lane] : 0;
+        bool bad = lane < pages && !in_pool(row_id);
+        for (int k = lane + 32; k < pages; k += 32) bad |= !in_pool(trow[k]);
+        row_bad = __any_sync(0xffffffffu, bad);
+      }
+      const int count = pg1 - pg0;
+      const bool last = pg1 == pages;
+      // (partials of the items before: eight a head)
+      if (!describe(256ll * cta + own_part + 8ll * Gp * ((long long)row * p.hkv + kvh),
+                    row_bad ? 0 : count, row, kvh, 1,
+                    SharedSeg::fields(true, 1, 0, 0, last ? n % kPage : kPage - 1)))
+        return false;
+      if (row_bad) {
+        if (lane == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
         return true;
       }
-      if (own) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[d], C::kBoxes * G * 128);
-          for (int bx = 0; bx < C::kBoxes; ++bx)
-            tma_load_3d(q_small + d * C::kSmallQBytes + bx * 1024, &q_small_map, 64 * bx, kvh * G,
-                        row0, &q_full[d]);
-        }
-      } else {
-        // once the products that read these Q tiles are done
-        for (int t = q_tile; t < q_tile + tiles; ++t) {
-          if (q_used[t] > 0 && !all_ok(wait(&q_free[t], (q_used[t] - 1) & 1))) return false;
-          ++q_used[t];
-        }
-        q_next = tiles == 2 ? 0 : q_next ^ 1;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[d], tiles * C::kBoxes * T * G * 128);
-          for (int t = 0; t < tiles; ++t)
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_3d(q_smem + (q_tile + t) * C::kQTileBytes + bx * C::kQBoxBytes, &q_map,
-                          64 * bx, kvh * G, row0 + t * T, &q_full[d]);
-        }
-      }
-      qn = seq;
-      if (p.k_new != nullptr && own && pg1 == it.pages) {
+      if (p.k_new != nullptr && last) {
         // the step's key and value at position n, ahead of the copy of their page
-        const int page = trow[count - 1];
-        const size_t dst = ((size_t)tile_first_row(p.layout, page, kvh, p.hkv, p.num_pages,
-                                                   p.maxp) + it.n % kPage) * D;
-        const size_t src = ((size_t)row0 * p.hkv + kvh) * D;
+        const size_t dst =
+            ((size_t)trow[pages - 1] * y_page + kvh * y_head + n % kPage) * D;
+        const size_t src = ((size_t)row * p.hkv + kvh) * D;
         if (lane < 2 * (D / 8)) {
           const int c = lane % (D / 8);
           const bool is_v = lane >= D / 8;
@@ -396,102 +518,154 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         asm volatile("fence.proxy.async.global;" ::: "memory");
         __syncwarp();
       }
-      for (int k = 0; k < count; ++k) {
-        if ((k & 31) == 0) {
-          __syncwarp();
-          if (k + lane < count)
-            y_ring[lane] = (int)tile_first_row(p.layout, trow[k + lane], kvh, p.hkv, p.num_pages,
-                                               p.maxp);
-          __syncwarp();
-        }
-        const int st = kn % STAGES;
-        const uint32_t ph = (kn / STAGES - 1) & 1;
-        unsigned char* slot = stages + st * C::kStageBytes;
-        if (kn >= STAGES && !all_ok(wait(&k_empty[st], ph))) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
-          load_tile(slot, &k_map, y_ring[k & 31], &k_full[st]);
-        }
-        ++kn;
-        if (vn >= STAGES && !all_ok(wait(&v_empty[st], ph))) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
-          load_tile(slot + C::kTileBytes, &v_map, y_ring[k & 31], &v_full[st]);
-        }
-        ++vn;
-      }
-      return true;
+      const int id = pg0 == 0 ? row_id : lane < count ? trow[pg0 + lane] : 0;
+      return copy_pages(trow + pg0, id, count, kvh * y_head);
     };
-    // walk the list from the start item on
-    long long u = u0, rem = 0;
-    int item = start_item, g = start_group;
-    if (item >= 0) rem = start_rem;
-    while (ok && u < u1 && item >= 0 && item < items) {
-      const bool own = item >= S;
-      SharedItem it;
-      int s, e;
-      if (!own) {
-        s = p.starts[item];
-        e = p.starts[item + 1];
-        it = shared_group(p, s, e, p.pages[item]);
-      } else {
-        s = item - S;
-        e = s + 1;
-        while (g < S && S > 0 && p.starts[g + 1] <= s) ++g;
-        it = shared_row(p, s, g >= 0 && g < S ? p.pages[g] : 0);
+    // walk the list from the start item on, 32 entries at a time, one a lane
+    const int T2 = 2 * T;
+    long long u = u0, rem = start_item >= 0 ? start_rem : 0;
+    int win = -32;
+    int l_first = 0, l_pages = 0, l_n = 0, l_row = 0, l_end = 0;
+      for (int item = start_item; ok && u < u1 && item >= 0 && item < items; ++item, rem = 0) {
+      if (item >= win + 32) {
+        // (the first time round the last stage still holds the list)
+        const bool listed = win < 0 && items <= C::kThreads;
+        win = item;
+        const int i = win + lane;
+        l_pages = 0;
+        if (i < items && listed) {
+          const int4 it = list[i];
+          l_pages = it.x;
+          l_first = it.y;
+          l_row = it.z;
+          l_n = l_end = it.w;
+        } else if (i < items) {
+          SharedItem it;
+          if (i < S) {
+            l_row = p.starts[i];
+            l_end = p.starts[i + 1];
+            it = shared_group(p, l_row, l_end, p.pages[i]);
+          } else {
+            l_row = i - S;
+            const int g = S > 0 ? shared_find(p.starts, S, l_row) : -1;
+            it = shared_row(p, p.positions[l_row], g >= 0 && g < S ? p.pages[g] : 0);
+          }
+          l_first = it.first;
+          l_pages = it.pages;
+          l_n = it.n;
+        }
+        if (i >= S) l_end = l_row + 1;
+        if (listed) fence_proxy_async_shared();
+        __syncwarp();
       }
-      if (it.weight > 0) {
-        const int block = 2 * T;
-        const long long per = (long long)it.pages * it.unit;  // of one (block, kv head)
-        int bh = (int)(rem / per);
-        long long at = rem - bh * per;
-        for (; ok && u < u1 && bh < it.count * p.hkv; ++bh, at = 0) {
-          // the pages whose weight begins in [u, u1)
-          const int pg0 = (int)((at + it.unit - 1) / it.unit);
-          const int pg1 = (int)min((long long)it.pages, (u1 - u + at + it.unit - 1) / it.unit);
-          u += per - at;
-          const int row0 = s + bh / p.hkv * block;
-          if (pg0 < pg1)
-            ok = segment(it, own, row0, min(block, e - row0), bh % p.hkv, pg0, pg1);
+      const int j = item - win;
+      const bool own = item >= S;
+      const int pages = __shfl_sync(0xffffffffu, l_pages, j);
+      if (pages == 0) continue;
+      const int first = __shfl_sync(0xffffffffu, l_first, j), n = __shfl_sync(0xffffffffu, l_n, j);
+      const int s = __shfl_sync(0xffffffffu, l_row, j), e = __shfl_sync(0xffffffffu, l_end, j);
+      const int unit = own ? kUnitOwn : e - s > T ? kUnitTwo : kUnitOne;
+      const int fixed = own ? kFixedOwn : kFixedBlock;
+      // the next row's page ids, needed once this row's heads are through
+      int ahead_row = -1, ahead_id = 0;
+      if (own && j < 31) {
+        const int np = __shfl_sync(0xffffffffu, l_pages, j + 1);
+        const int nf = __shfl_sync(0xffffffffu, l_first, j + 1);
+        if (np > 0) {
+          ahead_row = s + 1;
+          if (lane < np) ahead_id = p.table[(size_t)(s + 1) * p.maxp + nf + lane];
         }
       }
-      rem = 0;
-      if (++item == S) g = -1;
+      const long long per = fixed + (long long)pages * unit;  // of one (block, kv head)
+      const int blocks = own ? 1 : (e - s + T2 - 1) / T2;
+      int bh = rem == 0 ? 0 : (int)shared_divide(rem, per);
+      long long at = rem - bh * per;
+      int blk = bh / p.hkv, kvh = bh - blk * p.hkv;
+      for (; ok && u < u1 && blk < blocks; at = 0) {
+        // the pages whose weight begins in [u, u1)
+        int pg0 = 0, pg1 = pages;
+        if (at > fixed) pg0 = (int)shared_divide(at - fixed + unit - 1, unit);
+        const long long left = u1 - u + at;
+        if (left < per)
+          pg1 = left > fixed
+                    ? (int)min((long long)pages, shared_divide(left - fixed + unit - 1, unit))
+                    : 0;
+        u += per - at;
+        if (pg0 < pg1)
+          ok = own ? row_segment(s, kvh, first, pages, n, pg0, pg1)
+                   : block_segment(s + blk * T2, min(T2, e - s - blk * T2), kvh, pg0, pg1);
+        if (++kvh == p.hkv) {
+          kvh = 0;
+          ++blk;
+        }
+      }
+      next_row = ahead_row;
+      next_id = ahead_id;
     }
     if (ok) {  // the end
       const int d = seq % C::kSegs;
       if ((seq < C::kSegs || all_ok(wait(&seg_free[d], (seq / C::kSegs - 1) & 1))) && lane == 0) {
-        segs[d].valid = 0;
+        segs[d].what = 0;
         mbar_arrive(&seg_ready[d]);
       }
     }
     // drain: no copy may still be landing when the CTA exits
     if (lane == 0) {
+      shared_store_count(&k_total, kn);
       for (int j = max(0, kn - STAGES); j < kn; ++j)
         mbar_wait_bounded(&k_full[j % STAGES], (j / STAGES) & 1, p.err);
+      for (int j = max(0, blocks_seen - 2); j < blocks_seen; ++j)
+        mbar_wait_bounded(&q_full[j & 1], (j / 2) & 1, p.err);
+    }
+  } else if (warp == C::kVWarp) {
+    // ------------------------------------------------------------ V producer
+    if (lane == 0) {
+      int vn = 0, vs = 0;  // copies issued, the next one's stage
+      uint32_t vph = 1;
+      bool ok = true;
+      while (ok) {
+        const int issued = shared_wait_count(&k_issued, &k_total, vn, p.err, &abort_flag);
+        if (issued <= vn) break;  // the end
+        for (; vn < issued; ++vn) {
+          if (vn >= STAGES && !wait(&v_empty[vs], vph)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+          unsigned char* slot = stages + vs * C::kStageBytes + C::kTileBytes;
+          if constexpr (D == 128)
+            tma_load_3d(slot, &v_map, 0, y_ring[vn & 63], 0, &v_full[vs]);
+          else
+            tma_load_2d(slot, &v_map, 0, y_ring[vn & 63], &v_full[vs]);
+          shared_store_count(&v_issued, vn + 1);
+          if (++vs == STAGES) {
+            vs = 0;
+            vph ^= 1;
+          }
+        }
+      }
       for (int j = max(0, vn - STAGES); j < vn; ++j)
         mbar_wait_bounded(&v_full[j % STAGES], (j / STAGES) & 1, p.err);
-      for (int j = max(0, qn - C::kSegs); j < qn; ++j)
-        mbar_wait_bounded(&q_full[j % C::kSegs], (j / C::kSegs) & 1, p.err);
     }
   } else if (warp == C::kSWarp) {
     // ------------------------------------------------------------ S issuer
     if (lane == 0) {
       int i = 0;             // pages
       int ip[2] = {0, 0};    // pages of each tile
+      int blocks = 0;
       bool issued = false, ok = true;
       for (int seq = 0; ok; ++seq) {
         const int d = seq % C::kSegs;
         if (!wait(&seg_ready[d], (seq / C::kSegs) & 1)) break;
         const SharedSeg& sg = segs[d];
-        if (!sg.valid) break;
-        if (!wait(&q_full[d], (seq / C::kSegs) & 1)) break;
-        const bool small = sg.q_tile < 0;
-        const uint32_t q_addr =
-            small ? smem_addr(q_small) + d * C::kSmallQBytes
-                  : smem_addr(q_smem) + sg.q_tile * C::kQTileBytes;
-        const uint32_t box = small ? 1024 : C::kQBoxBytes;
-        const int t0 = sg.tile, t1 = t0 + sg.tiles, pages = sg.pages;
+        if (sg.what == 0) break;
+        const uint32_t q_addr = smem_addr(q_smem) + sg.q_tile() * C::kQTileBytes;
+        const int t0 = sg.tile(), t1 = t0 + sg.tiles(), pages = sg.own() ? 0 : sg.pages;
+        if (sg.own()) i += sg.pages;
+        if (pages > 0) {
+          if (!wait(&q_full[blocks & 1], (blocks / 2) & 1)) break;
+          ++blocks;
+        }
         for (int k = 0; k < pages && ok; ++k, ++i) {
           const int st = i % STAGES;
           if (!wait(&k_full[st], (i / STAGES) & 1)) {
@@ -511,7 +685,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
             const uint64_t qd = umma_desc_sw128(q_addr + (t - t0) * C::kQTileBytes, 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_bf16(sb, umma_desc_advance(qd, (kk >> 2) * box + (kk & 3) * 32),
+              umma_bf16(sb, umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
                         umma_desc_advance(kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32), C::kIdescS,
                         kk > 0);
             umma_commit(&s_full[tb]);
@@ -521,8 +695,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           if (ok) umma_commit(&k_empty[st]);
         }
         if (!ok) break;
-        if (!small && pages > 0)
-          for (int t = 0; t < sg.tiles; ++t) umma_commit(&q_free[sg.q_tile + t]);
+        if (pages > 0)
+          for (int t = 0; t < sg.tiles(); ++t) umma_commit(&q_free[sg.q_tile() + t]);
         mbar_arrive(&seg_free[d]);
       }
       if (issued) {  // TMEM is freed once every product is done
@@ -540,8 +714,9 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         const int d = seq % C::kSegs;
         if (!wait(&seg_ready[d], (seq / C::kSegs) & 1)) break;
         const SharedSeg& sg = segs[d];
-        if (!sg.valid) break;
-        const int t0 = sg.tile, t1 = t0 + sg.tiles, pages = sg.pages;
+        if (sg.what == 0) break;
+        const int t0 = sg.tile(), t1 = t0 + sg.tiles(), pages = sg.own() ? 0 : sg.pages;
+        if (sg.own()) i += sg.pages;
         for (int k = 0; k < pages && ok; ++k, ++i) {
           const int st = i % STAGES;
           if (!wait(&v_full[st], (i / STAGES) & 1)) {
@@ -587,16 +762,85 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = p.q_scale_log2;
     const float cc = c > 0.f ? c : 1.f;  // folded into the exponent's FMA if positive
-    int n = 0;  // pages of this tile
-    int i = 0;  // pages
+    int n = 0;   // pages of this tile
+    int i = 0;   // pages
+    int on = 0;  // pages of rows' own
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int d = seq % C::kSegs;
       if (!all_ok(wait(&seg_ready[d], (seq / C::kSegs) & 1))) break;
-      const SharedSeg& sg = segs[d];
-      if (!sg.valid) break;
-      const int pages = sg.pages, t0 = sg.tile, rhi = sg.rhi;
-      const bool mine = t >= t0 && t < t0 + sg.tiles;
+      const SharedSeg sg = segs[d];
+      if (sg.what == 0) break;
+      const int pages = sg.pages;
+      if (sg.own()) {
+        // page k of the segment is warp (on + k) % 8's, and partial k % 8
+        const int k0 = (warp - on) & 7;  // this warp's first page
+        if (k0 < pages) {
+          MmaConsumer<D, SharedScore> cons;
+          cons.init(p, sg.row0, sg.kvh * G, lane, nullptr);
+          for (int k = k0; k < pages; k += 8) {
+            const int ik = i + k, st = ik % STAGES;
+            const uint32_t ph = (ik / STAGES) & 1;
+            if (!all_ok(shared_wait_count(&k_issued, nullptr, ik, p.err, &abort_flag) > ik) ||
+                !all_ok(wait(&k_full[st], ph))) {
+              ok = false;
+              break;
+            }
+            unsigned char* kt = stages + st * C::kStageBytes;
+            auto k_done = [&]() {  // K's slot is free while the weights are computed
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&k_empty[st]);
+            };
+            const int rhi = k == pages - 1 ? sg.rhi() : kPage - 1;
+            auto v_ready = [&]() {
+              ok = all_ok(shared_wait_count(&v_issued, nullptr, ik, p.err, &abort_flag) > ik) &&
+                   all_ok(wait(&v_full[st], ph));
+              // V rows past the last position may hold anything: zero weights need
+              // zeros (eight lanes a row: lanes 128 bytes apart would meet at one bank)
+              unsigned char* vt = kt + C::kTileBytes;
+              for (int r = rhi + 1 + (lane >> 3); r < kPage; r += 4)
+#pragma unroll
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                  *reinterpret_cast<uint4*>(vt + bx * kBoxBytes + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              __syncwarp();
+            };
+            if (cons.template page<4>(smem_addr(kt), kt + C::kTileBytes, 0, rhi, lane, k_done,
+                                      v_ready))
+              fence_proxy_async_shared();
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_empty[st]);
+          }
+          if (!ok) break;
+          cons.finish();
+          // [D][heads], so that the lanes' pairs of heads lie side by side
+          const long long part = sg.part + k0 * Gp;
+          if (2 * cons.tig < Gp) {
+            float* acc = p.part_acc + part * D + cons.gid * Gp + 2 * cons.tig;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<float2*>(acc + (16 * mt + 8 * half) * Gp) =
+                    make_float2(cons.o[mt][2 * half], cons.o[mt][2 * half + 1]);
+            if (cons.gid == 0)
+              *reinterpret_cast<float4*>(p.part_ml + 2 * (part + 2 * cons.tig)) =
+                  make_float4(cons.m[0], cons.l[0], cons.m[1], cons.l[1]);
+          }
+        } else if (pages == 0 && warp == 0 && lane < Gp) {
+          // not read: the row's output is zero
+          p.part_ml[2 * (sg.part + lane)] = -INFINITY;
+          p.part_ml[2 * (sg.part + lane) + 1] = -1.f;
+        }
+        on += pages;
+        i += pages;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_free[d]);
+        continue;
+      }
+      const int t0 = sg.tile();
+      const bool mine = t >= t0 && t < t0 + sg.tiles();
       // lanes that hold a (row, head) pair: the tile's first ones
       const int lanes = mine ? min(max(sg.rows - (t - t0) * T, 0), T) * G : 0;
       const long long part = sg.part + (long long)(t - t0) * T * G + m;
@@ -625,11 +869,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
             if (!(c > 0.f)) {
 #pragma unroll
               for (int j = 0; j < kPage; ++j) sv[j] *= c;
-            }
-            if (k == pages - 1 && rhi < kPage - 1) {
-#pragma unroll
-              for (int j = 0; j < kPage; ++j)
-                if (j > rhi) sv[j] = -INFINITY;
             }
             float top[8];
 #pragma unroll
@@ -697,21 +936,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
               }
             }
           }
-          if (k == pages - 1 && rhi < kPage - 1) {
-            // V rows past the last position may hold anything: zero weights need zeros
-            const int ik = i + k;
-            if (!all_ok(wait(&v_full[ik % STAGES], (ik / STAGES) & 1))) {
-              ok = false;
-              break;
-            }
-            unsigned char* vt = stages + (ik % STAGES) * C::kStageBytes + C::kTileBytes;
-            for (int e = (rhi + 1) * (D / 8) + m; e < kPage * (D / 8); e += C::kLanes) {
-              const int row = e / (D / 8), ch = e % (D / 8);
-              *reinterpret_cast<uint4*>(vt + (ch >> 3) * kBoxBytes + row * 128 + (ch & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_shared();
-          }
           tmem_wait_st();
           tc_fence_before_sync();
           __syncwarp();
@@ -759,115 +983,143 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   }
 }
 
-// Joins a (row, query head)'s partials: those over its group's pages, then those
-// over its own, each kind one a CTA of the range that its pages fell to, 256
-// places apart.  Zeros for an inactive row (n < 0), for one that the cut found
-// bad, and where a page was outside the pool (l < 0).  One warp each.
+// Joins the partials of a row's G heads at one kv head: those over its group's pages,
+// one a CTA of the range that they fell to ([lane][D]), then those over its own, up to eight
+// a CTA ([D][heads]).  Zeros for an inactive row (n < 0), for one that the cut found
+// bad, and where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the
+// maxima pass over it).  One thread a dim; every thread forms all the weights
+// itself (their m and l are the same few words for all).
 template <int D>
-__global__ void __launch_bounds__(128) shared_combine_kernel(const SharedParams p) {
-  constexpr int kDims = D / 32;
-  using Vec = typename std::conditional<kDims == 2, float2, float4>::type;
-  const int b = blockIdx.y;
-  const int h = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(D) shared_combine_kernel(const SharedParams p) {
+  const int kvh = blockIdx.x, b = blockIdx.y, d = threadIdx.x, lane = threadIdx.x & 31;
+  const int G = p.group, Gp = (G + 1) & ~1, h0 = kvh * G;
   // (inputs of the kernel before as well, which waited for them)
-  const float sk = p.sinks && h < p.hq ? p.sinks[h] * kLog2e : -INFINITY;
+  // everything but the partials is an input of the kernel before as well, which waited
+  // for it; read here, off the path that starts once that kernel is done
+  const int S = p.groups;
+  const int n = p.positions[b];
+  float sink = p.sinks && lane < G ? p.sinks[h0 + lane] * kLog2e : -INFINITY;
+  int g = S > 0 ? shared_find(p.starts, S, b) : -1, s = 0, e = 0, shared = 0;
+  if (g >= S) g = -1;
+  if (g >= 0) {
+    s = p.starts[g];
+    e = p.starts[g + 1];
+    shared = p.pages[g];
+  }
   pdl_wait();
   pdl_allow_dependents();
-  if (h >= p.hq) return;
-  uint16_t* o = p.out + ((size_t)b * p.hq + h) * D + lane * kDims;
-  const int S = p.groups, items = S + p.rows;
-  const long long Q = p.item_off[items];
-  const long long own_off = p.item_off[S + b];
-  const int g = p.row_group[b];
-  float res[kDims];
-#pragma unroll
-  for (int j = 0; j < kDims; ++j) res[j] = 0.f;
-  if (own_off >= 0) {
-    const int G = p.group, kvh = h / G, T = 128 / G, block = 2 * T;
-    long long at[2] = {0, 0};  // first partial of each kind
-    int count[2] = {0, 0};
-    int shared = 0;
-    if (g >= 0) {
-      const long long off = p.item_off[g];
-      const int s = p.starts[g], e = p.starts[g + 1];
-      shared = p.pages[g];
-      if (off >= 0) {
-        const SharedItem it = shared_group(p, s, e, shared);
-        const int blk = (b - s) / block, row0 = s + blk * block, rows = min(block, e - row0);
-        const long long first =
-            off + ((long long)blk * p.hkv + kvh) * it.pages * it.unit;
-        const long long c0 = first / Q, c1 = (first + (long long)(it.pages - 1) * it.unit) / Q;
-        count[0] = (int)(c1 - c0) + 1;
-        at[0] = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G +
-                (b - row0) * G + h % G;
-      }
-    }
-    {
-      const SharedItem it = shared_row(p, b, shared);
-      const long long first = own_off + (long long)kvh * it.pages * it.unit;
-      const long long c0 = first / Q, c1 = (first + (long long)(it.pages - 1) * it.unit) / Q;
-      count[1] = (int)(c1 - c0) + 1;
-      at[1] = 256 * c0 + (long long)p.rows * p.hq + (long long)b * p.hq + h;
-    }
-    const int n = count[0] + count[1];
-    auto place = [&](int i) {
-      return i < count[0] ? at[0] + 256ll * i : at[1] + 256ll * (i - count[0]);
-    };
-    float mx = sk;
-    bool skipped = false, nan = false;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const float2 ml = i < n ? *reinterpret_cast<const float2*>(p.part_ml + 2 * place(i))
-                              : make_float2(-INFINITY, 0.f);
-      mx = fmaxf(mx, warp_max(ml.x));
-      skipped |= __any_sync(0xffffffffu, ml.y < 0.f);
-      nan |= __any_sync(0xffffffffu, ml.y != ml.y);
-    }
-    if (!skipped && (nan || mx == -INFINITY)) {
-      const uint16_t v = nan ? 0x7fff : 0;
-#pragma unroll
-      for (int j = 0; j < kDims; ++j) o[j] = v;
-      return;
-    }
-    if (!skipped) {
-      float den = exp2_approx(sk - mx);
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        const float2 ml = i < n ? *reinterpret_cast<const float2*>(p.part_ml + 2 * place(i))
-                                : make_float2(-INFINITY, 0.f);
-        const float f = i < n ? exp2_approx(ml.x - mx) : 0.f;
-        den += warp_sum(ml.y * f);
-        const int some = min(32, n - i0);
-#pragma unroll 4
-        for (int k = 0; k < some; ++k) {
-          const float fk = __shfl_sync(0xffffffffu, f, k);
-          const Vec v =
-              *reinterpret_cast<const Vec*>(p.part_acc + place(i0 + k) * D + lane * kDims);
-          res[0] = fmaf(v.x, fk, res[0]);
-          res[1] = fmaf(v.y, fk, res[1]);
-          if constexpr (kDims == 4) {
-            res[2] = fmaf(v.z, fk, res[2]);
-            res[3] = fmaf(v.w, fk, res[3]);
-          }
-        }
-      }
-      const float inv = 1.f / den;
-#pragma unroll
-      for (int j = 0; j < kDims; ++j) res[j] *= inv;
+  const long long Q = p.item_off[S + p.rows], own_off = p.item_off[S + b];
+  const long long off = g >= 0 ? p.item_off[g] : -1;
+  uint16_t* out = p.out + ((size_t)b * p.hq + h0) * D + d;
+  if (own_off < 0) {
+    for (int h = 0; h < G; ++h) out[(size_t)h * D] = 0;
+    return;
+  }
+  // the shared pages' partials
+  long long at0 = 0;
+  int count0 = 0;
+  if (off >= 0) {
+    const SharedItem it = shared_group(p, s, e, shared);
+    const int block = 2 * (128 / G), blk = (b - s) / block, row0 = s + blk * block;
+    const int rows = min(block, e - row0);
+    const long long first = off + ((long long)blk * p.hkv + kvh) * it.pair() + it.fixed;
+    const long long c0 = shared_divide(first, Q);
+    count0 = (int)(shared_divide(first + (long long)(it.pages - 1) * it.unit, Q) - c0) + 1;
+    at0 = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G;
+  }
+  // its own pages'
+  const SharedItem it = shared_row(p, n, shared);
+  const long long first = own_off + kvh * it.pair() + it.fixed;
+  const long long c0 = shared_divide(first, Q);
+  const int ranges =
+      (int)(shared_divide(first + (long long)(it.pages - 1) * it.unit, Q) - c0) + 1;
+  const long long at1 = 256 * c0 + (long long)p.rows * p.hq +
+                        8ll * Gp * ((long long)b * p.hkv + kvh);
+  // pages that start before the end of range i
+  auto before = [&](int i) {
+    return i + 1 >= ranges
+               ? it.pages
+               : (int)shared_divide((c0 + i + 1) * Q - first + it.unit - 1, it.unit);
+  };
+
+  // the heads' maxima: lane 8 k + h looks at partial k, k + 4, .. of head h
+  const int lh = lane & 7;
+  float mx = -INFINITY;
+  bool skipped = false, nan = false;
+  auto look = [&](long long part) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (part + lh));
+    mx = fmaxf(mx, ml.x);
+    skipped |= ml.y < 0.f;
+    nan |= ml.y != ml.y;
+  };
+  if (lh < G) {
+    for (int i = lane >> 3; i < count0; i += 4) look(at0 + 256ll * i);
+    for (int i = 0, pg = 0; i < ranges; ++i) {
+      const int end = before(i);
+      for (int j = lane >> 3; j < min(end - pg, 8); j += 4) look(at1 + 256ll * i + j * Gp);
+      pg = end;
     }
   }
-  if constexpr (kDims == 4)
-    *reinterpret_cast<uint2*>(o) =
-        make_uint2(pack_bf16x2(res[0], res[1]), pack_bf16x2(res[2], res[3]));
-  else
-    *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(res[0], res[1]);
+  skipped = __any_sync(0xffffffffu, skipped);
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const unsigned nans = __ballot_sync(0xffffffffu, nan);
+  sink = __shfl_sync(0xffffffffu, sink, lh);
+  mx = fmaxf(mx, sink);
+
+  float ref[8], den[8], acc[8];
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    const float m = __shfl_sync(0xffffffffu, mx, h);
+    ref[h] = m == -INFINITY ? 0.f : m;
+    den[h] = exp2_approx(__shfl_sync(0xffffffffu, sink, h) - ref[h]);
+    acc[h] = 0.f;
+  }
+  auto add = [&](int h, const float2& ml, float v) {
+    const float f = exp2_approx(ml.x - ref[h]);
+    den[h] = fmaf(ml.y, f, den[h]);
+    acc[h] = fmaf(v, f, acc[h]);
+  };
+#pragma unroll 4
+  for (int i = 0; i < count0; ++i) {
+    const long long part = at0 + 256ll * i;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml + 2 * part);
+    const float* v = p.part_acc + part * D + d;
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < G) add(h, ml[h], v[h * D]);
+  }
+  for (int i = 0, pg = 0; i < ranges; ++i) {
+    const int end = before(i), some = min(end - pg, 8);
+    pg = end;
+#pragma unroll 4
+    for (int j = 0; j < some; ++j) {
+      const long long part = at1 + 256ll * i + j * Gp;
+      const float4* ml = reinterpret_cast<const float4*>(p.part_ml + 2 * part);
+      const float2* v = reinterpret_cast<const float2*>(p.part_acc + part * D + d * Gp);
+#pragma unroll
+      for (int h = 0; h < 8; h += 2)
+        if (h < Gp) {
+          const float2 a = v[h / 2];
+          const float4 w = ml[h / 2];
+          add(h, make_float2(w.x, w.y), a.x);
+          add(h + 1, make_float2(w.z, w.w), a.y);
+        }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 8; ++h)
+    if (h < G) {
+      uint16_t r = __bfloat16_as_ushort(__float2bfloat16_rn(den[h] == 0.f ? 0.f : acc[h] / den[h]));
+      if (nans & (0x01010101u << h)) r = 0x7fff;
+      out[(size_t)h * D] = skipped ? 0 : r;
+    }
 }
 
 template <int D, int STAGES>
 cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& k_map,
-                          const CUtensorMap& v_map, const CUtensorMap& q_map,
-                          const CUtensorMap& q_small_map, int ctas, cudaStream_t stream) {
+                          const CUtensorMap& v_map, const CUtensorMap& q_map, int ctas,
+                          cudaStream_t stream) {
   using C = SharedCfg<D, STAGES>;
   auto kern = shared_decode_kernel<D, STAGES>;
   static std::atomic<bool> configured[64];
@@ -879,11 +1131,25 @@ cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& k_map,
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
   }
-  e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kSmemBytes, stream, k_map, v_map, q_map,
-                 q_small_map, p);
+  // Clusters of two put neighbouring CTAs on the two SMs of a TPC: an SM that reads
+  // rows' own pages (mma.sync) slows its neighbour's tcgen05 products (a page of two
+  // tiles 1.3 -> 2.0-2.9 us), so both had better do the same.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, k_map, v_map, q_map, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(shared_combine_kernel<D>, dim3((p.hq + 3) / 4, p.rows), dim3(128), 0, stream,
-                    p);
+  return launch_pdl(shared_combine_kernel<D>, dim3(p.hkv, p.rows), dim3(D), 0, stream, p);
 }
 
 }  // namespace pgd

@@ -5,8 +5,8 @@ namespace pgd {
 
 cudaError_t launch_shared_d64(const SharedParams& p, const CUtensorMap& k_map,
                              const CUtensorMap& v_map, const CUtensorMap& q_map,
-                             const CUtensorMap& q_small_map, int ctas, cudaStream_t stream) {
-  return launch_shared<64, 9>(p, k_map, v_map, q_map, q_small_map, ctas, stream);
+                             int ctas, cudaStream_t stream) {
+  return launch_shared<64, 9>(p, k_map, v_map, q_map, ctas, stream);
 }
 
 }  // namespace pgd
