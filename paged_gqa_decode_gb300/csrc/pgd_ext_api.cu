@@ -598,7 +598,6 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.maxp = dims->max_pages_per_row;
   p.num_pages = dims->num_pages;
   p.layout = dims->layout;
-  p.min_units = 24;
   p.q_scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.k_new = static_cast<const uint16_t*>(k_new);
   p.v_new = static_cast<const uint16_t*>(v_new);

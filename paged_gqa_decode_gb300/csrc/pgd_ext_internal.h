@@ -109,7 +109,6 @@ struct SharedParams {
   int64_t* item_off;   // [groups + rows + 1]
   unsigned int* err;
   int rows, groups, hq, hkv, group, maxp, num_pages, layout;
-  int64_t min_units;   // least weight of a CTA's range
   float q_scale_log2;
   const uint16_t* k_new;  // or nullptr
   const uint16_t* v_new;

@@ -80,11 +80,13 @@ struct SharedCfg {
                 "the list of items behind them");
 };
 
-// Weights in the cut, in about 0.1 us: a page of a block of one or two tiles (two
-// tiles' products and exponentials take longer than the page's bytes), a page of
-// a row's own, and what a (block or row, kv head) costs besides.
-constexpr int kUnitOne = 7, kUnitTwo = 13, kUnitOwn = 7;
-constexpr int kFixedBlock = 25, kFixedOwn = 4;
+// Weights in the cut, in about 0.1 us on GB300, fitted to what CTAs of mixed calls
+// took: a page of a block of one or two tiles (two tiles' products and
+// exponentials take longer than the page's bytes), a page of a row's own, and what
+// a (block or row, kv head) costs besides.
+constexpr int kUnitOne = 7, kUnitTwo = 13, kFixedBlock = 30, kFixedOwn = 4;
+constexpr int kMinPages = 4;  // of a CTA's range, at least
+__host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 4 : 6; }
 
 // A run of pages of one item, as the producer lays it out for the other roles.
 struct alignas(16) SharedSeg {
@@ -130,6 +132,7 @@ __device__ __forceinline__ SharedItem shared_group(const SharedParams& p, int s,
 }
 
 // A row at position n; `shared`: pages of its group (0: in none).
+template <int D>
 __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, int shared) {
   SharedItem it;
   it.n = n;
@@ -138,7 +141,7 @@ __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, i
   it.first = shared;
   it.pages = it.n < 0 || it.bad ? 0 : it.n / kPage + 1 - shared;
   it.count = 1;
-  it.unit = kUnitOwn;
+  it.unit = unit_own(D);
   it.fixed = kFixedOwn;
   return it;
 }
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         return shared_group(p, g_start[i], g_start[i + 1], g_pages[i]);
       }
       g = S > 0 ? shared_find(g_start, S, i - S) : -1;
-      return shared_row(p, run == 1 ? n_mine : p.positions[i - S],
+      return shared_row<D>(p, run == 1 ? n_mine : p.positions[i - S],
                         g >= 0 && g < S ? g_pages[g] : 0);
     };
     long long sum = 0;
@@ -338,7 +341,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       total += warp_sum[w];
     }
     Q = shared_divide(total + ctas - 1, ctas);
-    if (Q < p.min_units) Q = p.min_units;
+    if (Q < kMinPages * unit_own(D)) Q = kMinPages * unit_own(D);
+    if (Q < kUnitTwo) Q = kUnitTwo;  // (no range between two pages' beginnings)
     u0 = min(Q * cta, total);
     u1 = min(u0 + Q, total);
     if (cta == 0 && tid == 0) {
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           } else {
             l_row = i - S;
             const int g = S > 0 ? shared_find(p.starts, S, l_row) : -1;
-            it = shared_row(p, p.positions[l_row], g >= 0 && g < S ? p.pages[g] : 0);
+            it = shared_row<D>(p, p.positions[l_row], g >= 0 && g < S ? p.pages[g] : 0);
           }
           l_first = it.first;
           l_pages = it.pages;
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (pages == 0) continue;
       const int first = __shfl_sync(0xffffffffu, l_first, j), n = __shfl_sync(0xffffffffu, l_n, j);
       const int s = __shfl_sync(0xffffffffu, l_row, j), e = __shfl_sync(0xffffffffu, l_end, j);
-      const int unit = own ? kUnitOwn : e - s > T ? kUnitTwo : kUnitOne;
+      const int unit = own ? unit_own(D) : e - s > T ? kUnitTwo : kUnitOne;
       const int fixed = own ? kFixedOwn : kFixedBlock;
       // the next row's page ids, needed once this row's heads are through
       int ahead_row = -1, ahead_id = 0;
@@ -814,16 +818,14 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           }
           if (!ok) break;
           cons.finish();
-          // [D][heads], so that the lanes' pairs of heads lie side by side
           const long long part = sg.part + k0 * Gp;
           if (2 * cons.tig < Gp) {
-            float* acc = p.part_acc + part * D + cons.gid * Gp + 2 * cons.tig;
+            float* acc = p.part_acc + (part + 2 * cons.tig) * D + cons.gid;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
-                *reinterpret_cast<float2*>(acc + (16 * mt + 8 * half) * Gp) =
-                    make_float2(cons.o[mt][2 * half], cons.o[mt][2 * half + 1]);
+              for (int e = 0; e < 4; ++e)
+                acc[(e & 1) * D + 16 * mt + (e >> 1) * 8] = cons.o[mt][e];
             if (cons.gid == 0)
               *reinterpret_cast<float4*>(p.part_ml + 2 * (part + 2 * cons.tig)) =
                   make_float4(cons.m[0], cons.l[0], cons.m[1], cons.l[1]);
@@ -983,22 +985,23 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   }
 }
 
-// Joins the partials of a row's G heads at one kv head: those over its group's pages,
-// one a CTA of the range that they fell to ([lane][D]), then those over its own, up to eight
-// a CTA ([D][heads]).  Zeros for an inactive row (n < 0), for one that the cut found
-// bad, and where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the
-// maxima pass over it).  One thread a dim; every thread forms all the weights
-// itself (their m and l are the same few words for all).
+// Joins the partials of a (row, query head): those over its group's pages, one a CTA of the
+// range that they fell to, then those over its own, up to eight a CTA.  Zeros for an inactive row (n < 0), for one that the cut found bad, and
+// where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the maxima
+// pass over it).  A warp each, a CTA the heads of a kv head.  Bound by latency: the
+// places of the partials are worked out from the cut's offsets (one round trip),
+// then 32 partials' (m, l), one a lane, and the first eight partials' values load
+// together.
 template <int D>
-__global__ void __launch_bounds__(D) shared_combine_kernel(const SharedParams p) {
-  const int kvh = blockIdx.x, b = blockIdx.y, d = threadIdx.x, lane = threadIdx.x & 31;
-  const int G = p.group, Gp = (G + 1) & ~1, h0 = kvh * G;
-  // (inputs of the kernel before as well, which waited for them)
+__global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams p) {
+  constexpr int kDims = D / 32, kEarly = 8;
+  const int kvh = blockIdx.x, b = blockIdx.y, g_head = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.group, Gp = (G + 1) & ~1, h = kvh * G + g_head;
   // everything but the partials is an input of the kernel before as well, which waited
   // for it; read here, off the path that starts once that kernel is done
   const int S = p.groups;
   const int n = p.positions[b];
-  float sink = p.sinks && lane < G ? p.sinks[h0 + lane] * kLog2e : -INFINITY;
+  const float sink = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
   int g = S > 0 ? shared_find(p.starts, S, b) : -1, s = 0, e = 0, shared = 0;
   if (g >= S) g = -1;
   if (g >= 0) {
@@ -1006,114 +1009,120 @@ __global__ void __launch_bounds__(D) shared_combine_kernel(const SharedParams p)
     e = p.starts[g + 1];
     shared = p.pages[g];
   }
+  const SharedItem group = shared_group(p, s, e, shared), own = shared_row<D>(p, n, shared);
   pdl_wait();
   pdl_allow_dependents();
   const long long Q = p.item_off[S + p.rows], own_off = p.item_off[S + b];
   const long long off = g >= 0 ? p.item_off[g] : -1;
-  uint16_t* out = p.out + ((size_t)b * p.hq + h0) * D + d;
-  if (own_off < 0) {
-    for (int h = 0; h < G; ++h) out[(size_t)h * D] = 0;
-    return;
-  }
-  // the shared pages' partials
-  long long at0 = 0;
-  int count0 = 0;
-  if (off >= 0) {
-    const SharedItem it = shared_group(p, s, e, shared);
-    const int block = 2 * (128 / G), blk = (b - s) / block, row0 = s + blk * block;
-    const int rows = min(block, e - row0);
-    const long long first = off + ((long long)blk * p.hkv + kvh) * it.pair() + it.fixed;
+  uint16_t* out = p.out + ((size_t)b * p.hq + h) * D + lane * kDims;
+  float res[kDims];
+#pragma unroll
+  for (int j = 0; j < kDims; ++j) res[j] = 0.f;
+  if (own_off >= 0) {
+    // the shared pages' partials
+    long long at0 = 0;
+    int count0 = 0;
+    if (off >= 0) {
+      const int block = 2 * (128 / G), blk = (b - s) / block, row0 = s + blk * block;
+      const int rows = min(block, e - row0);
+      const long long first = off + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
+      const long long c0 = shared_divide(first, Q);
+      count0 =
+          (int)(shared_divide(first + (long long)(group.pages - 1) * group.unit, Q) - c0) + 1;
+      at0 = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G + g_head;
+    }
+    // its own pages': range i of a CTA has one for each page, at most eight
+    const long long first = own_off + kvh * own.pair() + own.fixed;
     const long long c0 = shared_divide(first, Q);
-    count0 = (int)(shared_divide(first + (long long)(it.pages - 1) * it.unit, Q) - c0) + 1;
-    at0 = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G;
-  }
-  // its own pages'
-  const SharedItem it = shared_row(p, n, shared);
-  const long long first = own_off + kvh * it.pair() + it.fixed;
-  const long long c0 = shared_divide(first, Q);
-  const int ranges =
-      (int)(shared_divide(first + (long long)(it.pages - 1) * it.unit, Q) - c0) + 1;
-  const long long at1 = 256 * c0 + (long long)p.rows * p.hq +
-                        8ll * Gp * ((long long)b * p.hkv + kvh);
-  // pages that start before the end of range i
-  auto before = [&](int i) {
-    return i + 1 >= ranges
-               ? it.pages
-               : (int)shared_divide((c0 + i + 1) * Q - first + it.unit - 1, it.unit);
-  };
-
-  // the heads' maxima: lane 8 k + h looks at partial k, k + 4, .. of head h
-  const int lh = lane & 7;
-  float mx = -INFINITY;
-  bool skipped = false, nan = false;
-  auto look = [&](long long part) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (part + lh));
-    mx = fmaxf(mx, ml.x);
-    skipped |= ml.y < 0.f;
-    nan |= ml.y != ml.y;
-  };
-  if (lh < G) {
-    for (int i = lane >> 3; i < count0; i += 4) look(at0 + 256ll * i);
+    const int ranges =
+        (int)(shared_divide(first + (long long)(own.pages - 1) * own.unit, Q) - c0) + 1;
+    const long long at1 = 256 * c0 + (long long)p.rows * p.hq +
+                          8ll * Gp * ((long long)b * p.hkv + kvh);
+    // pages that start before the end of range i
+    auto before = [&](int i) {
+      return i + 1 >= ranges
+                 ? own.pages
+                 : (int)shared_divide((c0 + i + 1) * Q - first + own.unit - 1, own.unit);
+    };
+    int count = count0;
     for (int i = 0, pg = 0; i < ranges; ++i) {
       const int end = before(i);
-      for (int j = lane >> 3; j < min(end - pg, 8); j += 4) look(at1 + 256ll * i + j * Gp);
+      count += min(end - pg, 8);
       pg = end;
     }
-  }
-  skipped = __any_sync(0xffffffffu, skipped);
+    auto own_place = [&](int j) {  // j of the row's own partials
+      long long at = at1;
+      for (int i = 0, pg = 0; i + 1 < ranges; ++i) {
+        const int end = before(i), some = min(end - pg, 8);
+        if (j < some) break;
+        j -= some;
+        pg = end;
+        at += 256;
+      }
+      return at + j * Gp;
+    };
+    auto place = [&](int i) {
+      return i < count0 ? at0 + 256ll * i : own_place(i - count0) + g_head;
+    };
+    auto values = [&](int i, float (&v)[kDims]) {
+      const float* a = p.part_acc + place(i) * D + lane * kDims;
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const unsigned nans = __ballot_sync(0xffffffffu, nan);
-  sink = __shfl_sync(0xffffffffu, sink, lh);
-  mx = fmaxf(mx, sink);
-
-  float ref[8], den[8], acc[8];
+      for (int j = 0; j < kDims; j += 2) {
+        const float2 w = *reinterpret_cast<const float2*>(a + j);
+        v[j] = w.x;
+        v[j + 1] = w.y;
+      }
+    };
+    auto weight = [&](int i) {
+      if (i >= count) return make_float2(-INFINITY, 0.f);
+      return *reinterpret_cast<const float2*>(p.part_ml + 2 * place(i));
+    };
+    float2 ml = weight(lane);
+    float early[kEarly][kDims];
 #pragma unroll
-  for (int h = 0; h < 8; ++h) {
-    const float m = __shfl_sync(0xffffffffu, mx, h);
-    ref[h] = m == -INFINITY ? 0.f : m;
-    den[h] = exp2_approx(__shfl_sync(0xffffffffu, sink, h) - ref[h]);
-    acc[h] = 0.f;
-  }
-  auto add = [&](int h, const float2& ml, float v) {
-    const float f = exp2_approx(ml.x - ref[h]);
-    den[h] = fmaf(ml.y, f, den[h]);
-    acc[h] = fmaf(v, f, acc[h]);
-  };
-#pragma unroll 4
-  for (int i = 0; i < count0; ++i) {
-    const long long part = at0 + 256ll * i;
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml + 2 * part);
-    const float* v = p.part_acc + part * D + d;
-#pragma unroll
-    for (int h = 0; h < 8; ++h)
-      if (h < G) add(h, ml[h], v[h * D]);
-  }
-  for (int i = 0, pg = 0; i < ranges; ++i) {
-    const int end = before(i), some = min(end - pg, 8);
-    pg = end;
-#pragma unroll 4
-    for (int j = 0; j < some; ++j) {
-      const long long part = at1 + 256ll * i + j * Gp;
-      const float4* ml = reinterpret_cast<const float4*>(p.part_ml + 2 * part);
-      const float2* v = reinterpret_cast<const float2*>(p.part_acc + part * D + d * Gp);
-#pragma unroll
-      for (int h = 0; h < 8; h += 2)
-        if (h < Gp) {
-          const float2 a = v[h / 2];
-          const float4 w = ml[h / 2];
-          add(h, make_float2(w.x, w.y), a.x);
-          add(h + 1, make_float2(w.z, w.w), a.y);
-        }
+    for (int k = 0; k < kEarly; ++k)
+      if (k < count) values(k, early[k]);
+    float mx = sink;
+    bool skipped = false, nan = false;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      const float2 w = i0 == 0 ? ml : weight(i0 + lane);
+      mx = fmaxf(mx, warp_max(w.x));
+      skipped |= __any_sync(0xffffffffu, w.y < 0.f);
+      nan |= __any_sync(0xffffffffu, w.y != w.y);
     }
-  }
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float den = exp2_approx(sink - ref);
+    auto add = [&](const float (&v)[kDims], float f) {
 #pragma unroll
-  for (int h = 0; h < 8; ++h)
-    if (h < G) {
-      uint16_t r = __bfloat16_as_ushort(__float2bfloat16_rn(den[h] == 0.f ? 0.f : acc[h] / den[h]));
-      if (nans & (0x01010101u << h)) r = 0x7fff;
-      out[(size_t)h * D] = skipped ? 0 : r;
+      for (int j = 0; j < kDims; ++j) res[j] = fmaf(v[j], f, res[j]);
+    };
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      if (i0 > 0) ml = weight(i0 + lane);
+      const float f = exp2_approx(ml.x - ref);  // (past the end: 0)
+      den += warp_sum(ml.y * f);
+      const int some = min(32, count - i0);
+      int k = 0;
+      if (i0 == 0) {
+#pragma unroll
+        for (; k < kEarly; ++k)
+          if (k < some) add(early[k], __shfl_sync(0xffffffffu, f, k));
+      }
+#pragma unroll 8
+      for (; k < some; ++k) {
+        float v[kDims];
+        values(i0 + k, v);
+        add(v, __shfl_sync(0xffffffffu, f, k));
+      }
     }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+    for (int j = 0; j < kDims; ++j) res[j] = skipped ? 0.f : nan ? NAN : res[j] * inv;
+  }
+  if constexpr (kDims == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(res[0], res[1]), pack_bf16x2(res[2], res[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(res[0], res[1]);
 }
 
 template <int D, int STAGES>
@@ -1149,7 +1158,8 @@ cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& k_map,
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, k_map, v_map, q_map, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(shared_combine_kernel<D>, dim3(p.hkv, p.rows), dim3(D), 0, stream, p);
+  return launch_pdl(shared_combine_kernel<D>, dim3(p.hkv, p.rows), dim3(32 * p.group), 0, stream,
+                    p);
 }
 
 }  // namespace pgd
