@@ -80,13 +80,13 @@ struct SharedCfg {
                 "the list of items behind them");
 };
 
-// Weights in the cut, in about 0.1 us on GB300, fitted to what CTAs of mixed calls
+// Weights in the cut, in about 0.05 us on GB300, fitted to what CTAs of mixed calls
 // took: a page of a block of one or two tiles (two tiles' products and
 // exponentials take longer than the page's bytes), a page of a row's own, and what
 // a (block or row, kv head) costs besides.
-constexpr int kUnitOne = 7, kUnitTwo = 13, kFixedBlock = 30, kFixedOwn = 4;
+constexpr int kUnitOne = 14, kUnitTwo = 26, kFixedBlock = 60, kFixedOwn = 8;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
-__host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 4 : 6; }
+__host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 7 : 10; }
 
 // A run of pages of one item, as the producer lays it out for the other roles.
 struct alignas(16) SharedSeg {
