@@ -228,7 +228,7 @@ PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const p
  * positions it keeps, over reference-counted pages: forks (parents[r] = the
  * row forked), beam search's reordering (any map), releases (parents[r] = -1) and
  * cuts (keep) in one call.
- *   rows         R in 0 .. 12288; max_pages_per_row: W, R * W <= 2^30.
+ *   rows         R in 0 .. 8192; max_pages_per_row: W, R * W <= 2^30.
  *   table        int32 [R][W], read and rewritten in place: row i's first
  *                ceil(lengths[i] / 64) entries are its pages.
  *   lengths      int32 [R]: positions of each row in the cache.

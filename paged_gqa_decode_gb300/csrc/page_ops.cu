@@ -70,10 +70,54 @@ cudaError_t launch_cluster(void (*kernel)(Params), int ctas, size_t smem, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// f(r, e, entry) for the entries lo(r) .. hi(r) - 1 of a table's rows r, shared out
+// over `warps` warps of which this is number `warp`, N rows at a time (rows N w ..
+// N w + N - 1 of every round are warp w's) and 256 / N entries of each, so that a thread
+// has eight loads in flight.
+template <int N, class Lo, class Hi, class F>
+__device__ __forceinline__ void each_entry_of(const int32_t* table, int rows, int width, int warp,
+                                              int warps, Lo lo, Hi hi, F f) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kEach = 8 / N;  // loads of a row
+  for (int r0 = N * warp; r0 < rows; r0 += N * warps) {
+    int from[N], to[N], most = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      from[k] = r0 + k < rows ? lo(r0 + k) : 0;
+      to[k] = r0 + k < rows ? hi(r0 + k) : 0;
+      most = max(most, to[k] - from[k]);
+    }
+    for (int e0 = lane; e0 - lane < most; e0 += 32 * kEach) {
+      int page[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = from[k / kEach] + e0 + 32 * (k % kEach);
+        if (e < to[k / kEach]) page[k] = table[(size_t)(r0 + k / kEach) * width + e];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = from[k / kEach] + e0 + 32 * (k % kEach);
+        if (e < to[k / kEach]) f(r0 + k / kEach, e, page[k]);
+      }
+    }
+  }
+}
+
+// A warp takes one row at a time where there is a warp for every row, else four.
+__device__ __forceinline__ int rows_at_a_time(int rows, int warps) { return rows <= warps ? 1 : 4; }
+template <class Lo, class Hi, class F>
+__device__ __forceinline__ void each_table_entry(const int32_t* table, int rows, int width,
+                                                 int warp, int warps, Lo lo, Hi hi, F f) {
+  if (rows_at_a_time(rows, warps) == 1)
+    each_entry_of<1>(table, rows, width, warp, warps, lo, hi, f);
+  else
+    each_entry_of<4>(table, rows, width, warp, warps, lo, hi, f);
+}
+
 // ------------------------------------------------------------------ fork_rows
 
-// One cluster; its CTAs share out the rows (a warp each) and meet at cluster
-// barriers, since every step needs the counts that the one before left:
+// Seven steps over rows and entries, each of which needs the counts that all of the one
+// before left:
 //   1  a parent of c >= 2 children: its pages' shares grow by c - 1
 //   2  entries that no child takes over: their pages' shares fall by one, so
 //      a page that nobody holds any more is left at -1
@@ -88,261 +132,471 @@ cudaError_t launch_cluster(void (*kernel)(Params), int ctas, size_t smem, cudaSt
 // Shares in between stay above -2^30 (a row's claims and its leaving its last
 // page count one each); claims of entries are below that, claims of last pages
 // from there up, so that neither is taken for the other.
+// Bound by latency: each step is a table load and an atomic or load in L2 for every
+// entry, eight a thread in flight.  Up to kForkClusterEntries entries one cluster
+// does all steps and meets at cluster barriers (1-2 us a step), with what the rows are
+// in every CTA's shared memory.  Past that its eight SMs' rate of scattered accesses
+// binds (0.3 a cycle each: 30 us a step at 143 000 entries), and a launch a step over
+// all SMs is faster: 4096 rows of 130 entries 166 -> 46 us.
 constexpr int kForkThreads = 1024;
 constexpr int kForkClaim = INT32_MIN, kForkTail = INT32_MIN / 2;
+constexpr int64_t kForkClusterEntries = 20000;
 
-struct ForkRow {
-  int parent;  // -1: none
-  int kept, pages, had;  // positions and pages of the row, pages of its parent
+// What a row is and becomes.  In shared memory, for a CTA that meets with others at
+// every step:
+struct ForkRows {
+  int* kept_;       // positions it gets
+  int* old_pages_;  // pages it had
+  int* least_;      // fewest pages that a child of it takes
+  int* aux;         // see the steps
+  int16_t* parent_;  // -1: none
+  uint16_t* children_;
+  __device__ int parent(int r) const { return parent_[r]; }
+  __device__ int kept(int r) const { return kept_[r]; }
+  __device__ int old_pages(int r) const { return old_pages_[r]; }
+  __device__ int children(int r) const { return children_[r]; }
+  __device__ int least(int r) const { return least_[r]; }
 };
 
-__device__ __forceinline__ int fork_length(const ForkParams& p, int r) {
-  const int n = p.lengths[r];
-  return n >= 0 && n <= p.width * kPage ? n : 0;  // (reported once, below)
-}
-
-__device__ __forceinline__ ForkRow fork_row(const ForkParams& p, int r) {
-  ForkRow f;
-  f.parent = p.parents[r];
-  if (f.parent < 0 || f.parent >= p.rows) f.parent = -1;
-  const int n = f.parent < 0 ? 0 : fork_length(p, f.parent);
-  f.kept = n;
-  if (p.keep) f.kept = min(n, max(p.keep[r], 0));
-  f.pages = (f.kept + kPage - 1) / kPage;
-  f.had = (n + kPage - 1) / kPage;
-  return f;
-}
-
-__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
-  extern __shared__ int smem[];
-  int* children = smem;            // [rows]
-  int* least = children + p.rows;  // [rows] fewest pages that a child takes
-  int* slab = least + p.rows;
-  __shared__ int warps[33];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gwarp = cta * (kForkThreads / 32) + warp, gwarps = ctas * (kForkThreads / 32);
-  const int gtid = cta * kForkThreads + tid, gthreads = ctas * kForkThreads;
-  auto in_pool = [&](int page) { return page >= 0 && page < p.num_pages; };
-  auto report = [&]() { record_error(p.err, PGD_EDEVICE_BOUNDS); };
-
-  for (int r = tid; r < p.rows; r += kForkThreads) {
-    children[r] = 0;
-    least[r] = INT32_MAX;
+// or from the arguments, with the first step's children and least pages in counts and
+// new_lengths until the sixth writes those:
+struct ForkInputs {
+  const ForkParams& p;
+  __device__ int length(int r) const {
+    const int n = p.lengths[r];
+    return n >= 0 && n <= p.width * kPage ? n : 0;
   }
-  pdl_wait();
-  pdl_allow_dependents();
-  const int head0 = p.free_head ? *p.free_head : 0;
-  const bool bad_head = head0 < 0 || head0 > p.num_free;
-  if (bad_head && gtid == 0) report();
-  __syncthreads();
-  for (int r = tid; r < p.rows; r += kForkThreads) {
-    const ForkRow f = fork_row(p, r);
-    if (f.parent >= 0) {
-      atomicAdd(&children[f.parent], 1);
-      atomicMin(&least[f.parent], f.pages);
-    }
-    if (cta == 0) {
-      const int n = p.lengths[r], q = p.parents[r];
-      if (n < 0 || n > p.width * kPage || q < -1 || q >= p.rows) report();
-    }
+  __device__ int parent(int r) const {
+    const int q = p.parents[r];
+    return q >= 0 && q < p.rows ? q : -1;
   }
-  __syncthreads();
-  // old row i loses entries lo .. hi - 1 (some child, if any, takes fewer pages)
-  auto dropped = [&](int i, int& lo, int& hi) {
-    hi = (fork_length(p, i) + kPage - 1) / kPage;
-    lo = children[i] == 0 ? 0 : min(least[i], hi);
-  };
+  __device__ int kept(int r) const {
+    const int q = parent(r), most = p.keep ? max(p.keep[r], 0) : INT32_MAX;
+    return q < 0 ? 0 : min(length(q), most);
+  }
+  __device__ int old_pages(int r) const { return (length(r) + kPage - 1) / kPage; }
+  __device__ int children(int r) const { return p.counts[r]; }
+  __device__ int least(int r) const { return p.new_lengths[r]; }
+};
 
-  // 1
-  for (int i = gwarp; i < p.rows; i += gwarps) {
-    const int more = children[i] - 1;
-    if (more < 1) continue;
-    const int had = (fork_length(p, i) + kPage - 1) / kPage;
-    for (int e = lane; e < had; e += 32) {
-      const int page = p.table[(size_t)i * p.width + e];
-      if (in_pool(page)) atomicAdd(&p.shares[page], more);
-      else report();
-    }
+// The steps, for CTA `cta` of `ctas`.
+template <class Rows>
+struct Fork {
+  const ForkParams& p;
+  const Rows& rows;
+  int cta, ctas;
+
+  // (neighbouring numbers in different CTAs)
+  __device__ int warp() const { return (int)(threadIdx.x >> 5) * ctas + cta; }
+  __device__ int warps() const { return ctas * (kForkThreads / 32); }
+  __device__ int thread() const { return (int)threadIdx.x * ctas + cta; }
+  __device__ int threads() const { return ctas * kForkThreads; }
+  __device__ bool in_pool(int page) const { return page >= 0 && page < p.num_pages; }
+  __device__ void report() const { record_error(p.err, PGD_EDEVICE_BOUNDS); }
+  __device__ int pages(int r) const { return (rows.kept(r) + kPage - 1) / kPage; }
+  __device__ int entry(int r, int e) const { return (int)((size_t)r * p.width + e); }
+  // an old row loses its entries from here on (some child, if any, takes fewer)
+  __device__ int lost_from(int r) const {
+    const int children = rows.children(r), least = rows.least(r);
+    return children == 0 ? 0 : min(least, rows.old_pages(r));
   }
-  cluster.sync();
-  // 2
-  for (int i = gwarp; i < p.rows; i += gwarps) {
-    if (children[i] == 0) {
-      const int had = (fork_length(p, i) + kPage - 1) / kPage;
-      for (int e = lane; e < had; e += 32) {
-        const int page = p.table[(size_t)i * p.width + e];
-        if (in_pool(page)) atomicSub(&p.shares[page], 1);
-        else report();
+  __device__ int tail_page(int r) const {  // -1: the last page is full, or there is none
+    const int n = rows.kept(r);
+    return n % kPage ? p.table[(size_t)rows.parent(r) * p.width + n / kPage] : -1;
+  }
+  __device__ bool claimed(int page, int r, int e) const {
+    return in_pool(page) && __ldcg(&p.shares[page]) == kForkClaim + entry(r, e);
+  }
+  template <class Lo, class F>
+  __device__ void each_entry(Lo lo, F f) const {
+    each_table_entry(p.table, p.rows, p.width, warp(), warps(), lo,
+                     [&](int r) { return rows.old_pages(r); }, f);
+  }
+  // the list's next page: before, and once the freed pages are back
+  __device__ int head() const { return p.free_head ? *p.free_head : 0; }
+  __device__ bool bad_head() const { return head() < 0 || head() > p.num_free; }
+
+  __device__ void grow() const {
+    each_entry([&](int r) { return rows.children(r) < 2 ? rows.old_pages(r) : 0; },
+               [&](int r, int, int page) {
+                 if (in_pool(page))
+                   atomicAdd(&p.shares[page], rows.children(r) - 1);
+                 else
+                   report();
+               });
+  }
+  __device__ void give_back() const {
+    auto one = [&](int, int, int page) {
+      if (in_pool(page))
+        atomicSub(&p.shares[page], 1);
+      else
+        report();
+    };
+    each_entry([&](int r) { return rows.children(r) > 0 ? rows.old_pages(r) : 0; }, one);
+    if (p.keep)  // rows that their parents' entries are cut for
+      for (int r = warp(); r < p.rows; r += warps()) {
+        const int q = rows.parent(r);
+        if (q < 0) continue;
+        for (int e = pages(r) + (threadIdx.x & 31); e < rows.old_pages(q); e += 32)
+          one(q, e, p.table[(size_t)q * p.width + e]);
       }
-    }
-    const ForkRow f = fork_row(p, i);
-    for (int e = f.pages + lane; e < f.had; e += 32) {
-      const int page = p.table[(size_t)f.parent * p.width + e];
-      if (in_pool(page)) atomicSub(&p.shares[page], 1);
-      else report();
-    }
   }
-  cluster.sync();
-  // 3
-  for (int i = gwarp; i < p.rows; i += gwarps) {
-    int lo, hi;
-    dropped(i, lo, hi);
-    for (int e = lo + lane; e < hi; e += 32) {
-      const int page = p.table[(size_t)i * p.width + e];
-      if (!in_pool(page)) continue;
+  __device__ void claim() const {
+    each_entry([&](int r) { return lost_from(r); }, [&](int r, int e, int page) {
+      if (!in_pool(page)) return;
       const int held = __ldcg(&p.shares[page]);
       if (held < 0) {
         if (held < -1 && held > kForkTail) report();  // given back more often than held
-        atomicMin(&p.shares[page], kForkClaim + (int)((size_t)i * p.width + e));
+        atomicMin(&p.shares[page], kForkClaim + entry(r, e));
       }
+    });
+  }
+  // the claims of a row to `counts` of it, zero before (and each row's of one warp)
+  __device__ void count(int* counts) const {
+    each_entry([&](int r) { return lost_from(r); }, [&](int r, int e, int page) {
+      if (claimed(page, r, e)) atomicAdd(&counts[r], 1);
+    });
+  }
+  __device__ void leave_tails() const {
+    for (int r = thread(); r < p.rows; r += threads()) {
+      const int page = tail_page(r);
+      if (in_pool(page)) atomicSub(&p.shares[page], 1);
     }
   }
-  cluster.sync();
-  // 4: the claims of a row are counted in its place of `sources`
-  auto claimed = [&](int i, int e, int& page) {
-    page = p.table[(size_t)i * p.width + e];
-    return in_pool(page) &&
-           __ldcg(&p.shares[page]) == kForkClaim + (int)((size_t)i * p.width + e);
-  };
-  for (int i = gwarp; i < p.rows; i += gwarps) {
-    int lo, hi, n = 0, page;
-    dropped(i, lo, hi);
-    for (int e = lo + lane; e < hi; e += 32) n += claimed(i, e, page);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) p.sources[i] = n;
-  }
-  auto tail_page = [&](const ForkRow& f) {  // -1: the last page is full, or there is none
-    return f.kept % kPage ? p.table[(size_t)f.parent * p.width + f.pages - 1] : -1;
-  };
-  for (int r = gtid; r < p.rows; r += gthreads) {
-    const int page = tail_page(fork_row(p, r));
-    if (in_pool(page)) atomicSub(&p.shares[page], 1);
-  }
-  cluster.sync();
-  // 5
-  int freed = 0;  // of all rows
-  for (int r0 = 0; r0 < p.rows; r0 += kForkThreads) {
-    const int r = r0 + tid;
-    int total;
-    const int at = block_scan(r < p.rows ? __ldcg(&p.sources[r]) : 0, warps, total);
-    if (r < p.rows) slab[r] = freed + at;
-    freed += total;
-    __syncthreads();
-  }
-  const int head1 = bad_head ? head0 : max(head0 - freed, 0);  // the list after the pages freed
-  if (!bad_head && head0 < freed && gtid == 0) report();      // (the list has no room for some)
-  for (int i = gwarp; i < p.rows; i += gwarps) {
-    int lo, hi;
-    dropped(i, lo, hi);
-    int at = slab[i];
-    for (int e0 = lo; e0 < hi; e0 += 32) {
+  // row r's `n` claimed pages, the `at`-th of `freed` on, to the list (a warp)
+  __device__ void list(int r, int at, int n, int freed) const {
+    const int lane = threadIdx.x & 31, hi = rows.old_pages(r), end = at + n;
+    for (int e0 = lost_from(r); at < end && e0 < hi; e0 += 32) {
       int page = -1;
-      const bool mine = e0 + lane < hi && claimed(i, e0 + lane, page);
+      bool mine = false;
+      if (e0 + lane < hi) {
+        page = p.table[(size_t)r * p.width + e0 + lane];
+        mine = claimed(page, r, e0 + lane);
+      }
       const unsigned who = __ballot_sync(0xffffffffu, mine);
       if (mine) {
-        const int to = head0 - freed + at + __popc(who & ((1u << lane) - 1u));
-        if (!bad_head && to >= 0) p.free_pages[to] = page;
+        const int to = head() - freed + at + __popc(who & ((1u << lane) - 1u));
+        if (!bad_head() && to >= 0) p.free_pages[to] = page;
         p.shares[page] = 0;
       }
       at += __popc(who);
     }
   }
-  for (int r = gtid; r < p.rows; r += gthreads) {
-    const int page = tail_page(fork_row(p, r));
-    if (in_pool(page) && __ldcg(&p.shares[page]) < 0) atomicMin(&p.shares[page], kForkTail + r);
-  }
-  cluster.sync();
-  // 6: every CTA ranks all rows; slab[r] is the page that row r's last entry gets
-  // (-1: as it is; -2: none, the row loses its last page)
-  int copies = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += kForkThreads) {
-    const int r = r0 + tid;
-    bool copy = false, lost = false;
-    if (r < p.rows) {
-      const ForkRow f = fork_row(p, r);
-      const int page = tail_page(f);
-      if (in_pool(page))
-        copy = __ldcg(&p.shares[page]) != kForkTail + r;
-      else
-        lost = f.kept % kPage != 0;
+  __device__ void claim_tails() const {
+    for (int r = thread(); r < p.rows; r += threads()) {
+      const int page = tail_page(r);
+      if (in_pool(page) && __ldcg(&p.shares[page]) < 0)
+        atomicMin(&p.shares[page], kForkTail + r);
     }
-    int total;
-    const int at = copies + block_scan(copy, warps, total);
-    copies += total;
-    if (r < p.rows) {
-      int to = -1;
-      if (copy) {
-        to = -2;
-        if (!bad_head && at < p.num_free - head1) {
-          const int page = __ldcg(&p.free_pages[head1 + at]);
-          if (in_pool(page)) to = page;
-        }
-      }
-      if (lost) to = -2;
-      if (to == -2 && cta == 0) report();
-      slab[r] = to;
-    }
-    __syncthreads();
   }
-  cluster.sync();
-  // 7
-  for (int r = gtid; r < p.rows; r += gthreads) {
-    const ForkRow f = fork_row(p, r);
-    const int page = tail_page(f), to = slab[r];
-    p.new_lengths[r] = to == -2 ? f.kept - f.kept % kPage : f.kept;
+  __device__ int listed_head(int freed) const {  // (a list may have no room for some)
+    return bad_head() ? head() : max(head() - freed, 0);
+  }
+  // What becomes of row r's last page, `page` (-1: full or none): 1: a copy; -1: as it
+  // is; -2: none, the row loses it.
+  __device__ int last(int r, int page) const {
+    if (in_pool(page)) return __ldcg(&p.shares[page]) != kForkTail + r ? 1 : -1;
+    return rows.kept(r) % kPage != 0 ? -2 : -1;
+  }
+  // The page for the copy that `at` rows before want one too (-2: none).
+  __device__ int copy_page(int at, int head1) const {
+    if (bad_head() || at >= p.num_free - head1) return -2;
+    const int page = __ldcg(&p.free_pages[head1 + at]);
+    return in_pool(page) ? page : -2;
+  }
+  // Row r's outputs; to: the last page it gets, or as last (not 1).
+  __device__ void write(int r, int to, int page, int kept) const {
+    p.new_lengths[r] = to == -2 ? kept - kept % kPage : kept;
     p.sources[r] = to >= 0 ? page : -1;
     p.targets[r] = to >= 0 ? to : -1;
-    p.counts[r] = to >= 0 ? f.kept % kPage : 0;
+    p.counts[r] = to >= 0 ? kept % kPage : 0;
     if (to == -1 && in_pool(page)) p.shares[page] = 0;  // the one that keeps it
   }
-  if (gtid == 0)
-    *p.free_head_out = bad_head ? head0 : min(head1 + copies, p.num_free);
-  for (int r = tid; r < p.rows; r += kForkThreads) {
-    const ForkRow f = fork_row(p, r);
-    children[r] = f.parent;
-    least[r] = 2 * f.pages + (f.kept % kPage != 0);  // pages, and whether the last is in part use
+  // Moves the rows: row r gets n_pages(r) pages of row parent(r), the last one to(r) (-1, -2
+  // as last).  `cells`: rows << p.slab_shift words.
+  template <class Parent, class Pages, class To>
+  __device__ void move(int* cells, Parent parent, Pages n_pages, To to) const {
+    const int shift = p.slab_shift, columns = 1 << shift, R = p.rows;
+    for (int c0 = cta << shift; c0 < p.width; c0 += ctas << shift) {
+      const int n = min(columns, p.width - c0);
+#pragma unroll 4
+      for (int k = threadIdx.x; k < R << shift; k += kForkThreads) {
+        const int r = k >> shift, c = k & (columns - 1);
+        if (c < n) cells[k] = p.table[(size_t)r * p.width + c0 + c];
+      }
+      __syncthreads();
+      for (int k = threadIdx.x; k < R << shift; k += kForkThreads) {
+        const int r = k >> shift, c = k & (columns - 1), e = c0 + c;
+        const int q = parent(r), pages = n_pages(r), last = to(r);
+        if (c >= n || e >= pages) continue;
+        const bool tail = e == pages - 1 && last != -1;  // (-1 where the last page is full)
+        if (tail && last >= 0)
+          p.table[(size_t)r * p.width + e] = last;
+        else if (q != r && !tail)
+          p.table[(size_t)r * p.width + e] = cells[(q << shift) + c];
+      }
+      __syncthreads();
+    }
   }
-  cluster.sync();  // the last entries of the parents were read above
-  int* cells = slab + p.rows;
-  const int columns = p.slab_columns;
-  for (int c0 = cta * columns; c0 < p.width; c0 += ctas * columns) {
-    const int n = min(columns, p.width - c0);
-    for (int k = tid; k < p.rows * columns; k += kForkThreads) {
-      const int r = k / columns, c = k % columns;
-      if (c < n) cells[k] = p.table[(size_t)r * p.width + c0 + c];
+};
+
+// Children and least pages of all rows, by each CTA for itself: rows.aux and rows.least
+// (the latter, like kept and old_pages, of all fields filled here).
+__device__ void fork_count_children(const ForkParams& p, const ForkRows& rows, int* scratch,
+                                    bool reports) {
+  const int tid = threadIdx.x, R = p.rows;
+#pragma unroll 4
+  for (int r = tid; r < R; r += kForkThreads) {
+    const int n = p.lengths[r], q = p.parents[r];
+    const bool good = n >= 0 && n <= p.width * kPage;
+    rows.old_pages_[r] = good ? (n + kPage - 1) / kPage : 0;
+    rows.kept_[r] = good ? n : 0;  // for now, what a child has of it
+    rows.parent_[r] = (int16_t)(q >= 0 && q < R ? q : -1);
+    rows.least_[r] = INT32_MAX;
+    rows.aux[r] = 0;
+    if (reports && (!good || q < -1 || q >= R)) record_error(p.err, PGD_EDEVICE_BOUNDS);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int r = tid; r < R; r += kForkThreads) {
+    const int q = rows.parent_[r];
+    int n = q < 0 ? 0 : rows.kept_[q];
+    if (p.keep) n = min(n, max(p.keep[r], 0));
+    scratch[r] = n;
+    if (q >= 0) {
+      atomicAdd(&rows.aux[q], 1);
+      atomicMin(&rows.least_[q], (n + kPage - 1) / kPage);
     }
+  }
+  __syncthreads();
+  for (int r = tid; r < R; r += kForkThreads) {
+    rows.kept_[r] = scratch[r];
+    rows.children_[r] = (uint16_t)rows.aux[r];
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ ForkRows fork_rows_at(int* smem, int R) {
+  ForkRows rows;
+  rows.kept_ = smem;
+  rows.old_pages_ = smem + R;
+  rows.least_ = smem + 2 * R;
+  rows.aux = smem + 3 * R;
+  rows.parent_ = reinterpret_cast<int16_t*>(smem + 4 * R);
+  rows.children_ = reinterpret_cast<uint16_t*>(rows.parent_ + R);
+  return rows;  // five words a row
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
+  extern __shared__ int smem[];
+  __shared__ int warps[33];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = p.rows, tid = threadIdx.x;
+  const ForkRows rows = fork_rows_at(smem, R);
+  int* cells = smem + 5 * R;
+  const Fork<ForkRows> fork{p, rows, (int)cluster.block_rank(), (int)cluster.num_blocks()};
+  pdl_wait();
+  pdl_allow_dependents();
+  if (fork.thread() == 0 && fork.bad_head()) fork.report();
+  fork_count_children(p, rows, cells, fork.cta == 0);
+  fork.grow();
+  cluster.sync();
+  fork.give_back();
+  cluster.sync();
+  fork.claim();
+  cluster.sync();
+  for (int r = tid; r < R; r += kForkThreads) rows.aux[r] = 0;
+  __syncthreads();
+  fork.count(rows.aux);
+  fork.leave_tails();
+  __syncthreads();
+  // (each_entry's rows of this CTA)
+  const int n = rows_at_a_time(R, fork.warps());
+  for (int r = tid; r < R; r += kForkThreads)
+    if (r / n % fork.ctas == fork.cta) p.sources[r] = rows.aux[r];
+  cluster.sync();
+  int freed = 0;  // of all rows
+  for (int r0 = 0; r0 < R; r0 += kForkThreads) {
+    const int r = r0 + tid;
+    int total;
+    const int at = block_scan(r < R ? __ldcg(&p.sources[r]) : 0, warps, total);
+    if (r < R) rows.aux[r] = freed + at;
+    freed += total;
     __syncthreads();
-    for (int k = tid; k < p.rows * columns; k += kForkThreads) {
-      const int r = k / columns, c = k % columns, e = c0 + c;
-      const int parent = children[r], pages = least[r] >> 1, to = slab[r];
-      if (c >= n || e >= pages) continue;
-      const bool tail = (least[r] & 1) != 0 && e == pages - 1;
-      if (tail && to >= 0)
-        p.table[(size_t)r * p.width + e] = to;
-      else if (parent != r && !(tail && to == -2))
-        p.table[(size_t)r * p.width + e] = cells[parent * columns + c];
-    }
+  }
+  if (fork.thread() == 0 && !fork.bad_head() && fork.head() < freed) fork.report();
+  for (int r = fork.warp(); r < R; r += fork.warps()) {
+    const int at = rows.aux[r], end = r + 1 < R ? rows.aux[r + 1] : freed;
+    if (at < end) fork.list(r, at, end - at, freed);
+  }
+  fork.claim_tails();
+  cluster.sync();
+  const int head1 = fork.listed_head(freed);
+  int copies = 0;
+  for (int r0 = 0; r0 < R; r0 += kForkThreads) {  // (every CTA, all rows)
+    const int r = r0 + tid;
+    int to = r < R ? fork.last(r, fork.tail_page(r)) : -1, total;
+    const int at = copies + block_scan(to == 1, warps, total);
+    copies += total;
+    if (to == 1) to = fork.copy_page(at, head1);
+    if (to == -2 && fork.cta == 0) fork.report();
+    if (r < R) rows.aux[r] = to;
     __syncthreads();
   }
   cluster.sync();
+  for (int r = fork.thread(); r < R; r += fork.threads())
+    fork.write(r, rows.aux[r], fork.tail_page(r), rows.kept(r));
+  if (fork.thread() == 0)
+    *p.free_head_out = fork.bad_head() ? head1 : min(head1 + copies, p.num_free);
+  cluster.sync();  // the last entries of the parents were read above
+  fork.move(
+      cells, [&](int r) { return rows.parent(r); }, [&](int r) { return fork.pages(r); },
+      [&](int r) { return rows.aux[r]; });
 }
 
-cudaError_t launch_fork_rows(const ForkParams& params, cudaStream_t stream) {
-  ForkParams p = params;
-  // shared memory: three words a row and the slab
-  const int limit = 200 * 1024;
-  p.slab_columns = 8;
-  while (p.slab_columns > 1 && (3 + p.slab_columns) * 4ll * p.rows > limit) p.slab_columns /= 2;
-  const size_t smem = (size_t)(3 + p.slab_columns) * 4 * p.rows;
+// The steps as launches of their own.
+enum ForkStep { kForkGrow, kForkGiveBack, kForkClaims, kForkCount, kForkList, kForkLast, kForkMove };
+
+template <int STEP>
+__global__ void __launch_bounds__(kForkThreads) fork_step_kernel(ForkParams p) {
+  extern __shared__ int smem[];
+  __shared__ int warps[33];
+  const int R = p.rows, tid = threadIdx.x;
+  const ForkInputs inputs{p};
+  const Fork<ForkInputs> fork{p, inputs, (int)blockIdx.x, (int)gridDim.x};
+  pdl_wait();
+  pdl_allow_dependents();
+  if constexpr (STEP == kForkGrow) {
+    // every CTA counts the children; the first leaves them for the other steps
+    const ForkRows rows = fork_rows_at(smem, R);
+    fork_count_children(p, rows, smem + 5 * R, fork.cta == 0);
+    if (fork.cta == 0) {
+      if (tid == 0 && fork.bad_head()) fork.report();
+      for (int r = tid; r < R; r += kForkThreads) {
+        p.counts[r] = rows.children_[r];
+        p.new_lengths[r] = rows.least_[r];
+        p.sources[r] = 0;
+      }
+    }
+    const Fork<ForkRows> all{p, rows, fork.cta, fork.ctas};
+    all.grow();
+  } else if constexpr (STEP == kForkGiveBack) {
+    fork.give_back();
+  } else if constexpr (STEP == kForkClaims) {
+    fork.claim();
+  } else if constexpr (STEP == kForkCount) {
+    fork.count(p.sources);
+    fork.leave_tails();
+  } else if constexpr (STEP == kForkList) {
+    // a run of rows a CTA: the claims before it, and in all
+    const int lo = (int)((int64_t)R * fork.cta / fork.ctas);
+    const int hi = (int)((int64_t)R * (fork.cta + 1) / fork.ctas);
+    int before = 0, freed = 0;
+#pragma unroll 4
+    for (int r = tid; r < R; r += kForkThreads) {
+      const int n = p.sources[r];
+      freed += n;
+      if (r < lo) before += n;
+    }
+    int total;
+    block_scan(before, warps, total);
+    before = total;
+    __syncthreads();
+    block_scan(freed, warps, total);
+    freed = total;
+    if (fork.thread() == 0) {
+      p.targets[0] = freed;  // (for the next step; the last one's are written there)
+      if (!fork.bad_head() && fork.head() < freed) fork.report();
+    }
+    for (int r = lo + (tid >> 5); r < hi; r += kForkThreads / 32) {
+      const int n = p.sources[r];
+      if (n == 0) continue;
+      int at = before;
+      for (int k = lo + (tid & 31); k < r; k += 32) at += p.sources[k];
+      at = before + __reduce_add_sync(0xffffffffu, at - before);
+      fork.list(r, at, n, freed);
+    }
+    fork.claim_tails();
+  } else if constexpr (STEP == kForkLast) {  // (one CTA)
+    const int head1 = fork.listed_head(p.targets[0]);
+    int* to = smem;
+    int* page = smem + R;
+    int* kept = smem + 2 * R;
+#pragma unroll 4
+    for (int r = tid; r < R; r += kForkThreads) {
+      kept[r] = inputs.kept(r);
+      page[r] = fork.tail_page(r);
+      to[r] = fork.last(r, page[r]);
+    }
+    __syncthreads();
+    int copies = 0;
+    for (int r0 = 0; r0 < R; r0 += kForkThreads) {
+      const int r = r0 + tid;
+      const bool copy = r < R && to[r] == 1;
+      int total;
+      const int at = copies + block_scan(copy, warps, total);
+      copies += total;
+      if (copy) to[r] = fork.copy_page(at, head1);
+      if (r < R && to[r] == -2) fork.report();
+      if (r < R) fork.write(r, to[r], page[r], kept[r]);
+      __syncthreads();
+    }
+    if (tid == 0) *p.free_head_out = fork.bad_head() ? head1 : min(head1 + copies, p.num_free);
+  } else {
+    int* parent = smem;
+    int* pages = smem + R;
+    int* to = smem + 2 * R;
+#pragma unroll 4
+    for (int r = tid; r < R; r += kForkThreads) {
+      const int kept = inputs.kept(r), target = p.targets[r], length = p.new_lengths[r];
+      parent[r] = inputs.parent(r);
+      pages[r] = (kept + kPage - 1) / kPage;
+      to[r] = target >= 0 ? target : length == kept ? -1 : -2;
+    }
+    __syncthreads();
+    fork.move(
+        smem + 3 * R, [&](int r) { return parent[r]; }, [&](int r) { return pages[r]; },
+        [&](int r) { return to[r]; });
+  }
+}
+
+template <int STEP>
+cudaError_t launch_fork_step(const ForkParams& p, int ctas, size_t smem, cudaStream_t stream) {
   static std::atomic<bool> configured[64];
-  cudaError_t e = allow_smem(fork_rows_kernel, limit, configured);
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = allow_smem(fork_step_kernel<STEP>, 220 * 1024, configured);
+  return e != cudaSuccess ? e : launch_pdl(fork_step_kernel<STEP>, dim3(ctas), dim3(kForkThreads),
+                                           smem, stream, p);
+}
+
+cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_t stream) {
+  ForkParams p = params;
   const int64_t entries = (int64_t)p.rows * p.width;
-  int ctas = 1;
-  while (ctas < 8 && entries > 8192ll * ctas) ctas *= 2;
-  return launch_cluster(fork_rows_kernel, ctas, smem, stream, p);
+  const int limit = 220 * 1024;
+  // a slab as wide as there is room and use for, beside `words` a row
+  auto slab = [&](int ctas, int words) {
+    p.slab_shift = 0;
+    while (p.slab_shift < 6 && ((int64_t)ctas << p.slab_shift) < p.width &&
+           (words + (2ll << p.slab_shift)) * 4 * p.rows <= limit)
+      ++p.slab_shift;
+    return (words + (1ll << p.slab_shift)) * 4 * (size_t)p.rows;
+  };
+  if (entries <= kForkClusterEntries) {
+    static std::atomic<bool> configured[64];
+    const cudaError_t e = allow_smem(fork_rows_kernel, limit, configured);
+    if (e != cudaSuccess) return e;
+    int ctas = 1;
+    while (ctas < 8 && entries > 2048ll * ctas) ctas *= 2;
+    return launch_cluster(fork_rows_kernel, ctas, slab(ctas, 5), stream, p);
+  }
+  cudaError_t e = launch_fork_step<kForkGrow>(p, sm_count, 24 * (size_t)p.rows, stream);
+  if (e == cudaSuccess) e = launch_fork_step<kForkGiveBack>(p, sm_count, 0, stream);
+  if (e == cudaSuccess) e = launch_fork_step<kForkClaims>(p, sm_count, 0, stream);
+  if (e == cudaSuccess) e = launch_fork_step<kForkCount>(p, sm_count, 0, stream);
+  if (e == cudaSuccess) e = launch_fork_step<kForkList>(p, sm_count, 0, stream);
+  if (e == cudaSuccess) e = launch_fork_step<kForkLast>(p, 1, 12 * (size_t)p.rows, stream);
+  if (e != cudaSuccess) return e;
+  const size_t smem = slab(sm_count, 3);
+  return launch_fork_step<kForkMove>(p, sm_count, smem, stream);
 }
 
 // ------------------------------------------------------------------ copy_pages
@@ -406,200 +660,263 @@ cudaError_t launch_copy_pages(const CopyParams& p, int head_dim, int sm_count,
 // ------------------------------------------------------------------ compact_pages
 
 // Two bitmaps over the pool -- pages listed as free, pages held by a row -- made
-// with atomics in the workspace; every CTA of the one cluster then sums their
-// words' bits into prefixes in shared memory (a prefix per `step` words), from
-// which the rank of any page among the free or the held is one look-up.
+// with atomics in the workspace; then their words' bits are summed into prefixes (one
+// per `step` words), from which the rank of any page among the free or the held is one
+// look-up.
 //   moves: the k-th held page from the top goes to the k-th free page from the
 //   bottom while the latter is lower.  Without a limit that is all held pages
 //   past the first `held` places of the free and held pages together.
 //   free list: free pages left and vacated ones, each at its rank.
+// Bound by latency and the rate of scattered accesses in L2, as fork_rows: one cluster
+// for small pools and tables, its steps between cluster barriers; else a launch a step
+// over all SMs, where every CTA sums the bits for itself (250 007 pages, 514 000
+// entries: 82 -> 30 us).
 constexpr int kCompactThreads = 1024;
+constexpr int64_t kCompactClusterWork = 100000;  // entries and pages
+enum CompactStep { kCompactAll = -1, kCompactClear, kCompactMark, kCompactMoves, kCompactApply };
 
+// The bitmaps' sums, and what they come to; in the workspace after the flag.
+struct CompactSums {
+  int held_total, moves, wrong, pad;
+};
+
+template <int STEP>
 __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactParams p) {
+  constexpr bool kAll = STEP == kCompactAll;
   extern __shared__ int smem[];
   __shared__ int warps[33];
   __shared__ int unlimited;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
+  const int ctas = kAll ? (int)cluster.num_blocks() : (int)gridDim.x;
+  const int cta = kAll ? (int)cluster.block_rank() : (int)blockIdx.x;
+  auto step_done = [&]() {
+    if constexpr (kAll) cluster.sync();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gwarp = cta * (kCompactThreads / 32) + warp, gwarps = ctas * (kCompactThreads / 32);
+  const int gwarp = warp * ctas + cta, gwarps = ctas * (kCompactThreads / 32);
   const int gtid = cta * kCompactThreads + tid, gthreads = ctas * kCompactThreads;
   const int words = (p.num_pages + 31) / 32, blocks = (words + p.step - 1) / p.step;
   uint32_t* free_bits = p.bits;
   uint32_t* held_bits = p.bits + words;
   uint32_t* bad = p.bits + 2 * words;
-  int* free_at = smem;  // [blocks + 1] free pages before the block's words
-  int* held_at = smem + blocks + 1;
+  CompactSums* sums = reinterpret_cast<CompactSums*>(bad + 1);
+  int* free_sums = reinterpret_cast<int*>(sums + 1);  // [blocks] pages before the block's words
+  int* held_sums = free_sums + blocks;
+  int* free_at = STEP == kCompactApply ? free_sums : smem;
+  int* held_at = STEP == kCompactApply ? held_sums : smem + blocks;
   pdl_wait();
   pdl_allow_dependents();
-  for (int w = gtid; w < 2 * words + 1; w += gthreads) p.bits[w] = 0;
-  cluster.sync();
   const int head = p.free_head ? *p.free_head : 0;
   const bool bad_head = head < 0 || head > p.num_free;
-  if (bad_head && gtid == 0) atomicOr(bad, 1u);
-  for (int k = (bad_head ? p.num_free : head) + gtid; k < p.num_free; k += gthreads) {
-    const int page = p.free_pages[k];
-    if (page < 0 || page >= p.num_pages)
-      atomicOr(bad, 1u);
-    else if (atomicOr(&free_bits[page >> 5], 1u << (page & 31)) >> (page & 31) & 1u)
-      atomicOr(bad, 1u);  // listed twice
-  }
   auto pages_of = [&](int r) {
     const int n = p.lengths[r];
     return n >= 0 && n <= p.width * kPage ? (n + kPage - 1) / kPage : -1;
   };
-  for (int r = gwarp; r < p.rows; r += gwarps) {
-    const int n = pages_of(r);
-    if (n < 0 && lane == 0) atomicOr(bad, 1u);
-    for (int e = lane; e < n; e += 32) {
-      const int page = p.table[(size_t)r * p.width + e];
-      if (page < 0 || page >= p.num_pages)
-        atomicOr(bad, 1u);
-      else
-        atomicOr(&held_bits[page >> 5], 1u << (page & 31));
-    }
-  }
-  cluster.sync();
-
-  // prefixes: thread t sums a run of blocks
-  const int run = (blocks + kCompactThreads - 1) / kCompactThreads;
-  const int b0 = min(tid * run, blocks), b1 = min(b0 + run, blocks);
-  int nf = 0, nh = 0;
-  bool both = false;
-  for (int w = b0 * p.step; w < min(b1 * p.step, words); ++w) {
-    const uint32_t f = __ldcg(&free_bits[w]), h = __ldcg(&held_bits[w]);
-    nf += __popc(f);
-    nh += __popc(h);
-    both |= (f & h) != 0;
-  }
-  int free_total, held_total;
-  int f_at = block_scan(nf, warps, free_total);
-  __syncthreads();
-  int h_at = block_scan(nh, warps, held_total);
-  for (int b = b0; b < b1; ++b) {
-    free_at[b] = f_at;
-    held_at[b] = h_at;
-    for (int w = b * p.step; w < min((b + 1) * p.step, words); ++w) {
-      f_at += __popc(__ldcg(&free_bits[w]));
-      h_at += __popc(__ldcg(&held_bits[w]));
-    }
-  }
-  if (tid == 0) unlimited = 0;
-  const bool wrong = __syncthreads_or(both) || __ldcg(bad) != 0;
-  // held pages of the union's places past the first held_total
-  for (int b = b0; b < b1; ++b) {
-    int f = free_at[b], h = held_at[b];
-    for (int w = b * p.step; w < min((b + 1) * p.step, words); ++w) {
-      const uint32_t fw = __ldcg(&free_bits[w]), hw = __ldcg(&held_bits[w]), all = fw | hw;
-      const int n = __popc(all);
-      if (f + h < held_total && f + h + n >= held_total) {
-        uint32_t rest = all;  // the word that holds the last of these places
-        int h_in = 0;
-        for (int k = f + h; k < held_total; ++k) {
-          const uint32_t low = rest & -rest;
-          h_in += (hw & low) != 0;
-          rest ^= low;
-        }
-        unlimited = held_total - (h + h_in);
-      }
-      f += __popc(fw);
-      h += __popc(hw);
-    }
-  }
-  __syncthreads();
-  const int moves = wrong ? 0 : min(unlimited, p.max_moves);
-  if (wrong && gtid == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
-  const int kept = held_total - moves;  // held pages of a lower rank stay
-  auto rank = [&](const uint32_t* bits, const int* at, int page) {
-    const int w = page >> 5, b = w / p.step;
+  auto in_pool = [&](int page) { return page >= 0 && page < p.num_pages; };
+  // set bits before word w
+  auto word_rank = [&](const uint32_t* bits, const int* at, int w) {
+    if (p.step == 1) return at[w];
+    const int b = w / p.step;
     int n = at[b];
     for (int k = b * p.step; k < w; ++k) n += __popc(bits[k]);
-    return n + __popc(bits[w] & ((1u << (page & 31)) - 1u));
+    return n;
   };
-
-  // the moves: sources from the top, targets from the bottom
-  for (int w = gtid; w < words; w += gthreads) {
-    for (uint32_t m = free_bits[w]; m; m &= m - 1) {
-      const int page = 32 * w + __ffs(m) - 1, k = rank(free_bits, free_at, page);
-      if (k < moves) p.targets[k] = page;
-    }
-    for (uint32_t m = held_bits[w]; m; m &= m - 1) {
-      const int page = 32 * w + __ffs(m) - 1, k = held_total - 1 - rank(held_bits, held_at, page);
-      if (k < moves) p.sources[k] = page;
-    }
+  if constexpr (kAll || STEP == kCompactClear) {
+    for (int w = gtid; w < 2 * words + 1; w += gthreads) p.bits[w] = 0;
+    step_done();
   }
-  for (int k = moves + gtid; k < p.max_moves; k += gthreads) p.sources[k] = p.targets[k] = -1;
-  cluster.sync();
-
-  // table, shares, list
-  for (int64_t k = gtid; k < (int64_t)p.rows * p.width; k += gthreads) {
-    const int r = (int)(k / p.width), e = (int)(k % p.width);
-    int page = p.table[k];
-    if (moves > 0 && e < pages_of(r)) {
-      const int h = rank(held_bits, held_at, page);
-      if (h >= kept) page = __ldcg(&p.targets[held_total - 1 - h]);
+  if constexpr (kAll || STEP == kCompactMark) {
+    if (bad_head && gtid == 0) atomicOr(bad, 1u);
+#pragma unroll 4
+    for (int k = (bad_head ? p.num_free : head) + gtid; k < p.num_free; k += gthreads) {
+      const int page = p.free_pages[k];
+      if (!in_pool(page))
+        atomicOr(bad, 1u);
+      else if (atomicOr(&free_bits[page >> 5], 1u << (page & 31)) >> (page & 31) & 1u)
+        atomicOr(bad, 1u);  // listed twice
     }
-    p.new_table[k] = page;
+    each_table_entry(
+        p.table, p.rows, p.width, gwarp, gwarps, [](int) { return 0; },
+        [&](int r) {
+          const int n = pages_of(r);
+          if (n < 0) atomicOr(bad, 1u);
+          return n;
+        },
+        [&](int, int, int page) {
+          if (in_pool(page))
+            atomicOr(&held_bits[page >> 5], 1u << (page & 31));
+          else
+            atomicOr(bad, 1u);
+        });
+    step_done();
   }
-  auto bit = [](const uint32_t* bits, int page) { return bits[page >> 5] >> (page & 31) & 1u; };
-  for (int page = gtid; page < p.num_pages; page += gthreads) {
-    const bool f = bit(free_bits, page), h = bit(held_bits, page);
-    if (wrong) {
-      p.new_shares[page] = p.shares[page];
-      continue;
+
+  CompactSums sum;
+  if constexpr (kAll || STEP == kCompactMoves) {
+    // prefixes: thread t sums a run of blocks
+    const int run = (blocks + kCompactThreads - 1) / kCompactThreads;
+    const int b0 = min(tid * run, blocks), b1 = min(b0 + run, blocks);
+    int nf = 0, nh = 0;
+    bool both = false;
+#pragma unroll 8
+    for (int w = b0 * p.step; w < min(b1 * p.step, words); ++w) {
+      const uint32_t f = __ldcg(&free_bits[w]), h = __ldcg(&held_bits[w]);
+      nf += __popc(f);
+      nh += __popc(h);
+      both |= (f & h) != 0;
     }
-    const int fr = rank(free_bits, free_at, page), hr = rank(held_bits, held_at, page);
-    const int vacated = max(hr - kept, 0);  // pages moved out below this one
-    if (f && fr >= moves) {
-      p.new_free[head + fr - moves + vacated] = page;
-      p.new_shares[page] = p.shares[page];
-    } else if (h && hr >= kept) {
-      p.new_free[head + fr - moves + vacated] = page;
-      const int to = __ldcg(&p.targets[held_total - 1 - hr]);
-      const int n = p.shares[page];  // (this thread alone touches the two)
+    int free_total;
+    const int f_at = block_scan(nf, warps, free_total);
+    __syncthreads();
+    const int h_at = block_scan(nh, warps, sum.held_total);
+    if (tid == 0) unlimited = 0;
+    sum.wrong = __syncthreads_or(both) || __ldcg(bad) != 0;
+    // without a limit the held pages past the first held_total places of the union move
+    int f = f_at, h = h_at;
+    for (int b = b0; b < b1; ++b) {
+      free_at[b] = f;
+      held_at[b] = h;
+      if (!kAll && cta == 0) {
+        free_sums[b] = f;
+        held_sums[b] = h;
+      }
+#pragma unroll 4
+      for (int w = b * p.step; w < min((b + 1) * p.step, words); ++w) {
+        const uint32_t fw = free_bits[w], hw = held_bits[w], all = fw | hw;
+        if (f + h < sum.held_total && f + h + __popc(all) >= sum.held_total) {
+          uint32_t rest = all;  // the word that holds the last of these places
+          int h_in = 0;
+          for (int k = f + h; k < sum.held_total; ++k) {
+            const uint32_t low = rest & -rest;
+            h_in += (hw & low) != 0;
+            rest ^= low;
+          }
+          unlimited = sum.held_total - (h + h_in);
+        }
+        f += __popc(fw);
+        h += __popc(hw);
+      }
+    }
+    __syncthreads();
+    sum.moves = sum.wrong ? 0 : min(unlimited, p.max_moves);
+    if (sum.wrong && gtid == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
+    if (!kAll && gtid == 0) *sums = sum;
+    // the moves: sources from the top, targets from the bottom
+    const int moves = sum.moves;
+    for (int w = tid * ctas + cta; moves > 0 && w < words; w += gthreads) {
+      const uint32_t fw = free_bits[w], hw = held_bits[w];
+      int k = word_rank(free_bits, free_at, w);
+      for (uint32_t m = fw; m && k < moves; m &= m - 1, ++k) p.targets[k] = 32 * w + __ffs(m) - 1;
+      k = sum.held_total - word_rank(held_bits, held_at, w);  // held pages from this word up
+      for (uint32_t m = hw; m && k - __popc(m) < moves; m &= m - 1)
+        if (--k < moves) p.sources[k] = 32 * w + __ffs(m) - 1;
+    }
+    for (int k = moves + gtid; k < p.max_moves; k += gthreads) p.sources[k] = p.targets[k] = -1;
+    step_done();
+  }
+
+  if constexpr (kAll || STEP == kCompactApply) {
+    if constexpr (!kAll) sum = *sums;
+    const int moves = sum.moves, kept = sum.held_total - moves;  // held pages of a lower rank stay
+    const bool wrong = sum.wrong != 0;
+    // the held pages from `lowest` up have moved, to the free ones up to `highest`
+    const int lowest = moves > 0 ? __ldcg(&p.sources[moves - 1]) : INT32_MAX;
+    const int highest = moves > 0 ? __ldcg(&p.targets[moves - 1]) : -1;
+    each_table_entry(
+        p.table, p.rows, p.width, gwarp, gwarps, [](int) { return 0; },
+        [&](int) { return p.width; },
+        [&](int r, int e, int page) {
+          if (page >= lowest && page < p.num_pages && e < pages_of(r)) {
+            const int w = page >> 5;
+            const int k = sum.held_total - 1 - word_rank(held_bits, held_at, w) -
+                          __popc(held_bits[w] & ((1u << (page & 31)) - 1u));
+            page = __ldcg(&p.targets[k]);
+          }
+          p.new_table[(size_t)r * p.width + e] = page;
+        });
+    // shares, and the list: free pages left and vacated ones, a word a warp at a time
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int w = gwarp; w < words; w += gwarps) {
+      const int page = 32 * w + lane;
+      const uint32_t fw = free_bits[w], hw = held_bits[w];
+      const bool vacated = !wrong && (hw >> lane & 1u) && page >= lowest;
+      const bool left = (fw >> lane & 1u) && page > highest;
+      const uint32_t listed = __ballot_sync(0xffffffffu, vacated || left);
+      if (!wrong && listed) {
+        const int at = max(word_rank(free_bits, free_at, w) - moves, 0) +
+                       max(word_rank(held_bits, held_at, w) - kept, 0);
+        if (listed >> lane & 1u) p.new_free[head + at + __popc(listed & below)] = page;
+      }
+      const bool taken = !wrong && (fw >> lane & 1u) && page <= highest;
+      if (page < p.num_pages && !vacated && !taken) p.new_shares[page] = p.shares[page];
+    }
+    for (int k = gtid; k < moves; k += gthreads) {  // (nobody else touches the two)
+      const int from = __ldcg(&p.sources[k]), to = __ldcg(&p.targets[k]);
+      const int n = p.shares[from];
       p.new_shares[to] = n;
-      p.new_shares[page] = 0;
-    } else if (!f) {
-      p.new_shares[page] = p.shares[page];
+      p.new_shares[from] = 0;
     }
-  }
-  for (int k = gtid; k < (wrong ? p.num_free : head); k += gthreads)
-    p.new_free[k] = p.free_pages[k];
-  // the end of the pages in use: the highest held page left, or the highest target
-  if (gtid == 0) {
-    int end = moves > 0 ? __ldcg(&p.targets[moves - 1]) + 1 : 0;
-    if (kept > 0) {
-      int lo = 0, hi = blocks;  // the last block with fewer than kept before it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (held_at[mid] < kept)
-          lo = mid;
-        else
-          hi = mid;
+    for (int k = gtid; k < (wrong ? p.num_free : head); k += gthreads)
+      p.new_free[k] = p.free_pages[k];
+    // the end of the pages in use: the highest held page left, or the highest target
+    if (gtid == 0) {
+      int end = highest + 1;
+      if (kept > 0) {
+        int lo = 0, hi = blocks;  // the last block with fewer than kept before it
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (held_at[mid] < kept)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        int n = held_at[lo];
+        for (int w = lo * p.step; w < min((lo + 1) * p.step, words); ++w)
+          for (uint32_t m = held_bits[w]; m; m &= m - 1)
+            if (++n == kept) end = max(end, 32 * w + __ffs(m));
       }
-      int n = held_at[lo];
-      for (int w = lo * p.step; w < min((lo + 1) * p.step, words); ++w) {
-        for (uint32_t m = held_bits[w]; m; m &= m - 1)
-          if (++n == kept) end = max(end, 32 * w + __ffs(m));
-      }
+      *p.end = end;
     }
-    *p.end = end;
   }
 }
 
-cudaError_t launch_compact_pages(const CompactParams& params, cudaStream_t stream) {
+template <int STEP>
+cudaError_t launch_compact_step(const CompactParams& p, int ctas, size_t smem,
+                                cudaStream_t stream) {
+  static std::atomic<bool> configured[64];
+  const cudaError_t e = allow_smem(compact_pages_kernel<STEP>, 200 * 1024, configured);
+  if (e != cudaSuccess) return e;
+  if constexpr (STEP == kCompactAll)
+    return launch_cluster(compact_pages_kernel<STEP>, ctas, smem, stream, p);
+  else
+    return launch_pdl(compact_pages_kernel<STEP>, dim3(ctas), dim3(kCompactThreads), smem, stream,
+                      p);
+}
+
+size_t compact_workspace_bytes(int num_pages) {
+  const size_t words = ((size_t)num_pages + 31) / 32;
+  // bitmaps and flag, sums, prefixes
+  return (2 * words + 1 + 4 + 2 * (words < kMaxCompactPrefixes ? words : kMaxCompactPrefixes)) * 4;
+}
+
+cudaError_t launch_compact_pages(const CompactParams& params, int sm_count, cudaStream_t stream) {
   CompactParams p = params;
   const int words = (p.num_pages + 31) / 32;
   p.step = 1;
-  while ((words + p.step - 1) / p.step > 24 * 1024) p.step *= 2;
-  const size_t smem = ((size_t)(words + p.step - 1) / p.step + 1) * 8;
-  static std::atomic<bool> configured[64];
-  cudaError_t e = allow_smem(compact_pages_kernel, 200 * 1024, configured);
-  if (e != cudaSuccess) return e;
+  while ((words + p.step - 1) / p.step > kMaxCompactPrefixes) p.step *= 2;
+  const size_t smem = (size_t)((words + p.step - 1) / p.step) * 8;
   const int64_t work = (int64_t)p.rows * p.width + p.num_pages;
-  int ctas = 1;
-  while (ctas < 8 && work > 8192ll * ctas) ctas *= 2;
-  return launch_cluster(compact_pages_kernel, ctas, smem, stream, p);
+  if (work <= kCompactClusterWork) {
+    int ctas = 1;
+    while (ctas < 8 && work > 2048ll * ctas) ctas *= 2;
+    return launch_compact_step<kCompactAll>(p, ctas, smem, stream);
+  }
+  cudaError_t e = launch_compact_step<kCompactClear>(p, 32, 0, stream);
+  if (e == cudaSuccess) e = launch_compact_step<kCompactMark>(p, sm_count, 0, stream);
+  if (e == cudaSuccess) e = launch_compact_step<kCompactMoves>(p, sm_count, smem, stream);
+  if (e != cudaSuccess) return e;
+  return launch_compact_step<kCompactApply>(p, sm_count, 0, stream);
 }
 
 }  // namespace pgd

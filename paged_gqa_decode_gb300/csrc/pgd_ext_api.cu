@@ -453,8 +453,9 @@ int pgdx_fork_rows(int32_t rows, int32_t max_pages_per_row, int32_t num_pages, i
   p.width = max_pages_per_row;
   p.num_pages = num_pages;
   p.num_free = num_free;
-  return launch_fork_rows(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PGD_OK
-                                                                                    : PGD_ECUDA;
+  return launch_fork_rows(p, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PGD_OK
+             : PGD_ECUDA;
 }
 
 int pgdx_copy_pages(const pgd_dims* dims, int32_t layers, void* const* k_pools,
@@ -496,7 +497,7 @@ int pgdx_copy_pages(const pgd_dims* dims, int32_t layers, void* const* k_pools,
 
 size_t pgdx_compact_workspace_bytes(int32_t num_pages) {
   if (num_pages <= 0) return 0;
-  return ((size_t)(((int64_t)num_pages + 31) / 32) * 2 + 1) * sizeof(uint32_t);
+  return compact_workspace_bytes(num_pages);
 }
 
 int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
@@ -546,7 +547,8 @@ int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_page
   p.num_pages = num_pages;
   p.num_free = num_free;
   p.max_moves = max_moves;
-  return launch_compact_pages(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_compact_pages(p, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? PGD_OK
              : PGD_ECUDA;
 }

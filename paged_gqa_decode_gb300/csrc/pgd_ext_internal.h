@@ -58,10 +58,10 @@ struct ForkParams {
   int32_t* free_head_out;
   unsigned int* err;
   int rows, width, num_pages, num_free;
-  int slab_columns;  // (the launcher's)
+  int slab_shift;  // (the launcher's)
 };
-constexpr int kMaxForkRows = 12288;  // three words a row and a column of them in shared memory
-cudaError_t launch_fork_rows(const ForkParams& p, cudaStream_t stream);
+constexpr int kMaxForkRows = 8192;  // five words a row and a column of them in shared memory
+cudaError_t launch_fork_rows(const ForkParams& p, int sm_count, cudaStream_t stream);
 
 constexpr int kMaxCopyPools = 128;  // of one launch
 struct CopyParams {
@@ -87,12 +87,14 @@ struct CompactParams {
   int32_t* sources;  // [max_moves]
   int32_t* targets;
   int32_t* end;
-  uint32_t* bits;  // workspace: two bitmaps over the pool and a flag
+  uint32_t* bits;  // workspace: two bitmaps over the pool, a flag, and sums
   unsigned int* err;
   int rows, width, num_pages, num_free, max_moves;
   int step;  // (the launcher's)
 };
-cudaError_t launch_compact_pages(const CompactParams& p, cudaStream_t stream);
+constexpr int kMaxCompactPrefixes = 24 * 1024;  // of a bitmap, in shared memory
+size_t compact_workspace_bytes(int num_pages);
+cudaError_t launch_compact_pages(const CompactParams& p, int sm_count, cudaStream_t stream);
 
 constexpr int kMaxSharedGroups = 8192;  // two words a group in shared memory
 constexpr int kMaxSharedCtas = 160;

@@ -43,12 +43,13 @@ def fork_rows(table, lengths, parents, keep, shares, free, head, num_pages):
             p = table[r, e] = old[parents[r], e]
             if 0 <= p < num_pages:
                 holders[p] += 1
-    gone = []
+    gone, seen = [], set()
     for i in range(rows):
         for e in range(pages_of(lengths[i])):
             p = old[i, e]
-            if 0 <= p < num_pages and holders[p] <= 0 and p not in gone:
+            if 0 <= p < num_pages and holders[p] <= 0 and p not in seen:
                 gone.append(p)
+                seen.add(p)
                 error |= holders[p] < 0
     if not bad_head:
         error |= head < len(gone)

@@ -248,3 +248,18 @@ def test_compact_refusals():
                           out=pgd.CompactPlan(i(2, 3), i(9), i(5), good["lengths"], i(2), i(1)))
     assert e.value.status == pgd.EINVAL
     assert pgd.get_device_error() == pgd.OK
+
+
+@pytest.mark.parametrize("moves", [0, 5, 30000, None])
+def test_compact_in_a_launch_a_step(moves):
+    """More entries and pages than one cluster takes, then the same state gone wrong."""
+    rng = np.random.default_rng(5)
+    table, lengths, shares, free, head, pages = side.random_state(rng, 300, 4, 9000, 300,
+                                                                  spare=20000)
+    assert table.size + pages > 100000
+    check_compact(table, lengths, shares, free, head, pages, moves)
+    if moves is not None:
+        check_compact(table, lengths, shares, free, head, pages, moves, True)
+        twice = free.copy()
+        twice[-1] = twice[-9]
+        check_compact(table, lengths, shares, twice, head, pages, moves, True)

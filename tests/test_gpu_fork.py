@@ -118,7 +118,7 @@ def test_wide_tables_and_many_rows():
 
 
 def test_the_most_rows():
-    rows = 12288
+    rows = 8192
     table = np.zeros((rows, 1), dtype=np.int64)
     table[:, 0] = np.arange(rows)
     lengths = np.full(rows, 64)
@@ -267,3 +267,29 @@ def test_captured_and_replayed():
             np.testing.assert_array_equal(got.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
         state = (want[0], np.asarray(want[3]), np.asarray(want[1]), want[2], want[7], pages)
     assert pgd.get_device_error() == pgd.OK
+
+
+def test_many_entries_take_a_launch_a_step():
+    """Past the entries that one cluster takes; then with cuts, releases, too few pages and errors."""
+    rng = np.random.default_rng(21)
+    for requests, beams, hi, grown in ((40, 8, 9000, 300), (500, 8, 900, 200)):
+        rows = requests * beams
+        state = side.random_state(rng, requests, beams, hi, grown)
+        assert state[0].size > 40000
+        for step in range(3):
+            parents = np.arange(rows) // beams * beams + rng.integers(0, beams, rows)
+            keep = np.where(rng.random(rows) < 0.2, rng.integers(0, hi, rows), 2 ** 31 - 1)
+            parents = np.where(rng.random(rows) < 0.05, -1, parents)
+            state = check(state, parents, keep if step else None, status=pgd.OK)
+    table, lengths, shares, free, head, pages = state
+    parents = np.arange(rows) // beams * beams + rng.integers(0, beams, rows)
+    few = free[:head + 20]
+    check((table, lengths, shares, few, head, pages), parents)
+    check((table, lengths, shares, free[head - 3:], 3, pages), np.full(rows, -1),
+          status=pgd.EDEVICE_BOUNDS)
+    check((table, lengths, shares, free, -7, pages), parents, status=pgd.EDEVICE_BOUNDS)
+    holes, wrong = table.copy(), lengths.copy()
+    holes[rng.random(table.shape) < 0.01] = pages
+    wrong[5] = -1
+    parents[17], parents[33] = rows, -2
+    check((holes, wrong, shares, free, head, pages), parents, status=pgd.EDEVICE_BOUNDS)
