@@ -287,17 +287,6 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
 // to 4000, 64 / 8 heads of 64), 255 and 278 (32 / 8 heads of 128, up to 8192).
 constexpr float kSteepSlope = 4.f;
 
-// True for one lane of a converged warp, always the same one.  The compiler knows
-// that what it guards runs in one thread of a warp with uniform control, and keeps
-// the descriptors of MMAs in uniform registers (as `lane == 0` it does not).
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // kParts: built for key parts (`parts` units per item, partials to
 // part_acc / part_ml for the combine launch); otherwise parts is 1 and each
 // item's outputs are written directly.

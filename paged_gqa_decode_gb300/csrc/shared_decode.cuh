@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     };
     auto copy_k = [&](int y) -> bool {
       if (kn >= STAGES && !all_ok(wait(&k_empty[ks], kph))) return false;
-      if (lane == 0) {
+      if (elect_lane()) {
         mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
         load_tile(stages + ks * C::kStageBytes, &k_map, y, &k_full[ks]);
         y_ring[kn & 63] = y;
@@ -623,142 +623,178 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     }
   } else if (warp == C::kVWarp) {
     // ------------------------------------------------------------ V producer
-    if (lane == 0) {
-      int vn = 0, vs = 0;  // copies issued, the next one's stage
-      uint32_t vph = 1;
-      bool ok = true;
-      while (ok) {
-        const int issued = shared_wait_count(&k_issued, &k_total, vn, p.err, &abort_flag);
-        if (issued <= vn) break;  // the end
-        for (; vn < issued; ++vn) {
-          if (vn >= STAGES && !wait(&v_empty[vs], vph)) {
-            ok = false;
-            break;
-          }
+    int vn = 0, vs = 0;  // copies issued, the next one's stage
+    uint32_t vph = 1;
+    bool ok = true;
+    while (ok) {
+      int issued = lane == 0 ? shared_wait_count(&k_issued, &k_total, vn, p.err, &abort_flag) : 0;
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      if (issued <= vn) break;  // the end
+      for (; vn < issued; ++vn) {
+        if (vn >= STAGES && !all_ok(wait(&v_empty[vs], vph))) {
+          ok = false;
+          break;
+        }
+        const int y = y_ring[vn & 63];
+        if (elect_lane()) {
           mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
           unsigned char* slot = stages + vs * C::kStageBytes + C::kTileBytes;
           if constexpr (D == 128)
-            tma_load_3d(slot, &v_map, 0, y_ring[vn & 63], 0, &v_full[vs]);
+            tma_load_3d(slot, &v_map, 0, y, 0, &v_full[vs]);
           else
-            tma_load_2d(slot, &v_map, 0, y_ring[vn & 63], &v_full[vs]);
+            tma_load_2d(slot, &v_map, 0, y, &v_full[vs]);
           shared_store_count(&v_issued, vn + 1);
-          if (++vs == STAGES) {
-            vs = 0;
-            vph ^= 1;
-          }
+        }
+        if (++vs == STAGES) {
+          vs = 0;
+          vph ^= 1;
         }
       }
+    }
+    if (lane == 0)
       for (int j = max(0, vn - STAGES); j < vn; ++j)
         mbar_wait_bounded(&v_full[j % STAGES], (j / STAGES) & 1, p.err);
-    }
   } else if (warp == C::kSWarp) {
     // ------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      int i = 0;             // pages
-      int ip[2] = {0, 0};    // pages of each tile
-      int blocks = 0;
-      bool issued = false, ok = true;
-      for (int seq = 0; ok; ++seq) {
-        const int d = seq % C::kSegs;
-        if (!wait(&seg_ready[d], (seq / C::kSegs) & 1)) break;
-        const SharedSeg& sg = segs[d];
-        if (sg.what == 0) break;
-        const uint32_t q_addr = smem_addr(q_smem) + sg.q_tile() * C::kQTileBytes;
-        const int t0 = sg.tile(), t1 = t0 + sg.tiles(), pages = sg.own() ? 0 : sg.pages;
-        if (sg.own()) i += sg.pages;
-        if (pages > 0) {
-          if (!wait(&q_full[blocks & 1], (blocks / 2) & 1)) break;
-          ++blocks;
+    // (It and the P V issuer are on every tile's path: both wait as whole warps and
+    // issue under elect_lane, which leaves the products' operands in uniform registers;
+    // one thread each took 240 us for 256 rows over 32768 shared positions.)
+    int i = 0, st = 0;     // pages, and the next one's stage
+    uint32_t ph = 0;       // its parity
+    int ip[2] = {0, 0};    // pages of each tile
+    int blocks = 0;
+    bool issued = false, ok = true;
+    auto skip = [&](int pages) {
+      i += pages;
+      st = i % STAGES;
+      ph = (i / STAGES) & 1;
+    };
+    for (int seq = 0; ok; ++seq) {
+      const int d = seq % C::kSegs;
+      if (!all_ok(wait(&seg_ready[d], (seq / C::kSegs) & 1))) break;
+      const SharedSeg sg = segs[d];
+      if (sg.what == 0) break;
+      if (sg.own() || sg.pages == 0) {
+        skip(sg.pages);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_free[d]);
+        continue;
+      }
+      if (!all_ok(wait(&q_full[blocks & 1], (blocks / 2) & 1))) break;
+      ++blocks;
+      const int t0 = sg.tile(), t1 = t0 + sg.tiles();
+      const uint64_t q0 =
+          umma_desc_sw128(smem_addr(q_smem) + (sg.q_tile() - t0) * C::kQTileBytes, 16, 1024);
+      const uint64_t k0 = umma_desc_sw128(smem_addr(stages), 16, 1024);
+      for (int k = 0; k < sg.pages && ok; ++k) {
+        if (!all_ok(wait(&k_full[st], ph))) {
+          ok = false;
+          break;
         }
-        for (int k = 0; k < pages && ok; ++k, ++i) {
-          const int st = i % STAGES;
-          if (!wait(&k_full[st], (i / STAGES) & 1)) {
+        const uint64_t kd = umma_desc_advance(k0, st * C::kStageBytes);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t < t0 || t >= t1) continue;
+          const int n = ip[t], tb = 2 * t + (n & 1);
+          // the buffer holds P of the tile's page n - 2 until P V has read it
+          if (n >= 2 && !all_ok(wait(&o_done[tb], (n / 2 - 1) & 1))) {
             ok = false;
             break;
           }
-          const uint64_t kd = umma_desc_sw128(smem_addr(stages) + st * C::kStageBytes, 16, 1024);
-          for (int t = t0; t < t1; ++t) {
-            const int n = ip[t], tb = 2 * t + (n & 1);
-            // the buffer holds P of the tile's page n - 2 until P V has read it
-            if (n >= 2 && !wait(&o_done[tb], (n / 2 - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t sb = tmem + C::kSCol + tb * kPage;
-            const uint64_t qd = umma_desc_sw128(q_addr + (t - t0) * C::kQTileBytes, 16, 1024);
+          tc_fence_after_sync();
+          const uint64_t qd = umma_desc_advance(q0, t * C::kQTileBytes);
+          if (elect_lane()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_bf16(sb, umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
+              umma_bf16(tmem + C::kSCol + tb * kPage,
+                        umma_desc_advance(qd, (kk >> 2) * C::kQBoxBytes + (kk & 3) * 32),
                         umma_desc_advance(kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32), C::kIdescS,
                         kk > 0);
             umma_commit(&s_full[tb]);
-            ++ip[t];
-            issued = true;
           }
-          if (ok) umma_commit(&k_empty[st]);
+          ++ip[t];
+          issued = true;
         }
         if (!ok) break;
-        if (pages > 0)
-          for (int t = 0; t < sg.tiles(); ++t) umma_commit(&q_free[sg.q_tile() + t]);
+        if (elect_lane()) umma_commit(&k_empty[st]);
+        ++i;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (elect_lane()) {
+        for (int t = 0; t < sg.tiles(); ++t) umma_commit(&q_free[sg.q_tile() + t]);
         mbar_arrive(&seg_free[d]);
       }
-      if (issued) {  // TMEM is freed once every product is done
-        umma_commit(&fin[0]);
-        mbar_wait_bounded(&fin[0], 0, p.err);
-      }
+    }
+    if (issued && elect_lane()) {  // TMEM is freed once every product is done
+      umma_commit(&fin[0]);
+      mbar_wait_bounded(&fin[0], 0, p.err);
     }
   } else if (warp == C::kPvWarp) {
     // ------------------------------------------------------------ P V issuer
-    if (lane == 0) {
-      int i = 0;
-      int ip[2] = {0, 0};
-      bool issued = false, ok = true;
-      for (int seq = 0; ok; ++seq) {
-        const int d = seq % C::kSegs;
-        if (!wait(&seg_ready[d], (seq / C::kSegs) & 1)) break;
-        const SharedSeg& sg = segs[d];
-        if (sg.what == 0) break;
-        const int t0 = sg.tile(), t1 = t0 + sg.tiles(), pages = sg.own() ? 0 : sg.pages;
-        if (sg.own()) i += sg.pages;
-        for (int k = 0; k < pages && ok; ++k, ++i) {
-          const int st = i % STAGES;
-          if (!wait(&v_full[st], (i / STAGES) & 1)) {
+    int i = 0, st = 0;
+    uint32_t ph = 0;
+    int ip[2] = {0, 0};
+    bool issued = false, ok = true;
+    for (int seq = 0; ok; ++seq) {
+      const int d = seq % C::kSegs;
+      if (!all_ok(wait(&seg_ready[d], (seq / C::kSegs) & 1))) break;
+      const SharedSeg sg = segs[d];
+      if (sg.what == 0) break;
+      if (sg.own()) {
+        i += sg.pages;
+        st = i % STAGES;
+        ph = (i / STAGES) & 1;
+      }
+      const int t0 = sg.tile(), t1 = t0 + sg.tiles(), pages = sg.own() ? 0 : sg.pages;
+      const uint64_t v0 =
+          umma_desc_sw128(smem_addr(stages) + C::kTileBytes, kBoxBytes, 1024);
+      for (int k = 0; k < pages && ok; ++k) {
+        if (!all_ok(wait(&v_full[st], ph))) {
+          ok = false;
+          break;
+        }
+        const uint64_t vd = umma_desc_advance(v0, st * C::kStageBytes);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t < t0 || t >= t1) continue;
+          const int n = ip[t], tb = 2 * t + (n & 1);
+          // (P of a segment's first page comes after its tile's last O was read)
+          if (!all_ok(wait(&p_full[tb], (n / 2) & 1))) {
             ok = false;
             break;
           }
-          const uint64_t vd = umma_desc_sw128(
-              smem_addr(stages) + st * C::kStageBytes + C::kTileBytes, kBoxBytes, 1024);
-          for (int t = t0; t < t1; ++t) {
-            const int n = ip[t], tb = 2 * t + (n & 1);
-            // (P of a segment's first page comes after its tile's last O was read)
-            if (!wait(&p_full[tb], (n / 2) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t pb = tmem + C::kSCol + tb * kPage, od = tmem + t * D;
-            // keys 16 kk ..: P's head in columns 8 kk, its residual 32 further
+          tc_fence_after_sync();
+          const uint32_t pb = tmem + C::kSCol + tb * kPage;
+          // keys 16 kk ..: P's head in columns 8 kk, its residual 32 further
+          if (elect_lane()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_tmem_a(od, pb + 8 * kk, umma_desc_advance(vd, kk * 2048), C::kIdescPV,
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_tmem_a(tmem + t * D, pb + 8 * kk,
+                               umma_desc_advance(vd, (kk & 3) * 2048), C::kIdescPV,
                                k > 0 || kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_tmem_a(od, pb + 32 + 8 * kk, umma_desc_advance(vd, kk * 2048), C::kIdescPV,
-                               true);
             umma_commit(&o_done[tb]);
-            ++ip[t];
-            issued = true;
           }
-          if (ok) umma_commit(&v_empty[st]);
+          ++ip[t];
+          issued = true;
         }
-        if (ok) mbar_arrive(&seg_free[d]);
+        if (!ok) break;
+        if (elect_lane()) umma_commit(&v_empty[st]);
+        ++i;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      if (issued) {
-        umma_commit(&fin[1]);
-        mbar_wait_bounded(&fin[1], 0, p.err);
-      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&seg_free[d]);
+    }
+    if (issued && elect_lane()) {
+      umma_commit(&fin[1]);
+      mbar_wait_bounded(&fin[1], 0, p.err);
     }
   } else if (warp < C::kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax
