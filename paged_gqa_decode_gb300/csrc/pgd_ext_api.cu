@@ -60,15 +60,16 @@ int check_table(int32_t rows, int32_t width, int32_t num_pages) {
 struct SharedLayout {
   size_t ml, off, bytes;
 };
-SharedLayout shared_layout(const pgd_dims* d, int32_t groups) {
-  // one a (row, head) for the shared pages, eight for its own (of an even count of heads)
+SharedLayout shared_layout(const pgd_dims* d) {
+  // one a (row, head) for the shared pages, eight for its own (of an even count of heads,
+  // at an even place)
   const size_t group = d->num_q_heads / d->num_kv_heads;
   const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + 8 * ((group + 1) & ~size_t(1))) +
-                       256 * (size_t)kMaxSharedCtas;
+                       256 * (size_t)kMaxSharedCtas + 1;
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);
-  l.off = l.ml + parts * 2 * sizeof(float);
-  l.bytes = l.off + ((size_t)groups + d->rows + 1) * sizeof(int64_t);
+  l.off = (l.ml + parts * 2 * sizeof(float) + 15) / 16 * 16;
+  l.bytes = l.off + (size_t)d->rows * sizeof(SharedRecord) + sizeof(int64_t);
   return l;
 }
 
@@ -554,7 +555,7 @@ int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_page
 }
 
 size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups) {
-  return check_shared(dims, groups) == PGD_OK ? shared_layout(dims, groups).bytes : 0;
+  return check_shared(dims, groups) == PGD_OK ? shared_layout(dims).bytes : 0;
 }
 
 int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* group_starts,
@@ -574,7 +575,7 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   if ((k_new == nullptr) != (v_new == nullptr) ||
       (k_new && (!aligned16(k_new) || !aligned16(v_new))))
     return PGD_EINVAL;
-  const SharedLayout l = shared_layout(dims, groups);
+  const SharedLayout l = shared_layout(dims);
   if (workspace_size < l.bytes) return PGD_EWORKSPACE;
   if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
   DeviceInfo* dev = nullptr;
@@ -590,7 +591,8 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.out = static_cast<uint16_t*>(out);
   p.part_acc = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + l.ml);
-  p.item_off = reinterpret_cast<int64_t*>(ws + l.off);
+  p.records = reinterpret_cast<SharedRecord*>(ws + l.off);
+  p.units = reinterpret_cast<int64_t*>(ws + l.off + (size_t)dims->rows * sizeof(SharedRecord));
   p.err = dev->err;
   p.rows = dims->rows;
   p.groups = groups;

@@ -98,6 +98,13 @@ cudaError_t launch_compact_pages(const CompactParams& p, int sm_count, cudaStrea
 
 constexpr int kMaxSharedGroups = 8192;  // two words a group in shared memory
 constexpr int kMaxSharedCtas = 160;
+// What the combine needs of a row: where its own pages and its group's begin in the cut
+// (-1: it has none), its group's rows and pages, and its position.
+struct SharedRecord {
+  long long own, group;
+  int start, end, shared, n;
+};
+
 struct SharedParams {
   const uint16_t* q;
   const int32_t* table;
@@ -108,7 +115,8 @@ struct SharedParams {
   uint16_t* out;
   float* part_acc;     // D values of each partial
   float* part_ml;      // (m, l) of each
-  int64_t* item_off;   // [groups + rows + 1]
+  SharedRecord* records;  // [rows], for the combine, with
+  int64_t* units;                // the weight of a CTA's range
   unsigned int* err;
   int rows, groups, hq, hkv, group, maxp, num_pages, layout;
   float q_scale_log2;

@@ -76,15 +76,16 @@ struct SharedCfg {
   static_assert(kSCol + kTiles * 2 * kPage <= kTmemCols, "TMEM columns");
   static_assert((2 * kMaxSharedGroups + 1) * 4 <= STAGES * kStageBytes, "groups in the stages");
   static_assert(kSmemBytes + kSegs * 32 + 448 <= 227 * 1024, "shared memory (dynamic + static)");
-  static_assert((2 * kMaxSharedGroups + 1) * 4 + kThreads * 16 <= STAGES * kStageBytes,
-                "the list of items behind them");
+  static_assert((2 * kMaxSharedGroups + 2) * 4 + kMaxSharedGroups * 8 + kThreads * 16 <=
+                    STAGES * kStageBytes,
+                "their offsets and the list of items behind them");
 };
 
 // Weights in the cut, in about 0.05 us on GB300, fitted to what CTAs of mixed calls
 // took: a page of a block of one or two tiles (two tiles' products and
 // exponentials take longer than the page's bytes), a page of a row's own, and what
 // a (block or row, kv head) costs besides.
-constexpr int kUnitOne = 14, kUnitTwo = 26, kFixedBlock = 60, kFixedOwn = 8;
+constexpr int kUnitOne = 13, kUnitTwo = 22, kFixedBlock = 60, kFixedOwn = 8;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
 __host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 7 : 10; }
 
@@ -144,6 +145,12 @@ __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, i
   it.unit = unit_own(D);
   it.fixed = kFixedOwn;
   return it;
+}
+
+// The rows' partials come after the blocks', at an even place (as all steps from there
+// are): two heads' (m, l) are stored together.
+__device__ __forceinline__ long long shared_own_part(const SharedParams& p) {
+  return ((long long)p.rows * p.hq + 1) & ~1ll;
 }
 
 // a / b of weights, a >= 0, b > 0 (64-bit division is a hundred instructions).
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   const int G = p.group;
   const int T = C::kLanes / G;  // rows of a tile
   const int Gp = (G + 1) & ~1;  // heads of a row's partial
-  const long long own_part = (long long)p.rows * p.hq;  // the rows' partials come after the blocks'
+  const long long own_part = shared_own_part(p);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
@@ -345,11 +352,14 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     if (Q < kUnitTwo) Q = kUnitTwo;  // (no range between two pages' beginnings)
     u0 = min(Q * cta, total);
     u1 = min(u0 + Q, total);
-    if (cta == 0 && tid == 0) {
-      p.item_off[items] = Q;
+    // the last CTA, whose range may be short, leaves the combine what it needs
+    const bool records = cta == ctas - 1;
+    if (records && tid == 0) {
+      *p.units = Q;
       if (unsorted) record_error(p.err, PGD_EDEVICE_BOUNDS);
     }
-    if (cta == 0 || (at <= u0 && u0 < at + sum)) {
+    auto each_item = [&](auto f) {  // f(item, group, offset, weight, bad) of this thread's items
+      long long off = at;
       for (int i = i0; i < i1; ++i) {
         int g = g_mine;
         long long weight = sum;
@@ -359,16 +369,39 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           weight = it.weight(p.hkv);
           bad = it.bad;
         }
-        if (cta == 0) {  // for the combine; -1: no pages
-          p.item_off[i] = weight > 0 ? at : -1;
-          if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
-        }
-        if (at <= u0 && u0 < at + weight && u0 < u1) {
-          start_item = i;
-          start_rem = u0 - at;
-        }
-        at += weight;
+        f(i, g, off, weight, bad);
+        off += weight;
       }
+    };
+    if (u0 < u1 && at <= u0 && u0 < at + sum)
+      each_item([&](int i, int, long long off, long long weight, bool) {
+        if (off <= u0 && u0 < off + weight) {
+          start_item = i;
+          start_rem = u0 - off;
+        }
+      });
+    if (records) {
+      long long* g_off = reinterpret_cast<long long*>(stages + ((2 * S + 1) * 4 + 7) / 8 * 8);
+      each_item([&](int i, int, long long off, long long weight, bool bad) {
+        if (i < S) g_off[i] = weight > 0 ? off : -1;
+        if (bad) record_error(p.err, PGD_EDEVICE_BOUNDS);
+      });
+      __syncthreads();
+      each_item([&](int i, int g, long long off, long long weight, bool) {
+        if (i < S) return;
+        const bool grouped = g >= 0 && g < S && !unsorted;
+        SharedRecord r;
+        r.own = weight > 0 ? off : -1;
+        r.group = grouped ? g_off[g] : -1;
+        r.start = grouped ? g_start[g] : 0;
+        r.end = grouped ? g_start[g + 1] : 0;
+        r.shared = grouped ? g_pages[g] : 0;
+        r.n = run == 1 ? n_mine : p.positions[i - S];
+        const int4* words = reinterpret_cast<const int4*>(&r);
+        int4* to = reinterpret_cast<int4*>(p.records + (i - S));
+        to[0] = words[0];
+        to[1] = words[1];
+      });
     }
   }
   fence_proxy_async_shared();  // the stages are TMA's from here on
@@ -704,6 +737,10 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           tc_fence_after_sync();
           const uint64_t qd = umma_desc_advance(q0, t * C::kQTileBytes);
           if (elect_lane()) {
+            // (the last tile's P V, whose commit covers the other's: that page's V slot is
+            // free; the last two pages' the softmax warps free)
+            if (k >= 2 && t == t1 - 1)
+              mbar_arrive(&v_empty[st >= 2 ? st - 2 : st + STAGES - 2]);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_bf16(tmem + C::kSCol + tb * kPage,
@@ -716,7 +753,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           issued = true;
         }
         if (!ok) break;
-        if (elect_lane()) umma_commit(&k_empty[st]);
         ++i;
         if (++st == STAGES) {
           st = 0;
@@ -771,6 +807,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           const uint32_t pb = tmem + C::kSCol + tb * kPage;
           // keys 16 kk ..: P's head in columns 8 kk, its residual 32 further
           if (elect_lane()) {
+            // (the last tile's S was read, whose commit covers the other's: K's slot is free)
+            if (t == t1 - 1) mbar_arrive(&k_empty[st]);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               umma_bf16_tmem_a(tmem + t * D, pb + 8 * kk,
@@ -782,7 +820,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           issued = true;
         }
         if (!ok) break;
-        if (elect_lane()) umma_commit(&v_empty[st]);
         ++i;
         if (++st == STAGES) {
           st = 0;
@@ -984,6 +1021,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         const int tl = 2 * t + ((n - 1) & 1);
         if (!all_ok(wait(&o_done[tl], ((n - 1) / 2) & 1))) break;
         tc_fence_after_sync();
+        if (t == t0 + sg.tiles() - 1 && (warp & 3) == 0 && lane == 0)
+          for (int k = max(pages - 2, 0); k < pages; ++k) mbar_arrive(&v_empty[(i + k) % STAGES]);
         if (live_warp) {
           if (live) {
             p.part_ml[2 * part] = m_run;
@@ -1025,7 +1064,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
 // range that they fell to, then those over its own, up to eight a CTA.  Zeros for an inactive row (n < 0), for one that the cut found bad, and
 // where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the maxima
 // pass over it).  A warp each, a CTA the heads of a kv head.  Bound by latency: the
-// places of the partials are worked out from the cut's offsets (one round trip),
+// places of the partials are worked out from the row's record (one round trip),
 // then 32 partials' (m, l), one a lane, and the first eight partials' values load
 // together.
 template <int D>
@@ -1033,23 +1072,18 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
   constexpr int kDims = D / 32, kEarly = 8;
   const int kvh = blockIdx.x, b = blockIdx.y, g_head = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, Gp = (G + 1) & ~1, h = kvh * G + g_head;
-  // everything but the partials is an input of the kernel before as well, which waited
-  // for it; read here, off the path that starts once that kernel is done
-  const int S = p.groups;
-  const int n = p.positions[b];
-  const float sink = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-  int g = S > 0 ? shared_find(p.starts, S, b) : -1, s = 0, e = 0, shared = 0;
-  if (g >= S) g = -1;
-  if (g >= 0) {
-    s = p.starts[g];
-    e = p.starts[g + 1];
-    shared = p.pages[g];
-  }
-  const SharedItem group = shared_group(p, s, e, shared), own = shared_row<D>(p, n, shared);
+  const float sink = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;  // (an input of both kernels)
   pdl_wait();
   pdl_allow_dependents();
-  const long long Q = p.item_off[S + p.rows], own_off = p.item_off[S + b];
-  const long long off = g >= 0 ? p.item_off[g] : -1;
+  const int4* words = reinterpret_cast<const int4*>(p.records + b);
+  const int4 w0 = words[0], w1 = words[1];
+  const long long Q = *p.units;
+  SharedRecord r;
+  *reinterpret_cast<int4*>(&r) = w0;
+  *(reinterpret_cast<int4*>(&r) + 1) = w1;
+  const long long own_off = r.own;
+  const SharedItem group = shared_group(p, r.start, r.end, r.shared);
+  const SharedItem own = shared_row<D>(p, r.n, r.shared);
   uint16_t* out = p.out + ((size_t)b * p.hq + h) * D + lane * kDims;
   float res[kDims];
 #pragma unroll
@@ -1058,10 +1092,11 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     // the shared pages' partials
     long long at0 = 0;
     int count0 = 0;
-    if (off >= 0) {
-      const int block = 2 * (128 / G), blk = (b - s) / block, row0 = s + blk * block;
-      const int rows = min(block, e - row0);
-      const long long first = off + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
+    if (r.group >= 0) {
+      const int block = 2 * (128 / G), blk = (b - r.start) / block, row0 = r.start + blk * block;
+      const int rows = min(block, r.end - row0);
+      const long long first =
+          r.group + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
       const long long c0 = shared_divide(first, Q);
       count0 =
           (int)(shared_divide(first + (long long)(group.pages - 1) * group.unit, Q) - c0) + 1;
@@ -1072,7 +1107,7 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     const long long c0 = shared_divide(first, Q);
     const int ranges =
         (int)(shared_divide(first + (long long)(own.pages - 1) * own.unit, Q) - c0) + 1;
-    const long long at1 = 256 * c0 + (long long)p.rows * p.hq +
+    const long long at1 = 256 * c0 + shared_own_part(p) +
                           8ll * Gp * ((long long)b * p.hkv + kvh);
     // pages that start before the end of range i
     auto before = [&](int i) {
@@ -1100,21 +1135,17 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     auto place = [&](int i) {
       return i < count0 ? at0 + 256ll * i : own_place(i - count0) + g_head;
     };
-    auto values = [&](int i, float (&v)[kDims]) {
-      const float* a = p.part_acc + place(i) * D + lane * kDims;
-#pragma unroll
-      for (int j = 0; j < kDims; j += 2) {
-        const float2 w = *reinterpret_cast<const float2*>(a + j);
-        v[j] = w.x;
-        v[j + 1] = w.y;
-      }
+    auto values = [&](int i, float* v) {
+      using Vec = typename std::conditional<kDims == 2, float2, float4>::type;
+      *reinterpret_cast<Vec*>(v) =
+          *reinterpret_cast<const Vec*>(p.part_acc + place(i) * D + lane * kDims);
     };
     auto weight = [&](int i) {
       if (i >= count) return make_float2(-INFINITY, 0.f);
       return *reinterpret_cast<const float2*>(p.part_ml + 2 * place(i));
     };
     float2 ml = weight(lane);
-    float early[kEarly][kDims];
+    alignas(16) float early[kEarly][kDims];
 #pragma unroll
     for (int k = 0; k < kEarly; ++k)
       if (k < count) values(k, early[k]);
@@ -1145,7 +1176,7 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
       }
 #pragma unroll 8
       for (; k < some; ++k) {
-        float v[kDims];
+        alignas(16) float v[kDims];
         values(i0 + k, v);
         add(v, __shfl_sync(0xffffffffu, f, k));
       }

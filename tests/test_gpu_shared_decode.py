@@ -341,3 +341,16 @@ def test_on_a_side_stream():
     assert pgd.get_device_error(stream) == pgd.OK
     for out in outs:
         b.compare(out, 64 ** -0.5)
+
+
+def test_more_rows_and_groups_than_threads():
+    """A thread of the cut sums several items; odd counts of everything."""
+    rng = np.random.default_rng(30)
+    groups = [(1, None)] + [(int(n), int(p)) for n, p in zip(rng.integers(0, 9, 301),
+                                                            rng.integers(0, 4, 301))] + [(2, None)]
+    own = rng.integers(0, 130, sum(n for n, _ in groups))
+    assert len(own) > 1000
+    b = Batch(30, groups, own, 3, 1, 64)
+    b.check(sinks=rng.normal(size=3))
+    b.starts[7] = b.starts[8] + 1                 # decreasing, seen by every thread
+    b.check(status=pgd.EDEVICE_BOUNDS, bad=range(len(own)))
