@@ -61,10 +61,10 @@ struct SharedLayout {
   size_t ml, off, bytes;
 };
 SharedLayout shared_layout(const pgd_dims* d) {
-  // one a (row, head) for the shared pages, eight for its own (of an even count of heads,
+  // one a (row, head) for the shared pages, four for its own (of an even count of heads,
   // at an even place)
   const size_t group = d->num_q_heads / d->num_kv_heads;
-  const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + 8 * ((group + 1) & ~size_t(1))) +
+  const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + 4 * ((group + 1) & ~size_t(1))) +
                        256 * (size_t)kMaxSharedCtas + 1;
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);

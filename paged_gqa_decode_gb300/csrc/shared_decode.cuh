@@ -16,7 +16,7 @@
 // pages: two query tiles of 128 (row, head) pairs, one per TMEM lane, that
 // share each K and V page; one tile where a block's rows fit it.  (row, kv head)
 // over the row's own pages: G query heads, on mma.sync (MmaConsumer of
-// paged_decode.cuh), eight warps taking pages in turn -- a tile of tcgen05 would
+// paged_decode.cuh), four warps taking pages in turn -- a tile of tcgen05 would
 // have G of 128 lanes in use and one warp's exponentials to wait for on every
 // page (measured so: a page of 16 KB in 0.8 us, its share of HBM 0.37).
 // All items' pages form one sequence, cut into ranges of near-equal weight, one
@@ -27,8 +27,7 @@
 // next CTA), so segment (item, cta) keeps its partials at
 //   [partials of the items before] + 256 * cta + its own
 // without a table: a block's, one per lane, then a row's, one per head from each of
-// the eight warps that had a page (a merge of the warps cost 2 us a segment, the
-// partials 6 % of the pages' bytes, in L2).  Offsets: every CTA sums the items' weights itself (two
+// the four warps that had a page (a merge of the warps cost 2 us a segment).  Offsets: every CTA sums the items' weights itself (two
 // barriers, less than a launch); CTA 0 leaves them for the combine.
 //
 // Roles of a CTA (384 threads): warps 0-3 and 4-7 softmax of tile 0 and 1, one
@@ -532,8 +531,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       }
       const int count = pg1 - pg0;
       const bool last = pg1 == pages;
-      // (partials of the items before: eight a head)
-      if (!describe(256ll * cta + own_part + 8ll * Gp * ((long long)row * p.hkv + kvh),
+      // (partials of the items before: four a head)
+      if (!describe(256ll * cta + own_part + 4ll * Gp * ((long long)row * p.hkv + kvh),
                     row_bad ? 0 : count, row, kvh, 1,
                     SharedSeg::fields(true, 1, 0, 0, last ? n % kPage : kPage - 1)))
         return false;
@@ -841,7 +840,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     const float cc = c > 0.f ? c : 1.f;  // folded into the exponent's FMA if positive
     int n = 0;   // pages of this tile
     int i = 0;   // pages
-    int on = 0;  // pages of rows' own
+    int turn = 0;  // the next segment's first warp, % 8
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int d = seq % C::kSegs;
@@ -850,12 +849,14 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (sg.what == 0) break;
       const int pages = sg.pages;
       if (sg.own()) {
-        // page k of the segment is warp (on + k) % 8's, and partial k % 8
-        const int k0 = (warp - on) & 7;  // this warp's first page
-        if (k0 < pages) {
+        // at most four of the warps a segment, the next ones the next: page k is warp
+        // (turn + k % 4) % 8's, and partial k % 4
+        const int k0 = (warp - turn) & 7;  // this warp's first page
+        turn += min(pages, 4);
+        if (k0 < min(pages, 4)) {
           MmaConsumer<D, SharedScore> cons;
           cons.init(p, sg.row0, sg.kvh * G, lane, nullptr);
-          for (int k = k0; k < pages; k += 8) {
+          for (int k = k0; k < pages; k += 4) {
             const int ik = i + k, st = ik % STAGES;
             const uint32_t ph = (ik / STAGES) & 1;
             if (!all_ok(shared_wait_count(&k_issued, nullptr, ik, p.err, &abort_flag) > ik) ||
@@ -908,7 +909,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           p.part_ml[2 * (sg.part + lane)] = -INFINITY;
           p.part_ml[2 * (sg.part + lane) + 1] = -1.f;
         }
-        on += pages;
         i += pages;
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_free[d]);
@@ -1061,15 +1061,16 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
 }
 
 // Joins the partials of a (row, query head): those over its group's pages, one a CTA of the
-// range that they fell to, then those over its own, up to eight a CTA.  Zeros for an inactive row (n < 0), for one that the cut found bad, and
+// range that they fell to, then those over its own, up to four a CTA.  Zeros for an inactive row (n < 0), for one that the cut found bad, and
 // where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the maxima
 // pass over it).  A warp each, a CTA the heads of a kv head.  Bound by latency: the
 // places of the partials are worked out from the row's record (one round trip),
-// then 32 partials' (m, l), one a lane, and the first eight partials' values load
-// together.
+// then 32 partials' (m, l), one a lane, and the first four partials' values load
+// together, and four at a time from there (eight or sixteen: more registers and, what
+// counts more for so short a kernel, more code; 16 groups of 4 rows 54 us in all, 56, 58).
 template <int D>
 __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams p) {
-  constexpr int kDims = D / 32, kEarly = 8;
+  constexpr int kDims = D / 32, kBatch = 4;
   const int kvh = blockIdx.x, b = blockIdx.y, g_head = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, Gp = (G + 1) & ~1, h = kvh * G + g_head;
   const float sink = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;  // (an input of both kernels)
@@ -1102,13 +1103,13 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
           (int)(shared_divide(first + (long long)(group.pages - 1) * group.unit, Q) - c0) + 1;
       at0 = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G + g_head;
     }
-    // its own pages': range i of a CTA has one for each page, at most eight
+    // its own pages': range i of a CTA has one for each page, at most four
     const long long first = own_off + kvh * own.pair() + own.fixed;
     const long long c0 = shared_divide(first, Q);
     const int ranges =
         (int)(shared_divide(first + (long long)(own.pages - 1) * own.unit, Q) - c0) + 1;
     const long long at1 = 256 * c0 + shared_own_part(p) +
-                          8ll * Gp * ((long long)b * p.hkv + kvh);
+                          4ll * Gp * ((long long)b * p.hkv + kvh);
     // pages that start before the end of range i
     auto before = [&](int i) {
       return i + 1 >= ranges
@@ -1118,13 +1119,13 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     int count = count0;
     for (int i = 0, pg = 0; i < ranges; ++i) {
       const int end = before(i);
-      count += min(end - pg, 8);
+      count += min(end - pg, 4);
       pg = end;
     }
     auto own_place = [&](int j) {  // j of the row's own partials
       long long at = at1;
       for (int i = 0, pg = 0; i + 1 < ranges; ++i) {
-        const int end = before(i), some = min(end - pg, 8);
+        const int end = before(i), some = min(end - pg, 4);
         if (j < some) break;
         j -= some;
         pg = end;
@@ -1145,10 +1146,13 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
       return *reinterpret_cast<const float2*>(p.part_ml + 2 * place(i));
     };
     float2 ml = weight(lane);
-    alignas(16) float early[kEarly][kDims];
+    alignas(16) float v[kBatch][kDims];
+    auto load = [&](int i0) {  // four partials' values
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-      if (k < count) values(k, early[k]);
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + k < count) values(i0 + k, v[k]);
+    };
+    load(0);
     float mx = sink;
     bool skipped = false, nan = false;
     for (int i0 = 0; i0 < count; i0 += 32) {
@@ -1159,26 +1163,20 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     }
     const float ref = mx == -INFINITY ? 0.f : mx;
     float den = exp2_approx(sink - ref);
-    auto add = [&](const float (&v)[kDims], float f) {
-#pragma unroll
-      for (int j = 0; j < kDims; ++j) res[j] = fmaf(v[j], f, res[j]);
-    };
     for (int i0 = 0; i0 < count; i0 += 32) {
       if (i0 > 0) ml = weight(i0 + lane);
       const float f = exp2_approx(ml.x - ref);  // (past the end: 0)
       den += warp_sum(ml.y * f);
       const int some = min(32, count - i0);
-      int k = 0;
-      if (i0 == 0) {
+      for (int k0 = 0; k0 < some; k0 += kBatch) {
+        if (i0 + k0 > 0) load(i0 + k0);
 #pragma unroll
-        for (; k < kEarly; ++k)
-          if (k < some) add(early[k], __shfl_sync(0xffffffffu, f, k));
-      }
-#pragma unroll 8
-      for (; k < some; ++k) {
-        alignas(16) float v[kDims];
-        values(i0 + k, v);
-        add(v, __shfl_sync(0xffffffffu, f, k));
+        for (int k = 0; k < kBatch; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+          if (i0 + k0 + k < count)
+#pragma unroll
+            for (int j = 0; j < kDims; ++j) res[j] = fmaf(v[k][j], fk, res[j]);
+        }
       }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
