@@ -84,7 +84,7 @@ struct SharedCfg {
 // took: a page of a block of one or two tiles (two tiles' products and
 // exponentials take longer than the page's bytes), a page of a row's own, and what
 // a (block or row, kv head) costs besides.
-constexpr int kUnitOne = 13, kUnitTwo = 22, kFixedBlock = 60, kFixedOwn = 8;
+constexpr int kUnitOne = 13, kUnitTwo = 23, kFixedBlock = 60, kFixedOwn = 8;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
 __host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 7 : 10; }
 

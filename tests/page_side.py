@@ -147,19 +147,24 @@ def random_state(rng, requests, beams, hi, grown, width=None, spare=0, filler=-7
 
 
 def attention(q, k_pages, v_pages, table, positions, scale, sinks=None):
-    """Decode attention in 64 bits: q [R, Hq, D], pages [pages, Hkv, 64, D].  Returns the
+    """Decode attention in 64 bits: q [R, Hq, D], pages [pages, Hkv, 64, D], as attend_rows."""
+    def row(pages, b, n):
+        return np.concatenate(list(pages[table[b, : n // PAGE + 1]]), axis=1)[:, : n + 1]
+    return attend_rows(q, [None if n < 0 else (row(k_pages, b, n), row(v_pages, b, n))
+                           for b, n in enumerate(positions)], scale, sinks)
+
+
+def attend_rows(q, rows, scale, sinks=None):
+    """Row b's queries over rows[b] = its (keys, values), [Hkv, n, D] each, or None.  Returns the
     result, sum_j p_j |v_j|, max_j scale sum_i |q_i k_ij| and sum_j |v_j|."""
-    rows, hq, d = q.shape
-    hkv = k_pages.shape[1]
-    group = hq // hkv
     out, mass, every = (np.zeros(q.shape) for _ in range(3))
-    size = np.zeros((rows, hq, 1))
-    for b, n in enumerate(positions):
-        if n < 0:
+    size = np.zeros(q.shape[:2] + (1,))
+    for b, kv in enumerate(rows):
+        if kv is None:
             continue
-        at = table[b, : n // PAGE + 1]
-        k, v = (np.concatenate(list(p[at]), axis=1)[:, : n + 1] for p in (k_pages, v_pages))
-        for h in range(hq):
+        k, v = kv
+        group = q.shape[1] // len(k)
+        for h in range(q.shape[1]):
             kk, vv = k[h // group], v[h // group]
             x = kk @ q[b, h] * scale
             top = max(x.max(), -np.inf if sinks is None else sinks[h])
