@@ -479,23 +479,33 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         id = ahead;
       }
     };
-    // Pages pg0 .. pg1 - 1 of a block's shared ones.
+    // Pages pg0 .. pg1 - 1 of a block's shared ones, by the table row of its first active
+    // row (an inactive one may hold others, or none).
     auto block_segment = [&](int row0, int rows, int kvh, int pg0, int pg1) -> bool {
-      const int count = pg1 - pg0;
       const int32_t* trow = p.table + (size_t)row0 * p.maxp + pg0;
-      const int id = lane < count ? trow[lane] : 0;
+      int count = pg1 - pg0, id = lane < count ? trow[lane] : 0;
+      if (p.positions[row0] < 0) {
+        int at = 0;
+        unsigned active = 0;
+        for (; at < rows && active == 0; at += 32)
+          active = __ballot_sync(0xffffffffu, at + lane < rows && p.positions[row0 + at + lane] >= 0);
+        if (active == 0) count = 0;  // none: nothing is read
+        trow += (size_t)(active ? at - 32 + __ffs(active) - 1 : 0) * p.maxp;
+        id = lane < count ? trow[lane] : 0;
+      }
       bool bad = lane < count && !in_pool(id);
       for (int k = lane + 32; k < count; k += 32) bad |= !in_pool(trow[k]);
       bad = __any_sync(0xffffffffu, bad);
       if (bad && lane == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
+      if (bad) count = 0;
       const int tiles = rows > T ? 2 : 1;
       const int q_tile = tiles == 2 ? 0 : q_next;
       // (partials of the items before: one a lane)
       if (!describe(256ll * cta + (long long)row0 * p.hq + (long long)kvh * rows * G,
-                    bad ? 0 : count, row0, kvh, rows,
+                    count, row0, kvh, rows,
                     SharedSeg::fields(false, tiles, tiles == 2 ? 0 : tile_next, q_tile, kPage - 1)))
         return false;
-      if (bad) return true;
+      if (count == 0) return true;
       if (tiles == 1) tile_next ^= 1;
       // Q, once the products that read its tiles are done
       if (q_tile == 0) {

@@ -354,3 +354,18 @@ def test_more_rows_and_groups_than_threads():
     b.check(sinks=rng.normal(size=3))
     b.starts[7] = b.starts[8] + 1                 # decreasing, seen by every thread
     b.check(status=pgd.EDEVICE_BOUNDS, bad=range(len(own)))
+
+
+def test_inactive_rows_may_hold_anything():
+    """The first rows of groups and of blocks among them, their table entries out of the pool."""
+    own = np.full(180, 50)
+    own[:3] = own[64:100] = own[150:153] = 0
+    own[160:170] = 0                               # a whole group
+    b = Batch(31, [(150, 5), (10, 3), (10, 4), (10, 2)], own, 32, 8, 128)
+    b.table[np.asarray(own) == 0] = -5
+    b.check()
+    own = np.full(40, 70)
+    own[:39] = 0
+    b = Batch(32, [(40, 6)], own, 14, 2, 64)
+    b.table[:39] = 2 ** 30
+    b.check()
