@@ -324,11 +324,15 @@ PGD_API int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t 
  *   dims         rows at most 65535; layout PAGE_MAJOR or HEAD_MAJOR (else PGD_EUNSUPPORTED).
  *   workspace    pgdx_shared_decode_workspace_bytes(dims, groups) bytes (0 for dims or groups
  *                that the call refuses).
+ *   opts         kernel: PREFILL_UMMA (the groups' pages once), TENSOR_CORE (every row by itself,
+ *                by its own table entries, without a look at the groups) or AUTO (TENSOR_CORE where
+ *                all rows' tables come to 128 MB of pages at most, where that is faster); else
+ *                PGD_EUNSUPPORTED.  pages_per_split is not used.
  * Everything else, inactive rows among it, as there.  Device errors
- * (PGD_EDEVICE_BOUNDS, the rows concerned give zeros, a step leaves them unwritten): starts
- * that decrease or lie outside (all rows), group_pages outside [0, max_pages_per_row] (its
- * rows), a row whose position is beyond its table or in its group's pages, a page outside
- * the pool.  A step writes its rows' keys and values to pages of their own: two rows must
+ * (PGD_EDEVICE_BOUNDS, the rows concerned give zeros, a step leaves them unwritten): a
+ * row whose position is beyond its table, a page outside the pool and, with PREFILL_UMMA,
+ * starts that decrease or lie outside (all rows), group_pages outside [0,
+ * max_pages_per_row] (its rows), a row whose position is in its group's pages.  A step writes its rows' keys and values to pages of their own: two rows must
  * not hold the page of their positions together.
  */
 PGD_API size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups);
@@ -337,7 +341,7 @@ PGD_API int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32
                                const void* v_new, void* k_pool, void* v_pool,
                                const int32_t* table, const int32_t* positions, const float* sinks,
                                float scale, void* out, void* workspace, size_t workspace_bytes,
-                               pgd_stream_t stream);
+                               const pgd_decode_options* opts, pgd_stream_t stream);
 
 /* As pgd_get_device_error, for this library's error word. */
 PGD_API int pgdx_get_device_error(pgd_stream_t stream);

@@ -189,7 +189,7 @@ def load_extension(path: str | None = None) -> ctypes.CDLL:
                     [vp] * 7 + [size, vp]
                 lib.pgdx_shared_decode_workspace_bytes.argtypes = [dims_p, i32]
                 lib.pgdx_shared_decode.argtypes = [dims_p, i32] + [vp] * 10 + \
-                    [ctypes.c_float, vp, vp, size, vp]
+                    [ctypes.c_float, vp, vp, size, opts_p, vp]
                 lib.pgdx_get_device_error.argtypes = [vp]
                 for name in ("assign_pages", "rotary_init", "rotary_append", "paged_decode",
                              "paged_prefill", "fork_rows", "copy_pages", "compact_pages",
@@ -383,7 +383,8 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     group_starts (int32 [S + 1]) and group_pages (int32 [S]): rows group_starts[g] ..
     group_starts[g + 1] - 1 hold the same first group_pages[g] pages, which are read
     once for all of them (full attention, none of the above; a workspace of
-    shared_decode_workspace_bytes).  Returns bf16 [R, Hq, D]."""
+    shared_decode_workspace_bytes; kernel KERNEL_PREFILL_UMMA does so always, KERNEL_TENSOR_CORE
+    never, AUTO where it is faster).  Returns bf16 [R, Hq, D]."""
     if group_starts is not None or group_pages is not None:
         return _shared_decode(q, None, None, k_pool, v_pool, table, positions, sinks, window,
                               scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,
@@ -515,8 +516,8 @@ def _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, win
         raise ValueError("group_starts and group_pages go together")
     if window > 0 or score is not None:
         raise ValueError("group_starts: full attention, without softcap, alibi_slopes or first_key")
-    if pages_per_split > 0 or kernel != KERNEL_AUTO:
-        raise ValueError("group_starts: the split and the kernel are the library's")
+    if pages_per_split > 0:
+        raise ValueError("group_starts: the split is the library's")
     dev = _check_cuda(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, out, workspace,
                       group_starts, group_pages)
     if _current_device() != dev:
@@ -562,7 +563,7 @@ def _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, win
         dims, groups, group_starts.data_ptr(), group_pages.data_ptr(), q.data_ptr(), _ptr(k_new),
         _ptr(v_new), k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(), positions.data_ptr(),
         _ptr(sinks), float(scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _stream_handle(stream, dev))
+        ctypes.byref(_opts_of(0, kernel)), _stream_handle(stream, dev))
     if rc != OK:
         raise PgdError(rc, what)
     return out

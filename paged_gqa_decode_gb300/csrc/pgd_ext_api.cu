@@ -73,6 +73,23 @@ SharedLayout shared_layout(const pgd_dims* d) {
   return l;
 }
 
+// SMs of the current device, for a plan (0: none; the plan is then the smallest device's).
+int device_sms() {
+  DeviceInfo* dev = nullptr;
+  return current_device(&dev) == PGD_OK ? dev->sm_count : 0;
+}
+
+// Whether AUTO reads a call's rows one by one, groups or not: where all of their tables'
+// pages fit L2, which then serves all but the first of a group's reads, and the shared kernel's
+// cut, partials and their join cost more than it saves.  Rows by themselves against shared, us:
+// 4 MB 12 : 15, 32 MB 8.8 : 16, 64 MB 11.8 : 15.4, 96 MB 13 : 18, 112 MB 17 : 26, 136 MB 19 : 19,
+// 190 MB 19.5 : 18.5, 270 MB 34 : 20, 340 MB 43 : 23, 690 MB 60 : 23.
+constexpr int64_t kSharedRowBytes = 128ll << 20;
+bool shared_row_by_row(const pgd_dims* d) {
+  return (int64_t)d->rows * d->num_kv_heads * d->max_pages_per_row * kPageSize * d->head_dim * 4 <=
+         kSharedRowBytes;
+}
+
 int check_shared(const pgd_dims* d, int32_t groups) {
   const int rc = check_dims(d);
   if (rc != PGD_OK) return rc;
@@ -555,16 +572,25 @@ int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t num_page
 }
 
 size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups) {
-  return check_shared(dims, groups) == PGD_OK ? shared_layout(dims).bytes : 0;
+  if (check_shared(dims, groups) != PGD_OK) return 0;
+  const size_t shared = shared_layout(dims).bytes;
+  const size_t rows = pgd::workspace_bytes(dims, make_plan(dims, nullptr, device_sms()));
+  return shared > rows ? shared : rows;  // (for either kernel)
 }
 
 int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* group_starts,
                        const int32_t* group_pages, const void* q, const void* k_new,
                        const void* v_new, void* k_pool, void* v_pool, const int32_t* table,
                        const int32_t* positions, const float* sinks, float scale, void* out,
-                       void* workspace, size_t workspace_size, pgd_stream_t stream) {
+                       void* workspace, size_t workspace_size, const pgd_decode_options* opts,
+                       pgd_stream_t stream) {
   int rc = check_shared(dims, groups);
   if (rc != PGD_OK) return rc;
+  const int32_t asked = opts ? opts->kernel : PGD_KERNEL_AUTO;
+  if (asked < PGD_KERNEL_AUTO || asked > PGD_KERNEL_PREFILL_PAIR) return PGD_EINVAL;
+  if (asked != PGD_KERNEL_AUTO && asked != PGD_KERNEL_TENSOR_CORE &&
+      asked != PGD_KERNEL_PREFILL_UMMA)
+    return PGD_EUNSUPPORTED;
   if (!std::isfinite(scale)) return PGD_EINVAL;
   if (dims->rows == 0) return PGD_OK;
   if (!q || !k_pool || !v_pool || !table || !positions || !out) return PGD_EINVAL;
@@ -575,9 +601,15 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   if ((k_new == nullptr) != (v_new == nullptr) ||
       (k_new && (!aligned16(k_new) || !aligned16(v_new))))
     return PGD_EINVAL;
-  const SharedLayout l = shared_layout(dims);
-  if (workspace_size < l.bytes) return PGD_EWORKSPACE;
+  if (workspace_size < pgdx_shared_decode_workspace_bytes(dims, groups)) return PGD_EWORKSPACE;
   if (!workspace || !aligned16(workspace)) return PGD_EINVAL;
+  if (asked == PGD_KERNEL_TENSOR_CORE || (asked == PGD_KERNEL_AUTO && shared_row_by_row(dims))) {
+    const pgdx_score plain = {0.f, nullptr, nullptr, nullptr};
+    return attention_impl(dims, dims->rows, nullptr, &plain, q, k_new, v_new, k_pool, v_pool, table,
+                          positions, sinks, 0, scale, out, workspace, workspace_size, nullptr,
+                          stream);
+  }
+  const SharedLayout l = shared_layout(dims);
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev)) != PGD_OK) return rc;
   char* ws = static_cast<char*>(workspace);

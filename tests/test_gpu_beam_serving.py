@@ -30,7 +30,8 @@ def dev(a):
 class Server:
     """Requests of `beams` rows each.  history[layer][row]: (keys, values), [n, Hkv, D]."""
 
-    def __init__(self, seed, prompts, beams, hq, hkv, d, layout):
+    def __init__(self, seed, prompts, beams, hq, hkv, d, layout, kernel=pgd.KERNEL_PREFILL_UMMA):
+        self.kernel = kernel
         self.rng = np.random.default_rng(seed)
         self.gen = torch.Generator().manual_seed(seed)
         self.beams, self.hq, self.hkv, self.d, self.layout = beams, hq, hkv, d, layout
@@ -117,7 +118,8 @@ class Server:
             k, v = self.values(self.rows, self.hkv), self.values(self.rows, self.hkv)
             out = pgd.paged_decode_step(q, k, v, self.k[layer], self.v[layer], self.table,
                                         positions, num_kv_heads=self.hkv, layout=self.layout,
-                                        group_starts=self.starts, group_pages=groups)
+                                        group_starts=self.starts, group_pages=groups,
+                                        kernel=self.kernel)
             at = np.nonzero(live)[0]
             self.extend(layer, at, k[dev(at).long()], v[dev(at).long()])
             assert pgd.get_device_error() == pgd.OK
@@ -143,10 +145,12 @@ class Server:
         return held
 
 
-@pytest.mark.parametrize("hq,hkv,d,layout", [(14, 2, 64, pgd.PAGE_MAJOR), (32, 8, 128, pgd.HEAD_MAJOR),
-                                             (8, 8, 128, pgd.PAGE_MAJOR)])
-def test_beam_search_over_shared_pages(hq, hkv, d, layout):
-    s = Server(1, [200, 63, 64, 129], 4, hq, hkv, d, layout)
+@pytest.mark.parametrize("hq,hkv,d,layout,kernel", [
+    (14, 2, 64, pgd.PAGE_MAJOR, pgd.KERNEL_PREFILL_UMMA),
+    (32, 8, 128, pgd.HEAD_MAJOR, pgd.KERNEL_PREFILL_UMMA),
+    (8, 8, 128, pgd.PAGE_MAJOR, pgd.KERNEL_AUTO)])
+def test_beam_search_over_shared_pages(hq, hkv, d, layout, kernel):
+    s = Server(1, [200, 63, 64, 129], 4, hq, hkv, d, layout, kernel)
     s.prefill()
     s.books()
     first = np.arange(s.rows) // 4 * 4
@@ -215,7 +219,8 @@ def test_a_step_captured_with_its_reordering():
         s.lengths.copy_(page.lengths)
         s.head.copy_(page.free_head)
         pgd.paged_decode_step(q, k, v, s.k[0], s.v[0], s.table, page.positions, num_kv_heads=hkv,
-                              out=out, workspace=work, group_starts=s.starts, group_pages=groups)
+                              out=out, workspace=work, group_starts=s.starts, group_pages=groups,
+                              kernel=pgd.KERNEL_PREFILL_UMMA)
     for turn in range(80):
         chosen = np.arange(s.rows) // beams * beams + s.rng.integers(0, beams, s.rows)
         parents.copy_(dev(chosen))

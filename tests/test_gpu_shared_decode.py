@@ -82,7 +82,8 @@ class Batch:
     def call(self, k_new=None, v_new=None, **kw):
         args = (dev(self.table), dev(self.positions))
         kw = dict(dict(num_kv_heads=self.hkv, layout=self.layout, group_starts=dev(self.starts or [0]),
-                       group_pages=dev(self.shared)), **kw)
+                       group_pages=dev(self.shared),
+                       kernel=pgd.KERNEL_PREFILL_UMMA), **kw)
         if k_new is None:
             return pgd.paged_decode_attention(self.q.to(DEV), self.k_pool, self.v_pool, *args, **kw)
         return pgd.paged_decode_step(self.q.to(DEV), k_new, v_new, self.k_pool, self.v_pool, *args,
@@ -284,9 +285,12 @@ def test_refusals():
                dict(alibi_slopes=torch.zeros(32, device=DEV))):
         with pytest.raises(ValueError, match="full attention"):
             b.call(**kw)
-    for kw in (dict(pages_per_split=4), dict(kernel=pgd.KERNEL_CUDA_CORE)):
-        with pytest.raises(ValueError, match="library's"):
-            b.call(**kw)
+    with pytest.raises(ValueError, match="library's"):
+        b.call(pages_per_split=4)
+    for kernel, status in ((pgd.KERNEL_CUDA_CORE, pgd.EUNSUPPORTED), (9, pgd.EINVAL)):
+        with pytest.raises(pgd.PgdError) as e:
+            b.call(kernel=kernel)
+        assert e.value.status == status
     with pytest.raises(ValueError, match=r"\[S"):
         b.call(group_starts=dev([0, 2, 4]))
     with pytest.raises(ValueError, match="int32"):
@@ -309,7 +313,8 @@ def test_captured_with_changing_groups():
     kp, vp = (torch.zeros(pages, hkv, 64, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
     out = torch.empty_like(q)
     call = lambda: pgd.paged_decode_attention(  # noqa: E731
-        q, kp, vp, t, n, num_kv_heads=hkv, out=out, group_starts=starts, group_pages=shared)
+        q, kp, vp, t, n, num_kv_heads=hkv, out=out, group_starts=starts, group_pages=shared,
+        kernel=pgd.KERNEL_PREFILL_UMMA)
     call()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -369,3 +374,38 @@ def test_inactive_rows_may_hold_anything():
     b = Batch(32, [(40, 6)], own, 14, 2, 64)
     b.table[:39] = 2 ** 30
     b.check()
+
+
+@pytest.mark.parametrize("kernel", [pgd.KERNEL_AUTO, pgd.KERNEL_TENSOR_CORE])
+def test_row_by_row(kernel):
+    """Small calls by AUTO, any by choice: the rows' own table entries, the step among them."""
+    groups = [(2, None), (4, 5), (1, 3), (9, 2), (1, None)]
+    own = np.arange(17) * 13 % 150 + 1
+    own[4] = 0
+    for hq, hkv, d in ((14, 2, 64), (16, 4, 128)):
+        b = Batch(33, groups, own, hq, hkv, d)
+        b.check(sinks=np.linspace(-1, 1, hq), kernel=kernel)
+        k_new, v_new = (torch.randn(17, hkv, d, generator=b.gen).bfloat16() for _ in range(2))
+        for r, n in enumerate(b.positions):
+            if n >= 0:
+                page = b.table[r, n // 64]
+                b.k[page, :, n % 64], b.v[page, :, n % 64] = k_new[r], v_new[r]
+        out = b.call(k_new.to(DEV), v_new.to(DEV), kernel=kernel)
+        assert pgd.get_device_error() == pgd.OK
+        b.compare(out, d ** -0.5)
+        assert torch.equal(b.k_pool.view(torch.int16), b.lay(b.k).view(torch.int16))
+    # the groups are not looked at
+    b.starts, b.shared = [9, 3], [1000]
+    b.check(kernel=kernel)
+
+
+def test_auto_goes_by_the_tables_pages():
+    """The same rows in a table of 128 MB of pages and in one a page wider."""
+    rows, hkv, d = 32, 8, 64
+    width = (128 << 20) // (rows * hkv * 64 * d * 4)
+    for more in (0, 1):
+        b = Batch(34, [(rows, 3)], np.arange(1, rows + 1) * 7, 16, hkv, d, width=width + more)
+        auto, umma, single = (b.call(kernel=k) for k in (pgd.KERNEL_AUTO, pgd.KERNEL_PREFILL_UMMA,
+                                                        pgd.KERNEL_TENSOR_CORE))
+        assert torch.equal(auto, umma if more else single)
+        b.compare(auto, d ** -0.5)

@@ -148,7 +148,7 @@ def test_compact_pages_workspace(ext):
 
 # ----------------------------------------------------------------- shared_decode
 
-def shared(ext, groups=1, scale=0.125, workspace_bytes=None, by=0, **kw):
+def shared(ext, groups=1, scale=0.125, workspace_bytes=None, kernel=0, **kw):
     buf = ctypes.create_string_buffer(1 << 14)
     at = (ctypes.addressof(buf) + 15) & ~15
     names = ("q", "k_pool", "v_pool", "out", "starts", "pages", "table", "positions", "workspace")
@@ -163,10 +163,13 @@ def shared(ext, groups=1, scale=0.125, workspace_bytes=None, by=0, **kw):
     return ext.pgdx_shared_decode(
         ctypes.byref(d), groups, ptr["starts"], ptr["pages"], ptr["q"], ptr["k_new"], ptr["v_new"],
         ptr["k_pool"], ptr["v_pool"], ptr["table"], ptr["positions"], None, scale, ptr["out"],
-        ptr["workspace"], need if workspace_bytes is None else workspace_bytes, None)
+        ptr["workspace"], need if workspace_bytes is None else workspace_bytes,
+        ctypes.byref(pgd.DecodeOptions(0, kernel)), None)
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(kernel=6), 1), (dict(kernel=-1), 1), (dict(kernel=pgd.KERNEL_CUDA_CORE), 2),
+    (dict(kernel=pgd.KERNEL_PREFILL_PAIR), 2),
     (dict(groups=-1), 1), (dict(groups=8193), 2), (dict(rows=65536), 2), (dict(rows=-1), 1),
     (dict(layout=pgd.ROW_MAJOR, num_pages=6), 2), (dict(head_dim=32), 2),
     (dict(num_q_heads=18), 2), (dict(num_q_heads=3), 1), (dict(scale=float("nan")), 1),
