@@ -116,18 +116,18 @@ __device__ __forceinline__ void each_table_entry(const int32_t* table, int rows,
 
 // ------------------------------------------------------------------ fork_rows
 
-// Seven steps over rows and entries, each of which needs the counts that all of the one
-// before left:
-//   1  a parent of c >= 2 children: its pages' shares grow by c - 1
-//   2  entries that no child takes over: their pages' shares fall by one, so
-//      a page that nobody holds any more is left at -1
-//   3  the first such entry (row-major) claims the page: min of -2^31 + entry
-//   4  claims counted by row; meanwhile each row whose last page is in part use
+// Six steps over rows and entries, each of which needs what all of the one before left:
+//   1  the pages' shares: c - 1 more for the entries of a parent of c children, one
+//      less for each that a child cuts off, so a page that nobody holds any more is
+//      left at -1
+//   2  the first entry of such a page that no child takes (row-major) claims it: min
+//      of -2^31 + entry
+//   3  claims counted by row; meanwhile each row whose last page is in part use
 //      leaves that page (one share less)
-//   5  the claimed pages go to the list; a last page that all its holders left
+//   4  the claimed pages go to the list; a last page that all its holders left
 //      (-1) is claimed by the lowest of them, which keeps it
-//   6  the other rows take pages off the list, in row order
-//   7  the rows are moved, a slab of columns at a time through shared memory
+//   5  the other rows take pages off the list, in row order
+//   6  the rows are moved, a slab of columns at a time through shared memory
 //      (a row may be its neighbour's parent and child at once)
 // Shares in between stay above -2^30 (a row's claims and its leaving its last
 // page count one each); claims of entries are below that, claims of last pages
@@ -216,29 +216,23 @@ struct Fork {
   __device__ int head() const { return p.free_head ? *p.free_head : 0; }
   __device__ bool bad_head() const { return head() < 0 || head() > p.num_free; }
 
-  __device__ void grow() const {
-    each_entry([&](int r) { return rows.children(r) < 2 ? rows.old_pages(r) : 0; },
-               [&](int r, int, int page) {
-                 if (in_pool(page))
-                   atomicAdd(&p.shares[page], rows.children(r) - 1);
-                 else
-                   report();
-               });
-  }
-  __device__ void give_back() const {
-    auto one = [&](int, int, int page) {
+  // shares as if every entry that no child takes were given up (a row's children, all
+  // told, hold its pages once each; the sums need no order)
+  __device__ void adjust() const {
+    auto add = [&](int page, int n) {
       if (in_pool(page))
-        atomicSub(&p.shares[page], 1);
+        atomicAdd(&p.shares[page], n);
       else
         report();
     };
-    each_entry([&](int r) { return rows.children(r) > 0 ? rows.old_pages(r) : 0; }, one);
+    each_entry([&](int r) { return rows.children(r) == 1 ? rows.old_pages(r) : 0; },
+               [&](int r, int, int page) { add(page, rows.children(r) - 1); });
     if (p.keep)  // rows that their parents' entries are cut for
       for (int r = warp(); r < p.rows; r += warps()) {
         const int q = rows.parent(r);
         if (q < 0) continue;
         for (int e = pages(r) + (threadIdx.x & 31); e < rows.old_pages(q); e += 32)
-          one(q, e, p.table[(size_t)q * p.width + e]);
+          add(p.table[(size_t)q * p.width + e], -1);
       }
   }
   __device__ void claim() const {
@@ -399,9 +393,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
   pdl_allow_dependents();
   if (fork.thread() == 0 && fork.bad_head()) fork.report();
   fork_count_children(p, rows, cells, fork.cta == 0);
-  fork.grow();
-  cluster.sync();
-  fork.give_back();
+  fork.adjust();
   cluster.sync();
   fork.claim();
   cluster.sync();
@@ -455,7 +447,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
 }
 
 // The steps as launches of their own.
-enum ForkStep { kForkGrow, kForkGiveBack, kForkClaims, kForkCount, kForkList, kForkLast, kForkMove };
+enum ForkStep { kForkAdjust, kForkClaims, kForkCount, kForkList, kForkLast, kForkMove };
 
 template <int STEP>
 __global__ void __launch_bounds__(kForkThreads) fork_step_kernel(ForkParams p) {
@@ -466,7 +458,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_step_kernel(ForkParams p) {
   const Fork<ForkInputs> fork{p, inputs, (int)blockIdx.x, (int)gridDim.x};
   pdl_wait();
   pdl_allow_dependents();
-  if constexpr (STEP == kForkGrow) {
+  if constexpr (STEP == kForkAdjust) {
     // every CTA counts the children; the first leaves them for the other steps
     const ForkRows rows = fork_rows_at(smem, R);
     fork_count_children(p, rows, smem + 5 * R, fork.cta == 0);
@@ -479,9 +471,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_step_kernel(ForkParams p) {
       }
     }
     const Fork<ForkRows> all{p, rows, fork.cta, fork.ctas};
-    all.grow();
-  } else if constexpr (STEP == kForkGiveBack) {
-    fork.give_back();
+    all.adjust();
   } else if constexpr (STEP == kForkClaims) {
     fork.claim();
   } else if constexpr (STEP == kForkCount) {
@@ -588,8 +578,7 @@ cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_
     while (ctas < 8 && entries > 2048ll * ctas) ctas *= 2;
     return launch_cluster(fork_rows_kernel, ctas, slab(ctas, 5), stream, p);
   }
-  cudaError_t e = launch_fork_step<kForkGrow>(p, sm_count, 24 * (size_t)p.rows, stream);
-  if (e == cudaSuccess) e = launch_fork_step<kForkGiveBack>(p, sm_count, 0, stream);
+  cudaError_t e = launch_fork_step<kForkAdjust>(p, sm_count, 24 * (size_t)p.rows, stream);
   if (e == cudaSuccess) e = launch_fork_step<kForkClaims>(p, sm_count, 0, stream);
   if (e == cudaSuccess) e = launch_fork_step<kForkCount>(p, sm_count, 0, stream);
   if (e == cudaSuccess) e = launch_fork_step<kForkList>(p, sm_count, 0, stream);
