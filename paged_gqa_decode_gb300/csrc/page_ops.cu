@@ -70,6 +70,61 @@ cudaError_t launch_cluster(void (*kernel)(Params), int ctas, size_t smem, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// One CTA of 1024 threads for every SM, all resident at once (they meet).
+template <class Params>
+cudaError_t launch_grid(void (*kernel)(Params), int ctas, size_t smem, cudaStream_t stream,
+                        const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Where the CTAs of such a launch meet: a count of arrivals, zero before the launch.
+struct GridBarrier {
+  unsigned int* count;
+  unsigned int* err;
+  unsigned int ctas, arrivals = 0;
+
+  __device__ void arrive() {
+    __syncthreads();
+    arrivals += ctas;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicAdd(count, 1u);
+    }
+  }
+  // Until all have arrived as often as this CTA; false after the limit of every wait.
+  __device__ bool wait() const {
+    bool late = false;
+    if (threadIdx.x == 0) {
+      const unsigned long long t0 = global_ns();
+      for (unsigned int it = 1;; ++it) {
+        unsigned int n;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(count) : "memory");
+        if (n >= arrivals) break;
+        if ((it & 63u) == 0u && global_ns() - t0 > kWaitLimitNs) {
+          record_error(err, PGD_EDEVICE_TIMEOUT);
+          late = true;
+          break;
+        }
+      }
+    }
+    return !__syncthreads_or(late);
+  }
+  __device__ bool meet() {
+    arrive();
+    return wait();
+  }
+};
+
 // f(r, e, entry) for the entries lo(r) .. hi(r) - 1 of a table's rows r, shared out
 // over `warps` warps of which this is number `warp`, N rows at a time (rows N w ..
 // N w + N - 1 of every round are warp w's) and 256 / N entries of each, so that a thread
@@ -446,116 +501,104 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
       [&](int r) { return rows.aux[r]; });
 }
 
-// The steps as launches of their own.
-enum ForkStep { kForkAdjust, kForkClaims, kForkCount, kForkList, kForkLast, kForkMove };
+// Larger tables: the first step, which leaves the children and least pages (and zeros for
+// claims and for the count of the barriers that follow) in the outputs,
+__global__ void __launch_bounds__(kForkThreads) fork_adjust_kernel(ForkParams p) {
+  extern __shared__ int smem[];
+  const int R = p.rows, tid = threadIdx.x;
+  const ForkRows rows = fork_rows_at(smem, R);
+  const Fork<ForkRows> fork{p, rows, (int)blockIdx.x, (int)gridDim.x};
+  pdl_wait();
+  pdl_allow_dependents();
+  fork_count_children(p, rows, smem + 5 * R, fork.cta == 0);
+  if (fork.cta == 0) {
+    if (tid == 0) {
+      if (fork.bad_head()) fork.report();
+      *p.free_head_out = 0;
+    }
+    for (int r = tid; r < R; r += kForkThreads) {
+      p.counts[r] = rows.children_[r];
+      p.new_lengths[r] = rows.least_[r];
+      p.sources[r] = 0;
+    }
+  }
+  fork.adjust();
+}
 
-template <int STEP>
-__global__ void __launch_bounds__(kForkThreads) fork_step_kernel(ForkParams p) {
+// and the others, on all SMs.  A thread sees to a row's last page (there is one for each).
+__global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p) {
   extern __shared__ int smem[];
   __shared__ int warps[33];
   const int R = p.rows, tid = threadIdx.x;
   const ForkInputs inputs{p};
   const Fork<ForkInputs> fork{p, inputs, (int)blockIdx.x, (int)gridDim.x};
-  pdl_wait();
-  pdl_allow_dependents();
-  if constexpr (STEP == kForkAdjust) {
-    // every CTA counts the children; the first leaves them for the other steps
-    const ForkRows rows = fork_rows_at(smem, R);
-    fork_count_children(p, rows, smem + 5 * R, fork.cta == 0);
-    if (fork.cta == 0) {
-      if (tid == 0 && fork.bad_head()) fork.report();
-      for (int r = tid; r < R; r += kForkThreads) {
-        p.counts[r] = rows.children_[r];
-        p.new_lengths[r] = rows.least_[r];
-        p.sources[r] = 0;
-      }
-    }
-    const Fork<ForkRows> all{p, rows, fork.cta, fork.ctas};
-    all.adjust();
-  } else if constexpr (STEP == kForkClaims) {
-    fork.claim();
-  } else if constexpr (STEP == kForkCount) {
-    fork.count(p.sources);
-    fork.leave_tails();
-  } else if constexpr (STEP == kForkList) {
-    // a run of rows a CTA: the claims before it, and in all
-    const int lo = (int)((int64_t)R * fork.cta / fork.ctas);
-    const int hi = (int)((int64_t)R * (fork.cta + 1) / fork.ctas);
-    int before = 0, freed = 0;
+  GridBarrier all{reinterpret_cast<unsigned int*>(p.free_head_out), p.err, gridDim.x};
+  const int mine = fork.thread() < R ? fork.thread() : -1;
+  const int tail = mine >= 0 ? fork.tail_page(mine) : -1;
+  fork.claim();
+  if (!all.meet()) return;
+  fork.count(p.sources);
+  if (fork.in_pool(tail)) atomicSub(&p.shares[tail], 1);
+  if (!all.meet()) return;
+  // a run of rows a CTA: the claims before it, and in all
+  const int lo = (int)((int64_t)R * fork.cta / fork.ctas);
+  const int hi = (int)((int64_t)R * (fork.cta + 1) / fork.ctas);
+  int before = 0, freed = 0;
 #pragma unroll 4
-    for (int r = tid; r < R; r += kForkThreads) {
-      const int n = p.sources[r];
-      freed += n;
-      if (r < lo) before += n;
-    }
-    int total;
-    block_scan(before, warps, total);
-    before = total;
-    __syncthreads();
-    block_scan(freed, warps, total);
-    freed = total;
-    if (fork.thread() == 0) {
-      p.targets[0] = freed;  // (for the next step; the last one's are written there)
-      if (!fork.bad_head() && fork.head() < freed) fork.report();
-    }
-    for (int r = lo + (tid >> 5); r < hi; r += kForkThreads / 32) {
-      const int n = p.sources[r];
-      if (n == 0) continue;
-      int at = before;
-      for (int k = lo + (tid & 31); k < r; k += 32) at += p.sources[k];
-      at = before + __reduce_add_sync(0xffffffffu, at - before);
-      fork.list(r, at, n, freed);
-    }
-    fork.claim_tails();
-  } else if constexpr (STEP == kForkLast) {  // (one CTA)
-    const int head1 = fork.listed_head(p.targets[0]);
-    int* to = smem;
-    int* page = smem + R;
-    int* kept = smem + 2 * R;
-#pragma unroll 4
-    for (int r = tid; r < R; r += kForkThreads) {
-      kept[r] = inputs.kept(r);
-      page[r] = fork.tail_page(r);
-      to[r] = fork.last(r, page[r]);
-    }
-    __syncthreads();
-    int copies = 0;
-    for (int r0 = 0; r0 < R; r0 += kForkThreads) {
-      const int r = r0 + tid;
-      const bool copy = r < R && to[r] == 1;
-      int total;
-      const int at = copies + block_scan(copy, warps, total);
-      copies += total;
-      if (copy) to[r] = fork.copy_page(at, head1);
-      if (r < R && to[r] == -2) fork.report();
-      if (r < R) fork.write(r, to[r], page[r], kept[r]);
-      __syncthreads();
-    }
-    if (tid == 0) *p.free_head_out = fork.bad_head() ? head1 : min(head1 + copies, p.num_free);
-  } else {
-    int* parent = smem;
-    int* pages = smem + R;
-    int* to = smem + 2 * R;
-#pragma unroll 4
-    for (int r = tid; r < R; r += kForkThreads) {
-      const int kept = inputs.kept(r), target = p.targets[r], length = p.new_lengths[r];
-      parent[r] = inputs.parent(r);
-      pages[r] = (kept + kPage - 1) / kPage;
-      to[r] = target >= 0 ? target : length == kept ? -1 : -2;
-    }
-    __syncthreads();
-    fork.move(
-        smem + 3 * R, [&](int r) { return parent[r]; }, [&](int r) { return pages[r]; },
-        [&](int r) { return to[r]; });
+  for (int r = tid; r < R; r += kForkThreads) {
+    const int n = p.sources[r];
+    freed += n;
+    if (r < lo) before += n;
   }
-}
-
-template <int STEP>
-cudaError_t launch_fork_step(const ForkParams& p, int ctas, size_t smem, cudaStream_t stream) {
-  static std::atomic<bool> configured[64];
-  const cudaError_t e = allow_smem(fork_step_kernel<STEP>, 220 * 1024, configured);
-  return e != cudaSuccess ? e : launch_pdl(fork_step_kernel<STEP>, dim3(ctas), dim3(kForkThreads),
-                                           smem, stream, p);
+  int total;
+  block_scan(before, warps, total);
+  before = total;
+  __syncthreads();
+  block_scan(freed, warps, total);
+  freed = total;
+  if (fork.thread() == 0 && !fork.bad_head() && fork.head() < freed) fork.report();
+  for (int r = lo + (tid >> 5); r < hi; r += kForkThreads / 32) {
+    const int n = p.sources[r];
+    if (n == 0) continue;
+    int at = 0;
+    for (int k = lo + (tid & 31); k < r; k += 32) at += p.sources[k];
+    fork.list(r, before + __reduce_add_sync(0xffffffffu, at), n, freed);
+  }
+  if (fork.in_pool(tail) && __ldcg(&p.shares[tail]) < 0)
+    atomicMin(&p.shares[tail], kForkTail + mine);
+  if (!all.meet()) return;
+  if (mine >= 0) {  // for all CTAs' sums
+    p.targets[mine] = fork.last(mine, tail);
+    p.counts[mine] = tail;
+  }
+  if (!all.meet()) return;
+  const int head1 = fork.listed_head(freed);
+  int* parent = smem;
+  int* pages = smem + R;
+  int* to = smem + 2 * R;
+  int copies = 0;
+  for (int r0 = 0; r0 < R; r0 += kForkThreads) {
+    const int r = r0 + tid;
+    int last = r < R ? p.targets[r] : -1;
+    const int at = copies + block_scan(last == 1, warps, total);
+    copies += total;
+    if (last == 1) last = fork.copy_page(at, head1);
+    if (last == -2 && fork.cta == 0) fork.report();
+    if (r < R) {
+      parent[r] = inputs.parent(r);
+      pages[r] = fork.pages(r);
+      to[r] = last;
+    }
+    __syncthreads();
+  }
+  all.arrive();
+  fork.move(
+      smem + 3 * R, [&](int r) { return parent[r]; }, [&](int r) { return pages[r]; },
+      [&](int r) { return to[r]; });
+  // the outputs, once nobody needs what they held so far
+  if (fork.cta != 0 || !all.wait()) return;
+  for (int r = tid; r < R; r += kForkThreads) fork.write(r, to[r], p.counts[r], inputs.kept(r));
+  if (tid == 0) *p.free_head_out = fork.bad_head() ? head1 : min(head1 + copies, p.num_free);
 }
 
 cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_t stream) {
@@ -578,14 +621,15 @@ cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_
     while (ctas < 8 && entries > 2048ll * ctas) ctas *= 2;
     return launch_cluster(fork_rows_kernel, ctas, slab(ctas, 5), stream, p);
   }
-  cudaError_t e = launch_fork_step<kForkAdjust>(p, sm_count, 24 * (size_t)p.rows, stream);
-  if (e == cudaSuccess) e = launch_fork_step<kForkClaims>(p, sm_count, 0, stream);
-  if (e == cudaSuccess) e = launch_fork_step<kForkCount>(p, sm_count, 0, stream);
-  if (e == cudaSuccess) e = launch_fork_step<kForkList>(p, sm_count, 0, stream);
-  if (e == cudaSuccess) e = launch_fork_step<kForkLast>(p, 1, 12 * (size_t)p.rows, stream);
+  static std::atomic<bool> configured[2][64];
+  cudaError_t e = allow_smem(fork_adjust_kernel, limit, configured[0]);
+  if (e == cudaSuccess) e = allow_smem(fork_grid_kernel, limit, configured[1]);
+  if (e == cudaSuccess)
+    e = launch_pdl(fork_adjust_kernel, dim3(sm_count), dim3(kForkThreads), 24 * (size_t)p.rows,
+                   stream, p);
   if (e != cudaSuccess) return e;
   const size_t smem = slab(sm_count, 3);
-  return launch_fork_step<kForkMove>(p, sm_count, smem, stream);
+  return launch_grid(fork_grid_kernel, sm_count, smem, stream, p);
 }
 
 // ------------------------------------------------------------------ copy_pages
@@ -657,30 +701,35 @@ cudaError_t launch_copy_pages(const CopyParams& p, int head_dim, int sm_count,
 //   past the first `held` places of the free and held pages together.
 //   free list: free pages left and vacated ones, each at its rank.
 // Bound by latency and the rate of scattered accesses in L2, as fork_rows: one cluster
-// for small pools and tables, its steps between cluster barriers; else a launch a step
-// over all SMs, where every CTA sums the bits for itself (250 007 pages, 514 000
-// entries: 82 -> 30 us).
+// for small pools and tables, all SMs past that (250 007 pages, 514 000 entries: 82 us in
+// the cluster).
 constexpr int kCompactThreads = 1024;
 constexpr int64_t kCompactClusterWork = 100000;  // entries and pages
-enum CompactStep { kCompactAll = -1, kCompactClear, kCompactMark, kCompactMoves, kCompactApply };
 
-// The bitmaps' sums, and what they come to; in the workspace after the flag.
+// What the bitmaps' sums come to.
 struct CompactSums {
-  int held_total, moves, wrong, pad;
+  int held_total, moves;
+  bool wrong;
 };
 
-template <int STEP>
-__global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactParams p) {
-  constexpr bool kAll = STEP == kCompactAll;
+// Before the larger: bitmaps, flag and the count of the barriers.
+__global__ void __launch_bounds__(kCompactThreads) compact_clear_kernel(CompactParams p) {
+  pdl_wait();
+  pdl_allow_dependents();
+  const int words = (p.num_pages + 31) / 32;
+  for (int w = blockIdx.x * kCompactThreads + threadIdx.x; w < 2 * words + 2;
+       w += gridDim.x * kCompactThreads)
+    p.bits[w] = 0;
+}
+
+template <bool GRID>
+__global__ void __launch_bounds__(kCompactThreads, 1) compact_pages_kernel(CompactParams p) {
   extern __shared__ int smem[];
   __shared__ int warps[33];
   __shared__ int unlimited;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = kAll ? (int)cluster.num_blocks() : (int)gridDim.x;
-  const int cta = kAll ? (int)cluster.block_rank() : (int)blockIdx.x;
-  auto step_done = [&]() {
-    if constexpr (kAll) cluster.sync();
-  };
+  const int ctas = GRID ? (int)gridDim.x : (int)cluster.num_blocks();
+  const int cta = GRID ? (int)blockIdx.x : (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gwarp = warp * ctas + cta, gwarps = ctas * (kCompactThreads / 32);
   const int gtid = cta * kCompactThreads + tid, gthreads = ctas * kCompactThreads;
@@ -688,11 +737,14 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
   uint32_t* free_bits = p.bits;
   uint32_t* held_bits = p.bits + words;
   uint32_t* bad = p.bits + 2 * words;
-  CompactSums* sums = reinterpret_cast<CompactSums*>(bad + 1);
-  int* free_sums = reinterpret_cast<int*>(sums + 1);  // [blocks] pages before the block's words
-  int* held_sums = free_sums + blocks;
-  int* free_at = STEP == kCompactApply ? free_sums : smem;
-  int* held_at = STEP == kCompactApply ? held_sums : smem + blocks;
+  GridBarrier all{bad + 1, p.err, gridDim.x};
+  auto step_done = [&]() {
+    if constexpr (GRID) return all.meet();
+    cluster.sync();
+    return true;
+  };
+  int* free_at = smem;  // [blocks] pages before the block's words
+  int* held_at = smem + blocks;
   pdl_wait();
   pdl_allow_dependents();
   const int head = p.free_head ? *p.free_head : 0;
@@ -710,11 +762,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
     for (int k = b * p.step; k < w; ++k) n += __popc(bits[k]);
     return n;
   };
-  if constexpr (kAll || STEP == kCompactClear) {
+  if constexpr (!GRID) {
     for (int w = gtid; w < 2 * words + 1; w += gthreads) p.bits[w] = 0;
     step_done();
   }
-  if constexpr (kAll || STEP == kCompactMark) {
+  {
     if (bad_head && gtid == 0) atomicOr(bad, 1u);
 #pragma unroll 4
     for (int k = (bad_head ? p.num_free : head) + gtid; k < p.num_free; k += gthreads) {
@@ -737,11 +789,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
           else
             atomicOr(bad, 1u);
         });
-    step_done();
+    if (!step_done()) return;
   }
 
   CompactSums sum;
-  if constexpr (kAll || STEP == kCompactMoves) {
+  {
     // prefixes: thread t sums a run of blocks
     const int run = (blocks + kCompactThreads - 1) / kCompactThreads;
     const int b0 = min(tid * run, blocks), b1 = min(b0 + run, blocks);
@@ -765,10 +817,6 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
     for (int b = b0; b < b1; ++b) {
       free_at[b] = f;
       held_at[b] = h;
-      if (!kAll && cta == 0) {
-        free_sums[b] = f;
-        held_sums[b] = h;
-      }
 #pragma unroll 4
       for (int w = b * p.step; w < min((b + 1) * p.step, words); ++w) {
         const uint32_t fw = free_bits[w], hw = held_bits[w], all = fw | hw;
@@ -789,7 +837,6 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
     __syncthreads();
     sum.moves = sum.wrong ? 0 : min(unlimited, p.max_moves);
     if (sum.wrong && gtid == 0) record_error(p.err, PGD_EDEVICE_BOUNDS);
-    if (!kAll && gtid == 0) *sums = sum;
     // the moves: sources from the top, targets from the bottom
     const int moves = sum.moves;
     for (int w = tid * ctas + cta; moves > 0 && w < words; w += gthreads) {
@@ -801,13 +848,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
         if (--k < moves) p.sources[k] = 32 * w + __ffs(m) - 1;
     }
     for (int k = moves + gtid; k < p.max_moves; k += gthreads) p.sources[k] = p.targets[k] = -1;
-    step_done();
+    if (!step_done()) return;
   }
 
-  if constexpr (kAll || STEP == kCompactApply) {
-    if constexpr (!kAll) sum = *sums;
+  {
     const int moves = sum.moves, kept = sum.held_total - moves;  // held pages of a lower rank stay
-    const bool wrong = sum.wrong != 0;
+    const bool wrong = sum.wrong;
     // the held pages from `lowest` up have moved, to the free ones up to `highest`
     const int lowest = moves > 0 ? __ldcg(&p.sources[moves - 1]) : INT32_MAX;
     const int highest = moves > 0 ? __ldcg(&p.targets[moves - 1]) : -1;
@@ -870,23 +916,9 @@ __global__ void __launch_bounds__(kCompactThreads) compact_pages_kernel(CompactP
   }
 }
 
-template <int STEP>
-cudaError_t launch_compact_step(const CompactParams& p, int ctas, size_t smem,
-                                cudaStream_t stream) {
-  static std::atomic<bool> configured[64];
-  const cudaError_t e = allow_smem(compact_pages_kernel<STEP>, 200 * 1024, configured);
-  if (e != cudaSuccess) return e;
-  if constexpr (STEP == kCompactAll)
-    return launch_cluster(compact_pages_kernel<STEP>, ctas, smem, stream, p);
-  else
-    return launch_pdl(compact_pages_kernel<STEP>, dim3(ctas), dim3(kCompactThreads), smem, stream,
-                      p);
-}
-
 size_t compact_workspace_bytes(int num_pages) {
   const size_t words = ((size_t)num_pages + 31) / 32;
-  // bitmaps and flag, sums, prefixes
-  return (2 * words + 1 + 4 + 2 * (words < kMaxCompactPrefixes ? words : kMaxCompactPrefixes)) * 4;
+  return (2 * words + 2) * 4;  // bitmaps, flag, count of the barriers
 }
 
 cudaError_t launch_compact_pages(const CompactParams& params, int sm_count, cudaStream_t stream) {
@@ -896,16 +928,18 @@ cudaError_t launch_compact_pages(const CompactParams& params, int sm_count, cuda
   while ((words + p.step - 1) / p.step > kMaxCompactPrefixes) p.step *= 2;
   const size_t smem = (size_t)((words + p.step - 1) / p.step) * 8;
   const int64_t work = (int64_t)p.rows * p.width + p.num_pages;
+  static std::atomic<bool> configured[2][64];
   if (work <= kCompactClusterWork) {
+    const cudaError_t e = allow_smem(compact_pages_kernel<false>, 200 * 1024, configured[0]);
+    if (e != cudaSuccess) return e;
     int ctas = 1;
     while (ctas < 8 && work > 2048ll * ctas) ctas *= 2;
-    return launch_compact_step<kCompactAll>(p, ctas, smem, stream);
+    return launch_cluster(compact_pages_kernel<false>, ctas, smem, stream, p);
   }
-  cudaError_t e = launch_compact_step<kCompactClear>(p, 32, 0, stream);
-  if (e == cudaSuccess) e = launch_compact_step<kCompactMark>(p, sm_count, 0, stream);
-  if (e == cudaSuccess) e = launch_compact_step<kCompactMoves>(p, sm_count, smem, stream);
-  if (e != cudaSuccess) return e;
-  return launch_compact_step<kCompactApply>(p, sm_count, 0, stream);
+  cudaError_t e = allow_smem(compact_pages_kernel<true>, 200 * 1024, configured[1]);
+  if (e == cudaSuccess)
+    e = launch_pdl(compact_clear_kernel, dim3(32), dim3(kCompactThreads), 0, stream, p);
+  return e == cudaSuccess ? launch_grid(compact_pages_kernel<true>, sm_count, smem, stream, p) : e;
 }
 
 }  // namespace pgd
