@@ -312,23 +312,28 @@ struct Fork {
       if (in_pool(page)) atomicSub(&p.shares[page], 1);
     }
   }
-  // row r's `n` claimed pages, the `at`-th of `freed` on, to the list (a warp)
+  // row r's `n` claimed pages, the `at`-th of `freed` on, to the list (a warp; four
+  // entries a lane at once: one at a time, rows of 126 entries took 5 us)
   __device__ void list(int r, int at, int n, int freed) const {
     const int lane = threadIdx.x & 31, hi = rows.old_pages(r), end = at + n;
-    for (int e0 = lost_from(r); at < end && e0 < hi; e0 += 32) {
-      int page = -1;
-      bool mine = false;
-      if (e0 + lane < hi) {
-        page = p.table[(size_t)r * p.width + e0 + lane];
-        mine = claimed(page, r, e0 + lane);
+    const int32_t* row = p.table + (size_t)r * p.width;
+    for (int e0 = lost_from(r) + lane; at < end && e0 - lane < hi; e0 += 128) {
+      int page[4];
+      bool mine[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) page[k] = e0 + 32 * k < hi ? row[e0 + 32 * k] : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine[k] = claimed(page[k], r, e0 + 32 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned who = __ballot_sync(0xffffffffu, mine[k]);
+        if (mine[k]) {
+          const int to = head() - freed + at + __popc(who & ((1u << lane) - 1u));
+          if (!bad_head() && to >= 0) p.free_pages[to] = page[k];
+          p.shares[page[k]] = 0;
+        }
+        at += __popc(who);
       }
-      const unsigned who = __ballot_sync(0xffffffffu, mine);
-      if (mine) {
-        const int to = head() - freed + at + __popc(who & ((1u << lane) - 1u));
-        if (!bad_head() && to >= 0) p.free_pages[to] = page;
-        p.shares[page] = 0;
-      }
-      at += __popc(who);
     }
   }
   __device__ void claim_tails() const {
@@ -528,8 +533,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_adjust_kernel(ForkParams p)
 // and the others, on all SMs.  A thread sees to a row's last page (there is one for each).
 __global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p) {
   extern __shared__ int smem[];
-  __shared__ int warps[33];
-  const int R = p.rows, tid = threadIdx.x;
+  __shared__ int sums[2][kForkThreads / 32];
+  const int R = p.rows, tid = threadIdx.x, lane = tid & 31;
   const ForkInputs inputs{p};
   const Fork<ForkInputs> fork{p, inputs, (int)blockIdx.x, (int)gridDim.x};
   GridBarrier all{reinterpret_cast<unsigned int*>(p.free_head_out), p.err, gridDim.x};
@@ -550,12 +555,15 @@ __global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p
     freed += n;
     if (r < lo) before += n;
   }
-  int total;
-  block_scan(before, warps, total);
-  before = total;
+  before = __reduce_add_sync(0xffffffffu, before);
+  freed = __reduce_add_sync(0xffffffffu, freed);
+  if (lane == 0) {
+    sums[0][tid >> 5] = before;
+    sums[1][tid >> 5] = freed;
+  }
   __syncthreads();
-  block_scan(freed, warps, total);
-  freed = total;
+  before = __reduce_add_sync(0xffffffffu, sums[0][lane]);
+  freed = __reduce_add_sync(0xffffffffu, sums[1][lane]);
   if (fork.thread() == 0 && !fork.bad_head() && fork.head() < freed) fork.report();
   for (int r = lo + (tid >> 5); r < hi; r += kForkThreads / 32) {
     const int n = p.sources[r];
@@ -574,30 +582,43 @@ __global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p
   if (!all.meet()) return;
   const int head1 = fork.listed_head(freed);
   int* parent = smem;
-  int* pages = smem + R;
+  int* kept = smem + R;
   int* to = smem + 2 * R;
-  int copies = 0;
-  for (int r0 = 0; r0 < R; r0 += kForkThreads) {
-    const int r = r0 + tid;
-    int last = r < R ? p.targets[r] : -1;
-    const int at = copies + block_scan(last == 1, warps, total);
-    copies += total;
-    if (last == 1) last = fork.copy_page(at, head1);
-    if (last == -2 && fork.cta == 0) fork.report();
-    if (r < R) {
+  // copies before a row: a run of rows a warp, one of every 32 a lane
+  constexpr int kRun = kMaxForkRows / kForkThreads;
+  const int run = (R + kForkThreads - 1) / kForkThreads, r0 = (tid >> 5) * 32 * run + lane;
+  int last[kRun], before_run = 0;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k)
+    last[k] = k < run && r0 + 32 * k < R ? p.targets[r0 + 32 * k] : -1;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) before_run += __popc(__ballot_sync(0xffffffffu, last[k] == 1));
+  if (lane == 0) sums[0][tid >> 5] = before_run;
+  __syncthreads();
+  const int in_run = sums[0][lane];
+  const int copies = __reduce_add_sync(0xffffffffu, in_run);
+  int at = __reduce_add_sync(0xffffffffu, lane < tid >> 5 ? in_run : 0);
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int r = r0 + 32 * k;
+    const unsigned who = __ballot_sync(0xffffffffu, last[k] == 1);
+    if (last[k] == 1) last[k] = fork.copy_page(at + __popc(who & ((1u << lane) - 1u)), head1);
+    at += __popc(who);
+    if (last[k] == -2 && fork.cta == 0) fork.report();
+    if (k < run && r < R) {
       parent[r] = inputs.parent(r);
-      pages[r] = fork.pages(r);
-      to[r] = last;
+      kept[r] = inputs.kept(r);
+      to[r] = last[k];
     }
-    __syncthreads();
   }
   all.arrive();
   fork.move(
-      smem + 3 * R, [&](int r) { return parent[r]; }, [&](int r) { return pages[r]; },
-      [&](int r) { return to[r]; });
+      smem + 3 * R, [&](int r) { return parent[r]; },
+      [&](int r) { return (kept[r] + kPage - 1) / kPage; }, [&](int r) { return to[r]; });
   // the outputs, once nobody needs what they held so far
   if (fork.cta != 0 || !all.wait()) return;
-  for (int r = tid; r < R; r += kForkThreads) fork.write(r, to[r], p.counts[r], inputs.kept(r));
+#pragma unroll 4
+  for (int r = tid; r < R; r += kForkThreads) fork.write(r, to[r], p.counts[r], kept[r]);
   if (tid == 0) *p.free_head_out = fork.bad_head() ? head1 : min(head1 + copies, p.num_free);
 }
 
