@@ -251,7 +251,7 @@ def test_compact_refusals():
 
 
 @pytest.mark.parametrize("moves", [0, 5, 30000, None])
-def test_compact_in_a_launch_a_step(moves):
+def test_compact_on_all_sms(moves):
     """More entries and pages than one cluster takes, then the same state gone wrong."""
     rng = np.random.default_rng(5)
     table, lengths, shares, free, head, pages = side.random_state(rng, 300, 4, 9000, 300,
@@ -263,3 +263,29 @@ def test_compact_in_a_launch_a_step(moves):
         twice = free.copy()
         twice[-1] = twice[-9]
         check_compact(table, lengths, shares, twice, head, pages, moves, True)
+
+
+def test_large_pools_on_two_streams_and_replayed():
+    rng = np.random.default_rng(6)
+    runs = []
+    for k in range(2):
+        table, lengths, shares, free, head, pages = side.random_state(rng, 200, 4, 9000, 300,
+                                                                      spare=20000)
+        assert table.size + pages > 100000
+        args = tuple(dev(a) for a in (table, lengths, shares, free))
+        h = dev([head])
+        want = check_compact(table, lengths, shares, free, head, pages, 4000)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            plan = pgd.compact_pages(*args, free_head=h, max_moves=4000)
+        runs.append((graph, stream, plan, want, args, h))
+    for _ in range(10):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, plan, want, _, _ in runs:
+        for a, b in zip(plan, want):
+            assert torch.equal(a, b)
+    assert pgd.get_device_error() == pgd.OK

@@ -269,7 +269,7 @@ def test_captured_and_replayed():
     assert pgd.get_device_error() == pgd.OK
 
 
-def test_many_entries_take_a_launch_a_step():
+def test_many_entries_take_all_sms():
     """Past the entries that one cluster takes; then with cuts, releases, too few pages and errors."""
     rng = np.random.default_rng(21)
     for requests, beams, hi, grown in ((40, 8, 9000, 300), (500, 8, 900, 200)):
@@ -293,3 +293,50 @@ def test_many_entries_take_a_launch_a_step():
     wrong[5] = -1
     parents[17], parents[33] = rows, -2
     check((holes, wrong, shares, free, head, pages), parents, status=pgd.EDEVICE_BOUNDS)
+
+
+def test_the_most_rows_of_a_large_table():
+    rng = np.random.default_rng(22)
+    state = side.random_state(rng, 1024, 8, 300, 40, width=9)
+    rows = 8192
+    assert state[0].shape == (rows, 9)
+    for step in range(2):
+        parents = np.arange(rows) // 8 * 8 + rng.integers(0, 8, rows)
+        keep = np.where(rng.random(rows) < 0.3, rng.integers(0, 300, rows), 2 ** 31 - 1)
+        state = check(state, parents, keep, status=pgd.OK)
+
+
+def test_large_tables_on_two_streams_and_replayed():
+    """Calls whose blocks meet, at once and out of a graph."""
+    rng = np.random.default_rng(23)
+    states = [side.random_state(rng, 60, 8, 5000, 300) for _ in range(2)]
+    rows = 480
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for state, stream in zip(states, streams):
+        table, lengths, shares, free, head, pages = state
+        assert table.size > 20000
+        parents = np.arange(rows) // 8 * 8 + rng.integers(0, 8, rows)
+        first = tuple(dev(a) for a in (table, shares, free))
+        work = tuple(a.clone() for a in first)
+        plan = pgd.ForkPlan(*(torch.empty(k, dtype=torch.int32, device=DEV)
+                              for k in (rows, rows, rows, rows, 1)))
+        args = dev(lengths), dev(parents), dev([head])
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            for to, a in zip(work, first):
+                to.copy_(a)
+            pgd.fork_rows(work[0], args[0], args[1], work[1], work[2], free_head=args[2], out=plan)
+        want, error = side.fork_rows(table, lengths, list(parents), None, shares, free, head, pages)
+        assert not error
+        runs.append((graph, stream, work, plan, want, first, args))
+    for _ in range(10):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, work, plan, want, _, _ in runs:
+        for got, w in zip(work + tuple(plan), want):
+            np.testing.assert_array_equal(got.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    assert pgd.get_device_error() == pgd.OK
