@@ -35,6 +35,7 @@ Entry points (same names as the C ABI, without the ``pgd_`` / ``pgdx_`` prefix):
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import math
@@ -1217,20 +1218,19 @@ def copy_pages(k_pools: torch.Tensor | list[torch.Tensor], v_pools: torch.Tensor
     layers = len(k_pools)
     if layers == 0:
         return
-    shape = k_pools[0].shape
-    for name, pools in (("k_pools", k_pools), ("v_pools", v_pools)):
-        for pool in pools:
-            if pool.dtype is not _BF16:
-                _dtype(pool, torch.bfloat16, name)
-            if pool.shape != shape:
-                raise ValueError("the pools must have one shape")
+    pools, shape = (*k_pools, *v_pools), k_pools[0].shape
+    for pool in pools:
+        if pool.dtype is not _BF16:
+            _dtype(pool, torch.bfloat16, "k_pools and v_pools")
+    if list(map(torch.Tensor.size, pools)).count(shape) != len(pools):
+        raise ValueError("the pools must have one shape")
     dims = _dims_of(sources.shape[0], num_kv_heads, num_kv_heads, head_dim,
                     _pool_pages(k_pools[0], num_kv_heads, head_dim), 1, layout)
-    at = ctypes.c_void_p * layers
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, pools))
+    at = ptrs.buffer_info()[0]
     rc = load_extension().pgdx_copy_pages(
-        ctypes.byref(dims), layers, at(*[t.data_ptr() for t in k_pools]),
-        at(*[t.data_ptr() for t in v_pools]), sources.shape[0], sources.data_ptr(),
-        targets.data_ptr(), _ptr(counts), _stream_handle(stream, dev))
+        ctypes.byref(dims), layers, at, at + layers * ptrs.itemsize, sources.shape[0],
+        sources.data_ptr(), targets.data_ptr(), _ptr(counts), _stream_handle(stream, dev))
     if rc != OK:
         raise PgdError(rc, "copy_pages")
 
