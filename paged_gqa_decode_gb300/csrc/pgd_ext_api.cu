@@ -69,7 +69,7 @@ SharedLayout shared_layout(const pgd_dims* d) {
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);
   l.off = (l.ml + parts * 2 * sizeof(float) + 15) / 16 * 16;
-  l.bytes = l.off + (size_t)d->rows * sizeof(SharedRecord) + sizeof(int64_t);
+  l.bytes = l.off + (size_t)d->rows * sizeof(SharedRecord) + kSharedCutBytes;
   return l;
 }
 
@@ -624,7 +624,7 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.part_acc = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + l.ml);
   p.records = reinterpret_cast<SharedRecord*>(ws + l.off);
-  p.units = reinterpret_cast<int64_t*>(ws + l.off + (size_t)dims->rows * sizeof(SharedRecord));
+  p.cut = reinterpret_cast<SharedCut*>(ws + l.off + (size_t)dims->rows * sizeof(SharedRecord));
   p.err = dev->err;
   p.rows = dims->rows;
   p.groups = groups;
@@ -645,6 +645,7 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   if ((rc = encode_q_map(&q_map, q, dims)) != PGD_OK) return rc;
   // (an even number: pairs)
   const int ctas = (dev->sm_count < kMaxSharedCtas ? dev->sm_count : kMaxSharedCtas) & ~1;
+  if (ctas < 4) return PGD_EUNSUPPORTED;  // two for the groups' pages, two for the rows'
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
       dims->head_dim == 64 ? launch_shared_d64(p, k_map, v_map, q_map, ctas, st)

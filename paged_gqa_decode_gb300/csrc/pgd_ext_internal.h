@@ -105,6 +105,9 @@ struct SharedRecord {
   int start, end, shared, n;
 };
 
+struct SharedCut;  // what falls to which CTA (shared_decode.cuh)
+constexpr int kSharedCutBytes = 32;
+
 struct SharedParams {
   const uint16_t* q;
   const int32_t* table;
@@ -116,7 +119,7 @@ struct SharedParams {
   float* part_acc;     // D values of each partial
   float* part_ml;      // (m, l) of each
   SharedRecord* records;  // [rows], for the combine, with
-  int64_t* units;                // the weight of a CTA's range
+  SharedCut* cut;
   unsigned int* err;
   int rows, groups, hq, hkv, group, maxp, num_pages, layout;
   float q_scale_log2;

@@ -146,15 +146,54 @@ __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, i
   return it;
 }
 
+// a / b of weights, a >= 0, b > 0 (64-bit division is a hundred instructions).
+__device__ __forceinline__ long long shared_divide(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// The ranges of the blocks' weights and of the rows': so many CTAs each, an even number
+// (a pair of CTAs is a TPC, whose SMs slow each other's pages where one reads shared
+// pages and the other rows' own: two tiles' page 1.1 -> 1.6 us), whichever even number
+// leaves the least to the most loaded one.
+struct alignas(16) SharedCut {
+  long long blocks;  // weight of all blocks
+  long long block_range, row_range;  // weight of a CTA's range
+  int block_ctas, pad;
+  __device__ long long begin(int cta, long long total) const {
+    return cta < block_ctas ? min(block_range * cta, blocks)
+                            : min(blocks + row_range * (cta - block_ctas), total);
+  }
+  __device__ int block_cta(long long at) const { return (int)shared_divide(at, block_range); }
+  __device__ int row_cta(long long at) const {
+    return block_ctas + (int)shared_divide(at - blocks, row_range);
+  }
+};
+
+static_assert(sizeof(SharedCut) == kSharedCutBytes, "the host's share of the workspace");
+
+template <int D>
+__device__ __forceinline__ SharedCut shared_cut(long long blocks, long long total, int ctas) {
+  // (no range between two pages' beginnings)
+  const long long least = max(kMinPages * unit_own(D), kUnitTwo);
+  const long long rows = total - blocks;
+  SharedCut c;
+  c.blocks = blocks;
+  c.block_ctas = blocks == 0 ? 0 : ctas;
+  if (blocks > 0 && rows > 0) {
+    const float share = (float)blocks / (float)total * (float)ctas;
+    int n = min(max((int)share & ~1, 2), ctas - 2);  // or two more
+    if (n + 2 < ctas && (float)blocks * (float)(ctas - n - 2) > (float)rows * (float)n) n += 2;
+    c.block_ctas = n;
+  }
+  c.block_range = max(shared_divide(blocks + c.block_ctas - 1, max(c.block_ctas, 1)), least);
+  c.row_range = max(shared_divide(rows + ctas - c.block_ctas - 1, max(ctas - c.block_ctas, 1)), least);
+  return c;
+}
+
 // The rows' partials come after the blocks', at an even place (as all steps from there
 // are): two heads' (m, l) are stored together.
 __device__ __forceinline__ long long shared_own_part(const SharedParams& p) {
   return ((long long)p.rows * p.hq + 1) & ~1ll;
-}
-
-// a / b of weights, a >= 0, b > 0 (64-bit division is a hundred instructions).
-__device__ __forceinline__ long long shared_divide(long long a, long long b) {
-  return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // The last g of 0 .. groups with starts[g] <= b, -1: none.  Rows of g = -1 and
@@ -246,7 +285,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
   __shared__ volatile int abort_flag;
   __shared__ uint32_t tmem_slot;
   __shared__ long long warp_sum[C::kThreads / 32];
-  __shared__ long long start_rem;
+  __shared__ long long start_rem, block_weight;
   __shared__ int start_item;
   // tile rows of the pages by page % 64 (K is never that far ahead of V: a page's
   // consumer needs both, and eight or so are at work), how many copies are issued, and
@@ -293,7 +332,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
 
   // ---------------------------------------------------------------- the cut
   const int S = p.groups, items = S + p.rows;
-  long long Q, u0, u1;  // units a CTA, this one's range
+  long long u0, u1;  // this CTA's range of weights
   // pages, first page, first row, end or position of each item, where every thread has one
   int4* list = reinterpret_cast<int4*>(base + C::kBarOff) - C::kThreads;  // (the last stage's end)
   {
@@ -320,12 +359,13 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       return shared_row<D>(p, run == 1 ? n_mine : p.positions[i - S],
                         g >= 0 && g < S ? g_pages[g] : 0);
     };
-    long long sum = 0;
+    long long sum = 0, blocks_sum = 0;  // of these items, and of those that are blocks
     int g_mine = -1;
     bool bad_mine = unsorted;
     if (!unsorted)
       for (int i = i0; i < i1; ++i) {
         const SharedItem it = item_at(i, g_mine);
+        if (i == S) blocks_sum = sum;
         sum += it.weight(p.hkv);
         bad_mine = it.bad;
         if (run == 1)  // the producer's list
@@ -346,15 +386,15 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (w < warp) at += warp_sum[w];
       total += warp_sum[w];
     }
-    Q = shared_divide(total + ctas - 1, ctas);
-    if (Q < kMinPages * unit_own(D)) Q = kMinPages * unit_own(D);
-    if (Q < kUnitTwo) Q = kUnitTwo;  // (no range between two pages' beginnings)
-    u0 = min(Q * cta, total);
-    u1 = min(u0 + Q, total);
+    if (i0 <= S && S < i1) block_weight = at + blocks_sum;  // (there is a row)
+    __syncthreads();
+    const SharedCut cut = shared_cut<D>(block_weight, total, ctas);
+    u0 = cut.begin(cta, total);
+    u1 = cut.begin(cta + 1, total);
     // the last CTA, whose range may be short, leaves the combine what it needs
     const bool records = cta == ctas - 1;
     if (records && tid == 0) {
-      *p.units = Q;
+      *p.cut = cut;
       if (unsorted) record_error(p.err, PGD_EDEVICE_BOUNDS);
     }
     auto each_item = [&](auto f) {  // f(item, group, offset, weight, bad) of this thread's items
@@ -1088,7 +1128,7 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
   pdl_allow_dependents();
   const int4* words = reinterpret_cast<const int4*>(p.records + b);
   const int4 w0 = words[0], w1 = words[1];
-  const long long Q = *p.units;
+  const SharedCut cut = *p.cut;
   SharedRecord r;
   *reinterpret_cast<int4*>(&r) = w0;
   *(reinterpret_cast<int4*>(&r) + 1) = w1;
@@ -1108,23 +1148,22 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
       const int rows = min(block, r.end - row0);
       const long long first =
           r.group + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
-      const long long c0 = shared_divide(first, Q);
-      count0 =
-          (int)(shared_divide(first + (long long)(group.pages - 1) * group.unit, Q) - c0) + 1;
-      at0 = 256 * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G + g_head;
+      const int c0 = cut.block_cta(first);
+      count0 = cut.block_cta(first + (long long)(group.pages - 1) * group.unit) - c0 + 1;
+      at0 = 256ll * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G + g_head;
     }
     // its own pages': range i of a CTA has one for each page, at most four
     const long long first = own_off + kvh * own.pair() + own.fixed;
-    const long long c0 = shared_divide(first, Q);
-    const int ranges =
-        (int)(shared_divide(first + (long long)(own.pages - 1) * own.unit, Q) - c0) + 1;
-    const long long at1 = 256 * c0 + shared_own_part(p) +
+    const int c0 = cut.row_cta(first);
+    const int ranges = cut.row_cta(first + (long long)(own.pages - 1) * own.unit) - c0 + 1;
+    const long long rest = cut.blocks + (c0 - cut.block_ctas + 1) * cut.row_range - first;
+    const long long at1 = 256ll * c0 + shared_own_part(p) +
                           4ll * Gp * ((long long)b * p.hkv + kvh);
     // pages that start before the end of range i
     auto before = [&](int i) {
       return i + 1 >= ranges
                  ? own.pages
-                 : (int)shared_divide((c0 + i + 1) * Q - first + own.unit - 1, own.unit);
+                 : (int)shared_divide(rest + i * cut.row_range + own.unit - 1, own.unit);
     };
     int count = count0;
     for (int i = 0, pg = 0; i < ranges; ++i) {
