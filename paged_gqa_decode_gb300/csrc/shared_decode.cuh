@@ -480,16 +480,22 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     int row_seen = -1, row_id = 0, next_row = -1, next_id = 0;
     bool row_bad = false;
     auto in_pool = [&](int id) { return id >= 0 && id < p.num_pages; };
-    auto describe = [&](long long part, int pages, int row0, int kvh, int rows, int what) -> bool {
-      const int d = seq % C::kSegs;
-      if (seq >= C::kSegs && !all_ok(wait(&seg_free[d], (seq / C::kSegs - 1) & 1))) return false;
-      if (lane == 0) {
-        int4* at = reinterpret_cast<int4*>(&segs[d]);
-        at[0] = make_int4((int)part, (int)(part >> 32), pages, row0);
-        at[1] = make_int4(kvh, rows, what, 0);
+    // Descriptors of `heads` (at most kSegs) kv heads from kvh on, one a lane, their
+    // partials part_step apart.
+    auto describe = [&](int heads, long long part, int part_step, int pages, int row0, int kvh,
+                        int rows, int what) -> bool {
+      const int s = seq + lane, d = s % C::kSegs;
+      const bool writes = lane < heads;
+      if (!all_ok(!writes || s < C::kSegs || wait(&seg_free[d], (s / C::kSegs - 1) & 1)))
+        return false;
+      if (writes) {
+        const long long at = part + lane * part_step;
+        int4* to = reinterpret_cast<int4*>(&segs[d]);
+        to[0] = make_int4((int)at, (int)(at >> 32), pages, row0);
+        to[1] = make_int4(kvh + lane, rows, what, 0);
         mbar_arrive(&seg_ready[d]);
       }
-      ++seq;
+      seq += heads;
       return true;
     };
     auto copy_k = [&](int y) -> bool {
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       const int tiles = rows > T ? 2 : 1;
       const int q_tile = tiles == 2 ? 0 : q_next;
       // (partials of the items before: one a lane)
-      if (!describe(256ll * cta + (long long)row0 * p.hq + (long long)kvh * rows * G,
+      if (!describe(1, 256ll * cta + (long long)row0 * p.hq + (long long)kvh * rows * G, 0,
                     count, row0, kvh, rows,
                     SharedSeg::fields(false, tiles, tiles == 2 ? 0 : tile_next, q_tile, kPage - 1)))
         return false;
@@ -568,9 +574,11 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       ++blocks_seen;
       return copy_pages(trow, id, count, kvh * y_head);
     };
-    // Pages pg0 .. pg1 - 1 of a row's own, `pages` from place `first` of its table row on.
-    auto row_segment = [&](int row, int kvh, int first, int pages, int n, int pg0,
-                           int pg1) -> bool {
+    // Pages pg0 .. pg1 - 1 of a row's own, `pages` from place `first` of its table row on, for
+    // `heads` kv heads from kvh on.  (All heads' descriptors at once: head by head, a row of
+    // one page took the producer 0.8 us a head.)
+    auto row_segments = [&](int heads, int row, int kvh, int first, int pages, int n, int pg0,
+                            int pg1) -> bool {
       const int32_t* trow = p.table + (size_t)row * p.maxp + first;
       if (row_seen != row) {
         row_seen = row;
@@ -582,8 +590,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       const int count = pg1 - pg0;
       const bool last = pg1 == pages;
       // (partials of the items before: four a head)
-      if (!describe(256ll * cta + own_part + 4ll * Gp * ((long long)row * p.hkv + kvh),
-                    row_bad ? 0 : count, row, kvh, 1,
+      if (!describe(heads, 256ll * cta + own_part + 4ll * Gp * ((long long)row * p.hkv + kvh),
+                    4 * Gp, row_bad ? 0 : count, row, kvh, 1,
                     SharedSeg::fields(true, 1, 0, 0, last ? n % kPage : kPage - 1)))
         return false;
       if (row_bad) {
@@ -591,28 +599,33 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         return true;
       }
       if (p.k_new != nullptr && last) {
-        // the step's key and value at position n, ahead of the copy of their page
-        const size_t dst =
-            ((size_t)trow[pages - 1] * y_page + kvh * y_head + n % kPage) * D;
+        // the step's keys and values at position n, ahead of the copies of their page
+        constexpr int kWords = D / 8;
+        const size_t dst = ((size_t)trow[pages - 1] * y_page + kvh * y_head + n % kPage) * D;
         const size_t src = ((size_t)row * p.hkv + kvh) * D;
-        if (lane < 2 * (D / 8)) {
-          const int c = lane % (D / 8);
-          const bool is_v = lane >= D / 8;
-          *reinterpret_cast<uint4*>((is_v ? p.v_pool : p.k_pool) + dst + 8 * c) =
-              *reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + src + 8 * c);
+        for (int k = lane; k < 2 * kWords * heads; k += 32) {
+          const int c = k % kWords, h = k / (2 * kWords);
+          const bool is_v = k / kWords % 2;
+          *reinterpret_cast<uint4*>((is_v ? p.v_pool : p.k_pool) + dst + (size_t)h * y_head * D +
+                                    8 * c) =
+              *reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + src + (size_t)h * D +
+                                              8 * c);
         }
         asm volatile("fence.proxy.async.global;" ::: "memory");
         __syncwarp();
       }
       const int id = pg0 == 0 ? row_id : lane < count ? trow[pg0 + lane] : 0;
-      return copy_pages(trow + pg0, id, count, kvh * y_head);
+      for (int h = kvh; h < kvh + heads; ++h)
+        if (!copy_pages(trow + pg0, id, count, h * y_head)) return false;
+      return true;
     };
     // walk the list from the start item on, 32 entries at a time, one a lane
+    constexpr int kMaxHeads = C::kSegs / 2;  // described ahead of their copies
     const int T2 = 2 * T;
     long long u = u0, rem = start_item >= 0 ? start_rem : 0;
     int win = -32;
     int l_first = 0, l_pages = 0, l_n = 0, l_row = 0, l_end = 0;
-      for (int item = start_item; ok && u < u1 && item >= 0 && item < items; ++item, rem = 0) {
+    for (int item = start_item; ok && u < u1 && item >= 0 && item < items; ++item, rem = 0) {
       if (item >= win + 32) {
         // (the first time round the last stage still holds the list)
         const bool listed = win < 0 && items <= C::kThreads;
@@ -676,11 +689,18 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           pg1 = left > fixed
                     ? (int)min((long long)pages, shared_divide(left - fixed + unit - 1, unit))
                     : 0;
-        u += per - at;
+        // whole rows' heads together
+        int heads = 1;
+        if (own && at == 0 && left >= 2 * per) {
+          heads = min(p.hkv - kvh, kMaxHeads);
+          if (left < heads * per) heads = (int)shared_divide(left, per);
+        }
+        u += heads * per - at;
         if (pg0 < pg1)
-          ok = own ? row_segment(s, kvh, first, pages, n, pg0, pg1)
+          ok = own ? row_segments(heads, s, kvh, first, pages, n, pg0, pg1)
                    : block_segment(s + blk * T2, min(T2, e - s - blk * T2), kvh, pg0, pg1);
-        if (++kvh == p.hkv) {
+        kvh += heads;
+        if (kvh == p.hkv) {
           kvh = 0;
           ++blk;
         }
