@@ -69,7 +69,8 @@ SharedLayout shared_layout(const pgd_dims* d) {
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);
   l.off = (l.ml + parts * 2 * sizeof(float) + 15) / 16 * 16;
-  l.bytes = l.off + (size_t)d->rows * sizeof(SharedRecord) + kSharedCutBytes;
+  l.bytes = l.off + (size_t)d->rows * sizeof(SharedRecord) + kSharedCutBytes +
+            16;  // (to a 32-byte boundary, for stores of 32 bytes)
   return l;
 }
 
@@ -612,7 +613,7 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   const SharedLayout l = shared_layout(dims);
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev)) != PGD_OK) return rc;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
   SharedParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.table = table;

@@ -59,6 +59,7 @@ struct SharedCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kPage * D * 2;
   static constexpr int kStages = STAGES;
+  static constexpr int kAhead = STAGES;  // (page, kv head) tiles asked of L2 before the cut
   static constexpr int kQBoxBytes = kLanes * 128;
   static constexpr int kQTileBytes = kBoxes * kQBoxBytes;
   // segments in flight: a short one's round (its row's q, its pages, its products) takes 6 us
@@ -81,12 +82,12 @@ struct SharedCfg {
 };
 
 // Weights in the cut, in about 0.05 us on GB300, fitted to what CTAs of mixed calls
-// took: a page of a block of one or two tiles (two tiles' products and
-// exponentials take longer than the page's bytes), a page of a row's own, and what
-// a (block or row, kv head) costs besides.
-constexpr int kUnitOne = 13, kUnitTwo = 23, kFixedBlock = 60, kFixedOwn = 8;
+// took: a page of a block of one or two tiles (one tile's takes its share of HBM, two
+// tiles' products longer), a page of a row's own, and what a (block or row, kv head)
+// costs besides.  (Own pages at 10 and 8 at head_dim 128, as where they alone load HBM:
+// 256 rows over 65536 shared positions 201 us in place of 189.)
+constexpr int kUnitOne = 13, kUnitTwo = 23, kUnitOwn = 8, kFixedBlock = 60, kFixedOwn = 6;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
-__host__ __device__ constexpr int unit_own(int head_dim) { return head_dim == 64 ? 7 : 10; }
 
 // A run of pages of one item, as the producer lays it out for the other roles.
 struct alignas(16) SharedSeg {
@@ -132,7 +133,6 @@ __device__ __forceinline__ SharedItem shared_group(const SharedParams& p, int s,
 }
 
 // A row at position n; `shared`: pages of its group (0: in none).
-template <int D>
 __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, int shared) {
   SharedItem it;
   it.n = n;
@@ -141,7 +141,7 @@ __device__ __forceinline__ SharedItem shared_row(const SharedParams& p, int n, i
   it.first = shared;
   it.pages = it.n < 0 || it.bad ? 0 : it.n / kPage + 1 - shared;
   it.count = 1;
-  it.unit = unit_own(D);
+  it.unit = kUnitOwn;
   it.fixed = kFixedOwn;
   return it;
 }
@@ -171,10 +171,10 @@ struct alignas(16) SharedCut {
 
 static_assert(sizeof(SharedCut) == kSharedCutBytes, "the host's share of the workspace");
 
-template <int D>
 __device__ __forceinline__ SharedCut shared_cut(long long blocks, long long total, int ctas) {
   // (no range between two pages' beginnings)
-  const long long least = max(kMinPages * unit_own(D), kUnitTwo);
+  constexpr long long least = kMinPages * kUnitOwn;
+  static_assert(least >= kUnitTwo, "a page's weight");
   const long long rows = total - blocks;
   SharedCut c;
   c.blocks = blocks;
@@ -244,6 +244,18 @@ __device__ __forceinline__ int shared_wait_count(const int* issued, const int* t
       }
     }
   }
+}
+
+// Asks for `bytes` (of 16) at a 16-byte boundary.
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+
+// 32 bytes, a whole sector, at a 32-byte boundary.
+__device__ __forceinline__ void store8(float* at, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 struct SharedScore {
@@ -350,13 +362,29 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (g < S) g_pages[g] = p.pages[g];
     }
     unsorted = __syncthreads_or(unsorted);  // every row is bad then
+    // some of the groups' pages on their way to L2 while the cut is made: whose they are
+    // shows only then, and HBM would wait for it (16 groups of 4 rows
+    // 53.8 -> 53.1 us)
+    int ahead_id = -1;
+    const int ahead = cta / max(S, 1) * C::kAhead + lane;  // a (page, kv head) of group cta % S
+    if (warp == C::kVWarp && lane < C::kAhead && S > 0 && !unsorted) {
+      const int g = cta % S, pages = g_pages[g];
+      if (g_start[g] < g_start[g + 1] && pages <= p.maxp && ahead / p.hkv < pages)
+        ahead_id = p.table[(size_t)g_start[g] * p.maxp + ahead / p.hkv];
+      if (ahead_id >= 0 && ahead_id < p.num_pages) {
+        const size_t at = tile_first_row(p.layout, ahead_id, ahead % p.hkv, p.hkv, p.num_pages, 1) *
+                          (size_t)D;
+        prefetch_l2(p.k_pool + at, C::kTileBytes);
+        prefetch_l2(p.v_pool + at, C::kTileBytes);
+      }
+    }
     auto item_at = [&](int i, int& g) {
       if (i < S) {
         g = i;
         return shared_group(p, g_start[i], g_start[i + 1], g_pages[i]);
       }
       g = S > 0 ? shared_find(g_start, S, i - S) : -1;
-      return shared_row<D>(p, run == 1 ? n_mine : p.positions[i - S],
+      return shared_row(p, run == 1 ? n_mine : p.positions[i - S],
                         g >= 0 && g < S ? g_pages[g] : 0);
     };
     long long sum = 0, blocks_sum = 0;  // of these items, and of those that are blocks
@@ -388,7 +416,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     }
     if (i0 <= S && S < i1) block_weight = at + blocks_sum;  // (there is a row)
     __syncthreads();
-    const SharedCut cut = shared_cut<D>(block_weight, total, ctas);
+    const SharedCut cut = shared_cut(block_weight, total, ctas);
     u0 = cut.begin(cta, total);
     u1 = cut.begin(cta + 1, total);
     // the last CTA, whose range may be short, leaves the combine what it needs
@@ -647,7 +675,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
           } else {
             l_row = i - S;
             const int g = S > 0 ? shared_find(p.starts, S, l_row) : -1;
-            it = shared_row<D>(p, p.positions[l_row], g >= 0 && g < S ? p.pages[g] : 0);
+            it = shared_row(p, p.positions[l_row], g >= 0 && g < S ? p.pages[g] : 0);
           }
           l_first = it.first;
           l_pages = it.pages;
@@ -663,7 +691,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       if (pages == 0) continue;
       const int first = __shfl_sync(0xffffffffu, l_first, j), n = __shfl_sync(0xffffffffu, l_n, j);
       const int s = __shfl_sync(0xffffffffu, l_row, j), e = __shfl_sync(0xffffffffu, l_end, j);
-      const int unit = own ? unit_own(D) : e - s > T ? kUnitTwo : kUnitOne;
+      const int unit = own ? kUnitOwn : e - s > T ? kUnitTwo : kUnitOne;
       const int fixed = own ? kFixedOwn : kFixedBlock;
       // the next row's page ids, needed once this row's heads are through
       int ahead_row = -1, ahead_id = 0;
@@ -1105,10 +1133,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
             tmem_ld16(lane_base + t * D + 16 * q, ov);
             tmem_wait_ld();
             if (live) {
-              float4* dst = reinterpret_cast<float4*>(arow + 16 * q);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                dst[j] = make_float4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+              store8(arow + 16 * q, ov);
+              store8(arow + 16 * q + 8, ov + 8);
             }
           }
         }
@@ -1154,7 +1180,7 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
   *(reinterpret_cast<int4*>(&r) + 1) = w1;
   const long long own_off = r.own;
   const SharedItem group = shared_group(p, r.start, r.end, r.shared);
-  const SharedItem own = shared_row<D>(p, r.n, r.shared);
+  const SharedItem own = shared_row(p, r.n, r.shared);
   uint16_t* out = p.out + ((size_t)b * p.hq + h) * D + lane * kDims;
   float res[kDims];
 #pragma unroll

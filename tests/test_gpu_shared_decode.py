@@ -409,3 +409,15 @@ def test_auto_goes_by_the_tables_pages():
                                                         pgd.KERNEL_TENSOR_CORE))
         assert torch.equal(auto, umma if more else single)
         b.compare(auto, d ** -0.5)
+
+
+@pytest.mark.parametrize("at", [0, 16])
+def test_a_workspace_at_any_16_bytes(at):
+    b = Batch(35, [(5, 3), (70, 2)], np.arange(1, 76) * 5, 32, 8, 128)
+    dims = pgd.make_dims(rows=75, num_q_heads=32, num_kv_heads=8, head_dim=128,
+                         num_pages=b.k.shape[0], max_pages_per_row=b.table.shape[1])
+    need = pgd.shared_decode_workspace_bytes(dims, 2)
+    whole = torch.full((need + 64,), 0xa5, dtype=torch.uint8, device=DEV)
+    assert whole.data_ptr() % 32 == 0
+    b.check(workspace=whole[at:at + need])
+    assert (whole[:at] == 0xa5).all() and (whole[at + need:] == 0xa5).all()
