@@ -632,6 +632,8 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   p.hq = dims->num_q_heads;
   p.hkv = dims->num_kv_heads;
   p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.tile = 128 / p.group;
+  p.block_inverse = (uint32_t)(((1ull << 32) + 2 * p.tile - 1) / (2 * p.tile));
   p.maxp = dims->max_pages_per_row;
   p.num_pages = dims->num_pages;
   p.layout = dims->layout;

@@ -122,6 +122,8 @@ struct SharedParams {
   SharedCut* cut;
   unsigned int* err;
   int rows, groups, hq, hkv, group, maxp, num_pages, layout;
+  int tile;                // rows of a tile, 128 / group
+  uint32_t block_inverse;  // 2^32 / (2 tile), rounded up
   float q_scale_log2;
   const uint16_t* k_new;  // or nullptr
   const uint16_t* v_new;

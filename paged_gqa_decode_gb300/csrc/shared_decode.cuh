@@ -118,16 +118,24 @@ struct SharedItem {
   __device__ long long weight(int hkv) const { return pages > 0 ? count * hkv * pair() : 0; }
 };
 
+// Blocks of n rows, and the block of row n of a group: n / (2 tile) by a multiplication
+// (exact for n up to 65535 + 2 tile).
+__device__ __forceinline__ int shared_block_of(const SharedParams& p, int n) {
+  return (int)__umulhi((unsigned)n, p.block_inverse);
+}
+__device__ __forceinline__ int shared_blocks(const SharedParams& p, int n) {
+  return shared_block_of(p, n + 2 * p.tile - 1);
+}
+
 __device__ __forceinline__ SharedItem shared_group(const SharedParams& p, int s, int e,
                                                    int pages) {
-  const int tile = 128 / p.group, block = 2 * tile;
   SharedItem it;
   it.bad = pages < 0 || pages > p.maxp;
   it.pages = it.bad || e <= s ? 0 : pages;
   it.first = 0;
   it.n = 0;
-  it.count = (e - s + block - 1) / block;
-  it.unit = e - s > tile ? kUnitTwo : kUnitOne;
+  it.count = shared_blocks(p, e - s);
+  it.unit = e - s > p.tile ? kUnitTwo : kUnitOne;
   it.fixed = kFixedBlock;
   return it;
 }
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
                          const __grid_constant__ CUtensorMap q_map, const SharedParams p) {
   using C = SharedCfg<D, STAGES>;
   const int G = p.group;
-  const int T = C::kLanes / G;  // rows of a tile
+  const int T = p.tile;  // rows of a tile
   const int Gp = (G + 1) & ~1;  // heads of a row's partial
   const long long own_part = shared_own_part(p);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -704,10 +712,10 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         }
       }
       const long long per = fixed + (long long)pages * unit;  // of one (block, kv head)
-      const int blocks = own ? 1 : (e - s + T2 - 1) / T2;
+      const int blocks = own ? 1 : shared_blocks(p, e - s);
       int bh = rem == 0 ? 0 : (int)shared_divide(rem, per);
       long long at = rem - bh * per;
-      int blk = bh / p.hkv, kvh = bh - blk * p.hkv;
+      int blk = bh < p.hkv ? 0 : bh / p.hkv, kvh = bh - blk * p.hkv;
       for (; ok && u < u1 && blk < blocks; at = 0) {
         // the pages whose weight begins in [u, u1)
         int pg0 = 0, pg1 = pages;
@@ -1190,7 +1198,8 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     long long at0 = 0;
     int count0 = 0;
     if (r.group >= 0) {
-      const int block = 2 * (128 / G), blk = (b - r.start) / block, row0 = r.start + blk * block;
+      const int block = 2 * p.tile, blk = shared_block_of(p, b - r.start);
+      const int row0 = r.start + blk * block;
       const int rows = min(block, r.end - row0);
       const long long first =
           r.group + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
