@@ -106,7 +106,7 @@ struct SharedRecord {
 };
 
 struct SharedCut;  // what falls to which CTA (shared_decode.cuh)
-constexpr int kSharedCutBytes = 32;
+constexpr int kSharedCutBytes = 48;
 
 struct SharedParams {
   const uint16_t* q;

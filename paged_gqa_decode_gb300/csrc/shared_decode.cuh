@@ -166,36 +166,55 @@ __device__ __forceinline__ long long shared_divide(long long a, long long b) {
 struct alignas(16) SharedCut {
   long long blocks;  // weight of all blocks
   long long block_range, row_range;  // weight of a CTA's range
+  float block_inverse, row_inverse;  // 1 / these, near enough for ctas
   int block_ctas, pad;
   __device__ long long begin(int cta, long long total) const {
     return cta < block_ctas ? min(block_range * cta, blocks)
                             : min(blocks + row_range * (cta - block_ctas), total);
   }
-  __device__ int block_cta(long long at) const { return (int)shared_divide(at, block_range); }
+  __device__ static int cta_of(long long at, long long range, float inverse) {
+    const int n = (int)((float)at * inverse);  // off by one at most
+    const long long rest = at - n * range;
+    return rest < 0 ? n - 1 : rest >= range ? n + 1 : n;
+  }
+  __device__ int block_cta(long long at) const { return cta_of(at, block_range, block_inverse); }
   __device__ int row_cta(long long at) const {
-    return block_ctas + (int)shared_divide(at - blocks, row_range);
+    return block_ctas + cta_of(at - blocks, row_range, row_inverse);
   }
 };
-
 static_assert(sizeof(SharedCut) == kSharedCutBytes, "the host's share of the workspace");
 
-__device__ __forceinline__ SharedCut shared_cut(long long blocks, long long total, int ctas) {
-  // (no range between two pages' beginnings)
+// A CTA's range where n of them take a weight: no less than weight / n (by 2^-20, more than the
+// three roundings can take off), and no less than four pages of a row's own.
+__device__ __forceinline__ long long shared_range(long long weight, int n) {
   constexpr long long least = kMinPages * kUnitOwn;
-  static_assert(least >= kUnitTwo, "a page's weight");
+  static_assert(least >= kUnitTwo, "no range between two pages' beginnings");
+  return max((long long)(__fdividef((float)weight, (float)n) * 1.000001f) + 1, least);
+}
+
+__device__ __forceinline__ SharedCut shared_cut(long long blocks, long long total, int ctas) {
   const long long rows = total - blocks;
   SharedCut c;
+  c.pad = 0;
   c.blocks = blocks;
   c.block_ctas = blocks == 0 ? 0 : ctas;
   if (blocks > 0 && rows > 0) {
-    const float share = (float)blocks / (float)total * (float)ctas;
+    const float share = __fdividef((float)blocks, (float)total) * (float)ctas;
     int n = min(max((int)share & ~1, 2), ctas - 2);  // or two more
     if (n + 2 < ctas && (float)blocks * (float)(ctas - n - 2) > (float)rows * (float)n) n += 2;
     c.block_ctas = n;
   }
-  c.block_range = max(shared_divide(blocks + c.block_ctas - 1, max(c.block_ctas, 1)), least);
-  c.row_range = max(shared_divide(rows + ctas - c.block_ctas - 1, max(ctas - c.block_ctas, 1)), least);
+  c.block_range = shared_range(blocks, max(c.block_ctas, 1));
+  c.row_range = shared_range(rows, max(ctas - c.block_ctas, 1));
+  c.block_inverse = __fdividef(1.f, (float)c.block_range);
+  c.row_inverse = __fdividef(1.f, (float)c.row_range);
   return c;
+}
+
+// Pages whose weight begins before n (>= 0) of one (block or row, kv head)'s, `unit` each.
+__device__ __forceinline__ int shared_pages_before(long long n, int unit) {
+  const unsigned m = (unsigned)n + unit - 1;  // (2^25 pages at most)
+  return (int)(unit == kUnitTwo ? m / kUnitTwo : unit == kUnitOne ? m / kUnitOne : m / kUnitOwn);
 }
 
 // The rows' partials come after the blocks', at an even place (as all steps from there
@@ -719,12 +738,10 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       for (; ok && u < u1 && blk < blocks; at = 0) {
         // the pages whose weight begins in [u, u1)
         int pg0 = 0, pg1 = pages;
-        if (at > fixed) pg0 = (int)shared_divide(at - fixed + unit - 1, unit);
+        if (at > fixed) pg0 = shared_pages_before(at - fixed, unit);
         const long long left = u1 - u + at;
         if (left < per)
-          pg1 = left > fixed
-                    ? (int)min((long long)pages, shared_divide(left - fixed + unit - 1, unit))
-                    : 0;
+          pg1 = left > fixed ? min(pages, shared_pages_before(left - fixed, unit)) : 0;
         // whole rows' heads together
         int heads = 1;
         if (own && at == 0 && left >= 2 * per) {
@@ -1218,7 +1235,7 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     auto before = [&](int i) {
       return i + 1 >= ranges
                  ? own.pages
-                 : (int)shared_divide(rest + i * cut.row_range + own.unit - 1, own.unit);
+                 : shared_pages_before(rest + i * cut.row_range, own.unit);
     };
     int count = count0;
     for (int i = 0, pg = 0; i < ranges; ++i) {
