@@ -421,3 +421,58 @@ def test_a_workspace_at_any_16_bytes(at):
     assert whole.data_ptr() % 32 == 0
     b.check(workspace=whole[at:at + need])
     assert (whole[:at] == 0xa5).all() and (whole[at + need:] == 0xa5).all()
+
+
+@pytest.mark.parametrize("layout", [pgd.PAGE_MAJOR, pgd.HEAD_MAJOR])
+def test_pools_past_32_bits_of_bytes_and_values(layout):
+    """A small batch's pages at the ends of pools of 2.3e9 values, the step among them."""
+    b = Batch(36, [(6, 3), (2, None)], np.arange(1, 9) * 30, 16, 4, 128, layout)
+    pages = 70000
+    place = np.r_[0:3, pages - (b.pages - 3):pages]        # page i of the batch is page place[i]
+    rng = np.random.default_rng(1)
+    place = rng.permutation(place)
+    big = [torch.zeros(pages, 4, 64, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    k_new, v_new = (torch.randn(8, 4, 128, generator=b.gen).bfloat16() for _ in range(2))
+    views = [x if layout == pgd.PAGE_MAJOR else x.view(4, pages, 64, 128).transpose(0, 1) for x in big]
+    for view, small in zip(views, (b.k, b.v)):
+        view[torch.from_numpy(place).to(DEV)] = small.to(DEV)
+    for r, n in enumerate(b.positions):
+        page = b.table[r, n // 64]
+        b.k[page, :, n % 64], b.v[page, :, n % 64] = k_new[r], v_new[r]
+    table = np.where(b.table < b.pages, place[np.minimum(b.table, b.pages - 1)], -1)
+    out = pgd.paged_decode_step(
+        b.q.to(DEV), k_new.to(DEV), v_new.to(DEV), *big, dev(table), dev(b.positions), num_kv_heads=4,
+        layout=layout, group_starts=dev(b.starts), group_pages=dev(b.shared),
+        kernel=pgd.KERNEL_PREFILL_UMMA)
+    assert pgd.get_device_error() == pgd.OK
+    b.compare(out, 128 ** -0.5)
+    for view, small in zip(views, (b.k, b.v)):
+        got = view[torch.from_numpy(place).to(DEV)].cpu()
+        assert torch.equal(got.view(torch.int16), small.view(torch.int16))
+
+
+def test_two_calls_at_once():
+    """Captured steps of two batches, each with its own workspace, replayed on two streams."""
+    batches = [Batch(37, [(200, 40), (9, 3)], np.arange(209) * 7 % 300 + 1, 32, 8, 128),
+               Batch(38, [(3, 30)] * 20, np.arange(60) * 11 % 200 + 1, 64, 8, 64)]
+    runs = []
+    for b in batches:
+        args = (b.q.to(DEV), b.k_pool, b.v_pool, dev(b.table), dev(b.positions))
+        kw = dict(num_kv_heads=b.hkv, group_starts=dev(b.starts), group_pages=dev(b.shared),
+                  kernel=pgd.KERNEL_PREFILL_UMMA)
+        want = pgd.paged_decode_attention(*args, **kw)
+        b.compare(want, b.d ** -0.5)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(5):
+                out = pgd.paged_decode_attention(*args, **kw)
+        runs.append((graph, stream, out, want, args, kw))
+    for _ in range(10):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, _, _ in runs:
+        assert torch.equal(out, want)
+    assert pgd.get_device_error() == pgd.OK
