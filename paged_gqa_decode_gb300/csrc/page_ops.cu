@@ -191,11 +191,13 @@ __device__ __forceinline__ void each_table_entry(const int32_t* table, int rows,
 // entry, eight a thread in flight.  Up to kForkClusterEntries entries one cluster
 // does all steps and meets at cluster barriers (1-2 us a step), with what the rows are
 // in every CTA's shared memory.  Past that its eight SMs' rate of scattered accesses
-// binds (0.3 a cycle each: 30 us a step at 143 000 entries), and a launch a step over
-// all SMs is faster: 4096 rows of 130 entries 166 -> 46 us.
+// binds (0.3 a cycle each), and two launches over all SMs are faster, the second of CTAs
+// that meet at a barrier in memory (1.3 us a step; a launch a step took 3.5, and the
+// host as long as the GPU).  Cluster against grid: 64 rows of 306 entries 21 : 24 us,
+// 512 of 74 24 : 20, 1024 of 76 30 : 22, 4096 of 24 54 : 30.
 constexpr int kForkThreads = 1024;
 constexpr int kForkClaim = INT32_MIN, kForkTail = INT32_MIN / 2;
-constexpr int64_t kForkClusterEntries = 20000;
+constexpr int64_t kForkClusterEntries = 26000;
 
 // What a row is and becomes.  In shared memory, for a CTA that meets with others at
 // every step:
@@ -656,7 +658,10 @@ cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_
 // ------------------------------------------------------------------ copy_pages
 
 // A warp copies 4 KB pieces of (copy, pool, kv head) tiles, 8 x 16 bytes a lane
-// in flight.  Bound by HBM for copies past L2.
+// in flight: pieces, not copies, are shared out, so a few copies of many layers fill the
+// SMs too (40 copies in 24 pools of 2 kv heads of 64: 4.1 us), and a page in part use costs
+// its positions only.  Bound by HBM for copies past L2: 1101 pages of two layers (8 kv heads
+// of 128) in 177 us, 6.5 TB/s, 0.98 of a plain copy's rate.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPiece = 4096;
 
@@ -722,10 +727,12 @@ cudaError_t launch_copy_pages(const CopyParams& p, int head_dim, int sm_count,
 //   past the first `held` places of the free and held pages together.
 //   free list: free pages left and vacated ones, each at its rank.
 // Bound by latency and the rate of scattered accesses in L2, as fork_rows: one cluster
-// for small pools and tables, all SMs past that (250 007 pages, 514 000 entries: 82 us in
-// the cluster).
+// for small pools and tables; past that all SMs, after a launch that clears the bitmaps.
+// Every CTA sums all bits for itself (2 bits a page out of L2), which is less than handing
+// sums over.  Cluster against grid: 34 000 entries and pages 15 : 16 us, 70 000 20 : 17.5,
+// 128 000 28 : 19.5, 490 000 63 : 25.
 constexpr int kCompactThreads = 1024;
-constexpr int64_t kCompactClusterWork = 100000;  // entries and pages
+constexpr int64_t kCompactClusterWork = 48000;  // entries and pages
 
 // What the bitmaps' sums come to.
 struct CompactSums {

@@ -83,8 +83,8 @@ int device_sms() {
 // Whether AUTO reads a call's rows one by one, groups or not: where all of their tables'
 // pages fit L2, which then serves all but the first of a group's reads, and the shared kernel's
 // cut, partials and their join cost more than it saves.  Rows by themselves against shared, us:
-// 4 MB 12 : 15, 32 MB 8.8 : 16, 64 MB 11.8 : 15.4, 96 MB 13 : 18, 112 MB 17 : 26, 136 MB 19 : 19,
-// 190 MB 19.5 : 18.5, 270 MB 34 : 20, 340 MB 43 : 23, 690 MB 60 : 23.
+// 4 MB 12 : 15, 32 MB 8.8 : 16, 64 MB 12 : 17, 96 MB 13 : 17, 112 MB 17 : 21, 136 MB 19 : 19,
+// 190 MB 19.4 : 18.3, 270 MB 34 : 20, 340 MB 43 : 22, 690 MB 60 : 24.
 constexpr int64_t kSharedRowBytes = 128ll << 20;
 bool shared_row_by_row(const pgd_dims* d) {
   return (int64_t)d->rows * d->num_kv_heads * d->max_pages_per_row * kPageSize * d->head_dim * 4 <=

@@ -19,16 +19,28 @@
 // paged_decode.cuh), four warps taking pages in turn -- a tile of tcgen05 would
 // have G of 128 lanes in use and one warp's exponentials to wait for on every
 // page (measured so: a page of 16 KB in 0.8 us, its share of HBM 0.37).
-// All items' pages form one sequence, cut into ranges of near-equal weight, one
-// a CTA (one CTA per SM): no CTA ends early, whatever the groups' and rows'
-// lengths.  A CTA's range covers the end of one item, whole items, the start of
-// another; each such segment leaves partials (m, l, o), which the combine launch
-// joins.  Segments walk a staircase (each next one is of the next item or the
-// next CTA), so segment (item, cta) keeps its partials at
+// The blocks' pages form one sequence, the rows' own another, each cut into ranges
+// of near-equal weight, one a CTA (one CTA per SM; the blocks' CTAs first): no CTA ends
+// early, whatever the groups' and rows' lengths.  A CTA's range covers the end of one
+// item, whole items, the start of another; each such segment leaves partials (m, l, o),
+// which the combine launch joins.  Segments walk a staircase (each next one is of the
+// next item or the next CTA), so segment (item, cta) keeps its partials at
 //   [partials of the items before] + 256 * cta + its own
 // without a table: a block's, one per lane, then a row's, one per head from each of
-// the four warps that had a page (a merge of the warps cost 2 us a segment).  Offsets: every CTA sums the items' weights itself (two
-// barriers, less than a launch); CTA 0 leaves them for the combine.
+// the four warps that had a page (a merge of the warps cost 2 us a segment).  Offsets:
+// every CTA sums the items' weights itself (three barriers, less than a launch); the
+// last CTA leaves them for the combine.
+//
+// What bounds it (H query heads a kv head, pages of 64 x D):
+//   few rows a group: the bytes.  16 groups of 4 rows (32/8 heads of 128, 500 to 6000
+//   shared positions): 238 MB in 52 us; 131 rows, 128 of them over one prompt (64/8 heads of
+//   64): 288 MB in 63 us.  Of that 5 us pass from the launch to the first copies and 1 to the
+//   join, which takes 6 to 9: chains of loads, in code that no SM has in its caches yet.
+//   many rows: the tensor cores.  A page of two tiles costs 2090 cycles at D = 128, of
+//   which the products need 1792: per tile S 8 x 48 (N = 64: the 128 x 16 operand's
+//   shared-memory reads are longer than the product) and P V 8 x 64 (head and residual).
+//   256 rows over 32768 positions and 16 to 1024 of their own (32/8 heads of 128): 185 us,
+//   1110 TFLOP/s of products, 750 without the residual's.
 //
 // Roles of a CTA (384 threads): warps 0-3 and 4-7 softmax of tile 0 and 1, one
 // thread a TMEM lane (one-tile blocks alternate between the tiles, so that one's
@@ -62,7 +74,7 @@ struct SharedCfg {
   static constexpr int kAhead = STAGES;  // (page, kv head) tiles asked of L2 before the cut
   static constexpr int kQBoxBytes = kLanes * 128;
   static constexpr int kQTileBytes = kBoxes * kQBoxBytes;
-  // segments in flight: a short one's round (its row's q, its pages, its products) takes 6 us
+  // segments in flight: a short one's round (its row's q, its pages, its products) takes 4-6 us
   static constexpr int kSegs = 16;
   static constexpr int kStageOff = kTiles * kQTileBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
@@ -84,8 +96,8 @@ struct SharedCfg {
 // Weights in the cut, in about 0.05 us on GB300, fitted to what CTAs of mixed calls
 // took: a page of a block of one or two tiles (one tile's takes its share of HBM, two
 // tiles' products longer), a page of a row's own, and what a (block or row, kv head)
-// costs besides.  (Own pages at 10 and 8 at head_dim 128, as where they alone load HBM:
-// 256 rows over 65536 shared positions 201 us in place of 189.)
+// costs besides.  (A row's own at 10 and 8 at head_dim 128, as where they alone load HBM:
+// 256 rows over 32768 shared positions 201 us in place of 189.)
 constexpr int kUnitOne = 13, kUnitTwo = 23, kUnitOwn = 8, kFixedBlock = 60, kFixedOwn = 6;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
 
