@@ -410,12 +410,6 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
       const int g = cta % S, pages = g_pages[g];
       if (g_start[g] < g_start[g + 1] && pages <= p.maxp && ahead / p.hkv < pages)
         ahead_id = p.table[(size_t)g_start[g] * p.maxp + ahead / p.hkv];
-      if (ahead_id >= 0 && ahead_id < p.num_pages) {
-        const size_t at = tile_first_row(p.layout, ahead_id, ahead % p.hkv, p.hkv, p.num_pages, 1) *
-                          (size_t)D;
-        prefetch_l2(p.k_pool + at, C::kTileBytes);
-        prefetch_l2(p.v_pool + at, C::kTileBytes);
-      }
     }
     auto item_at = [&](int i, int& g) {
       if (i < S) {
@@ -455,6 +449,12 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
     }
     if (i0 <= S && S < i1) block_weight = at + blocks_sum;  // (there is a row)
     __syncthreads();
+    if (ahead_id >= 0 && ahead_id < p.num_pages) {
+      const size_t at_page =
+          tile_first_row(p.layout, ahead_id, ahead % p.hkv, p.hkv, p.num_pages, 1) * (size_t)D;
+      prefetch_l2(p.k_pool + at_page, C::kTileBytes);
+      prefetch_l2(p.v_pool + at_page, C::kTileBytes);
+    }
     const SharedCut cut = shared_cut(block_weight, total, ctas);
     u0 = cut.begin(cta, total);
     u1 = cut.begin(cta + 1, total);
