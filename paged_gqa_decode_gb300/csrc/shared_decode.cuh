@@ -39,8 +39,10 @@
 //   many rows: the tensor cores.  A page of two tiles costs 2090 cycles at D = 128, of
 //   which the products need 1792: per tile S 8 x 48 (N = 64: the 128 x 16 operand's
 //   shared-memory reads are longer than the product) and P V 8 x 64 (head and residual).
-//   256 rows over 32768 positions and 16 to 1024 of their own (32/8 heads of 128): 185 us,
-//   1110 TFLOP/s of products, 750 without the residual's.
+//   256 rows over 32768 positions and 16 to 1024 of their own (32/8 heads of 128): 182 us,
+//   1130 TFLOP/s of products, 770 without the residual's.
+//   rows' own pages beside those: the way into their SMs, 32 KB in 600 cycles (53 bytes a
+//   cycle); more stages for them or copies issued in pairs change nothing.
 //
 // Roles of a CTA (384 threads): warps 0-3 and 4-7 softmax of tile 0 and 1, one
 // thread a TMEM lane (one-tile blocks alternate between the tiles, so that one's
