@@ -64,7 +64,8 @@ SharedLayout shared_layout(const pgd_dims* d) {
   // one a (row, head) for the shared pages, four for its own (of an even count of heads,
   // at an even place)
   const size_t group = d->num_q_heads / d->num_kv_heads;
-  const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + 4 * ((group + 1) & ~size_t(1))) +
+  const size_t own = 4 * ((group + 1) & ~size_t(1));
+  const size_t parts = (size_t)d->rows * d->num_kv_heads * (group + own) +
                        256 * (size_t)kMaxSharedCtas + 1;
   SharedLayout l;
   l.ml = parts * d->head_dim * sizeof(float);
@@ -613,7 +614,8 @@ int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* grou
   const SharedLayout l = shared_layout(dims);
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev)) != PGD_OK) return rc;
-  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
+  char* ws =
+      reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
   SharedParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.table = table;

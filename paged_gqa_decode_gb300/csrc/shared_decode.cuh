@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         int at = 0;
         unsigned active = 0;
         for (; at < rows && active == 0; at += 32)
-          active = __ballot_sync(0xffffffffu, at + lane < rows && p.positions[row0 + at + lane] >= 0);
+          active = __ballot_sync(0xffffffffu,
+                                 at + lane < rows && p.positions[row0 + at + lane] >= 0);
         if (active == 0) count = 0;  // none: nothing is read
         trow += (size_t)(active ? at - 32 + __ffs(active) - 1 : 0) * p.maxp;
         id = lane < count ? trow[lane] : 0;
@@ -1196,13 +1197,15 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
 }
 
 // Joins the partials of a (row, query head): those over its group's pages, one a CTA of the
-// range that they fell to, then those over its own, up to four a CTA.  Zeros for an inactive row (n < 0), for one that the cut found bad, and
-// where a page was outside the pool (l < 0); NaN where a score was NaN (l is NaN, the maxima
-// pass over it).  A warp each, a CTA the heads of a kv head.  Bound by latency: the
-// places of the partials are worked out from the row's record (one round trip),
-// then 32 partials' (m, l), one a lane, and the first four partials' values load
-// together, and four at a time from there (eight or sixteen: more registers and, what
-// counts more for so short a kernel, more code; 16 groups of 4 rows 54 us in all, 56, 58).
+// range that they fell to, then those over its own, up to four a CTA.  Zeros for an
+// inactive row (n < 0), for one that the cut found bad, and where a page was outside the
+// pool (l < 0); NaN where a score was NaN (l is NaN, the maxima pass over it).  A warp each,
+// a CTA the heads of a kv head.  Bound by latency: 0.9 us after the other kernel's end the
+// row's record (0.6 us), from which the places of the partials are worked out (1.5, most of
+// it instructions on their way to the SM), then 32 partials' (m, l), one a lane, and the
+// first four partials' values load together (1.3), and four at a time from there (0.7 each;
+// eight or sixteen: more registers and, what counts more for so short a kernel, more code;
+// 16 groups of 4 rows 54 us in all, 56, 58).
 template <int D>
 __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams p) {
   constexpr int kDims = D / 32, kBatch = 4;
@@ -1236,7 +1239,8 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
           r.group + ((long long)blk * p.hkv + kvh) * group.pair() + group.fixed;
       const int c0 = cut.block_cta(first);
       count0 = cut.block_cta(first + (long long)(group.pages - 1) * group.unit) - c0 + 1;
-      at0 = 256ll * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G + g_head;
+      at0 = 256ll * c0 + (long long)row0 * p.hq + (long long)kvh * rows * G + (b - row0) * G +
+            g_head;
     }
     // its own pages': range i of a CTA has one for each page, at most four
     const long long first = own_off + kvh * own.pair() + own.fixed;
