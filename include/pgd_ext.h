@@ -318,7 +318,8 @@ PGD_API int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t 
  * pgd_paged_decode_step (both given), full attention, for rows in groups that share
  * their first pages: the rows b of group g, group_starts[g] <= b < group_starts[g + 1],
  * hold the same first group_pages[g] pages, which are read once for all of them (by the
- * table row of any active one; inactive rows, of positions < 0, may hold others).
+ * table row of any of them; rows that are inactive, of positions < 0, or whose position is
+ * in error may hold others).
  *   groups       S in 0 .. 8192; group_starts int32 [S + 1], not decreasing, in [0, rows];
  *                group_pages int32 [S].  Rows in no group are read on their own.
  *   dims         rows at most 65535; layout PAGE_MAJOR or HEAD_MAJOR (else PGD_EUNSUPPORTED).

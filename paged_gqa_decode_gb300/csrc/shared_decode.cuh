@@ -594,19 +594,19 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         id = ahead;
       }
     };
-    // Pages pg0 .. pg1 - 1 of a block's shared ones, by the table row of its first active
-    // row (an inactive one may hold others, or none).
-    auto block_segment = [&](int row0, int rows, int kvh, int pg0, int pg1) -> bool {
+    // Pages pg0 .. pg1 - 1 of a block's `pages` shared ones, by the table row of its first
+    // row that is neither inactive nor in error (those may hold others, or none).
+    auto block_segment = [&](int row0, int rows, int kvh, int pages, int pg0, int pg1) -> bool {
+      auto holds = [&](int row) { return shared_row(p, p.positions[row], pages).pages > 0; };
       const int32_t* trow = p.table + (size_t)row0 * p.maxp + pg0;
       int count = pg1 - pg0, id = lane < count ? trow[lane] : 0;
-      if (p.positions[row0] < 0) {
+      if (!holds(row0)) {
         int at = 0;
-        unsigned active = 0;
-        for (; at < rows && active == 0; at += 32)
-          active = __ballot_sync(0xffffffffu,
-                                 at + lane < rows && p.positions[row0 + at + lane] >= 0);
-        if (active == 0) count = 0;  // none: nothing is read
-        trow += (size_t)(active ? at - 32 + __ffs(active) - 1 : 0) * p.maxp;
+        unsigned held = 0;
+        for (; at < rows && held == 0; at += 32)
+          held = __ballot_sync(0xffffffffu, at + lane < rows && holds(row0 + at + lane));
+        if (held == 0) count = 0;  // none: nothing is read
+        trow += (size_t)(held ? at - 32 + __ffs(held) - 1 : 0) * p.maxp;
         id = lane < count ? trow[lane] : 0;
       }
       bool bad = lane < count && !in_pool(id);
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         u += heads * per - at;
         if (pg0 < pg1)
           ok = own ? row_segments(heads, s, kvh, first, pages, n, pg0, pg1)
-                   : block_segment(s + blk * T2, min(T2, e - s - blk * T2), kvh, pg0, pg1);
+                   : block_segment(s + blk * T2, min(T2, e - s - blk * T2), kvh, pages, pg0, pg1);
         kvh += heads;
         if (kvh == p.hkv) {
           kvh = 0;
