@@ -386,10 +386,12 @@ struct Fork {
         const int q = parent(r), pages = n_pages(r), last = to(r);
         if (c >= n || e >= pages) continue;
         const bool tail = e == pages - 1 && last != -1;  // (-1 where the last page is full)
+        const int page = cells[(q << shift) + c];
+        if (!in_pool(page)) report();  // (adjust looks at entries that some row gives up)
         if (tail && last >= 0)
           p.table[(size_t)r * p.width + e] = last;
         else if (q != r && !tail)
-          p.table[(size_t)r * p.width + e] = cells[(q << shift) + c];
+          p.table[(size_t)r * p.width + e] = page;
       }
       __syncthreads();
     }

@@ -1,12 +1,16 @@
-"""Rows in error beside rows that are not: what decode over shared pages reads for a group."""
+"""Rows in error beside rows that are not: what fork_rows reports, and what decode over shared
+pages reads for a group."""
 import numpy as np
 import pytest
 import torch
 
 import paged_gqa_decode_gb300 as pgd
+from tests import page_side as side
 from tests.test_gpu_shared_decode import Batch
 
 pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -15,6 +19,69 @@ def _built():
     __graft_entry__.build()
     yield
     torch.cuda.synchronize()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(DEV)
+
+
+def fork(state, parents, keep=None):
+    """The call's outputs as arrays, in the model's order, the model's, and the status."""
+    table, lengths, shares, free, head, pages = state
+    t, s, f = dev(table), dev(shares), dev(free)
+    plan = pgd.fork_rows(t, dev(lengths), dev(parents), s, f, free_head=dev([head]),
+                         keep=None if keep is None else dev(keep))
+    status = pgd.get_device_error()
+    want, _ = side.fork_rows(np.asarray(table), lengths, list(parents), keep, shares, free, head,
+                             pages)
+    return [a.cpu().numpy().reshape(-1) for a in (t, s, f) + tuple(plan)], want, status
+
+
+def same(got, want):
+    for name, g, w in zip(("table", "shares", "free_pages") + pgd.ForkPlan._fields, got, want):
+        np.testing.assert_array_equal(g, np.asarray(w).reshape(-1), err_msg=name)
+
+
+# one cluster's table, and one that all SMs take
+@pytest.mark.parametrize("requests,beams,width", [(3, 4, 12), (400, 8, 12)])
+@pytest.mark.parametrize("cut", [False, True])
+def test_an_entry_outside_the_pool_in_a_row_with_one_child(requests, beams, width, cut):
+    """A row that goes on as it is, or as another one, reports its entries outside the pool; one
+    past its pages, or in a row that nobody reads, is nobody's."""
+    rng = np.random.default_rng(31)
+    state = side.random_state(rng, requests, beams, 500, 90, width=width)
+    table, lengths, shares, free, head, pages = state
+    lengths[5] = 4 * 64 + 9
+    fresh = free[head:head + 5]
+    for p in table[5]:
+        if 0 <= p < pages and shares[p]:
+            shares[p] -= 1
+    table[5, :5], head = fresh, head + 5
+    shares[fresh] = 0
+    rows = requests * beams
+    state = table, lengths, shares, free, head, pages
+    keep = np.full(rows, 2 ** 31 - 1)
+    if cut:
+        keep[[5, 6]] = 2 * 64 + 3
+    itself = np.arange(rows)
+    swapped = itself.copy()
+    swapped[[5, 6]] = 6, 5
+    for parents in (itself, swapped):
+        got, want, status = fork(state, parents, keep)
+        assert status == pgd.OK
+        same(got, want)
+        for e in (0, 1, 2) if cut else (0, 1, 3, 4):
+            for page in (-1, pages):
+                holes = table.copy()
+                holes[5, e] = page
+                got, want, status = fork((holes,) + state[1:], parents, keep)
+                same(got, want)
+                assert status == pgd.EDEVICE_BOUNDS, (e, page)
+    past = table.copy()
+    past[5, 5:] = pages
+    got, want, status = fork((past,) + state[1:], swapped, keep)
+    same(got, want)
+    assert status == pgd.OK
 
 
 @pytest.mark.parametrize("hq,hkv,d,layout", [(32, 8, 128, pgd.PAGE_MAJOR), (14, 2, 64, pgd.HEAD_MAJOR)])
