@@ -257,10 +257,11 @@ PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const p
  * count as outputs).
  * Device errors (PGD_EDEVICE_BOUNDS): a length outside [0, 64 W] (taken as 0); a parent
  * outside [-1, R) (taken as -1); an entry outside the pool (its page is not
- * counted); a page given back more often than held; no page, or one outside the pool,
- * for a last page's copy, or a last page outside the pool: the row loses that page, its
- * new length is rounded down to whole pages; a *free_head outside [0, num_free]: nothing is taken
- * or given back; a list with too few places below *free_head: the pages without one are lost to it.
+ * counted); a page given back, or left for a copy of it, by more rows than hold it by its
+ * shares; no page, or one outside the pool, for a last page's copy, or a last page outside
+ * the pool: the row loses that page, its new length is rounded down to whole pages; a
+ * *free_head outside [0, num_free]: nothing is taken or given back; a list with too few
+ * places below *free_head: the pages without one are lost to it.
  */
 PGD_API int pgdx_fork_rows(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
                            int32_t* table, const int32_t* lengths, const int32_t* parents,

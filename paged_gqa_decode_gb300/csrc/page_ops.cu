@@ -308,11 +308,15 @@ struct Fork {
       if (claimed(page, r, e)) atomicAdd(&counts[r], 1);
     });
   }
+  // A row leaves `page`, its last one in part use: a share less, unless its shares say that
+  // nobody is left to hold it (a claim stays as it is for all that look for it).
+  __device__ void leave(int page) const {
+    if (in_pool(page) &&
+        (__ldcg(&p.shares[page]) < 0 || atomicSub(&p.shares[page], 1) < 0))
+      report();
+  }
   __device__ void leave_tails() const {
-    for (int r = thread(); r < p.rows; r += threads()) {
-      const int page = tail_page(r);
-      if (in_pool(page)) atomicSub(&p.shares[page], 1);
-    }
+    for (int r = thread(); r < p.rows; r += threads()) leave(tail_page(r));
   }
   // row r's `n` claimed pages, the `at`-th of `freed` on, to the list (a warp; four
   // entries a lane at once: one at a time, rows of 126 entries took 5 us)
@@ -338,12 +342,14 @@ struct Fork {
       }
     }
   }
+  // The lowest row to claim `page` keeps it, where all have left it and none gave it up.
+  __device__ void claim_tail(int r, int page) const {
+    if (!in_pool(page)) return;
+    const int held = __ldcg(&p.shares[page]);
+    if (held < 0 && held >= kForkTail) atomicMin(&p.shares[page], kForkTail + r);
+  }
   __device__ void claim_tails() const {
-    for (int r = thread(); r < p.rows; r += threads()) {
-      const int page = tail_page(r);
-      if (in_pool(page) && __ldcg(&p.shares[page]) < 0)
-        atomicMin(&p.shares[page], kForkTail + r);
-    }
+    for (int r = thread(); r < p.rows; r += threads()) claim_tail(r, tail_page(r));
   }
   __device__ int listed_head(int freed) const {  // (a list may have no room for some)
     return bad_head() ? head() : max(head() - freed, 0);
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p
   fork.claim();
   if (!all.meet()) return;
   fork.count(p.sources);
-  if (fork.in_pool(tail)) atomicSub(&p.shares[tail], 1);
+  fork.leave(tail);
   if (!all.meet()) return;
   // a run of rows a CTA: the claims before it, and in all
   const int lo = (int)((int64_t)R * fork.cta / fork.ctas);
@@ -576,8 +582,7 @@ __global__ void __launch_bounds__(kForkThreads, 1) fork_grid_kernel(ForkParams p
     for (int k = lo + (tid & 31); k < r; k += 32) at += p.sources[k];
     fork.list(r, before + __reduce_add_sync(0xffffffffu, at), n, freed);
   }
-  if (fork.in_pool(tail) && __ldcg(&p.shares[tail]) < 0)
-    atomicMin(&p.shares[tail], kForkTail + mine);
+  fork.claim_tail(mine, tail);
   if (!all.meet()) return;
   if (mine >= 0) {  // for all CTAs' sums
     p.targets[mine] = fork.last(mine, tail);

@@ -84,6 +84,42 @@ def test_an_entry_outside_the_pool_in_a_row_with_one_child(requests, beams, widt
     assert status == pgd.OK
 
 
+def rows_of_two_pages(rows, width):
+    """Row r holds pages 2 r and 2 r + 1, 100 positions; then row 1's last page is row 0's."""
+    table = np.full((rows, width), -7)
+    table[:, :2] = np.arange(2 * rows).reshape(rows, 2)
+    table[1, 1] = 1
+    return table, np.full(rows, 100), np.zeros(2 * rows + 40, dtype=int), \
+        np.r_[np.delete(np.arange(2 * rows), 3), 2 * rows:2 * rows + 40], 2 * rows - 1, 2 * rows + 40
+
+
+# one cluster's table, and one that all SMs take
+@pytest.mark.parametrize("rows,width", [(5, 3), (2600, 11)])
+def test_more_rows_leave_a_page_than_its_shares_say(rows, width):
+    """Rows 0 and 1 hold page 1, shares say one does.  Whatever becomes of it, it is an error, the
+    same outputs come of it every time, and no page is both held and listed, or listed twice."""
+    state = rows_of_two_pages(rows, width)
+    itself = np.arange(rows)
+    released, crossed = itself.copy(), itself.copy()
+    released[0] = -1                # gives it up; row 1 stays
+    crossed[2] = 1                  # three rows leave it
+    for parents in (released, itself, crossed):
+        runs = [fork(state, parents) for _ in range(20 if rows < 100 else 5)]
+        for got, want, status in runs:
+            assert status == pgd.EDEVICE_BOUNDS
+            for a, b in zip(got, runs[0][0]):
+                np.testing.assert_array_equal(a, b)
+        got, want, _ = runs[0]
+        if parents is released:
+            same(got, want)
+        table, _, free, lengths, _, targets, _, head = got
+        table = table.reshape(rows, width)
+        held = {p for r in range(rows) for p in table[r, :side.pages_of(lengths[r])]}
+        listed = list(free[head[0]:])
+        assert len(set(listed)) == len(listed) and not held & set(listed)
+        assert list(targets[:3] >= 0) == [False, True, parents is crossed]
+
+
 @pytest.mark.parametrize("hq,hkv,d,layout", [(32, 8, 128, pgd.PAGE_MAJOR), (14, 2, 64, pgd.HEAD_MAJOR)])
 def test_a_row_in_error_lends_its_group_no_pages(hq, hkv, d, layout):
     """The first rows of groups, and of a group's second block, are in error; their tables name
