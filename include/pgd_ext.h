@@ -332,11 +332,13 @@ PGD_API int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t 
  *                PGD_EUNSUPPORTED.  pages_per_split is not used.
  * Everything else, inactive rows among it, as there.  A step writes its rows' keys and
  * values to pages of their own: two rows must not hold the page of their positions
- * together.  Device errors (PGD_EDEVICE_BOUNDS, the rows concerned give zeros, a step
- * leaves them unwritten): a row whose position is beyond its table, a page outside the
- * pool and, with PREFILL_UMMA, starts that decrease or lie outside (all rows),
- * group_pages outside [0, max_pages_per_row] (its rows), a row whose position is in its
- * group's pages.
+ * together.  Device errors (PGD_EDEVICE_BOUNDS, the rows concerned give zeros): a row whose
+ * position is beyond its table and, with PREFILL_UMMA, starts that decrease or lie outside
+ * (all rows), group_pages outside [0, max_pages_per_row] (its rows), a row whose position is
+ * in its group's pages: a step leaves these rows unwritten.  A page outside the pool: a step
+ * leaves the row unwritten where that is a page of its own (with TENSOR_CORE: of its last
+ * split, as pgd_paged_decode_step), and writes it where it is one of the group's (of a
+ * split before).
  */
 PGD_API size_t pgdx_shared_decode_workspace_bytes(const pgd_dims* dims, int32_t groups);
 PGD_API int pgdx_shared_decode(const pgd_dims* dims, int32_t groups, const int32_t* group_starts,

@@ -155,3 +155,62 @@ def test_a_row_in_error_lends_its_group_no_pages(hq, hkv, d, layout):
         return r
     b.want = without
     b.check(status=pgd.EDEVICE_BOUNDS, bad=bad + [4])
+
+
+def step(b, kernel, written, **kw):
+    """A step of new values: the pools afterwards hold those of the rows `written`, and nothing
+    else that is new, bit for bit.  Returns the outputs and the status."""
+    rows = len(b.positions)
+    new = [torch.randn(rows, b.hkv, b.d, generator=b.gen).bfloat16() for _ in range(2)]
+    for r in written:
+        n = b.positions[r]
+        for pool, x in zip((b.k, b.v), new):
+            pool[b.table[r, n // 64], :, n % 64] = x[r]
+    out = b.call(*(x.to(DEV) for x in new), kernel=kernel, **kw)
+    status = pgd.get_device_error()
+    for pool, host in ((b.k_pool, b.k), (b.v_pool, b.v)):
+        assert torch.equal(pool.view(torch.int16), b.lay(host).view(torch.int16))
+    return out, status
+
+
+@pytest.mark.parametrize("hq,hkv,d,layout", [(32, 8, 128, pgd.PAGE_MAJOR), (14, 2, 64, pgd.HEAD_MAJOR)])
+def test_what_a_step_writes_of_rows_in_error(hq, hkv, d, layout):
+    """Rows with a page outside the pool among the group's (written), among their own (not),
+    with positions in error (not)."""
+    b = Batch(42, [(4, 6), (3, 2), (2, None)], [90] * 9, hq, hkv, d, layout)
+    good = b.table.copy()
+    b.table[4:7, 1] = b.pages                     # of the second group
+    b.table[1, 6] = -1                            # row 1's own first page, not the new token's
+    b.table[8, 1] = b.pages                       # row 8's, the new token's
+    true = b.positions.copy()
+    b.positions[2], b.positions[7] = 100, b.width * 64
+    out, status = step(b, pgd.KERNEL_PREFILL_UMMA, (0, 3, 4, 5, 6))
+    assert status == pgd.EDEVICE_BOUNDS
+    bad = (1, 2, 4, 5, 6, 7, 8)
+    assert not out[list(bad)].any()
+    at = b.positions.copy()
+    at[list(bad)] = -1
+    b.positions, b.table = at, good
+    b.compare(out, d ** -0.5)
+    # starts that decrease, pages of a group out of range: nothing of their rows is written
+    b = Batch(43, [(4, 6), (3, 2), (2, None)], [90] * 9, hq, hkv, d, layout)
+    shared = b.shared
+    b.shared = [6, 10 ** 6]
+    out, status = step(b, pgd.KERNEL_PREFILL_UMMA, (0, 1, 2, 3, 7, 8))
+    assert status == pgd.EDEVICE_BOUNDS and not out[4:7].any() and bool((out[:4] != 0).any())
+    b.shared, b.starts = shared, [0, 8, 7]
+    out, status = step(b, pgd.KERNEL_PREFILL_UMMA, ())
+    assert status == pgd.EDEVICE_BOUNDS and not out.any()
+
+
+def test_what_a_step_writes_row_by_row():
+    """A page outside the pool in a split before the last one: the row is written, its output zero."""
+    b = Batch(44, [(4, 40)], [1500] * 4, 32, 8, 128)  # 64 pages a row, splits of 24
+    good = b.table.copy()
+    b.table[1, 3] = b.table[2, 63] = b.pages
+    out, status = step(b, pgd.KERNEL_TENSOR_CORE, (0, 1, 3))
+    assert status == pgd.EDEVICE_BOUNDS and not out[1:3].any()
+    at = b.positions.copy()
+    at[1:3] = -1
+    b.positions, b.table = at, good
+    b.compare(out, 128 ** -0.5)
