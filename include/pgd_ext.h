@@ -262,6 +262,7 @@ PGD_API int pgdx_paged_prefill(const pgd_dims* dims, int32_t table_rows, const p
  * the pool: the row loses that page, its new length is rounded down to whole pages; a
  * *free_head outside [0, num_free]: nothing is taken or given back; a list with too few
  * places below *free_head: the pages without one are lost to it.
+ * PGD_ECUDA leaves table, shares and free_pages as they were, the other outputs undefined.
  */
 PGD_API int pgdx_fork_rows(int32_t rows, int32_t max_pages_per_row, int32_t num_pages,
                            int32_t* table, const int32_t* lengths, const int32_t* parents,

@@ -278,7 +278,7 @@ struct Fork {
   __device__ void adjust() const {
     auto add = [&](int page, int n) {
       if (in_pool(page))
-        atomicAdd(&p.shares[page], n);
+        atomicAdd(&p.shares[page], p.undo ? -n : n);
       else
         report();
     };
@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(ForkParams p) {
 }
 
 // Larger tables: the first step, which leaves the children and least pages (and zeros for
-// claims and for the count of the barriers that follow) in the outputs,
+// claims and for the count of the barriers that follow) in the outputs (p.undo: takes it
+// back, where the launch of the others is refused),
 __global__ void __launch_bounds__(kForkThreads) fork_adjust_kernel(ForkParams p) {
   extern __shared__ int smem[];
   const int R = p.rows, tid = threadIdx.x;
@@ -643,23 +644,34 @@ cudaError_t launch_fork_rows(const ForkParams& params, int sm_count, cudaStream_
       ++p.slab_shift;
     return (words + (1ll << p.slab_shift)) * 4 * (size_t)p.rows;
   };
-  if (entries <= kForkClusterEntries) {
+  auto cluster = [&]() {
     static std::atomic<bool> configured[64];
     const cudaError_t e = allow_smem(fork_rows_kernel, limit, configured);
     if (e != cudaSuccess) return e;
     int ctas = 1;
     while (ctas < 8 && entries > 2048ll * ctas) ctas *= 2;
     return launch_cluster(fork_rows_kernel, ctas, slab(ctas, 5), stream, p);
-  }
+  };
+  p.undo = 0;
+  if (entries <= kForkClusterEntries) return cluster();
   static std::atomic<bool> configured[2][64];
   cudaError_t e = allow_smem(fork_adjust_kernel, limit, configured[0]);
   if (e == cudaSuccess) e = allow_smem(fork_grid_kernel, limit, configured[1]);
-  if (e == cudaSuccess)
-    e = launch_pdl(fork_adjust_kernel, dim3(sm_count), dim3(kForkThreads), 24 * (size_t)p.rows,
-                   stream, p);
+  auto adjust = [&]() {
+    return launch_pdl(fork_adjust_kernel, dim3(sm_count), dim3(kForkThreads), 24 * (size_t)p.rows,
+                      stream, p);
+  };
+  if (e == cudaSuccess) e = adjust();
   if (e != cudaSuccess) return e;
   const size_t smem = slab(sm_count, 3);
-  return launch_grid(fork_grid_kernel, sm_count, smem, stream, p);
+  if (launch_grid(fork_grid_kernel, sm_count, smem, stream, p) == cudaSuccess) return cudaSuccess;
+  // Refused (a context of fewer SMs than the device's): the shares as they were, and all steps
+  // by one cluster, whatever the size.  Where that is refused too, nothing has changed.
+  (void)cudaGetLastError();
+  p.undo = 1;
+  e = adjust();
+  p.undo = 0;
+  return e == cudaSuccess ? cluster() : e;
 }
 
 // ------------------------------------------------------------------ copy_pages
@@ -964,17 +976,22 @@ cudaError_t launch_compact_pages(const CompactParams& params, int sm_count, cuda
   const size_t smem = (size_t)((words + p.step - 1) / p.step) * 8;
   const int64_t work = (int64_t)p.rows * p.width + p.num_pages;
   static std::atomic<bool> configured[2][64];
-  if (work <= kCompactClusterWork) {
+  auto cluster = [&]() {
     const cudaError_t e = allow_smem(compact_pages_kernel<false>, 200 * 1024, configured[0]);
     if (e != cudaSuccess) return e;
     int ctas = 1;
     while (ctas < 8 && work > 2048ll * ctas) ctas *= 2;
     return launch_cluster(compact_pages_kernel<false>, ctas, smem, stream, p);
-  }
+  };
+  if (work <= kCompactClusterWork) return cluster();
   cudaError_t e = allow_smem(compact_pages_kernel<true>, 200 * 1024, configured[1]);
   if (e == cudaSuccess)
     e = launch_pdl(compact_clear_kernel, dim3(32), dim3(kCompactThreads), 0, stream, p);
-  return e == cudaSuccess ? launch_grid(compact_pages_kernel<true>, sm_count, smem, stream, p) : e;
+  if (e != cudaSuccess) return e;
+  e = launch_grid(compact_pages_kernel<true>, sm_count, smem, stream, p);
+  if (e == cudaSuccess) return e;
+  (void)cudaGetLastError();  // refused, as in launch_fork_rows
+  return cluster();
 }
 
 }  // namespace pgd

@@ -58,7 +58,8 @@ struct ForkParams {
   int32_t* free_head_out;
   unsigned int* err;
   int rows, width, num_pages, num_free;
-  int slab_shift;  // (the launcher's)
+  int slab_shift;  // (the launcher's, as the next)
+  int undo;        // fork_adjust_kernel: take its changes to the shares back
 };
 constexpr int kMaxForkRows = 8192;  // five words a row and a column of them in shared memory
 cudaError_t launch_fork_rows(const ForkParams& p, int sm_count, cudaStream_t stream);
