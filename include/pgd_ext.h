@@ -329,8 +329,10 @@ PGD_API int pgdx_compact_pages(int32_t rows, int32_t max_pages_per_row, int32_t 
  *                that the call refuses).
  *   opts         kernel: PREFILL_UMMA (the groups' pages once), TENSOR_CORE (every row by itself,
  *                by its own table entries, without a look at the groups) or AUTO (TENSOR_CORE where
- *                all rows' tables come to 128 MB of pages at most, where that is faster); else
- *                PGD_EUNSUPPORTED.  pages_per_split is not used.
+ *                all rows' tables, whatever of their width is in use, come to 128 MB of pages at
+ *                most); else PGD_EUNSUPPORTED.  For short rows in wide tables and for rows that
+ *                share nothing TENSOR_CORE is the faster one to ask for.  pages_per_split is not
+ *                used.
  * Everything else, inactive rows among it, as there.  A step writes its rows' keys and
  * values to pages of their own: two rows must not hold the page of their positions
  * together.  Device errors (PGD_EDEVICE_BOUNDS, the rows concerned give zeros): a row whose

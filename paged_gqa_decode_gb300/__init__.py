@@ -385,7 +385,8 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     group_starts[g + 1] - 1 hold the same first group_pages[g] pages, which are read
     once for all of them (full attention, none of the above; a workspace of
     shared_decode_workspace_bytes; kernel KERNEL_PREFILL_UMMA does so always, KERNEL_TENSOR_CORE
-    never, AUTO where it is faster).  Returns bf16 [R, Hq, D]."""
+    never, AUTO where the rows' tables, at their full width, come to more than 128 MB of
+    pages).  Returns bf16 [R, Hq, D]."""
     if group_starts is not None or group_pages is not None:
         return _shared_decode(q, None, None, k_pool, v_pool, table, positions, sinks, window,
                               scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,
@@ -410,7 +411,8 @@ def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """kv_append_paged then paged_decode_attention in one launch: each row's
     new K/V (bf16 [R, Hkv, D]) goes to its slot in the pools and the row
-    attends over its pages, the new token included."""
+    attends over its pages, the new token included.  (With groups that are read once for
+    all of their rows, the two calls take less time than this one.)"""
     if group_starts is not None or group_pages is not None:
         return _shared_decode(q, k_new, v_new, k_pool, v_pool, table, positions, sinks, window,
                               scale, num_kv_heads, layout, out, workspace, pages_per_split, kernel,

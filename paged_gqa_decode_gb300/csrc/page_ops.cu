@@ -188,12 +188,13 @@ __device__ __forceinline__ void each_table_entry(const int32_t* table, int rows,
 // page count one each); claims of entries are below that, claims of last pages
 // from there up, so that neither is taken for the other.
 // Bound by latency: each step is a table load and an atomic or load in L2 for every
-// entry, eight a thread in flight.  Up to kForkClusterEntries entries one cluster
-// does all steps and meets at cluster barriers (1-2 us a step), with what the rows are
+// entry, eight a thread in flight.  Up to kForkClusterEntries entries (of the table, in use
+// or not: lengths are on the device) one cluster does all steps and meets at cluster barriers (1-2 us a step), with what the rows are
 // in every CTA's shared memory.  Past that its eight SMs' rate of scattered accesses
 // binds (0.3 a cycle each), and two launches over all SMs are faster, the second of CTAs
 // that meet at a barrier in memory (1.3 us a step; a launch a step took 3.5, and the
-// host as long as the GPU).  Cluster against grid: 64 rows of 306 entries 21 : 24 us,
+// host as long as the GPU).  That one starts once every SM has room for a CTA of it: it
+// waits for the CTAs of other streams' kernels that fill one.  Cluster against grid: 64 rows of 306 entries 21 : 24 us,
 // 512 of 74 24 : 20, 1024 of 76 30 : 22, 4096 of 24 54 : 30.
 constexpr int kForkThreads = 1024;
 constexpr int kForkClaim = INT32_MIN, kForkTail = INT32_MIN / 2;
@@ -746,7 +747,7 @@ cudaError_t launch_copy_pages(const CopyParams& p, int head_dim, int sm_count,
 //   past the first `held` places of the free and held pages together.
 //   free list: free pages left and vacated ones, each at its rank.
 // Bound by latency and the rate of scattered accesses in L2, as fork_rows: one cluster
-// for small pools and tables; past that all SMs, after a launch that clears the bitmaps.
+// for small pools and tables; past that all SMs at once, after a launch that clears the bitmaps.
 // Every CTA sums all bits for itself (2 bits a page out of L2), which is less than handing
 // sums over.  Cluster against grid: 34 000 entries and pages 15 : 16 us, 70 000 20 : 17.5,
 // 128 000 28 : 19.5, 490 000 63 : 25.

@@ -88,7 +88,7 @@ struct CompactParams {
   int32_t* sources;  // [max_moves]
   int32_t* targets;
   int32_t* end;
-  uint32_t* bits;  // workspace: two bitmaps over the pool, a flag, and sums
+  uint32_t* bits;  // workspace: two bitmaps over the pool, a flag, the barriers' count of arrivals
   unsigned int* err;
   int rows, width, num_pages, num_free, max_moves;
   int step;  // (the launcher's)

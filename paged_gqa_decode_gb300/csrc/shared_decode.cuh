@@ -39,8 +39,8 @@
 //   many rows: the tensor cores.  A page of two tiles costs 2090 cycles at D = 128, of
 //   which the products need 1792: per tile S 8 x 48 (N = 64: the 128 x 16 operand's
 //   shared-memory reads are longer than the product) and P V 8 x 64 (head and residual).
-//   256 rows over 32768 positions and 16 to 1024 of their own (32/8 heads of 128): 182 us,
-//   1130 TFLOP/s of products, 770 without the residual's.
+//   256 rows over 32768 positions and 16 to 1024 of their own (32/8 heads of 128): 185 us,
+//   1110 TFLOP/s of products, 757 without the residual's.
 //   rows' own pages beside those: the way into their SMs, 32 KB in 600 cycles (53 bytes a
 //   cycle); more stages for them or copies issued in pairs change nothing.
 //
@@ -98,8 +98,8 @@ struct SharedCfg {
 // Weights in the cut, in about 0.05 us on GB300, fitted to what CTAs of mixed calls
 // took: a page of a block of one or two tiles (one tile's takes its share of HBM, two
 // tiles' products longer), a page of a row's own, and what a (block or row, kv head)
-// costs besides.  (A row's own at 10 and 8 at head_dim 128, as where they alone load HBM:
-// 256 rows over 32768 shared positions 201 us in place of 189.)
+// costs besides.  (A row's own at 10 and 8, as where they alone load HBM: 256 rows over
+// 32768 shared positions 198 us in place of 185, 131 rows of 64 heads 63.8 in place of 62.9.)
 constexpr int kUnitOne = 13, kUnitTwo = 23, kUnitOwn = 8, kFixedBlock = 60, kFixedOwn = 6;
 constexpr int kMinPages = 4;  // of a CTA's range, at least
 
@@ -175,8 +175,9 @@ __device__ __forceinline__ long long shared_divide(long long a, long long b) {
 
 // The ranges of the blocks' weights and of the rows': so many CTAs each, an even number
 // (a pair of CTAs is a TPC, whose SMs slow each other's pages where one reads shared
-// pages and the other rows' own: two tiles' page 1.1 -> 1.6 us), whichever even number
-// leaves the least to the most loaded one.
+// pages and the other rows' own; one such pair among 76 shows little: any number takes 52.3,
+// 63.1, 185.2 us in place of 51.9, 62.9, 184.5 for the header's three calls), whichever even
+// number leaves the least to the most loaded one.
 struct alignas(16) SharedCut {
   long long blocks;  // weight of all blocks
   long long block_range, row_range;  // weight of a CTA's range
@@ -669,7 +670,10 @@ __global__ void __launch_bounds__(SharedCfg<D, STAGES>::kThreads, 1)
         return true;
       }
       if (p.k_new != nullptr && last) {
-        // the step's keys and values at position n, ahead of the copies of their page
+        // The step's keys and values at position n, ahead of the copies of their page.  (They
+        // hold up the producer: a step of 16 groups of 4 rows takes 74 us, of 131 rows of 64
+        // heads 75, of 256 rows over 32768 shared positions 274, where kv_append_paged and
+        // the attention take 55, 66 and 188.)
         constexpr int kWords = D / 8;
         const size_t dst = ((size_t)trow[pages - 1] * y_page + kvh * y_head + n % kPage) * D;
         const size_t src = ((size_t)row * p.hkv + kvh) * D;
@@ -1345,8 +1349,8 @@ cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& k_map,
     if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
   }
   // Clusters of two put neighbouring CTAs on the two SMs of a TPC: an SM that reads
-  // rows' own pages (mma.sync) slows its neighbour's tcgen05 products (a page of two
-  // tiles 1.3 -> 2.0-2.9 us), so both had better do the same.
+  // rows' own pages (mma.sync) slows its neighbour's tcgen05 products, so both had better
+  // do the same (256 rows over 32768 shared positions: 185 us, 226 without clusters).
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(C::kThreads);
